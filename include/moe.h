@@ -115,8 +115,32 @@ typedef enum {
   MOE_OP_COMBINE = 3,
   MOE_OP_FORWARD = 4,
   MOE_OP_FOLD = 5,
-  MOE_OP_PATH = 6   /* moe_path_route and moe_path_sources */
+  MOE_OP_PATH = 6,  /* moe_path_route and moe_path_sources */
+  MOE_OP_ROUTE_GROUPED = 7
 } moe_op;
+
+/* Expert scores of moe_route_grouped. */
+typedef enum {
+  MOE_SCORE_SIGMOID = 0, /* s_e = 1 / (1 + exp(-l_e)) */
+  MOE_SCORE_SOFTMAX = 1  /* s = softmax over all E logits */
+} moe_score;
+
+/* Value of a group of experts in moe_route_grouped. */
+typedef enum {
+  MOE_GROUP_MAX = 0,  /* its largest selection score */
+  MOE_GROUP_TOP2 = 1  /* the sum of its two largest (a group of one: that one) */
+} moe_group_score;
+
+/* Norms of moe_norm and moe_combine_norm. */
+typedef enum { MOE_NORM_RMS = 0, MOE_NORM_LAYER = 1 } moe_norm_kind;
+
+/* Shape of the gate in moe_norm and moe_combine_norm. */
+typedef enum {
+  MOE_GATE_NONE = 0,
+  MOE_GATE_CHANNEL = 1, /* [d]: one factor per channel */
+  MOE_GATE_TOKEN = 2,   /* [T]: one factor per token */
+  MOE_GATE_FULL = 3     /* [T][d] */
+} moe_gate_mode;
 
 /* Expert-folding selectors, for moe_fold. */
 typedef enum {
@@ -511,6 +535,136 @@ moe_status moe_forward(const moe_desc* desc, const void* x, const void* w_router
                        const void* w_up, const void* w_down, const void* ws_gate,
                        const void* ws_up, const void* ws_down, void* out, int32_t* stats,
                        int32_t* dev_status, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * Routing by score, balance bias and groups.  With the logits l of moe_route
+ * (float64 sum, router_bias added, one rounding to float32):
+ *   s_e = sigmoid(l_e) or softmax(l)_e             (float64)
+ *   c_e = s_e + select_bias_e                      (float64; decides, never weighs)
+ *   value of a group (E / n_group consecutive experts) from c: rule->group_score
+ *   the topk_group groups of largest value are kept (ties: lower group)
+ *   the k_t largest c in kept groups are chosen, best first (ties: lower expert)
+ *   w_j = routed_scale * s_j, divided by the sum of the chosen s if rule->renorm
+ * An expert whose c is -inf or NaN is out of service: it is never chosen and
+ * does not count in its group's value; a group without experts in service is
+ * kept last.  A token with fewer than k_t experts to choose from gets id -1 and
+ * weight 0 in its last slots, which moe_permute and moe_combine skip.  If the
+ * chosen scores sum to 0, their renormalised weights are 0.
+ *   rule         1 <= topk_group <= n_group <= 64, n_group divides E,
+ *                k_max <= topk_group * E / n_group (else MOE_ERR_SHAPE)
+ *   select_bias  float [E], or NULL for none
+ *   others       as in moe_route; budgets follow desc->k_policy; desc->router:
+ *                AUTO, FLOAT64 or SCREENED (same ids under each; the weights of
+ *                SCREENED and of AUTO's large bf16 batches are those of logits
+ *                within 2e-6 of sum |x_i w_i| / sqrt(d))
+ *   ws           scratch of moe_workspace_size(MOE_OP_ROUTE_GROUPED) bytes
+ * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED (rule values, or
+ * MOE_ROUTER_FUSED), MOE_ERR_ALIGN, MOE_ERR_WORKSPACE, MOE_ERR_LAUNCH.
+ */
+typedef struct moe_route_rule {
+  int32_t score;       /* moe_score */
+  int32_t n_group;     /* 1: no groups */
+  int32_t topk_group;
+  int32_t group_score; /* moe_group_score */
+  int32_t renorm;      /* 0 or 1 */
+} moe_route_rule;
+
+moe_status moe_route_grouped(const moe_desc* desc, const moe_route_rule* rule, const void* x, const void* w_router,
+                             const float* router_bias, const float* select_bias, const int32_t* k,
+                             int32_t* tok_off, int32_t* topk_ids, float* topk_w, int32_t* dev_status, void* ws,
+                             size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * The norms around a block with its gate and residual scale.  Per token:
+ *   p = post ? norm(y; post_w, post_b) : y
+ *   r = resid + alpha * gate * p                   -> resid_out
+ *   x = norm(r; pre_w, pre_b)                      -> x_out
+ *   norm(v; w, b) = (v - m) / sqrt(mean((v - m)^2) + eps) * (w_offset + w) + b,
+ *   m = mean(v) for MOE_NORM_LAYER, 0 for MOE_NORM_RMS
+ * in float32 throughout; r and x are rounded once each, x from the unrounded r.
+ *   y          ELT [T][d] block output, or NULL (then r = resid, and resid_out,
+ *              gate and the post norm must be absent): the plain norm
+ *   resid      ELT [T][d], or NULL for 0; y and resid not both NULL
+ *   *_w, *_b   ELT [d], or NULL (no weight: factor 1; no bias: 0); post_* are
+ *              ignored unless nd->post
+ *   gate       ELT of the shape nd->gate_mode says, NULL for MOE_GATE_NONE
+ *   resid_out, x_out  ELT [T][d] out, either may be NULL, not both
+ * Each output may be the same buffer as y or resid (in place), not overlap them
+ * in part, and the two outputs may not overlap (MOE_ERR_SHAPE).  Buffers are
+ * 16-byte aligned.  Ranges: T >= 0, 1 <= d <= 65536 (any d), eps >= 0 finite,
+ * alpha and w_offset finite.
+ *
+ * moe_combine_norm: the same with y = moe_combine's sum in float32 (not
+ * rounded), in one launch.  T, d and dtype come from desc and must equal nd's;
+ * y_perm and y_shared must not overlap the outputs.
+ * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED (dtype, kind or gate
+ * mode), MOE_ERR_ALIGN, MOE_ERR_LAUNCH.
+ */
+typedef struct moe_norm_desc {
+  int32_t T, d;
+  int32_t dtype;      /* moe_dtype */
+  int32_t kind;       /* moe_norm_kind of both norms */
+  int32_t post;       /* 1: y is normed before the gate */
+  int32_t gate_mode;  /* moe_gate_mode */
+  float eps;
+  float alpha;        /* residual scale */
+  float w_offset;     /* 1 for weights stored around 0 */
+} moe_norm_desc;
+
+moe_status moe_norm(const moe_norm_desc* nd, const void* y, const void* resid, const void* post_w,
+                    const void* post_b, const void* gate, const void* pre_w, const void* pre_b, void* resid_out,
+                    void* x_out, moe_stream_t stream);
+moe_status moe_combine_norm(const moe_desc* desc, const moe_norm_desc* nd, const void* y_perm, const void* y_shared,
+                            const int32_t* tok_off, const float* topk_w, const int32_t* inv_perm, const void* resid,
+                            const void* post_w, const void* post_b, const void* gate, const void* pre_w,
+                            const void* pre_b, void* resid_out, void* x_out, moe_stream_t stream);
+
+/*
+ * Low-rank adapters of many requests beside a projection y = W x: for row r of
+ * token t = row_tok[r] (r itself if row_tok is NULL) with adapter a =
+ * adapter_ids[t], and expert g (of the row group expert_off[g] ..
+ * expert_off[g+1]-1; 0 without groups),
+ *   y_out[r] = y_in[r] + scales[a] * B[a][g] (A[a][g] x[x_rows[r]])
+ * over the first ranks[a] ranks, both products summed in float32, one rounding
+ * to ELT.  A row without adapter (id outside [0, L), token outside [0, T) or x
+ * row out of range) keeps y_in's bits.  With expert_off, rows from
+ * expert_off[G] on are left as they were.
+ * The rows may be a batch's tokens (a dense projection: the always-on expert,
+ * or any other the caller runs) or moe_permute's rows beside moe_ffn_down
+ * (row_tok = perm_tok, expert_off = its offsets).
+ *   x            ELT [rows][K], or [T][K] with x_rows
+ *   x_rows       int32 [rows] or NULL (row r reads x row r)
+ *   a            ELT [L][G][R][K]
+ *   b            ELT [L][G][N][R]
+ *   ranks        int32 [L] in [0, R] (clamped), or NULL (R); what lies behind an
+ *                adapter's rank is not used
+ *   scales       float [L], or NULL (1)
+ *   adapter_ids  int32 [T]
+ *   row_tok      int32 [rows] or NULL (then T >= rows)
+ *   expert_off   int32 [G+1], or NULL (G = 1: every row)
+ *   y_in, y_out  ELT [rows][N]; the same buffer (in place) or not overlapping,
+ *                and y_out overlaps neither x, a nor b
+ *   ws           scratch of moe_adapt_workspace_size bytes
+ * Ranges: 0 <= rows, T; K and N multiples of 8 up to 65536; R a multiple of 8 up
+ * to 128; 1 <= L <= 65536; 1 <= G <= 1024.  Any ELT buffer: 16-byte aligned.
+ * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE (ranges, overlap), MOE_ERR_UNSUPPORTED
+ * (dtype), MOE_ERR_ALIGN, MOE_ERR_WORKSPACE, MOE_ERR_LAUNCH.
+ */
+typedef struct moe_adapter_desc {
+  int32_t T;      /* tokens (entries of adapter_ids) */
+  int32_t rows;   /* rows of y (with expert_off: their capacity) */
+  int32_t K, N;   /* inputs and outputs of the projection */
+  int32_t R;      /* rank that the matrices are stored with */
+  int32_t L;      /* adapters */
+  int32_t G;      /* experts, 1 for a dense projection */
+  int32_t dtype;  /* moe_dtype */
+} moe_adapter_desc;
+
+moe_status moe_adapt_workspace_size(const moe_adapter_desc* ad, size_t* bytes);
+moe_status moe_adapt(const moe_adapter_desc* ad, const void* x, const int32_t* x_rows, const void* a, const void* b,
+                     const int32_t* ranks, const float* scales, const int32_t* adapter_ids, const int32_t* row_tok,
+                     const int32_t* expert_off, const void* y_in, void* y_out, void* ws, size_t ws_bytes,
+                     moe_stream_t stream);
 
 /*
  * Streaming-read probe (measurement only, not a step of the layer): reads

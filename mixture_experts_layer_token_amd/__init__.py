@@ -17,7 +17,9 @@ from ._lib import (MOE_BF16, MOE_DEV_BAD_K, MOE_F32, MOE_OP_COMBINE, MOE_OP_FFN,
                    MOE_OP_FORWARD, MOE_OP_PERMUTE, MOE_OP_ROUTE, MOE_PATH_AUTO, MOE_PATH_GEMM,
                    MOE_PATH_STREAM, MOE_ROUTER_AUTO, MOE_ROUTER_FLOAT64, MOE_ROUTER_SCREENED, MOE_ROUTER_FUSED, MOE_K_EXACT,
                    MOE_K_BATCH_MAX, MOE_K_ROUND_UP, MOE_OP_FOLD, MOE_OP_PATH, MOE_FOLD_TOKEN, MOE_FOLD_POOL,
-                   MOE_W_ROWMAJOR, MOE_W_BLOCKED64, moe_desc)
+                   MOE_W_ROWMAJOR, MOE_W_BLOCKED64, MOE_OP_ROUTE_GROUPED, MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX,
+                   MOE_GROUP_MAX, MOE_GROUP_TOP2, MOE_NORM_RMS, MOE_NORM_LAYER, MOE_GATE_NONE, MOE_GATE_CHANNEL,
+                   MOE_GATE_TOKEN, MOE_GATE_FULL, moe_adapter_desc, moe_desc, moe_norm_desc, moe_route_rule)
 
 __all__ = [
     "MoeError", "make_desc", "pack_weights", "workspace_size", "resolve_path", "alloc_workspace", "moe_route", "moe_permute",
@@ -27,6 +29,8 @@ __all__ = [
     "moe_proxy_route", "moe_forward", "moe_forward_noalloc",
     "forward", "proxy_width", "proxy_pack", "ProxyRouter", "probe_read",
     "library_path",
+    "make_route_rule", "moe_route_grouped", "make_norm_desc", "moe_norm", "moe_combine_norm", "make_adapter_desc",
+    "adapt_workspace_size", "alloc_adapt_workspace", "moe_adapt", "BlockLayer",
 ]
 
 _DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
@@ -496,3 +500,237 @@ class PathLayer:
             moe_ffn(d, x, w_gate, w_up, w_down, *shared, self.zero_eoff, self.s_ptok, self.y, self.y_sh, self.ws_ffn,
                     stream)
         moe_combine(d, self.y, self.y_sh if d.I_shared else None, self.tok_off, self.w, self.t_inv, out, stream)
+
+
+_SCORES = {"sigmoid": MOE_SCORE_SIGMOID, "softmax": MOE_SCORE_SOFTMAX}
+_GROUP_SCORES = {"max": MOE_GROUP_MAX, "top2": MOE_GROUP_TOP2}
+_NORMS = {"rms": MOE_NORM_RMS, "layer": MOE_NORM_LAYER}
+_GATES = {"none": MOE_GATE_NONE, "channel": MOE_GATE_CHANNEL, "token": MOE_GATE_TOKEN, "full": MOE_GATE_FULL}
+
+
+class _Args:
+    """Addresses of one call's device arguments, which must lie on one GPU: that
+    of the first of them.  The call runs with that GPU current, on `stream` or
+    on the GPU's current stream.  The checks are _dev's, in the few attribute
+    reads that a call of some microseconds can afford."""
+
+    __slots__ = ("device",)
+
+    def __init__(self):
+        self.device = None
+
+    def __call__(self, t, name, dtype=None, numel=0):
+        if t is None:
+            return None
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
+        device = t.get_device()
+        if device != self.device:
+            if device < 0:
+                raise ValueError(f"{name}: must be a device tensor (got {t.device})")
+            if self.device is not None:
+                raise ValueError(f"{name}: on {t.device}, the call's other tensors are on cuda:{self.device}")
+            self.device = device
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: must be contiguous")
+        if dtype is not None and t.dtype is not dtype:
+            raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+        if t.numel() < numel:
+            raise ValueError(f"{name}: {t.numel()} elements, at least {numel} needed")
+        return t.data_ptr()
+
+    def run(self, fn, stream, *args):
+        if stream is not None and self.device is not None and stream.device_index != self.device:
+            raise ValueError(f"stream: on cuda:{stream.device_index}, the call's tensors are on cuda:{self.device}")
+        entry = getattr(_lib.load(), fn)
+        if self.device is None or self.device == torch.cuda.current_device():
+            status = entry(*args, (stream or torch.cuda.current_stream()).cuda_stream)
+        else:
+            with torch.cuda.device(self.device):
+                status = entry(*args, (stream or torch.cuda.current_stream()).cuda_stream)
+        if status != 0:
+            raise MoeError(fn, status)
+
+
+def make_route_rule(*, score: str = "sigmoid", n_group: int = 1, topk_group: int = 1, group_score: str = "top2",
+                    renorm: bool = True) -> moe_route_rule:
+    """Rule of moe_route_grouped.  score: "sigmoid" or "softmax"; n_group groups of
+    consecutive experts, of which the topk_group of largest group_score ("max" or
+    "top2") are kept; renorm: weights divided by the sum of the chosen scores."""
+    return moe_route_rule(_SCORES[score], n_group, topk_group, _GROUP_SCORES[group_score], int(bool(renorm)))
+
+
+def moe_route_grouped(desc, rule, x, w_router, router_bias, select_bias, k, tok_off, topk_ids, topk_w, dev_status, ws,
+                      stream=None) -> None:
+    """Routes by score, balance bias (select_bias, float32 [E]) and groups of
+    experts; the outputs are moe_route's.  A slot without an expert has id -1 and
+    weight 0.  ws: alloc_workspace(desc, MOE_OP_ROUTE_GROUPED)."""
+    T, d, E, el, p = desc.T, desc.d, desc.E, _ELT[desc.dtype], _Args()
+    p.run("moe_route_grouped", stream, desc, rule, p(x, "x", el, T * d), p(w_router, "w_router", el, E * d),
+          p(router_bias, "router_bias", _F32, E), p(select_bias, "select_bias", _F32, E), p(k, "k", _I32, T),
+          p(tok_off, "tok_off", _I32, T + 1), p(topk_ids, "topk_ids", _I32, T * desc.k_max),
+          p(topk_w, "topk_w", _F32, T * desc.k_max), p(dev_status, "dev_status", _I32, 1), p(ws, "ws"), _nbytes(ws))
+
+
+def make_norm_desc(T: int, d: int, *, dtype=torch.bfloat16, kind: str = "rms", eps: float = 1e-6, alpha: float = 1.0,
+                   w_offset: float = 0.0, gate: str = "none", post: bool = False) -> moe_norm_desc:
+    """Descriptor of moe_norm and moe_combine_norm.  kind: "rms" or "layer"; gate:
+    "none", "channel" ([d]), "token" ([T]) or "full" ([T, d]); post: the block's
+    output is normed before the gate; alpha: the residual scale; w_offset: added
+    to the norm weights (1 for weights stored around 0)."""
+    return moe_norm_desc(T, d, _DTYPES[dtype], _NORMS[kind], int(bool(post)), _GATES[gate], eps, alpha, w_offset)
+
+
+def _norm_args(p, nd, resid, post_w, post_b, gate, pre_w, pre_b, resid_out, x_out):
+    T, d, el = nd.T, nd.d, _ELT[nd.dtype]
+    n_gate = (0, d, T, T * d)[nd.gate_mode]
+    return (p(resid, "resid", el, T * d), p(post_w, "post_w", el, d), p(post_b, "post_b", el, d),
+            p(gate, "gate", el, n_gate), p(pre_w, "pre_w", el, d), p(pre_b, "pre_b", el, d),
+            p(resid_out, "resid_out", el, T * d), p(x_out, "x_out", el, T * d))
+
+
+def moe_norm(nd, y, resid, post_w, post_b, gate, pre_w, pre_b, resid_out, x_out, stream=None) -> None:
+    """r = resid + alpha * gate * (post norm of y, or y) into resid_out and the
+    norm of r into x_out (either may be None).  y None: the norm of resid."""
+    p = _Args()
+    p.run("moe_norm", stream, nd, p(y, "y", _ELT[nd.dtype], nd.T * nd.d),
+          *_norm_args(p, nd, resid, post_w, post_b, gate, pre_w, pre_b, resid_out, x_out))
+
+
+def moe_combine_norm(desc, nd, y_perm, y_shared, tok_off, topk_w, inv_perm, resid, post_w, post_b, gate, pre_w, pre_b,
+                     resid_out, x_out, stream=None) -> None:
+    """moe_norm with y = moe_combine's sum, kept in float32, in one launch."""
+    T, A, el, p = desc.T, desc.T * desc.k_max, _ELT[desc.dtype], _Args()
+    p.run("moe_combine_norm", stream, desc, nd, p(y_perm, "y_perm", el, A * desc.d),
+          p(y_shared, "y_shared", el, T * desc.d), p(tok_off, "tok_off", _I32, T + 1), p(topk_w, "topk_w", _F32, A),
+          p(inv_perm, "inv_perm", _I32, A),
+          *_norm_args(p, nd, resid, post_w, post_b, gate, pre_w, pre_b, resid_out, x_out))
+
+
+def make_adapter_desc(T: int, rows: int, K: int, N: int, R: int, L: int, G: int = 1, *,
+                      dtype=torch.bfloat16) -> moe_adapter_desc:
+    """Descriptor of moe_adapt: L adapters of rank up to R (matrices [L, G, R, K]
+    and [L, G, N, R]) beside a [K] -> [N] projection of `rows` rows, which belong
+    to T tokens and, behind the router, to G experts."""
+    return moe_adapter_desc(T, rows, K, N, R, L, G, _DTYPES[dtype])
+
+
+def adapt_workspace_size(ad: moe_adapter_desc) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_adapt_workspace_size", _lib.load().moe_adapt_workspace_size(ctypes.byref(ad), ctypes.byref(n)))
+    return n.value
+
+
+def alloc_adapt_workspace(ad: moe_adapter_desc, device="cuda") -> Optional[torch.Tensor]:
+    n = adapt_workspace_size(ad)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def moe_adapt(ad, x, x_rows, a, b, ranks, scales, adapter_ids, row_tok, expert_off, y_in, y_out, ws,
+              stream=None) -> None:
+    """y_out[r] = y_in[r] + scales[i] * b[i, g] (a[i, g] x[r]) with i the adapter of
+    row r's token (adapter_ids; outside [0, L): y_in's bits) and g the row's
+    expert.  y_out may be y_in.  x_rows, ranks, scales, row_tok and expert_off
+    may be None.  ws: alloc_adapt_workspace(ad)."""
+    T, rows, el, p = ad.T, ad.rows, _ELT[ad.dtype], _Args()
+    n = ad.L * ad.G * ad.R
+    p.run("moe_adapt", stream, ad, p(x, "x", el, (rows if x_rows is None else T) * ad.K),
+          p(x_rows, "x_rows", _I32, rows), p(a, "a", el, n * ad.K), p(b, "b", el, n * ad.N),
+          p(ranks, "ranks", _I32, ad.L), p(scales, "scales", _F32, ad.L), p(adapter_ids, "adapter_ids", _I32, T),
+          p(row_tok, "row_tok", _I32, rows), p(expert_off, "expert_off", _I32, ad.G + 1),
+          p(y_in, "y_in", el, rows * ad.N), p(y_out, "y_out", el, rows * ad.N), p(ws, "ws"), _nbytes(ws))
+
+
+class BlockLayer:
+    """Buffers and calls of one MoE block between two attention blocks, for a
+    fixed shape: the norm before the block fused with the residual add, grouped
+    routing, the permutation, the expert FFN, per-request adapters on the experts'
+    down projections (and on the always-on expert's), and the combine fused with
+    the norm behind the block, its gate, the residual and the next norm.
+    ``run`` only launches (no allocation), so it can be captured in a graph."""
+
+    def __init__(self, desc: moe_desc, rule: moe_route_rule, before: moe_norm_desc, behind: moe_norm_desc, *,
+                 adapters: int = 0, shared_adapters: int = 0, rank: int = 16, device="cuda"):
+        self.desc, self.rule, self.before, self.behind = desc, rule, before, behind
+        T, d, E, I, km = desc.T, desc.d, desc.E, desc.I, desc.k_max
+        if shared_adapters and not desc.I_shared:
+            raise ValueError("shared_adapters: the descriptor has no shared expert")
+        dtype = _ELT[desc.dtype]
+        i32 = dict(dtype=torch.int32, device=device)
+        A = max(T * km, 1)
+        self.x = torch.empty((max(T, 1), d), dtype=dtype, device=device)
+        self.resid = torch.empty_like(self.x)
+        self.tok_off = torch.empty(T + 1, **i32)
+        self.ids = torch.empty(A, **i32)
+        self.w = torch.empty(A, dtype=torch.float32, device=device)
+        self.status = torch.empty(1, **i32)
+        self.counts = torch.empty(E, **i32)
+        self.eoff = torch.empty(E + 1, **i32)
+        self.ptok, self.psrc, self.inv = (torch.empty(A, **i32) for _ in range(3))
+        self.nact = torch.empty(1, **i32)
+        self.y = torch.empty((A, d), dtype=dtype, device=device)
+        self.y_sh = torch.empty((max(T, 1), d), dtype=dtype, device=device) if desc.I_shared else None
+        self.ws_route = alloc_workspace(desc, MOE_OP_ROUTE_GROUPED, device)
+        self.ws_perm = alloc_workspace(desc, MOE_OP_PERMUTE, device)
+        self.ws_ffn = alloc_workspace(desc, MOE_OP_FFN, device)
+        self.adapt = self.adapt_shared = None
+        if adapters or shared_adapters:
+            self.h = torch.empty((A, I), dtype=dtype, device=device)
+        if adapters:
+            self.adapt = make_adapter_desc(T, T * km, I, d, rank, adapters, E, dtype=dtype)
+            self.ws_adapt = alloc_adapt_workspace(self.adapt, device)
+        if desc.I_shared and (adapters or shared_adapters):
+            # the FFN in parts: the routed experts alone, the always-on expert as a
+            # layer of one expert whose rows are the tokens
+            Is = desc.I_shared
+            self.sh = make_desc(T, d, 1, Is, 1, dtype=dtype)
+            self.sh.weight_layout = desc.weight_layout
+            self.sh_eoff = torch.tensor([0, T], **i32)
+            self.sh_tok = torch.arange(max(T, 1), **i32)
+            self.h_sh = torch.empty((max(T, 1), Is), dtype=dtype, device=device)
+            self.ws_sh = alloc_workspace(self.sh, MOE_OP_FFN, device)
+        if shared_adapters:
+            self.adapt_shared = make_adapter_desc(T, T, desc.I_shared, d, rank, shared_adapters, 1, dtype=dtype)
+            self.ws_adapt_sh = alloc_adapt_workspace(self.adapt_shared, device)
+
+    def run(self, y, resid, pre_w, w_router, select_bias, k, w_gate, w_up, w_down, resid_out, x_out, *, shared=None,
+            before_post_w=None, before_gate=None, behind_post_w=None, behind_gate=None, next_w=None, router_bias=None,
+            adapters=None, shared_adapters=None, stream=None):
+        """y: the attention block's output (None: resid is normed as it is).
+        adapters: (a, b, ranks, scales, adapter_ids) of moe_adapt with a [L, E, R, I]
+        and b [L, E, d, R]; shared_adapters the same with one expert."""
+        d = self.desc
+        if d.I_shared and shared is None:
+            raise ValueError("the descriptor has a shared expert: pass its weights")
+        if (adapters is None) != (self.adapt is None) or (shared_adapters is None) != (self.adapt_shared is None):
+            raise ValueError("adapters: pass what the layer was made for")
+        moe_norm(self.before, y, resid, before_post_w, None, before_gate, pre_w, None,
+                 None if y is None else self.resid, self.x, stream)
+        mid = resid if y is None else self.resid
+        moe_route_grouped(d, self.rule, self.x, w_router, router_bias, select_bias, k, self.tok_off, self.ids, self.w,
+                          self.status, self.ws_route, stream)
+        moe_permute(d, self.tok_off, self.ids, self.counts, self.eoff, self.ptok, self.psrc, self.inv, self.nact,
+                    self.ws_perm, stream)
+        sh = shared if shared is not None else (None, None, None)
+        if adapters is None and shared_adapters is None:
+            moe_ffn(d, self.x, w_gate, w_up, w_down, *sh, self.eoff, self.ptok, self.y, self.y_sh, self.ws_ffn, stream)
+        else:
+            h = self.h
+            moe_ffn_plan(d, self.eoff, self.ws_ffn, stream)
+            moe_ffn_gateup(d, self.x, w_gate, w_up, self.eoff, self.ptok, h, self.ws_ffn, stream)
+            moe_ffn_down(d, h, w_down, self.eoff, self.y, self.ws_ffn, stream)
+            if adapters is not None:
+                a, b, ranks, scales, ids = adapters
+                moe_adapt(self.adapt, h, None, a, b, ranks, scales, ids, self.ptok, self.eoff, self.y, self.y,
+                          self.ws_adapt, stream)
+            if d.I_shared:
+                moe_ffn_plan(self.sh, self.sh_eoff, self.ws_sh, stream)
+                moe_ffn_gateup(self.sh, self.x, sh[0], sh[1], self.sh_eoff, self.sh_tok, self.h_sh, self.ws_sh, stream)
+                moe_ffn_down(self.sh, self.h_sh, sh[2], self.sh_eoff, self.y_sh, self.ws_sh, stream)
+            if shared_adapters is not None:
+                a, b, ranks, scales, ids = shared_adapters
+                moe_adapt(self.adapt_shared, self.h_sh, None, a, b, ranks, scales, ids, None, None, self.y_sh,
+                          self.y_sh, self.ws_adapt_sh, stream)
+        moe_combine_norm(d, self.behind, self.y, self.y_sh, self.tok_off, self.w, self.inv, mid, behind_post_w, None,
+                         behind_gate, next_w, None, resid_out, x_out, stream)
+        return resid_out, x_out

@@ -15,6 +15,11 @@ MOE_PATH_AUTO, MOE_PATH_STREAM, MOE_PATH_GEMM = 0, 1, 2
 MOE_ROUTER_AUTO, MOE_ROUTER_FLOAT64, MOE_ROUTER_SCREENED, MOE_ROUTER_FUSED = 0, 1, 2, 3
 MOE_K_EXACT, MOE_K_BATCH_MAX, MOE_K_ROUND_UP = 0, 1, 2
 MOE_OP_ROUTE, MOE_OP_PERMUTE, MOE_OP_FFN, MOE_OP_COMBINE, MOE_OP_FORWARD, MOE_OP_FOLD, MOE_OP_PATH = 0, 1, 2, 3, 4, 5, 6
+MOE_OP_ROUTE_GROUPED = 7
+MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX = 0, 1
+MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
+MOE_NORM_RMS, MOE_NORM_LAYER = 0, 1
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN, MOE_GATE_FULL = 0, 1, 2, 3
 MOE_FOLD_TOKEN, MOE_FOLD_POOL = 0, 1
 MOE_DEV_BAD_K = 1
 MOE_W_ROWMAJOR, MOE_W_BLOCKED64 = 0, 1
@@ -31,7 +36,24 @@ class moe_desc(ctypes.Structure):
                 ("weight_layout", c_i32)]
 
 
+class moe_route_rule(ctypes.Structure):
+    _fields_ = [("score", c_i32), ("n_group", c_i32), ("topk_group", c_i32), ("group_score", c_i32),
+                ("renorm", c_i32)]
+
+
+class moe_norm_desc(ctypes.Structure):
+    _fields_ = [("T", c_i32), ("d", c_i32), ("dtype", c_i32), ("kind", c_i32), ("post", c_i32),
+                ("gate_mode", c_i32), ("eps", ctypes.c_float), ("alpha", ctypes.c_float),
+                ("w_offset", ctypes.c_float)]
+
+
+class moe_adapter_desc(ctypes.Structure):
+    _fields_ = [("T", c_i32), ("rows", c_i32), ("K", c_i32), ("N", c_i32), ("R", c_i32), ("L", c_i32),
+                ("G", c_i32), ("dtype", c_i32)]
+
+
 _P = ctypes.POINTER(moe_desc)
+_PR, _PN, _PA = (ctypes.POINTER(s) for s in (moe_route_rule, moe_norm_desc, moe_adapter_desc))
 
 # name -> argument types (return type is int: moe_status), as in include/moe.h
 SIGNATURES = {
@@ -64,6 +86,11 @@ SIGNATURES = {
     "moe_probe_read": [c_ptr, c_size, c_i32, c_ptr, c_ptr],
     "moe_forward_noalloc": [_P, c_ptr, c_ptr, c_ptr, c_ptr, c_ptr, c_ptr, c_ptr, c_ptr, c_ptr, c_ptr,
                             c_ptr, c_ptr, c_ptr, c_ptr],
+    "moe_route_grouped": [_P, _PR, *[c_ptr] * 10, c_size, c_ptr],
+    "moe_norm": [_PN, *[c_ptr] * 9, c_ptr],
+    "moe_combine_norm": [_P, _PN, *[c_ptr] * 13, c_ptr],
+    "moe_adapt_workspace_size": [_PA, ctypes.POINTER(c_size)],
+    "moe_adapt": [_PA, *[c_ptr] * 12, c_size, c_ptr],
     "moe_status_str": [c_i32],
 }
 

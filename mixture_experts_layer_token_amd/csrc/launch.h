@@ -168,6 +168,52 @@ hipError_t launch_path_sources(const int32_t* tok_off, const int32_t* psrc, int 
 hipError_t launch_path_rows(const int32_t* tok_off, int T, int k_max, const int32_t* perm_path, const int32_t* p2s,
                             const int32_t* src_inv, int32_t* row_map, hipStream_t st);
 
+// route_grouped.hip -- scores, groups and top-k_t from the float64 partial
+// logits of launch_router.
+struct GroupRule {
+  int softmax;     // scores: 1 softmax, 0 sigmoid
+  int n_group;     // groups of E / n_group consecutive experts (<= 64)
+  int topk_group;  // groups kept
+  int top2;        // group value: 1 the sum of the two largest keys, 0 the largest
+  int renorm;      // weights divided by the sum of the chosen scores
+};
+hipError_t launch_route_grouped(const double* part, int S, const float* bias, const float* sel_bias,
+                                const int32_t* tok_off, int T, int E, const GroupRule& rule, float scale,
+                                int32_t* ids, float* wts, hipStream_t st);
+
+// norm.hip -- the chain y -> (norm) -> gate, residual -> norm of one row.
+// Pointers are of the element type; those that may be null say what is left out.
+struct NormRow {
+  int d;
+  int layer;       // 1: layer norm, 0: RMS norm
+  int post;        // y is normed before the gate
+  int has_y;       // 0: the chain starts at resid
+  int gate_mode;   // moe_gate_mode
+  float eps, alpha, w_offset;
+  const void *resid, *post_w, *post_b, *gate, *pre_w, *pre_b;
+  void *resid_out, *x_out;
+};
+hipError_t launch_norm(int dtype, const void* y, const NormRow& n, int T, hipStream_t st);
+hipError_t launch_combine_norm(int dtype, const void* yp, const void* ysh, const int32_t* tok_off, const float* wts,
+                               const int32_t* inv_perm, const NormRow& n, int T, hipStream_t st);
+
+// adapt.hip -- low-rank adapters: out[r] = y[r] + scales[a] * B[a][g] (A[a][g] x[r]).
+struct AdaptArgs {
+  int rows, T, K, N, R, L, G;
+  int x_count;                // rows of x
+  const void *x, *a, *b, *y;  // a [L][G][R][K], b [L][G][N][R]
+  void* out;
+  const int32_t *ids;         // adapter of a token, [T]
+  const int32_t *row_tok;     // token of a row (null: row r is token r)
+  const int32_t *x_rows;      // x row of a row (null: row r reads x row r)
+  const int32_t *expert_off;  // [G + 1] (null: G = 1, every row)
+  const int32_t *ranks;       // [L] (null: R)
+  const float* scales;        // [L] (null: 1)
+};
+// Slices of K of the first product (partials part[S][rows][R], float).
+int adapt_splits(int rows, int K, int elt);
+hipError_t launch_adapt(int dtype, const AdaptArgs& p, float* part, int S, hipStream_t st);
+
 // moe_abi.cpp -- the forward of moe_forward over a caller-chosen scratch
 // region.  own_regions: `ws` holds only the forward's own regions
 // (forward_scratch_bytes), as the no-allocation entry point supplies;

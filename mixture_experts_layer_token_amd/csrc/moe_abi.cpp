@@ -184,6 +184,13 @@ void plan_path(const moe_desc& d, Carver& c, PathWs& w) {
   w.tmp = c.take<int32_t>(a_cap(d));
 }
 
+// Grouped routing: float64 partial logits.
+struct GroupedWs { double* part; int splits; };
+void plan_grouped(const moe_desc& d, Carver& c, GroupedWs& w) {
+  w.splits = router_splits(d.T, d.d, d.E);
+  w.part = c.take<double>((size_t)w.splits * d.T * d.E);
+}
+
 size_t ws_size(const moe_desc& d, int op) {
   Carver c(nullptr);
   switch (op) {
@@ -193,6 +200,7 @@ size_t ws_size(const moe_desc& d, int op) {
     case MOE_OP_COMBINE: break;
     case MOE_OP_FOLD: { FoldScratch w; plan_fold(d, c, w); break; }
     case MOE_OP_PATH: { PathWs w; plan_path(d, c, w); break; }
+    case MOE_OP_ROUTE_GROUPED: { GroupedWs w; plan_grouped(d, c, w); break; }
     default: {  // the forward's own regions; large enough for every other op
       FwdWs w;
       plan_forward(d, c, w);
@@ -201,7 +209,10 @@ size_t ws_size(const moe_desc& d, int op) {
       plan_fold(d, f, fw);
       PathWs pw;
       plan_path(d, p, pw);
-      return std::max({c.total(), f.total(), p.total()});
+      Carver g(nullptr);
+      GroupedWs gw;
+      plan_grouped(d, g, gw);
+      return std::max({c.total(), f.total(), p.total(), g.total()});
     }
   }
   return c.total();
@@ -338,7 +349,7 @@ extern "C" {
 moe_status moe_workspace_size(const moe_desc* desc, int32_t op, size_t* bytes) {
   MOE_TRY(check_desc(desc));
   if (!bytes) return MOE_ERR_NULL;
-  if (op < MOE_OP_ROUTE || op > MOE_OP_PATH) return MOE_ERR_UNSUPPORTED;
+  if (op < MOE_OP_ROUTE || op > MOE_OP_ROUTE_GROUPED) return MOE_ERR_UNSUPPORTED;
   *bytes = ws_size(*desc, op);
   return MOE_OK;
 }
@@ -382,6 +393,172 @@ moe_status moe_route(const moe_desc* desc, const void* x, const void* w_router, 
   plan_route(d, c, rw);
   return do_route(d, x, w_router, router_bias, k, tok_off, topk_ids, topk_w, dev_status, rw,
                   static_cast<hipStream_t>(stream));
+}
+
+moe_status moe_route_grouped(const moe_desc* desc, const moe_route_rule* rule, const void* x, const void* w_router,
+                             const float* router_bias, const float* select_bias, const int32_t* k,
+                             int32_t* tok_off, int32_t* topk_ids, float* topk_w, int32_t* dev_status, void* ws,
+                             size_t ws_bytes, moe_stream_t stream) {
+  MOE_TRY(check_desc(desc));
+  const moe_desc& d = *desc;
+  if (!rule) return MOE_ERR_NULL;
+  const moe_route_rule& r = *rule;
+  if (r.score != MOE_SCORE_SIGMOID && r.score != MOE_SCORE_SOFTMAX) return MOE_ERR_UNSUPPORTED;
+  if (r.group_score != MOE_GROUP_MAX && r.group_score != MOE_GROUP_TOP2) return MOE_ERR_UNSUPPORTED;
+  if ((r.renorm != 0 && r.renorm != 1) || d.router == MOE_ROUTER_FUSED) return MOE_ERR_UNSUPPORTED;
+  if (r.n_group < 1 || r.n_group > 64 || d.E % r.n_group || r.topk_group < 1 || r.topk_group > r.n_group ||
+      d.k_max > r.topk_group * (d.E / r.n_group))
+    return MOE_ERR_SHAPE;
+  if (!tok_ptr(d, x) || !w_router || !tok_ptr(d, k) || !tok_off || !tok_ptr(d, topk_ids) || !tok_ptr(d, topk_w))
+    return MOE_ERR_NULL;
+  if (!aligned16(x) || !aligned16(w_router)) return MOE_ERR_ALIGN;
+  MOE_TRY(check_ws(d, MOE_OP_ROUTE_GROUPED, ws, ws_bytes));
+  Carver c(ws);
+  GroupedWs gw;
+  plan_grouped(d, c, gw);
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const GroupRule gr{r.score == MOE_SCORE_SOFTMAX, r.n_group, r.topk_group, r.group_score == MOE_GROUP_TOP2, r.renorm};
+  hipError_t e = launch_router(d.dtype, x, w_router, k, d.T, d.d, d.E, d.k_max, budget(d), gw.splits, gw.part, tok_off,
+                               dev_status, st);
+  if (e == hipSuccess)
+    e = launch_route_grouped(gw.part, gw.splits, router_bias, select_bias, tok_off, d.T, d.E, gr, d.routed_scale,
+                             topk_ids, topk_w, st);
+  return launched(e);
+}
+
+// [p, p + n) and [q, q + m) share a byte (a null pointer shares none).
+static bool overlap(const void* p, size_t n, const void* q, size_t m) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p && q && a < b + m && b < a + n;
+}
+
+static moe_status check_norm(const moe_norm_desc* nd) {
+  if (!nd) return MOE_ERR_NULL;
+  if (nd->dtype != MOE_F32 && nd->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (nd->kind != MOE_NORM_RMS && nd->kind != MOE_NORM_LAYER) return MOE_ERR_UNSUPPORTED;
+  if (nd->gate_mode < MOE_GATE_NONE || nd->gate_mode > MOE_GATE_FULL) return MOE_ERR_UNSUPPORTED;
+  if (nd->post != 0 && nd->post != 1) return MOE_ERR_UNSUPPORTED;
+  if (nd->T < 0 || nd->d < 1 || nd->d > 65536) return MOE_ERR_SHAPE;
+  if (!(nd->eps >= 0.f) || !std::isfinite(nd->eps) || !std::isfinite(nd->alpha) || !std::isfinite(nd->w_offset))
+    return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+
+// The operands that moe_norm and moe_combine_norm share; fills the kernel's row.
+static moe_status norm_operands(const moe_norm_desc& n, bool has_y, const void* resid, const void* post_w,
+                                const void* post_b, const void* gate, const void* pre_w, const void* pre_b,
+                                void* resid_out, void* x_out, NormRow* row) {
+  if (!resid_out && !x_out) return n.T == 0 ? MOE_OK : MOE_ERR_NULL;
+  if ((gate != nullptr) != (n.gate_mode != MOE_GATE_NONE) && n.T > 0) return MOE_ERR_NULL;
+  for (const void* p : {resid, post_w, post_b, gate, pre_w, pre_b, (const void*)resid_out, (const void*)x_out})
+    if (!aligned16(p)) return MOE_ERR_ALIGN;
+  const size_t elt = n.dtype == MOE_BF16 ? 2 : 4, bytes = (size_t)n.T * n.d * elt, vec = (size_t)n.d * elt;
+  if (overlap(resid_out, bytes, x_out, bytes)) return MOE_ERR_SHAPE;
+  const size_t gate_bytes = n.gate_mode == MOE_GATE_FULL ? bytes : (n.gate_mode == MOE_GATE_TOKEN ? n.T * elt : vec);
+  for (const void* o : {(const void*)resid_out, (const void*)x_out}) {
+    if (resid != o && overlap(resid, bytes, o, bytes)) return MOE_ERR_SHAPE;
+    if (overlap(gate, gate_bytes, o, bytes)) return MOE_ERR_SHAPE;
+    for (const void* p : {post_w, post_b, pre_w, pre_b})
+      if (overlap(p, vec, o, bytes)) return MOE_ERR_SHAPE;
+  }
+  *row = NormRow{n.d, n.kind == MOE_NORM_LAYER, n.post, has_y, n.gate_mode, n.eps, n.alpha, n.w_offset,
+                 resid, post_w, post_b, gate, pre_w, pre_b, resid_out, x_out};
+  return MOE_OK;
+}
+
+moe_status moe_norm(const moe_norm_desc* nd, const void* y, const void* resid, const void* post_w,
+                    const void* post_b, const void* gate, const void* pre_w, const void* pre_b, void* resid_out,
+                    void* x_out, moe_stream_t stream) {
+  MOE_TRY(check_norm(nd));
+  const moe_norm_desc& n = *nd;
+  if (!y && !resid && n.T > 0) return MOE_ERR_NULL;
+  if (!y && n.T > 0 && (n.post || gate || resid_out)) return MOE_ERR_SHAPE;
+  if (!aligned16(y)) return MOE_ERR_ALIGN;
+  NormRow row;
+  MOE_TRY(norm_operands(n, y != nullptr, resid, post_w, post_b, gate, pre_w, pre_b, resid_out, x_out, &row));
+  if (n.T == 0) return MOE_OK;
+  const size_t bytes = (size_t)n.T * n.d * (n.dtype == MOE_BF16 ? 2 : 4);
+  for (const void* o : {(const void*)resid_out, (const void*)x_out})
+    if (y != o && overlap(y, bytes, o, bytes)) return MOE_ERR_SHAPE;
+  return launched(launch_norm(n.dtype, y, row, n.T, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_combine_norm(const moe_desc* desc, const moe_norm_desc* nd, const void* y_perm, const void* y_shared,
+                            const int32_t* tok_off, const float* topk_w, const int32_t* inv_perm, const void* resid,
+                            const void* post_w, const void* post_b, const void* gate, const void* pre_w,
+                            const void* pre_b, void* resid_out, void* x_out, moe_stream_t stream) {
+  MOE_TRY(check_desc(desc));
+  MOE_TRY(check_norm(nd));
+  const moe_desc& d = *desc;
+  const moe_norm_desc& n = *nd;
+  if (n.T != d.T || n.d != d.d || n.dtype != d.dtype) return MOE_ERR_SHAPE;
+  if (!tok_ptr(d, y_perm) || !tok_off || !tok_ptr(d, topk_w) || !tok_ptr(d, inv_perm)) return MOE_ERR_NULL;
+  if (!aligned16(y_perm) || !aligned16(y_shared)) return MOE_ERR_ALIGN;
+  NormRow row;
+  MOE_TRY(norm_operands(n, true, resid, post_w, post_b, gate, pre_w, pre_b, resid_out, x_out, &row));
+  if (n.T == 0) return MOE_OK;
+  const size_t bytes = (size_t)d.T * d.d * elt_size(d);
+  for (const void* o : {(const void*)resid_out, (const void*)x_out})
+    if (overlap(y_perm, a_cap(d) * d.d * elt_size(d), o, bytes) || overlap(y_shared, bytes, o, bytes))
+      return MOE_ERR_SHAPE;
+  return launched(launch_combine_norm(d.dtype, y_perm, y_shared, tok_off, topk_w, inv_perm, row, d.T,
+                                      static_cast<hipStream_t>(stream)));
+}
+
+static moe_status check_adapter(const moe_adapter_desc* ad) {
+  if (!ad) return MOE_ERR_NULL;
+  const moe_adapter_desc& a = *ad;
+  if (a.dtype != MOE_F32 && a.dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (a.T < 0 || a.rows < 0 || a.rows > (1 << 30) || a.L < 1 || a.L > 65536 || a.G < 1 || a.G > 1024) return MOE_ERR_SHAPE;
+  if (a.K < 8 || a.K > 65536 || a.K % 8 || a.N < 8 || a.N > 65536 || a.N % 8) return MOE_ERR_SHAPE;
+  if (a.R < 8 || a.R > 128 || a.R % 8) return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+
+static float* plan_adapt(const moe_adapter_desc& a, Carver& c, int* splits) {
+  *splits = adapt_splits(a.rows, a.K, a.dtype == MOE_BF16 ? 2 : 4);
+  return c.take<float>((size_t)*splits * a.rows * a.R);
+}
+
+moe_status moe_adapt_workspace_size(const moe_adapter_desc* ad, size_t* bytes) {
+  MOE_TRY(check_adapter(ad));
+  if (!bytes) return MOE_ERR_NULL;
+  Carver c(nullptr);
+  int s;
+  plan_adapt(*ad, c, &s);
+  *bytes = c.total();
+  return MOE_OK;
+}
+
+moe_status moe_adapt(const moe_adapter_desc* ad, const void* x, const int32_t* x_rows, const void* a, const void* b,
+                     const int32_t* ranks, const float* scales, const int32_t* adapter_ids, const int32_t* row_tok,
+                     const int32_t* expert_off, const void* y_in, void* y_out, void* ws, size_t ws_bytes,
+                     moe_stream_t stream) {
+  MOE_TRY(check_adapter(ad));
+  const moe_adapter_desc& d = *ad;
+  if (!expert_off && d.G > 1) return MOE_ERR_NULL;
+  if (!row_tok && d.T < d.rows) return MOE_ERR_SHAPE;
+  if (d.rows == 0) return MOE_OK;
+  if (!x || !a || !b || (!adapter_ids && d.T > 0) || !y_in || !y_out) return MOE_ERR_NULL;
+  for (const void* p : {x, a, b, y_in, (const void*)y_out})
+    if (!aligned16(p)) return MOE_ERR_ALIGN;
+  const size_t elt = d.dtype == MOE_BF16 ? 2 : 4, y_bytes = (size_t)d.rows * d.N * elt;
+  const int x_count = x_rows ? d.T : d.rows;
+  const size_t m = (size_t)d.L * d.G * d.R * elt;
+  if ((y_in != y_out && overlap(y_in, y_bytes, y_out, y_bytes)) ||
+      overlap(x, (size_t)x_count * d.K * elt, y_out, y_bytes) || overlap(a, m * d.K, y_out, y_bytes) ||
+      overlap(b, m * d.N, y_out, y_bytes))
+    return MOE_ERR_SHAPE;
+  size_t need = 0;
+  MOE_TRY(moe_adapt_workspace_size(ad, &need));
+  if (!ws || ws_bytes < need) return MOE_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return MOE_ERR_ALIGN;
+  Carver c(ws);
+  int splits;
+  float* part = plan_adapt(d, c, &splits);
+  const AdaptArgs p{d.rows, d.T, d.K, d.N, d.R, d.L, d.G, x_count, x, a, b, y_in, y_out, adapter_ids, row_tok,
+                    x_rows, expert_off, ranks, scales};
+  return launched(launch_adapt(d.dtype, p, part, splits, static_cast<hipStream_t>(stream)));
 }
 
 moe_status moe_permute(const moe_desc* desc, const int32_t* tok_off, const int32_t* topk_ids,

@@ -1,0 +1,300 @@
+// Norms before and after a block, fused with the block's gate, its residual
+// scale and (moe_combine_norm) with the weighted combine:
+//   y  = the block's output, or sum_j w_j Y[inv_perm_j] (+ Y_shared) in float32
+//   p  = post ? norm(y) : y
+//   r  = resid + alpha * gate * p          -> resid_out
+//   x  = norm(r)                           -> x_out
+//   norm(v) = (v - mean) * rsqrt(mean((v - mean)^2) + eps) * (w_offset + w) + b
+// with mean = 0 for the RMS norm.  One workgroup per row, the row in registers
+// from the first load to the last store: y, resid and each operand vector are
+// read once, r and x written once, nothing is rounded between (the second norm
+// takes r before its rounding to the element type).  All statistics are
+// float32; the layer norm centres before it squares, so its variance does not
+// cancel.
+#include "common.h"
+#include "launch.h"
+
+namespace moe {
+
+namespace {
+
+// LE elements of T starting at p, as floats (16 bytes).
+template <typename T>
+__device__ __forceinline__ void unpack16(const u32x4_t& v, float* f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 2) {
+      f[2 * i] = __uint_as_float(v[i] << 16);
+      f[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+    } else {
+      f[i] = __uint_as_float(v[i]);
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ u32x4_t pack16(const float* f) {
+  u32x4_t o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 2) o[i] = (uint32_t)f32_to_bf16(f[2 * i]) | ((uint32_t)f32_to_bf16(f[2 * i + 1]) << 16);
+    else o[i] = __float_as_uint(f[i]);
+  }
+  return o;
+}
+
+// Sum of one float per thread over the workgroup: a butterfly in each wave,
+// then the wave sums in ascending order (every thread adds them the same way).
+__device__ __forceinline__ float block_sum(float v, float* red) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, nw = blockDim.x >> 6;
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
+  if (nw == 1) return v;
+  if (lane == 0) red[w] = v;
+  __syncthreads();
+  float s = red[0];
+  for (int i = 1; i < nw; ++i) s += red[i];
+  __syncthreads();
+  return s;
+}
+
+}  // namespace
+
+// A thread owns CH chunks of LE = 16 / sizeof(T) elements.  VEC: chunk q is the
+// 16-byte chunk tid + blockDim * q of the row (d a multiple of LE, so that every
+// row starts on 16 bytes); otherwise element i of chunk q is element tid +
+// blockDim * (LE q + i), so that odd widths still read whole lines.
+template <typename T, int CH, bool VEC>
+struct RowIo {
+  static constexpr int LE = 16 / (int)sizeof(T);
+  int d;
+  __device__ __forceinline__ bool has(int q, int i) const {
+    return VEC ? (int)(threadIdx.x + blockDim.x * q) * LE < d : (int)(threadIdx.x + blockDim.x * (LE * q + i)) < d;
+  }
+  __device__ __forceinline__ int at(int q, int i) const {
+    return VEC ? (int)(threadIdx.x + blockDim.x * q) * LE + i : (int)(threadIdx.x + blockDim.x * (LE * q + i));
+  }
+  // Elements of the row that are not there read as 0.
+  __device__ __forceinline__ void load(const T* p, float (&f)[CH][LE]) const {
+#pragma unroll
+    for (int q = 0; q < CH; ++q) {
+      if constexpr (VEC) {
+        u32x4_t v = {0u, 0u, 0u, 0u};
+        if (has(q, 0)) v = *reinterpret_cast<const u32x4_t*>(p + at(q, 0));
+        unpack16<T>(v, f[q]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < LE; ++i) f[q][i] = has(q, i) ? Elt<T>::to_f32(p[at(q, i)]) : 0.f;
+      }
+    }
+  }
+  __device__ __forceinline__ void store(T* p, const float (&f)[CH][LE]) const {
+#pragma unroll
+    for (int q = 0; q < CH; ++q) {
+      if constexpr (VEC) {
+        if (has(q, 0)) *reinterpret_cast<u32x4_t*>(p + at(q, 0)) = pack16<T>(f[q]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < LE; ++i)
+          if (has(q, i)) p[at(q, i)] = Elt<T>::from_f32(f[q][i]);
+      }
+    }
+  }
+  // v = norm(v)
+  __device__ __forceinline__ void norm(float (&v)[CH][LE], const NormRow& n, const T* w, const T* b, float* red) const {
+    float wv[CH][LE], bv[CH][LE];
+    if (w) load(w, wv);
+    if (b) load(b, bv);
+    if (n.layer) {
+      float s = 0.f;
+#pragma unroll
+      for (int q = 0; q < CH; ++q)
+#pragma unroll
+        for (int i = 0; i < LE; ++i) s += v[q][i];
+      const float mean = block_sum(s, red) / (float)d;
+#pragma unroll
+      for (int q = 0; q < CH; ++q)
+#pragma unroll
+        for (int i = 0; i < LE; ++i) v[q][i] = has(q, i) ? v[q][i] - mean : 0.f;
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int q = 0; q < CH; ++q)
+#pragma unroll
+      for (int i = 0; i < LE; ++i) s = fmaf(v[q][i], v[q][i], s);
+    const float rs = 1.0f / sqrtf(block_sum(s, red) / (float)d + n.eps);
+#pragma unroll
+    for (int q = 0; q < CH; ++q)
+#pragma unroll
+      for (int i = 0; i < LE; ++i) {
+        float o = v[q][i] * rs;
+        if (w) o *= n.w_offset + wv[q][i];
+        if (b) o += bv[q][i];
+        v[q][i] = o;
+      }
+  }
+};
+
+// The chain behind y (v in: y, float32).  resid, y and the outputs may be the
+// same buffers: a thread writes only elements that it alone has read before.
+template <typename T, int CH, bool VEC>
+__device__ __forceinline__ void norm_chain(float (&v)[CH][16 / sizeof(T)], const RowIo<T, CH, VEC>& io,
+                                           const NormRow& n, int t, float* red) {
+  constexpr int LE = 16 / (int)sizeof(T);
+  const size_t row = (size_t)t * io.d;
+  float rv[CH][LE];
+  if (n.resid) io.load((const T*)n.resid + row, rv);
+  if (n.has_y) {
+    if (n.post) io.norm(v, n, (const T*)n.post_w, (const T*)n.post_b, red);
+    if (n.gate_mode == MOE_GATE_TOKEN) {
+      const float g = Elt<T>::to_f32(((const T*)n.gate)[t]);
+#pragma unroll
+      for (int q = 0; q < CH; ++q)
+#pragma unroll
+        for (int i = 0; i < LE; ++i) v[q][i] *= g;
+    } else if (n.gate_mode != MOE_GATE_NONE) {
+      float g[CH][LE];
+      io.load((const T*)n.gate + (n.gate_mode == MOE_GATE_FULL ? row : 0), g);
+#pragma unroll
+      for (int q = 0; q < CH; ++q)
+#pragma unroll
+        for (int i = 0; i < LE; ++i) v[q][i] *= g[q][i];
+    }
+#pragma unroll
+    for (int q = 0; q < CH; ++q)
+#pragma unroll
+      for (int i = 0; i < LE; ++i) v[q][i] = n.resid ? fmaf(n.alpha, v[q][i], rv[q][i]) : n.alpha * v[q][i];
+  } else {
+#pragma unroll
+    for (int q = 0; q < CH; ++q)
+#pragma unroll
+      for (int i = 0; i < LE; ++i) v[q][i] = rv[q][i];
+  }
+  if (n.resid_out) io.store((T*)n.resid_out + row, v);
+  if (n.x_out) {
+    // the elements past the row must not count: y * gate + resid is 0 there
+    io.norm(v, n, (const T*)n.pre_w, (const T*)n.pre_b, red);
+    io.store((T*)n.x_out + row, v);
+  }
+}
+
+template <typename T, int CH, bool VEC>
+__global__ __launch_bounds__(1024) void norm_kernel(const T* y, NormRow n) {
+  constexpr int LE = 16 / (int)sizeof(T);
+  __shared__ float red[16];
+  const RowIo<T, CH, VEC> io{n.d};
+  const int t = blockIdx.x;
+  float v[CH][LE];
+  if (n.has_y) io.load(y + (size_t)t * n.d, v);
+  norm_chain<T, CH, VEC>(v, io, n, t, red);
+}
+
+// The combine of combine.hip (same order of the same fused multiply-adds),
+// kept in float32 and followed by the chain above.  The rows of CBN
+// assignments are requested together.
+template <typename T, int CH, int CBN>
+__global__ __launch_bounds__(1024) void combine_norm_kernel(const T* __restrict__ yp, const T* __restrict__ ysh,
+                                                            const int32_t* __restrict__ tok_off,
+                                                            const float* __restrict__ wts,
+                                                            const int32_t* __restrict__ inv_perm, NormRow n) {
+  constexpr int LE = 16 / (int)sizeof(T);
+  __shared__ float red[16];
+  const RowIo<T, CH, true> io{n.d};
+  const int t = blockIdx.x;
+  const int a0 = tok_off[t], a1 = tok_off[t + 1];
+  float v[CH][LE];
+#pragma unroll
+  for (int q = 0; q < CH; ++q)
+#pragma unroll
+    for (int i = 0; i < LE; ++i) v[q][i] = 0.f;
+  for (int b = a0; b < a1; b += CBN) {
+    u32x4_t r[CBN][CH];
+#pragma unroll
+    for (int j = 0; j < CBN; ++j) {
+      const int p = b + j < a1 ? inv_perm[b + j] : -1;
+#pragma unroll
+      for (int q = 0; q < CH; ++q) {
+        r[j][q] = u32x4_t{0u, 0u, 0u, 0u};
+        if (p >= 0 && io.has(q, 0))
+          r[j][q] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(yp + (size_t)p * n.d + io.at(q, 0)));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < CBN; ++j) {
+      if (b + j < a1 && inv_perm[b + j] >= 0) {
+        const float w = wts[b + j];
+#pragma unroll
+        for (int q = 0; q < CH; ++q) {
+          float f[LE];
+          unpack16<T>(r[j][q], f);
+#pragma unroll
+          for (int i = 0; i < LE; ++i) v[q][i] = fmaf(w, f[i], v[q][i]);
+        }
+      }
+    }
+  }
+  if (ysh) {
+    float f[CH][LE];
+    io.load(ysh + (size_t)t * n.d, f);
+#pragma unroll
+    for (int q = 0; q < CH; ++q)
+#pragma unroll
+      for (int i = 0; i < LE; ++i) v[q][i] += f[q][i];
+  }
+  norm_chain<T, CH, true>(v, io, n, t, red);
+}
+
+// Threads of a row: enough for CH chunks each, in whole waves.
+static int row_threads(int nch, int ch) { return ((nch + ch - 1) / ch + 63) / 64 * 64; }
+
+template <typename T>
+static void launch_norm_t(const T* y, const NormRow& n, int T_, hipStream_t st) {
+  constexpr int LE = 16 / (int)sizeof(T);
+  const int nch = (n.d + LE - 1) / LE;
+  const bool vec = n.d % LE == 0;
+#define MOE_NORM(CH)                                                                                              \
+  do {                                                                                                            \
+    if (vec) hipLaunchKernelGGL((norm_kernel<T, CH, true>), dim3(T_), dim3(row_threads(nch, CH)), 0, st, y, n);   \
+    else hipLaunchKernelGGL((norm_kernel<T, CH, false>), dim3(T_), dim3(row_threads(nch, CH)), 0, st, y, n);      \
+  } while (0)
+  if (nch <= 512) MOE_NORM(1);
+  else if (nch <= 1024) MOE_NORM(2);
+  else if (nch <= 4096) MOE_NORM(4);
+  else if (nch <= 8192) MOE_NORM(8);
+  else MOE_NORM(16);
+#undef MOE_NORM
+}
+
+hipError_t launch_norm(int dtype, const void* y, const NormRow& n, int T, hipStream_t st) {
+  if (T == 0) return hipSuccess;
+  if (dtype == DT_BF16) launch_norm_t<bf16_t>((const bf16_t*)y, n, T, st);
+  else launch_norm_t<float>((const float*)y, n, T, st);
+  return hipGetLastError();
+}
+
+template <typename T>
+static void launch_combine_norm_t(const T* yp, const T* ysh, const int32_t* tok_off, const float* wts,
+                                  const int32_t* inv_perm, const NormRow& n, int T_, hipStream_t st) {
+  constexpr int LE = 16 / (int)sizeof(T);
+  const int nch = n.d / LE;
+#define MOE_CNORM(CH, CBN)                                                                                          \
+  hipLaunchKernelGGL((combine_norm_kernel<T, CH, CBN>), dim3(T_), dim3(row_threads(nch, CH)), 0, st, yp, ysh, tok_off, \
+                     wts, inv_perm, n)
+  if (nch <= 512) MOE_CNORM(1, 8);
+  else if (nch <= 1024) MOE_CNORM(2, 8);
+  else if (nch <= 4096) MOE_CNORM(4, 4);
+  else if (nch <= 8192) MOE_CNORM(8, 2);
+  else MOE_CNORM(16, 1);
+#undef MOE_CNORM
+}
+
+hipError_t launch_combine_norm(int dtype, const void* yp, const void* ysh, const int32_t* tok_off, const float* wts,
+                               const int32_t* inv_perm, const NormRow& n, int T, hipStream_t st) {
+  if (T == 0) return hipSuccess;
+  if (dtype == DT_BF16)
+    launch_combine_norm_t<bf16_t>((const bf16_t*)yp, (const bf16_t*)ysh, tok_off, wts, inv_perm, n, T, st);
+  else
+    launch_combine_norm_t<float>((const float*)yp, (const float*)ysh, tok_off, wts, inv_perm, n, T, st);
+  return hipGetLastError();
+}
+
+}  // namespace moe
