@@ -168,8 +168,7 @@ hipError_t launch_path_sources(const int32_t* tok_off, const int32_t* psrc, int 
 hipError_t launch_path_rows(const int32_t* tok_off, int T, int k_max, const int32_t* perm_path, const int32_t* p2s,
                             const int32_t* src_inv, int32_t* row_map, hipStream_t st);
 
-// route_grouped.hip -- scores, groups and top-k_t from the float64 partial
-// logits of launch_router.
+// route_grouped.hip -- float64 partial logits, then scores, groups and top-k_t.
 struct GroupRule {
   int softmax;     // scores: 1 softmax, 0 sigmoid
   int n_group;     // groups of E / n_group consecutive experts (<= 64)
@@ -177,6 +176,11 @@ struct GroupRule {
   int top2;        // group value: 1 the sum of the two largest keys, 0 the largest
   int renorm;      // weights divided by the sum of the chosen scores
 };
+// Partial logits part[S][T][E] in float64 (and the token scan); S from
+// logits_f64_splits.
+int logits_f64_splits(int T, int d, int E, int dtype);
+hipError_t launch_logits_f64(int dtype, const void* x, const void* w, const int32_t* k, int T, int d, int E, int k_max,
+                             BudgetPolicy pol, int S, double* part, int32_t* tok_off, int32_t* status, hipStream_t st);
 hipError_t launch_route_grouped(const double* part, int S, const float* bias, const float* sel_bias,
                                 const int32_t* tok_off, int T, int E, const GroupRule& rule, float scale,
                                 int32_t* ids, float* wts, hipStream_t st);

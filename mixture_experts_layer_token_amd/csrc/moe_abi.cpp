@@ -187,7 +187,7 @@ void plan_path(const moe_desc& d, Carver& c, PathWs& w) {
 // Grouped routing: float64 partial logits.
 struct GroupedWs { double* part; int splits; };
 void plan_grouped(const moe_desc& d, Carver& c, GroupedWs& w) {
-  w.splits = router_splits(d.T, d.d, d.E);
+  w.splits = logits_f64_splits(d.T, d.d, d.E, d.dtype);
   w.part = c.take<double>((size_t)w.splits * d.T * d.E);
 }
 
@@ -418,8 +418,8 @@ moe_status moe_route_grouped(const moe_desc* desc, const moe_route_rule* rule, c
   plan_grouped(d, c, gw);
   hipStream_t st = static_cast<hipStream_t>(stream);
   const GroupRule gr{r.score == MOE_SCORE_SOFTMAX, r.n_group, r.topk_group, r.group_score == MOE_GROUP_TOP2, r.renorm};
-  hipError_t e = launch_router(d.dtype, x, w_router, k, d.T, d.d, d.E, d.k_max, budget(d), gw.splits, gw.part, tok_off,
-                               dev_status, st);
+  hipError_t e = launch_logits_f64(d.dtype, x, w_router, k, d.T, d.d, d.E, d.k_max, budget(d), gw.splits, gw.part,
+                                   tok_off, dev_status, st);
   if (e == hipSuccess)
     e = launch_route_grouped(gw.part, gw.splits, router_bias, select_bias, tok_off, d.T, d.E, gr, d.routed_scale,
                              topk_ids, topk_w, st);

@@ -168,6 +168,152 @@ __device__ __forceinline__ void scores(const double (&l)[KPL], int E, int softma
 
 }  // namespace
 
+// ---------------------------------------------------------------------------
+// Partial logits in float64 on the matrix cores: v_mfma_f64_16x16x4_f64 is a
+// float64 fused multiply-add over 4 of K, so products of float32 or bf16 values
+// stay exact and only the accumulation rounds, as the routing contract asks.
+// A wave takes 16 ME experts x 16 NT tokens of a slice of K; a lane's 16-byte
+// load of row l % 16 holds LE values of K from LE * (l / 16) on, and instruction
+// i of a step multiplies value i of each lane group (any order of K will do, as
+// long as both operands have the same).  The four waves of a workgroup take
+// quarters of the slice and are added in wave order; slices are added by the
+// selection kernel.  One more slice (z = S) holds the token-offset scan.
+typedef double f64x4_t __attribute__((ext_vector_type(4)));
+
+template <typename T>
+__device__ __forceinline__ void widen(const u32x4_t& v, double* o) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 2) {
+      o[2 * i] = (double)__uint_as_float(v[i] << 16);
+      o[2 * i + 1] = (double)__uint_as_float(v[i] & 0xffff0000u);
+    } else {
+      o[i] = (double)__uint_as_float(v[i]);
+    }
+  }
+}
+
+template <typename T, int ME, int NT>
+__global__ __launch_bounds__(256) void logits_f64_kernel(const T* __restrict__ x, const T* __restrict__ w, int T_,
+                                                         int d, int E, double* __restrict__ part,
+                                                         const int32_t* __restrict__ k, int k_max, BudgetPolicy pol,
+                                                         int32_t* __restrict__ tok_off, int32_t* __restrict__ status) {
+  constexpr int LE = 16 / (int)sizeof(T), KS = 4 * LE;
+  constexpr int TE = 16 * ME, TT = 16 * NT, LD = TE + 1;
+  __shared__ double red[4 * TT * LD];
+  const int S = gridDim.z - 1;
+  if ((int)blockIdx.z == S) {
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
+      int32_t* sc = reinterpret_cast<int32_t*>(red);
+      token_offsets_block<256>(k, T_, k_max, pol, tok_off, status, sc, sc + 8);
+    }
+    return;
+  }
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, lg = lane >> 4;
+  const int e0 = blockIdx.x * TE, t0 = blockIdx.y * TT;
+  const int steps = d / KS, nq = S * 4, q = blockIdx.z * 4 + wave;
+  const int s0 = (int)((long long)steps * q / nq), s1 = (int)((long long)steps * (q + 1) / nq);
+  const T* wr[ME];
+  const T* xr[NT];
+#pragma unroll
+  for (int m = 0; m < ME; ++m) wr[m] = w + (size_t)min(e0 + 16 * m + l16, E - 1) * d + lg * LE;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) xr[n] = x + (size_t)min(t0 + 16 * n + l16, T_ - 1) * d + lg * LE;
+  f64x4_t acc[ME][NT];
+#pragma unroll
+  for (int m = 0; m < ME; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[m][n] = f64x4_t{0.0, 0.0, 0.0, 0.0};
+  // one step ahead in registers
+  constexpr int U = ME * NT <= 2 ? 4 : 2;
+  u32x4_t wv[U][ME], xv[U][NT];
+  auto load = [&](int u, int s) {
+    if (s >= s1) return;
+#pragma unroll
+    for (int m = 0; m < ME; ++m) wv[u][m] = *reinterpret_cast<const u32x4_t*>(wr[m] + (size_t)s * KS);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) xv[u][n] = *reinterpret_cast<const u32x4_t*>(xr[n] + (size_t)s * KS);
+  };
+#pragma unroll
+  for (int u = 0; u < U; ++u) load(u, s0 + u);
+  for (int s = s0; s < s1; s += U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (s + u >= s1) break;
+      double wd[ME][LE], xd[NT][LE];
+#pragma unroll
+      for (int m = 0; m < ME; ++m) widen<T>(wv[u][m], wd[m]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) widen<T>(xv[u][n], xd[n]);
+      load(u, s + u + U);
+#pragma unroll
+      for (int i = 0; i < LE; ++i)
+#pragma unroll
+        for (int m = 0; m < ME; ++m)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            acc[m][n] = __builtin_amdgcn_mfma_f64_16x16x4f64(wd[m][i], xd[n][i], acc[m][n], 0, 0, 0);
+    }
+  }
+  // acc[m][n][i]: expert 16 m + 4 i + lg, token 16 n + l16
+#pragma unroll
+  for (int m = 0; m < ME; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) red[(wave * TT + 16 * n + l16) * LD + 16 * m + 4 * i + lg] = acc[m][n][i];
+  __syncthreads();
+  double* const out = part + (size_t)blockIdx.z * T_ * E;
+  for (int i = threadIdx.x; i < TT * TE; i += 256) {
+    const int t = i / TE, e = i % TE;
+    if (t0 + t >= T_ || e0 + e >= E) continue;
+    const double* r = red + t * LD + e;
+    out[(size_t)(t0 + t) * E + e0 + e] = (r[0] + r[TT * LD]) + (r[2 * TT * LD] + r[3 * TT * LD]);
+  }
+}
+
+// Tile: 16 x 16 for a batch of one tile, 16 x 32 while the batch is small, 32 x
+// 64 (half the operand traffic) where the tiles alone fill the chip.
+static int f64_tile(int T, int E) {
+  if (T <= 16) return 0;
+  return (long long)((T + 63) / 64) * ((E + 31) / 32) >= 256 ? 2 : 1;
+}
+int logits_f64_splits(int T, int d, int E, int dtype) {
+  const int te = f64_tile(T, E) == 2 ? 32 : 16, tt = f64_tile(T, E) == 2 ? 64 : (f64_tile(T, E) == 1 ? 32 : 16);
+  const long long tiles = (long long)((max(T, 1) + tt - 1) / tt) * ((E + te - 1) / te);
+  const int steps = d / (dtype == DT_BF16 ? 32 : 16);
+  return (int)max(1LL, min(min((256 + tiles - 1) / tiles, 16LL), (long long)steps / 8));
+}
+
+template <typename T>
+static void launch_logits_f64_t(const T* x, const T* w, const int32_t* k, int T_, int d, int E, int k_max,
+                                BudgetPolicy pol, int S, double* part, int32_t* tok_off, int32_t* status,
+                                hipStream_t st) {
+#define MOE_LF(ME, NT)                                                                                             \
+  hipLaunchKernelGGL((logits_f64_kernel<T, ME, NT>),                                                               \
+                     dim3((E + 16 * ME - 1) / (16 * ME), max(1, (T_ + 16 * NT - 1) / (16 * NT)), S + 1), dim3(256), 0, \
+                     st, x, w, T_, d, E, part, k, k_max, pol, tok_off, status)
+  switch (T_ == 0 ? -1 : f64_tile(T_, E)) {
+    case -1:  // the token scan alone
+      hipLaunchKernelGGL((logits_f64_kernel<T, 1, 1>), dim3(1, 1, 1), dim3(256), 0, st, x, w, T_, d, E, part, k, k_max,
+                         pol, tok_off, status);
+      break;
+    case 0: MOE_LF(1, 1); break;
+    case 1: MOE_LF(1, 2); break;
+    default: MOE_LF(2, 4); break;
+  }
+#undef MOE_LF
+}
+
+hipError_t launch_logits_f64(int dtype, const void* x, const void* w, const int32_t* k, int T, int d, int E, int k_max,
+                             BudgetPolicy pol, int S, double* part, int32_t* tok_off, int32_t* status, hipStream_t st) {
+  if (dtype == DT_BF16)
+    launch_logits_f64_t<bf16_t>((const bf16_t*)x, (const bf16_t*)w, k, T, d, E, k_max, pol, S, part, tok_off, status, st);
+  else
+    launch_logits_f64_t<float>((const float*)x, (const float*)w, k, T, d, E, k_max, pol, S, part, tok_off, status, st);
+  return hipGetLastError();
+}
+
 // One wave per token.  `part`: float64 partial logits [S][T][E], added in
 // ascending slice order.  LDS per wave: E words (keys by expert, then the list
 // of the chosen, then their scores).
