@@ -185,6 +185,18 @@ hipError_t launch_route_grouped(const double* part, int S, const float* bias, co
                                 const int32_t* tok_off, int T, int E, const GroupRule& rule, float scale,
                                 int32_t* ids, float* wts, hipStream_t st);
 
+// Large bf16 batches: logits from bf16 matrix instructions with an error bound
+// (partials part[S][T][E], squared norms xn[S][T] and wn[S][E]), then the same
+// selection with exact logits where the bound leaves a decision open.
+int logits_tile_splits(int T, int d, int E);
+hipError_t launch_logits_tile(const void* x, const void* w, const int32_t* k, int T, int d, int E, int k_max,
+                              BudgetPolicy pol, int S, float* part, float* xn, float* wn, int32_t* tok_off,
+                              int32_t* status, hipStream_t st);
+hipError_t launch_route_grouped_screen(const float* part, const float* xn, const float* wn, int S, const void* x,
+                                       const void* w, int d, const float* bias, const float* sel_bias,
+                                       const int32_t* tok_off, int T, int E, const GroupRule& rule, float scale,
+                                       int32_t* ids, float* wts, hipStream_t st);
+
 // norm.hip -- the chain y -> (norm) -> gate, residual -> norm of one row.
 // Pointers are of the element type; those that may be null say what is left out.
 struct NormRow {

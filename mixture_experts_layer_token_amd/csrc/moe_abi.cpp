@@ -184,11 +184,25 @@ void plan_path(const moe_desc& d, Carver& c, PathWs& w) {
   w.tmp = c.take<int32_t>(a_cap(d));
 }
 
-// Grouped routing: float64 partial logits.
-struct GroupedWs { double* part; int splits; };
+// Grouped routing: float64 partial logits, or for large bf16 batches those of
+// the bf16 matrix instructions with the squared norms that bound their error.
+struct GroupedWs { double* part; int splits; float *approx, *xn, *wn; int tile_splits; };
+bool grouped_tile(const moe_desc& d) {
+  if (d.router == MOE_ROUTER_SCREENED) return true;
+  return d.router == MOE_ROUTER_AUTO && d.dtype == MOE_BF16 && (double)d.T * d.E * d.d >= 1073741824.0;
+}
 void plan_grouped(const moe_desc& d, Carver& c, GroupedWs& w) {
+  // the two ways share the region: which one runs depends on the rule as well
   w.splits = logits_f64_splits(d.T, d.d, d.E, d.dtype);
-  w.part = c.take<double>((size_t)w.splits * d.T * d.E);
+  size_t bytes = (size_t)w.splits * d.T * d.E * sizeof(double);
+  w.tile_splits = grouped_tile(d) ? logits_tile_splits(d.T, d.d, d.E) : 0;
+  const size_t n = (size_t)w.tile_splits * d.T * d.E, nx = (size_t)w.tile_splits * d.T;
+  bytes = std::max(bytes, (n + nx + (size_t)w.tile_splits * d.E) * sizeof(float));
+  char* p = static_cast<char*>(c.take_bytes(bytes));
+  w.part = reinterpret_cast<double*>(p);
+  w.approx = reinterpret_cast<float*>(p);
+  w.xn = p ? w.approx + n : nullptr;
+  w.wn = p ? w.xn + nx : nullptr;
 }
 
 size_t ws_size(const moe_desc& d, int op) {
@@ -418,6 +432,15 @@ moe_status moe_route_grouped(const moe_desc* desc, const moe_route_rule* rule, c
   plan_grouped(d, c, gw);
   hipStream_t st = static_cast<hipStream_t>(stream);
   const GroupRule gr{r.score == MOE_SCORE_SOFTMAX, r.n_group, r.topk_group, r.group_score == MOE_GROUP_TOP2, r.renorm};
+  // the screened softmax orders by logit, which a balance bias would not leave so
+  if (gw.tile_splits && !(gr.softmax && select_bias)) {
+    hipError_t e = launch_logits_tile(x, w_router, k, d.T, d.d, d.E, d.k_max, budget(d), gw.tile_splits, gw.approx,
+                                      gw.xn, gw.wn, tok_off, dev_status, st);
+    if (e == hipSuccess)
+      e = launch_route_grouped_screen(gw.approx, gw.xn, gw.wn, gw.tile_splits, x, w_router, d.d, router_bias,
+                                      select_bias, tok_off, d.T, d.E, gr, d.routed_scale, topk_ids, topk_w, st);
+    return launched(e);
+  }
   hipError_t e = launch_logits_f64(d.dtype, x, w_router, k, d.T, d.d, d.E, d.k_max, budget(d), gw.splits, gw.part,
                                    tok_off, dev_status, st);
   if (e == hipSuccess)
