@@ -15,6 +15,8 @@
 #include "screen.h"
 #include "select.h"
 
+#include <type_traits>
+
 namespace moe {
 
 namespace {
@@ -31,100 +33,79 @@ __device__ __forceinline__ double key_score(uint64_t k) {
   return __longlong_as_double((long long)((k >> 63) ? (k & ~(1ull << 63)) : ~k));
 }
 
+// The same for a float32 score.
+__device__ __forceinline__ uint32_t score_key32(float c) {
+  if (!(c > -INFINITY)) return 0;
+  return logit_key(c);
+}
+
 __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
   __builtin_amdgcn_wave_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-__device__ __forceinline__ uint64_t shfl_xor_u64(uint64_t v, int m) {
-  return (uint64_t)__shfl_xor((unsigned long long)v, m, 64);
+// v of one lane, the same for all.
+__device__ __forceinline__ uint64_t read_lane(uint64_t v, int lane) {
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+  const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane);
+  return ((uint64_t)hi << 32) | lo;
 }
-__device__ __forceinline__ double wave_max(double v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v = fmax(v, __shfl_xor(v, off, 64));
-  return v;
+// Reductions over the wave by DPP (a shuffle through LDS takes several times as
+// long): rows of 16 lanes, then the rows; lane 63 has the result, in a fixed order.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp(float old, float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp((int)__float_as_uint(old), (int)__float_as_uint(v), CTRL,
+                                                               ROWS, 0xf, false));
 }
-__device__ __forceinline__ double wave_sum(double v) {  // fixed order: every lane gets the same bits
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
-  return v;
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp(double old, double v) {
+  const uint64_t o = (uint64_t)__double_as_longlong(old), u = (uint64_t)__double_as_longlong(v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp((int)(uint32_t)o, (int)(uint32_t)u, CTRL, ROWS, 0xf, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp((int)(o >> 32), (int)(u >> 32), CTRL, ROWS, 0xf, false);
+  return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+}
+template <class F>
+__device__ __forceinline__ F last_lane(F v) {
+  if constexpr (sizeof(F) == 4) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
+  } else {
+    return __longlong_as_double((long long)read_lane((uint64_t)__double_as_longlong(v), 63));
+  }
+}
+template <class F>
+__device__ __forceinline__ F fmaxx(F a, F b) {
+  if constexpr (sizeof(F) == 4) return fmaxf(a, b);
+  else return fmax(a, b);
+}
+template <class F>
+__device__ __forceinline__ F wave_max(F v) {
+  v = fmaxx(v, dpp<0x111, 0xf>(v, v));  // row_shr 1, 2, 4, 8
+  v = fmaxx(v, dpp<0x112, 0xf>(v, v));
+  v = fmaxx(v, dpp<0x114, 0xf>(v, v));
+  v = fmaxx(v, dpp<0x118, 0xf>(v, v));
+  v = fmaxx(v, dpp<0x142, 0xa>(v, v));  // row_bcast 15, 31
+  v = fmaxx(v, dpp<0x143, 0xc>(v, v));
+  return last_lane(v);
+}
+template <class F>
+__device__ __forceinline__ F wave_sum(F v) {
+  v += dpp<0x111, 0xf>((F)0, v);
+  v += dpp<0x112, 0xf>((F)0, v);
+  v += dpp<0x114, 0xf>((F)0, v);
+  v += dpp<0x118, 0xf>((F)0, v);
+  v += dpp<0x142, 0xa>((F)0, v);
+  v += dpp<0x143, 0xc>((F)0, v);
+  return last_lane(v);
 }
 
 // The two largest of two pairs of keys (a1 >= a2, b1 >= b2).
-__device__ __forceinline__ void merge2(uint64_t& a1, uint64_t& a2, uint64_t b1, uint64_t b2) {
-  const uint64_t hi = a1 > b1 ? a1 : b1, lo = a1 > b1 ? b1 : a1;
-  const uint64_t s = a2 > b2 ? a2 : b2;
+template <class K>
+__device__ __forceinline__ void merge2(K& a1, K& a2, K b1, K b2) {
+  const K hi = a1 > b1 ? a1 : b1, lo = a1 > b1 ? b1 : a1;
+  const K s = a2 > b2 ? a2 : b2;
   a1 = hi;
   a2 = lo > s ? lo : s;
-}
-
-// The k largest keys (1 <= k <= keys > 0): sel marks them.  Radix search from
-// the top bit that stops as soon as exactly k keys reach the trial value; ties
-// at the last key go to the lower expert.
-template <int KPL>
-__device__ __forceinline__ void select_u64(const uint64_t (&key)[KPL], int k, bool (&sel)[KPL]) {
-  const int lane = threadIdx.x & 63;
-  uint64_t prefix = 0;
-  int got = -1;
-  for (int b = 63; b >= 0 && got != k; --b) {
-    const uint64_t trial = prefix | (1ull << b);
-    int c = 0;
-#pragma unroll
-    for (int s = 0; s < KPL; ++s) c += __popcll(__ballot(key[s] >= trial));
-    if (c >= k) {
-      prefix = trial;
-      got = c;
-    }
-  }
-  if (got == k) {
-#pragma unroll
-    for (int s = 0; s < KPL; ++s) sel[s] = key[s] >= prefix;
-    return;
-  }
-  int need = k;
-#pragma unroll
-  for (int s = 0; s < KPL; ++s) {
-    sel[s] = key[s] > prefix;
-    need -= __popcll(__ballot(sel[s]));
-  }
-  const uint64_t below = (1ull << lane) - 1ull;
-#pragma unroll
-  for (int s = 0; s < KPL; ++s) {
-    const uint64_t eq = __ballot(key[s] == prefix);
-    if (need > 0 && key[s] == prefix && __popcll(eq & below) < need) sel[s] = true;
-    need -= min(need, (int)__popcll(eq));
-  }
-}
-
-// Scores of the token's experts from their logits.
-template <int KPL>
-__device__ __forceinline__ void scores(const double (&l)[KPL], int E, int softmax, double (&s)[KPL]) {
-  const int lane = threadIdx.x & 63;
-  if (!softmax) {
-#pragma unroll
-    for (int q = 0; q < KPL; ++q) s[q] = 1.0 / (1.0 + exp(-l[q]));
-    return;
-  }
-  double m = -INFINITY;
-  bool nan = false;
-#pragma unroll
-  for (int q = 0; q < KPL; ++q)
-    if (lane + 64 * q < E) {
-      m = fmax(m, l[q]);
-      nan |= l[q] != l[q];
-    }
-  m = wave_max(m);
-  if (__ballot(nan)) m = NAN;  // a logit that is no number leaves no score of the token a number
-  double t = 0.0;
-#pragma unroll
-  for (int q = 0; q < KPL; ++q) {
-    s[q] = lane + 64 * q < E ? exp(l[q] - m) : 0.0;
-    t += s[q];
-  }
-  t = wave_sum(t);
-#pragma unroll
-  for (int q = 0; q < KPL; ++q) s[q] /= t;
 }
 
 }  // namespace
@@ -282,11 +263,12 @@ hipError_t launch_logits_f64(int dtype, const void* x, const void* w, const int3
 // 128-byte lines (the schedule of the screened router); wave w multiplies
 // experts [32 w, 32 w + 32) with the 64 tokens.  The float32 accumulators start
 // from zero at every stage and are added to float64 ones at its end, so that a
-// float32 sum has at most 64 products: with u = 2^-22 for each addition (the
-// margin of the screened router), a logit is off by at most
-//   r = (64 * 2^-22 + 2^-24) * |x|_2 * max_e |w_e|_2 + d * 2^-126
-// (sum |x_i w_i| <= |x| |w|; 2^-24: the slices are stored in float32), which is
-// 1/28 of what one float32 sum over a slice of 1,792 would leave.  The norms'
+// float32 sum has at most 64 products: with 2^-23 of the running sum for each
+// addition (the instruction may truncate), a logit is off by at most
+//   r = (66 * 2^-23 + 2^-24) * |x|_2 * max_e |w_e|_2 + d * 2^-126
+// (sum |x_i w_i| <= |x| |w|; 66 for 64 covers the second-order terms; 2^-24: the
+// slices are stored in float32).  One float32 sum over a slice of 1,792 would
+// leave 28 times as much.  The norms'
 // squares are summed beside the products, by the slices: xn[S][T], wn[S][E].
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 constexpr int RG_NW = 8, RG_TOK = 64, RG_EXP = 256, RG_STG = 3;
@@ -469,60 +451,313 @@ hipError_t launch_logits_tile(const void* x, const void* w, const int32_t* k, in
 // ---------------------------------------------------------------------------
 // Scores, groups, top-k_t and weights; one wave per token.
 //
-// SCREEN: the logits come from logits_tile_kernel and may be off by r.  A score
-// may then be off by R (sigmoid: r / 4; softmax: a factor within exp(+-2 r)),
-// and two keys whose distance is over 2 R are in their true order.  Only what is
-// closer and decides something is computed again, exactly:
-//  - groups whose value is within 2 R (top2: 4 R) of the last one kept or of the
-//    first one dropped: those of their experts that may be among the counted
-//    ones.  Every other group is certainly kept or certainly dropped.
-//  - then chosen experts and, of the kept groups, experts within 2 R of a chosen
-//    one.  An expert that is further from every chosen one is on its true side
-//    of each, and of anything that takes a chosen one's place.
-// So the ids are those of exact logits, whatever the rounding did.  Where r is
-// large (or no number) every logit of the token is computed exactly.
-// The softmax's sum keeps its screened terms: it scales all scores alike, so
-// the order needs select_bias to be absent (the host takes float64 otherwise).
+// A pass runs the steps in float32 first: two values further apart than the
+// radius of both are in their true order, and where nothing closer decides, the
+// result stands.  The radius is that of the logits (SCREEN: they come from
+// logits_tile_kernel and may be off by r, so a sigmoid by r / 4, a softmax by a
+// factor within exp(+-2 r); nothing for exact ones) plus what float32 rounds off,
+// 2^-20 of the largest score and key.  What is closer is looked at again:
+//  - inexact logits are computed exactly: of the groups whose value is within two
+//    radii of the last one kept or the first one dropped, the experts that may be
+//    among the counted ones (every other group is certainly kept or dropped);
+//    then the chosen, and the experts of kept groups, that are within two radii
+//    of another one across the border of the choice or within the chosen (one that
+//    is further off is on its true side of all of these, whichever is chosen);
+//  - what remains close although its logits are exact takes the same pass in
+//    float64, where exact logits decide by definition.
+// So the ids are those of exact logits and float64 scores.  Where r is large (or
+// no number) every logit is computed exactly.  The softmax's sum keeps screened
+// terms: it scales all scores alike, so the order needs select_bias to be absent
+// (the host takes float64 logits otherwise, and the pass starts in float64).
+//
+// A wave that runs alone waits above all for its instructions: the code of the
+// common pass is short, reductions go by DPP, loops over the chosen broadcast by
+// readlane.  One token, 256 experts in 8 groups: 10.7 -> 6.1 us for this kernel
+// against the same steps in float64 with shuffles and unrolled loops.
 struct ScreenIn {
   const bf16_t *x, *w;
   const float *part, *xn, *wn;
   int d;
 };
 
-// LDS words (8 bytes) of one wave.
-__host__ __device__ constexpr int rg_words(int E, bool screen) { return 2 * E + (screen ? SEL_GRP * 64 + E + E : 0); }
+// LDS words (8 bytes) of one wave: keys; logits; experts and places of the
+// chosen; with SCREEN the exact sums' shares, the sums and their experts.
+__host__ __device__ constexpr int rg_words(int E, bool screen) {
+  return 3 * E + (screen ? SEL_GRP * 64 + E + (E + 1) / 2 : 0);
+}
 
-// Group values of the keys (0: no expert in service), this lane's group in
-// `grp` (lanes of a group: lpg), and its second largest key in `second`.
+__device__ __forceinline__ uint64_t to_key(double c) { return score_key(c); }
+__device__ __forceinline__ uint32_t to_key(float c) { return score_key32(c); }
+__device__ __forceinline__ double to_score(uint64_t k) { return key_score(k); }
+__device__ __forceinline__ float to_score(uint32_t k) { return key_logit(k); }
+__device__ __forceinline__ uint64_t key_lane(uint64_t v, int lane) { return read_lane(v, lane); }
+__device__ __forceinline__ uint32_t key_lane(uint32_t v, int lane) {
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
+}
+__device__ __forceinline__ uint32_t shfl_key(uint32_t v, int lane) { return __shfl(v, lane, 64); }
+__device__ __forceinline__ uint64_t shfl_key(uint64_t v, int lane) {
+  return (uint64_t)__shfl((unsigned long long)v, lane, 64);
+}
+
+// The k-th largest key's value or a lower one that exactly k keys reach (1 <= k <=
+// keys > 0), by a radix search of two bits a step (three independent counts take
+// little longer than one); *got is how many keys reach it.
+template <int KPL, class K>
+__device__ __forceinline__ K kth_key(const K (&key)[KPL], int k, int* got) {
+  K v = 0;
+  int g = -1;
+#pragma unroll 1
+  for (int b = 8 * (int)sizeof(K) - 2; b >= 0 && g != k; b -= 2) {
+    int c[3] = {0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < KPL; ++s)
+#pragma unroll
+      for (int i = 0; i < 3; ++i) c[i] += __popcll(__ballot(key[s] >= (v | ((K)(i + 1) << b))));
+    const int i = c[2] >= k ? 3 : (c[1] >= k ? 2 : (c[0] >= k ? 1 : 0));
+    if (i) {
+      v |= (K)i << b;
+      g = c[2] >= k ? c[2] : (c[1] >= k ? c[1] : c[0]);
+    }
+  }
+  *got = g;
+  return v;
+}
+
+// What the selection of a token keeps between its passes, by slot s of a lane
+// (expert lane + 64 s), as bits of one word.
+struct Marks {
+  uint32_t there, exact, mark;
+};
+
+// p = exp(l - top) (softmax) or exp(-l) in float64, through this wave's E words of
+// LDS so that the long code of the exponential exists once and one slot's
+// temporaries live at a time (four in parallel held 128 registers more).
 template <int KPL>
-__device__ __forceinline__ uint64_t group_value(const uint64_t (&key)[KPL], int E, const GroupRule& g, int lpg,
-                                                uint64_t* lds, uint64_t* second) {
-  const int lane = threadIdx.x & 63, per = E / g.n_group, grp = lane / lpg, sub = lane % lpg;
+__device__ __forceinline__ void exp_by_lds(const double (&l)[KPL], bool softmax, double top, double* buf, int E,
+                                           double (&p)[KPL]) {
+  const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int s = 0; s < KPL; ++s)
-    if (lane + 64 * s < E) lds[lane + 64 * s] = key[s];
+    if (lane + 64 * s < E) buf[lane + 64 * s] = softmax ? l[s] - top : -l[s];
+#pragma unroll 1
+  for (int e = lane; e < E; e += 64) buf[e] = exp(buf[e]);
+#pragma unroll
+  for (int s = 0; s < KPL; ++s) p[s] = buf[min(lane + 64 * s, E - 1)];
   wave_sync();
-  uint64_t m1 = 0, m2 = 0;
-  if (grp < g.n_group)
-    for (int i = sub; i < per; i += lpg) merge2(m1, m2, lds[grp * per + i], 0);
-  for (int off = 1; off < lpg; off <<= 1) {
-    const uint64_t b1 = shfl_xor_u64(m1, off), b2 = shfl_xor_u64(m2, off);
-    merge2(m1, m2, b1, b2);
-  }
-  wave_sync();
-  *second = g.top2 && m2 ? m2 : m1;
-  // two keys above -inf never add to an empty key
-  return g.top2 && m1 && m2 ? score_key(key_score(m1) + key_score(m2)) : m1;
 }
-// Place of this lane's group among the groups (ties: lower group first).
-__device__ __forceinline__ int group_rank(uint64_t val, int n_group, int lpg) {
-  const int grp = (threadIdx.x & 63) / lpg;
-  int rank = 0;
-  for (int j = 0; j < n_group; ++j) {
-    const uint64_t vj = (uint64_t)__shfl((unsigned long long)val, j * lpg, 64);
-    rank += (vj > val || (vj == val && j < grp)) ? 1 : 0;
+
+// One pass in F (float or double).  Returns 0: decided (k chosen: chosen, ls =
+// their logits, place), 1: m.mark asks for exact logits, 2: float32 cannot tell.
+// r2: two radii of scores of inexact logits, per unit of the softmax's 1 / sum.
+template <class F, int KPL>
+__device__ __forceinline__ int route_pass(const double (&l)[KPL], const float (&sb)[KPL], bool biased, int E, int kt,
+                                          const GroupRule& rule, double rl, Marks& m, uint64_t* lds, double* ls,
+                                          int32_t* chosen, int32_t* place, int* k_out, double* top_out) {
+  using K = typename std::conditional<sizeof(F) == 4, uint32_t, uint64_t>::type;
+  constexpr bool F32 = sizeof(F) == 4;
+  constexpr F tiny = F32 ? (F)0x1p-20 : (F)0;
+  // opaque to the compiler: what follows from the lane is not worth a register
+  // for the whole loop of passes
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  K key[KPL];
+  F p[KPL], unit = 0, inv = 1;
+  const bool softmax = rule.softmax;
+  double topd = 0.0;
+  if (softmax) {
+    bool nan = false;
+    topd = -INFINITY;
+#pragma unroll
+    for (int s = 0; s < KPL; ++s)
+      if ((m.there >> s) & 1u) {
+        topd = fmax(topd, l[s]);
+        nan |= l[s] != l[s];
+      }
+    topd = wave_max(topd);
+    if (__ballot(nan)) topd = NAN;  // a logit that is no number leaves no score of the token a number
   }
-  return rank;
+  F sum = 0;
+  if constexpr (!F32) exp_by_lds<KPL>(l, softmax, topd, ls, E, p);
+#pragma unroll
+  for (int s = 0; s < KPL; ++s) {
+    if constexpr (F32) p[s] = expf((float)(softmax ? l[s] - topd : -l[s]));
+    sum += (m.there >> s) & 1u ? p[s] : (F)0;
+  }
+  if (softmax) inv = (F)1 / wave_sum(sum);
+  *top_out = topd;
+#pragma unroll
+  for (int s = 0; s < KPL; ++s) {
+    const F sc = softmax ? p[s] * inv : (F)1 / ((F)1 + p[s]);
+    const F c = biased ? sc + (F)sb[s] : sc;
+    key[s] = (m.there >> s) & 1u ? to_key(c) : 0;
+    if constexpr (F32) {
+      // float32: a few roundings of the score, |a| half steps of the exponent's
+      // argument, one of the key
+      const float a = fminf(fabsf((float)(softmax ? l[s] - topd : l[s])), 1e4f);
+      unit = fmaxf(unit, key[s] ? sc * (1.f + 0.125f * a) + fabsf(c) : 0.f);
+    }
+  }
+  // two radii: of exact logits, and of inexact ones (expm1(2 rl) <= 2.2 rl)
+  const F r0 = F32 ? tiny * wave_max(unit) + (F)0x1p-120 : (F)0;
+  const F r1 = r0 + (F)(softmax ? 4.5 * rl * (double)inv : 0.51 * rl);
+  auto apart = [&](F a, F b, bool both_exact) {  // certainly in order
+    const F r = both_exact ? r0 : r1;
+    return F32 || !both_exact ? fabs(a - b) > r : true;
+  };
+
+  if (rule.topk_group < rule.n_group) {
+    int gp = 1;
+    while (gp < rule.n_group) gp *= 2;
+    const int lpg = 64 / gp, per = E / rule.n_group, grp = lane / lpg, sub = lane % lpg;
+    K* const kl = reinterpret_cast<K*>(lds);
+    const float per_inv = (float)rule.n_group / (float)E;
+    int first[KPL];  // first lane of a slot's group (E <= 1024: the quotient is exact)
+#pragma unroll
+    for (int s = 0; s < KPL; ++s) {
+      const int e = min(lane + 64 * s, E - 1);
+      first[s] = (int)(((float)e + 0.5f) * per_inv) * lpg;
+      if ((m.there >> s) & 1u) kl[e] = key[s];
+    }
+    wave_sync();
+    const bool mine = grp < rule.n_group;
+    K m1 = 0, m2 = 0;
+    if (mine) {
+#pragma unroll 4
+      for (int i = sub; i < per; i += lpg) merge2<K>(m1, m2, kl[grp * per + i], (K)0);
+    }
+#pragma unroll 1
+    for (int off = 1; off < lpg; off <<= 1) {
+      const K b1 = shfl_key(m1, lane ^ off), b2 = shfl_key(m2, lane ^ off);
+      merge2<K>(m1, m2, b1, b2);
+    }
+    wave_sync();
+    // two keys above -inf never add to an empty key
+    const K val = rule.top2 && m1 && m2 ? to_key(to_score(m1) + to_score(m2)) : m1;
+    // place of the lane's group: each of its lpg lanes compares with every lpg-th
+    int rank = 0;
+    if (mine && sub == 0) kl[grp] = val;
+    wave_sync();
+    for (int j = sub; j < rule.n_group; j += lpg) {
+      const K vj = kl[j];
+      rank += (vj > val || (vj == val && j < grp)) ? 1 : 0;
+    }
+#pragma unroll 1
+    for (int off = 1; off < lpg; off <<= 1) rank += __shfl_xor(rank, off, 64);
+    wave_sync();
+    const uint64_t ml = __ballot(mine && rank == rule.topk_group - 1), mf = __ballot(mine && rank == rule.topk_group);
+    const K vl = key_lane(val, __builtin_ctzll(ml)), vf = key_lane(val, __builtin_ctzll(mf));
+    const F z = rule.top2 ? (F)2 : (F)1;
+    // a group without experts in service is last, whatever the scores
+    if (vf != 0 && !(to_score(vl) - to_score(vf) > z * r1 + r0)) {
+      const F v = to_score(val);
+      const bool zone = mine && val != 0 && (!(fabs(v - to_score(vl)) > z * r1 + r0) ||
+                                             !(fabs(v - to_score(vf)) > z * r1 + r0));
+      const uint64_t zones = __ballot(zone);
+      const K second = rule.top2 && m2 ? m2 : m1;
+      m.mark = 0;
+#pragma unroll
+      for (int s = 0; s < KPL; ++s) {
+        const K sec = shfl_key(second, first[s]);
+        if (key[s] != 0 && ((zones >> first[s]) & 1ull) && !(to_score(sec) - to_score(key[s]) > r1)) m.mark |= 1u << s;
+      }
+      m.mark &= ~m.exact;
+      if (__ballot(m.mark != 0)) return 1;
+      if (F32 && !(to_score(vl) - to_score(vf) > (z + 1) * r0)) return 2;
+    }
+    const uint64_t in_kept = __ballot(mine && rank < rule.topk_group);
+#pragma unroll
+    for (int s = 0; s < KPL; ++s)
+      if (!((in_kept >> first[s]) & 1ull)) key[s] = 0;
+  }
+
+  int avail = 0;
+#pragma unroll
+  for (int s = 0; s < KPL; ++s) avail += __popcll(__ballot(key[s] != 0));
+  const int k = min(kt, avail);
+  *k_out = k;
+  if (k == 0) return 0;
+  int got;
+  const K v = kth_key<KPL, K>(key, k, &got);
+  // experts on either side of v, within the radius of it
+  const F pv = to_score(v);
+  uint32_t near = 0, near0 = 0, above = 0;
+#pragma unroll
+  for (int s = 0; s < KPL; ++s) {
+    const F dist = fabs(to_score(key[s]) - pv);
+    if (key[s] != 0 && !(dist > r1)) near |= 1u << s;
+    if (F32 && key[s] != 0 && !(dist > r0)) near0 |= 1u << s;
+    if (key[s] >= v) above |= 1u << s;
+  }
+  m.mark = 0;
+  if (got != k || (__ballot((near & above) != 0) && __ballot((near & ~above) != 0))) m.mark = near & ~m.exact;
+  if (F32 && !__ballot(m.mark != 0) &&
+      (got != k || (__ballot((near0 & above) != 0) && __ballot((near0 & ~above) != 0))))
+    return 2;
+  // the chosen, listed in ascending expert order: the keys above v, then equal
+  // ones from the lower expert on until there are k
+  const uint64_t below = (1ull << lane) - 1ull;
+  int n = 0, need = k;
+  if (got != k) {
+#pragma unroll
+    for (int s = 0; s < KPL; ++s) need -= __popcll(__ballot(key[s] > v));
+  }
+  int slot[KPL];
+  K* const kl = reinterpret_cast<K*>(lds);
+#pragma unroll
+  for (int s = 0; s < KPL; ++s) {
+    bool sel = key[s] != 0 && key[s] >= v;
+    if (got != k) {
+      const uint64_t eq = __ballot(key[s] == v);
+      sel = key[s] > v || (key[s] == v && __popcll(eq & below) < need);
+      need -= min(need, (int)__popcll(eq));
+    }
+    const uint64_t b = __ballot(sel);
+    slot[s] = sel ? n + __popcll(b & below) : -1;
+    if (sel) {
+      kl[slot[s]] = key[s];
+      ls[slot[s]] = l[s];
+      chosen[slot[s]] = lane + 64 * s;
+      place[slot[s]] = (m.exact >> s) & 1u;  // for the loop below
+    }
+    n += __popcll(b);
+  }
+  wave_sync();
+  // a chosen one's place is the number of chosen keys that are larger, or equal
+  // with a lower expert: lanes hold pairs (i, j), P = 2^lp lanes for each i
+  bool unsure = false;
+  int lp = 0;
+  while ((1 << lp) < k && lp < 6) ++lp;
+  const int per_pass = 64 >> lp, pj = lane & ((1 << lp) - 1);
+#pragma unroll 1
+  for (int i0 = 0; i0 < k; i0 += per_pass) {
+    const int i = i0 + (lane >> lp);
+    const K ki = kl[min(i, k - 1)];
+    const F ci = to_score(ki);
+    const bool xi = place[min(i, k - 1)] & 1;
+    int r = 0;
+    bool close = false;
+#pragma unroll 1
+    for (int j0 = 0; j0 < k; j0 += 64) {
+      const int j = j0 + pj;
+      const bool pair = i < k && j < k;
+      const K kj = kl[min(j, k - 1)];
+      const bool xj = place[min(j, k - 1)] & 1;
+      const bool touch = pair && i != j && !apart(ci, to_score(kj), xi && xj);
+      unsure |= touch && xi && xj;
+      const uint64_t first_lanes = (lp == 6 ? ~0ull : (1ull << (1 << lp)) - 1) << (lane & ~((1 << lp) - 1));
+      r += __popcll(__ballot(pair && (kj > ki || (kj == ki && j < i))) & first_lanes);
+      close |= (__ballot(touch && !xi) & first_lanes) != 0;
+    }
+    wave_sync();
+    if (i < k && pj == 0) place[i] = (xi ? 1 : 0) | (r << 2) | (close ? 2 : 0);
+    wave_sync();
+  }
+#pragma unroll
+  for (int s = 0; s < KPL; ++s)
+    if (slot[s] >= 0 && (place[slot[s]] & 2)) m.mark |= 1u << s;
+  m.mark &= ~m.exact;
+  if (__ballot(m.mark != 0)) return 1;
+  return F32 && __ballot(unsure) ? 2 : 0;
 }
 
 template <int KPL, bool SCREEN>
@@ -533,241 +768,153 @@ __global__ __launch_bounds__(256) void route_grouped_kernel(const double* __rest
                                                             GroupRule rule, float scale, int32_t* __restrict__ ids,
                                                             float* __restrict__ wts) {
   extern __shared__ uint64_t rg_lds[];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  // wv is uniform: with it in a scalar register so are the token and its addresses
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int t = blockIdx.x * (blockDim.x >> 6) + wv;
   if (t >= T_) return;
   uint64_t* const lds = rg_lds + (size_t)wv * rg_words(E, SCREEN);
+  double* const ls = reinterpret_cast<double*>(lds + E);
+  int32_t* const chosen = reinterpret_cast<int32_t*>(lds + 2 * E);
+  int32_t* const place = chosen + E;
   const int base = tok_off[t];
   const int kt = tok_off[t + 1] - base;
-  const uint64_t below = (1ull << lane) - 1ull;
-  // slices are added in ascending order, G of them in flight
-  constexpr int G = 32 / KPL;
-  const size_t qstride = (size_t)T_ * E;
-  double l[KPL], sc[KPL];
+  // slices are added in ascending order, G of them in flight (the last one's
+  // address again behind the end: no branch between the loads)
+  constexpr int G = KPL <= 4 ? (SCREEN ? 4 : 8) : 2;
+  double l[KPL];
+  float wn[KPL], bs[KPL], sb[KPL], xx = 0.f;
+  Marks m{0u, 0u, 0u};
 #pragma unroll
-  for (int s = 0; s < KPL; ++s) l[s] = 0.0;
+  for (int s = 0; s < KPL; ++s) {
+    const uint32_t e = (uint32_t)min(lane + 64 * s, E - 1);
+    l[s] = 0.0;
+    wn[s] = 0.f;
+    bs[s] = bias ? bias[e] : 0.f;
+    sb[s] = sel_bias ? sel_bias[e] : 0.f;
+    if (lane + 64 * s < E) m.there |= 1u << s;
+  }
+  if constexpr (SCREEN) xx = lane < S ? in.xn[(size_t)lane * T_ + t] : 0.f;  // S <= 32
+#pragma unroll 1
   for (int q0 = 0; q0 < S; q0 += G) {
-    double v[KPL][G];
+    typename std::conditional<SCREEN, float, double>::type v[KPL][G];
+    float n[KPL][G];
 #pragma unroll
-    for (int s = 0; s < KPL; ++s) {
-      const size_t at = (size_t)t * E + min(lane + 64 * s, E - 1);
+    for (int i = 0; i < G; ++i) {
+      const size_t q = (size_t)min(q0 + i, S - 1);
 #pragma unroll
-      for (int i = 0; i < G; ++i) {
-        const size_t o = at + (size_t)(q0 + i) * qstride;
-        v[s][i] = q0 + i < S ? (SCREEN ? (double)in.part[o] : part[o]) : 0.0;
+      for (int s = 0; s < KPL; ++s) {
+        const uint32_t e = (uint32_t)min(lane + 64 * s, E - 1);
+        if constexpr (SCREEN) {
+          v[s][i] = (in.part + (q * T_ + t) * E)[e];
+          n[s][i] = (in.wn + q * E)[e];
+        } else {
+          v[s][i] = (part + (q * T_ + t) * E)[e];
+        }
       }
     }
 #pragma unroll
-    for (int s = 0; s < KPL; ++s)
+    for (int i = 0; i < G; ++i) {
+      if (q0 + i >= S) break;
 #pragma unroll
-      for (int i = 0; i < G; ++i) l[s] += v[s][i];
+      for (int s = 0; s < KPL; ++s) {
+        l[s] += (double)v[s][i];
+        if constexpr (SCREEN) wn[s] += n[s][i];
+      }
+    }
   }
   if (kt == 0) return;
-  float bs[KPL], sb[KPL];
 #pragma unroll
   for (int s = 0; s < KPL; ++s) {
-    const int e = lane + 64 * s;
-    bs[s] = bias && e < E ? bias[e] : 0.f;
-    sb[s] = sel_bias && e < E ? sel_bias[e] : 0.f;
     l[s] += (double)bs[s];
     if (!SCREEN) l[s] = (double)(float)l[s];
   }
-
-  double R2 = 0.0;  // twice the radius of a score
-  bool exact[KPL];  // slots whose logit is exact
-#pragma unroll
-  for (int s = 0; s < KPL; ++s) exact[s] = !SCREEN;
-  auto rescore = [&](uint64_t (&key)[KPL]) {
-    scores<KPL>(l, E, rule.softmax, sc);
-#pragma unroll
-    for (int s = 0; s < KPL; ++s)
-      key[s] = lane + 64 * s < E ? score_key(sel_bias ? sc[s] + (double)sb[s] : sc[s]) : 0;
-  };
-  // exact logits of the marked slots
-  auto refine = [&](const bool (&mark)[KPL]) -> bool {
-    int32_t* const list = reinterpret_cast<int32_t*>(lds + 2 * E + SEL_GRP * 64);
-    double* const val = reinterpret_cast<double*>(lds + 2 * E + SEL_GRP * 64 + E);
-    int n = 0, at[KPL];
-#pragma unroll
-    for (int s = 0; s < KPL; ++s) {
-      const bool want = mark[s] && !exact[s] && lane + 64 * s < E;
-      const uint64_t m = __ballot(want);
-      at[s] = want ? n + __popcll(m & below) : -1;
-      if (want) list[at[s]] = lane + 64 * s;
-      n += __popcll(m);
-    }
-    if (n == 0) return false;
-    wave_sync();
-    exact_dots<4, false, SEL_GRP>(
-        in.x + (size_t)t * in.d, in.d, n, [&](int c) { return in.w + (size_t)list[c] * in.d; },
-        reinterpret_cast<double*>(lds + 2 * E), [&](int c, double v) { val[c] = v; });
-#pragma unroll
-    for (int s = 0; s < KPL; ++s)
-      if (at[s] >= 0) {
-        l[s] = (double)(float)(val[at[s]] + (double)bs[s]);
-        exact[s] = true;
-      }
-    wave_sync();
-    return true;
-  };
-
-  uint64_t key[KPL];
+  if (!SCREEN) m.exact = m.there;
+  double rl = 0.0;  // how far a logit may be off
+  bool wide = rule.softmax && sel_bias;
+  bool all = false;
   if constexpr (SCREEN) {
-    double xx = 0.0, ww = 0.0, lm = 0.0;
-    for (int q = 0; q < S; ++q) xx += (double)in.xn[(size_t)q * T_ + t];
+    float ww = 0.f, lm = 0.f;
+    bool nan = false;
 #pragma unroll
     for (int s = 0; s < KPL; ++s) {
-      const int e = min(lane + 64 * s, E - 1);
-      double a = 0.0;
-      for (int q = 0; q < S; ++q) a += (double)in.wn[(size_t)q * E + e];
-      ww = a > ww || a != a ? a : ww;
-      lm = fmax(lm, fabs(l[s]));
+      nan |= wn[s] != wn[s] || l[s] != l[s];
+      ww = fmaxf(ww, wn[s]);
+      lm = fmaxf(lm, fabsf((float)l[s]));
     }
-    const bool nan = __ballot(ww != ww) != 0;
     // 1.01: the float32 sums of the squares (at most 65,536 terms of 2^-24 each)
-    const double prod = 1.01 * sqrt(xx) * sqrt(wave_max(ww));
-    const double r = prod * (64.0 * 0x1p-22 + 0x1p-24) + in.d * 0x1p-126;
-    const double rl = r + (wave_max(lm) + r) * 0x1p-24 + 0x1p-149;  // and the one rounding of the exact logit
-    rescore(key);
-    bool all[KPL];
-#pragma unroll
-    for (int s = 0; s < KPL; ++s) all[s] = true;
-    if (nan || !(rl < 0.0625)) {
-      if (refine(all)) rescore(key);
-    } else if (rule.softmax) {
-      double sm = 0.0;
-#pragma unroll
-      for (int s = 0; s < KPL; ++s)
-        if (lane + 64 * s < E) sm = fmax(sm, sc[s]);
-      R2 = 2.0 * expm1(2.0 * rl) * wave_max(sm) + 0x1p-50;
-    } else {
-      R2 = 0.5 * rl + 0x1p-50;
+    const double prod = 1.01 * (double)sqrtf(wave_sum(xx)) * (double)sqrtf(wave_max(ww));
+    const double r = prod * (66.0 * 0x1p-23 + 0x1p-24) + in.d * 0x1p-126;
+    rl = r + ((double)wave_max(lm) + r) * 0x1.1p-24 + 0x1p-149;  // and the one rounding of the exact logit
+    all = __ballot(nan) != 0 || !(rl < 0.0625);
+    if (all) {
+      m.mark = m.there;
+      rl = 0.0;
     }
-  } else {
-    rescore(key);
   }
 
-  // groups
-  if (rule.topk_group < rule.n_group) {
-    int gp = 1;
-    while (gp < rule.n_group) gp *= 2;
-    const int lpg = 64 / gp, per = E / rule.n_group, grp = lane / lpg;
-    uint64_t second;
-    uint64_t val = group_value<KPL>(key, E, rule, lpg, lds, &second);
-    int rank = group_rank(val, rule.n_group, lpg);
-    if constexpr (SCREEN) {
-      // values of the last group kept and the first dropped
-      const bool mine = grp < rule.n_group;
-      const uint64_t ml = __ballot(mine && rank == rule.topk_group - 1), mf = __ballot(mine && rank == rule.topk_group);
-      const uint64_t vl = (uint64_t)__shfl((unsigned long long)val, __builtin_ctzll(ml), 64);
-      const uint64_t vf = (uint64_t)__shfl((unsigned long long)val, __builtin_ctzll(mf), 64);
-      const double z2 = rule.top2 ? 2.0 * R2 : R2;
-      // a group without experts in service is last, whatever the scores
-      if (vf != 0 && !(key_score(vl) - key_score(vf) > z2)) {
-        const double v = key_score(val);
-        const bool zone = mine && val != 0 && (!(fabs(v - key_score(vl)) > z2) || !(fabs(v - key_score(vf)) > z2));
-        const uint64_t zones = __ballot(zone);
-        bool mark[KPL];
-#pragma unroll
-        for (int s = 0; s < KPL; ++s) {
-          const int e = lane + 64 * s, first = (min(e, E - 1) / per) * lpg;
-          const uint64_t sec = (uint64_t)__shfl((unsigned long long)second, first, 64);
-          mark[s] = e < E && key[s] != 0 && ((zones >> first) & 1ull) && !(key_score(sec) - key_score(key[s]) > R2);
-        }
-        if (refine(mark)) {
-          rescore(key);
-          val = group_value<KPL>(key, E, rule, lpg, lds, &second);
-          rank = group_rank(val, rule.n_group, lpg);
-        }
+  int k = 0, state = all ? 1 : 0;
+  double top = 0.0;
+#pragma unroll 1
+  for (;;) {
+    if (!all) {
+      if (!wide) {
+        state = route_pass<float, KPL>(l, sb, sel_bias != nullptr, E, kt, rule, rl, m, lds, ls, chosen, place, &k, &top);
+        wide = state == 2;
       }
+      if (wide)
+        state = route_pass<double, KPL>(l, sb, sel_bias != nullptr, E, kt, rule, rl, m, lds, ls, chosen, place, &k, &top);
+      if (state == 0) break;
     }
-    const uint64_t kept = __ballot(grp < rule.n_group && rank < rule.topk_group);
+    all = false;
+    if constexpr (SCREEN) {  // exact logits of the marked slots
+      int32_t* const list = reinterpret_cast<int32_t*>(lds + 4 * E + SEL_GRP * 64);
+      double* const val = reinterpret_cast<double*>(lds + 3 * E + SEL_GRP * 64);
+      const uint64_t below = (1ull << lane) - 1ull;
+      int n = 0, at[KPL];
 #pragma unroll
-    for (int s = 0; s < KPL; ++s) {
-      const int e = lane + 64 * s;
-      if (e < E && !((kept >> ((e / per) * lpg)) & 1ull)) sb[s] = -INFINITY;  // out of this token's reach
-      if (sb[s] == -INFINITY) key[s] = 0;
-    }
-  }
-  int avail = 0;
-#pragma unroll
-  for (int s = 0; s < KPL; ++s) avail += __popcll(__ballot(key[s] != 0));
-  const int k = min(kt, avail);
-
-  // the chosen, listed in ascending expert order
-  bool sel[KPL];
-  int slot[KPL];
-  auto choose = [&]() {
-#pragma unroll
-    for (int s = 0; s < KPL; ++s) sel[s] = false;
-    if (k > 0) select_u64<KPL>(key, k, sel);
-    int n = 0;
-#pragma unroll
-    for (int s = 0; s < KPL; ++s) {
-      const uint64_t m = __ballot(sel[s]);
-      slot[s] = sel[s] ? n + __popcll(m & below) : -1;
-      if (sel[s]) lds[slot[s]] = key[s];
-      n += __popcll(m);
-    }
-    wave_sync();
-  };
-  choose();
-  if constexpr (SCREEN) {
-    int32_t* const near = reinterpret_cast<int32_t*>(lds + E);
-    for (int j = lane; j < k; j += 64) near[j] = 0;
-    wave_sync();
-    bool mark[KPL];
-    bool any = false;
-#pragma unroll
-    for (int s = 0; s < KPL; ++s) {
-      mark[s] = false;
-      if (key[s] == 0) continue;
-      const double c = key_score(key[s]);
-      for (int j = 0; j < k; ++j)
-        if (j != slot[s] && !(fabs(c - key_score(lds[j])) > R2)) {
-          mark[s] = true;
-          near[j] = 1;
-        }
-      any |= mark[s];
-    }
-    if (__ballot(any)) {
+      for (int s = 0; s < KPL; ++s) {
+        const bool want = (m.mark >> s) & 1u;
+        const uint64_t b = __ballot(want);
+        at[s] = n + __popcll(b & below);
+        if (want) list[at[s]] = lane + 64 * s;
+        n += __popcll(b);
+      }
       wave_sync();
+      exact_dots<2, false, SEL_GRP>(
+          in.x + (size_t)t * in.d, in.d, n, [&](int c) { return in.w + (size_t)list[c] * in.d; },
+          reinterpret_cast<double*>(lds + 3 * E), [&](int c, double v) { val[c] = v; });
 #pragma unroll
       for (int s = 0; s < KPL; ++s)
-        if (sel[s] && near[slot[s]]) mark[s] = true;
-      if (refine(mark)) {
-        uint64_t nk[KPL];
-        rescore(nk);
-#pragma unroll
-        for (int s = 0; s < KPL; ++s) key[s] = key[s] != 0 ? nk[s] : 0;
-        choose();
-      }
+        if ((m.mark >> s) & 1u) l[s] = (double)(float)(val[at[s]] + (double)bs[s]);
+      m.exact |= m.mark;
+      m.mark = 0;
+      wave_sync();
     }
   }
-  // each one's place: the chosen keys that are larger, or equal with a lower expert
-  double* const ps = reinterpret_cast<double*>(lds + E);
+
+  // ids and weights: the chosen's scores in float64 from their logits (a softmax's
+  // sum cancels where the weights are renormalised)
+  double p = 0.0, denom = 1.0;
+  if (rule.softmax && !rule.renorm) {
+    double pe[KPL];
+    exp_by_lds<KPL>(l, true, top, reinterpret_cast<double*>(lds), E, pe);
 #pragma unroll
-  for (int s = 0; s < KPL; ++s) {
-    if (!sel[s]) continue;
-    int r = 0;
-    for (int j = 0; j < k; ++j) {
-      const uint64_t kj = lds[j];
-      r += (kj > key[s] || (kj == key[s] && j < slot[s])) ? 1 : 0;
-    }
-    slot[s] = r;
-    ps[r] = sc[s];
-    ids[base + r] = lane + 64 * s;
+    for (int s = 0; s < KPL; ++s) p += (m.there >> s) & 1u ? pe[s] : 0.0;
+    denom = wave_sum(p);
+    p = 0.0;
   }
-  wave_sync();
-  double total = 1.0;
-  if (rule.renorm) {
-    double p = 0.0;
-    for (int j = lane; j < k; j += 64) p += ps[j];
-    total = wave_sum(p);
+#pragma unroll 1
+  for (int i = lane; i < k; i += 64) {
+    const double a = ls[i], q = exp(rule.softmax ? a - top : -a);
+    ls[i] = (rule.softmax ? q : 1.0) / (rule.softmax ? denom : 1.0 + q);
+    p += ls[i];
+    ids[base + (place[i] >> 2)] = chosen[i];
   }
-#pragma unroll
-  for (int s = 0; s < KPL; ++s)
-    if (sel[s]) wts[base + slot[s]] = total > 0.0 ? (float)((double)scale * (sc[s] / total)) : 0.f;
+  const double total = rule.renorm ? wave_sum(p) : 1.0;
+#pragma unroll 1
+  for (int i = lane; i < k; i += 64)
+    wts[base + (place[i] >> 2)] = total > 0.0 ? (float)((double)scale * (ls[i] / total)) : 0.f;
+#pragma unroll 1
   for (int j = k + lane; j < kt; j += 64) {
     ids[base + j] = -1;
     wts[base + j] = 0.f;
