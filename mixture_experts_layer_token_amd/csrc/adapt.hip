@@ -81,15 +81,34 @@ __device__ __forceinline__ f32x4_t mma16(const u32x4_t& a, const u32x4_t& b, f32
 
 }  // namespace
 
-// v[r][:] = A[a][g] x[r], partial over slice blockIdx.y of K: part[s][r][R].
+// The distinct (adapter, expert) pairs of a window, as seen by every lane of a wave:
+// f(rows, a, g, rank, mine) for each z-th of Z of them, in the order of their first
+// rows.  `rank`: the lane's row's adapter's.
+template <class F>
+__device__ __forceinline__ void for_pairs(const AdaptRow& row, int rank, int z, int Z, F f) {
+  uint32_t todo = (uint32_t)__ballot(row.a >= 0) & 0xffffu;
+  for (int i = 0; todo; ++i) {
+    const int first = __builtin_ctz(todo);
+    const int a = __builtin_amdgcn_readlane(row.a, first), g = __builtin_amdgcn_readlane(row.g, first);
+    const bool mine = row.a == a && row.g == g;
+    const uint32_t rows = (uint32_t)__ballot(mine) & 0xffffu;
+    todo &= ~rows;
+    if (i % Z == z) f(rows, a, g, __builtin_amdgcn_readlane(rank, first), mine);
+  }
+}
+
+// v[r][:] = scale A[a][g] x[r], partial over slice blockIdx.y of K: part[s][r][R],
+// 0 behind the adapter's rank.
 // The workgroup's four waves take quarters of the slice and are added in wave
 // order.  A lane's 16 bytes of x row l % 16 and of A row l % 16 hold the same K.
+// blockIdx.z takes every Z-th pair of the window: where windows are few (decode)
+// and hold many adapters, their latencies pass side by side.
 template <typename T, int RT>
 __global__ __launch_bounds__(256) void adapt_shrink_kernel(AdaptArgs p, float* __restrict__ part) {
   constexpr int LE = 16 / (int)sizeof(T);
   constexpr int KS = 4 * LE;  // K of one step (four lane groups)
   __shared__ int32_t off[MAX_G + 1];
-  __shared__ float red[4][AW][16 * RT];
+  __shared__ float red[4][AW][16 * RT + 1], scale[AW];
   stage_offsets(p, off);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, lg = lane >> 4;
   const AdaptRow row = adapt_row(p, (int)blockIdx.x * AW + l16, off);
@@ -99,20 +118,16 @@ __global__ __launch_bounds__(256) void adapt_shrink_kernel(AdaptArgs p, float* _
 #pragma unroll
   for (int i = 0; i < RT; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   const T* const xr = (const T*)p.x + (size_t)row.x * p.K;
-  uint32_t todo = (uint32_t)__ballot(row.a >= 0) & 0xffffu;
-  const bool any = todo != 0;
-  while (todo) {
-    const int first = __builtin_ctz(todo);
-    const int a = __shfl(row.a, first, 64), g = __shfl(row.g, first, 64);
-    const bool mine = row.a == a && row.g == g;
-    const uint32_t rows = (uint32_t)__ballot(mine);
-    todo &= ~rows;
-    const int rank = adapt_rank(p, a);
+  uint32_t done = 0;  // rows that this workgroup computes
+  const int my_rank = row.a >= 0 ? adapt_rank(p, row.a) : 0;
+  const float my_scale = row.a >= 0 && p.scales ? p.scales[row.a] : 1.0f;
+  for_pairs(row, my_rank, blockIdx.z, gridDim.z, [&](uint32_t rows, int a, int g, int rank, bool mine) {
+    done |= rows;
     const T* const am = (const T*)p.a + ((size_t)a * p.G + g) * (size_t)p.R * p.K;
     f32x4_t t[RT];
 #pragma unroll
     for (int i = 0; i < RT; ++i) t[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    constexpr int U = RT <= 2 ? 4 : 2;
+    constexpr int U = RT <= 2 ? 8 : (RT <= 4 ? 4 : 2);  // steps in flight
     for (int s = s0; s < s1; s += U) {
       u32x4_t xv[U], av[U][RT];
 #pragma unroll
@@ -138,8 +153,9 @@ __global__ __launch_bounds__(256) void adapt_shrink_kernel(AdaptArgs p, float* _
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         if ((rows >> (4 * lg + r)) & 1u) acc[i][r] = t[i][r];
-  }
-  if (!any) return;  // no adapter in the window (the same for the four waves): never read
+  });
+  if (!done) return;  // the same for the four waves
+  if (threadIdx.x < AW) scale[threadIdx.x] = my_scale;
   // acc[i][r] is row 4 * lg + r, rank 16 * i + l16
 #pragma unroll
   for (int i = 0; i < RT; ++i)
@@ -147,169 +163,222 @@ __global__ __launch_bounds__(256) void adapt_shrink_kernel(AdaptArgs p, float* _
     for (int r = 0; r < 4; ++r) red[wave][4 * lg + r][16 * i + l16] = acc[i][r];
   __syncthreads();
   float* const out = part + ((size_t)blockIdx.y * p.rows + (size_t)blockIdx.x * AW) * p.R;
-  const int left = min(AW, p.rows - (int)blockIdx.x * AW);
-  for (int i = threadIdx.x; i < left * p.R; i += 256) {
+  for (int i = threadIdx.x; i < AW * p.R; i += 256) {
     const int r = i / p.R, c = i % p.R;
-    out[i] = (red[0][r][c] + red[1][r][c]) + (red[2][r][c] + red[3][r][c]);
+    if ((done >> r) & 1u) out[i] = scale[r] * ((red[0][r][c] + red[1][r][c]) + (red[2][r][c] + red[3][r][c]));
   }
 }
 
-// out[r] = y[r] + scale * B v: each wave takes 64 columns at a time of a window.
-// The matrix instruction's rows are the columns of y: row i of tile j is column
-// 16 * (i / 4) + 4 * j + i % 4 of the 64, so that a lane ends with 16 columns of
-// one row in a run and a row's 64 columns are one contiguous piece.
-template <typename T, int RT>
+// out[r] = y[r] + B v: a wave takes up to 4 chunks of 64 columns of a window, for
+// every Z-th of its pairs.  The matrix instruction's rows are the columns of y:
+// row i of tile j is column 32 (j / 2) + 8 (i / 4) + 4 (j % 2) + i % 4 of the
+// chunk, so that a lane ends with runs of 8 columns of one row and four lanes with
+// 64 contiguous bytes of it (bf16).  A fragment of B holds 4 * LE ranks (lane
+// group lg: LE of them); bf16 multiplies it with v and with its remainder.  A wave
+// has little to compute and much to wait for: all its rows of y are requested
+// first, and B of the next DEPTH (pair, chunk) items while one is multiplied.
+template <typename T, int NF>
 __global__ __launch_bounds__(256) void adapt_expand_kernel(AdaptArgs p, const float* __restrict__ part, int S,
-                                                           int cols) {
-  constexpr int LE = 16 / (int)sizeof(T);       // ranks of a lane's chunk
+                                                           int chunks) {
+  constexpr int LE = 16 / (int)sizeof(T);
   constexpr bool BF = sizeof(T) == 2;
-  constexpr int STEPS = RT;                     // bf16: 2 R / 32; float: R / 16
-  constexpr int YV = 16 / LE;                   // 16-byte pieces of a lane's 16 columns
+  constexpr int CM = 4;                                    // chunks of 64 columns at most
+  constexpr int YV = BF ? 2 : 4;                           // 16-byte pieces of a lane's 16 columns
+  constexpr int DEPTH = NF == 1 ? 4 : (NF == 2 ? 2 : 1);   // items of B in registers
   __shared__ int32_t off[MAX_G + 1];
   stage_offsets(p, off);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, lg = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l16 = lane & 15, lg = lane >> 4;
   const int r = (int)blockIdx.x * AW + l16;
-  const AdaptRow row = adapt_row(p, r, off);
-  const bool inplace = p.y == p.out;
-  const uint32_t all = (uint32_t)__ballot(row.a >= 0) & 0xffffu;
-  const int n_beg = ((int)blockIdx.y * 4 + wave) * cols, n_end = min(p.N, n_beg + cols);
+  const int n_beg = ((int)blockIdx.y * 4 + wave) * chunks * 64;
   if (n_beg >= p.N) return;
-  if (inplace && !all) return;
-
-  // this lane's chunks of v: step st, chunk 4 * st + lg
-  const int nchunk = p.R / LE;
-  u32x4_t vf[STEPS];
-  int bch[STEPS];  // the chunk of B's row that goes with it, -1: none
+  const bool inplace = p.y == p.out;
+  // this lane's ranks: LE from (4 f + lg) LE on, f < NF; parts of rows without an
+  // adapter were not written: they are read and left out
+  float v[NF][LE];
 #pragma unroll
-  for (int st = 0; st < STEPS; ++st) {
-    const int c = 4 * st + lg;
-    const bool lo = BF && c >= nchunk;
-    const int rc = lo ? c - nchunk : c;
-    bch[st] = rc < nchunk ? rc : -1;
-    vf[st] = u32x4_t{0u, 0u, 0u, 0u};
-    if (bch[st] < 0 || row.a < 0) continue;
-    const int rank = adapt_rank(p, row.a);
-    const float scale = p.scales ? p.scales[row.a] : 1.0f;
-    float v[LE];
+  for (int f = 0; f < NF; ++f)
 #pragma unroll
-    for (int i = 0; i < LE; ++i) v[i] = 0.f;
+    for (int i = 0; i < LE; ++i) v[f][i] = 0.f;
+  if (r < p.rows) {
     for (int s = 0; s < S; ++s) {
-      const float* src = part + ((size_t)s * p.rows + r) * p.R + rc * LE;
 #pragma unroll
-      for (int i = 0; i < LE; ++i) v[i] += src[i];
-    }
+      for (int f = 0; f < NF; ++f) {
+        const int c = (4 * f + lg) * LE;
+        if (c < p.R) {
+          const float4* src = reinterpret_cast<const float4*>(part + ((size_t)s * p.rows + r) * p.R + c);
 #pragma unroll
-    for (int i = 0; i < LE; ++i) v[i] = rc * LE + i < rank ? v[i] * scale : 0.f;
-    if constexpr (BF) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t h[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const bf16_t hi = f32_to_bf16(v[2 * i + e]);
-          h[e] = lo ? f32_to_bf16(v[2 * i + e] - bf16_to_f32(hi)) : hi;
+          for (int i = 0; i < LE / 4; ++i) {
+            const float4 q = src[i];
+            v[f][4 * i] += q.x;
+            v[f][4 * i + 1] += q.y;
+            v[f][4 * i + 2] += q.z;
+            v[f][4 * i + 3] += q.w;
+          }
         }
-        vf[st][i] = h[0] | (h[1] << 16);
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) vf[st][i] = __float_as_uint(v[i]);
     }
   }
+  const AdaptRow row = adapt_row(p, r, off);
+  const int my_rank = row.a >= 0 ? adapt_rank(p, row.a) : 0;
+  // the wave's pairs, one in each of the first lanes
+  int pa = 0, pg = 0, prank = 0, np = 0;
+  bool served = false;
+  for_pairs(row, my_rank, blockIdx.z, gridDim.z, [&](uint32_t, int a, int g, int rank, bool mine) {
+    if (lane == np) {
+      pa = a;
+      pg = g;
+      prank = rank;
+    }
+    served |= mine;
+    ++np;
+  });
+  // rows without an adapter are copied
+  const bool copied = blockIdx.z == 0 && !inplace && row.live && row.a < 0;
 
   const T* const yr = (const T*)p.y + (size_t)r * p.N;
   T* const outr = (T*)p.out + (size_t)r * p.N;
-  for (int n0 = n_beg; n0 < n_end; n0 += 64) {
-    u32x4_t yv[YV];
+  // column of piece i of a lane's share of chunk c
+  auto col = [&](int c, int i) {
+    return n_beg + 64 * c + (BF ? 32 * i + 8 * lg : 32 * (i >> 1) + 8 * lg + 4 * (i & 1));
+  };
+  u32x4_t yv[CM][YV];
+#pragma unroll
+  for (int c = 0; c < CM; ++c)
 #pragma unroll
     for (int i = 0; i < YV; ++i) {
-      const int n = n0 + 16 * lg + i * LE;
-      yv[i] = u32x4_t{0u, 0u, 0u, 0u};
-      if (row.live && n < p.N) yv[i] = *reinterpret_cast<const u32x4_t*>(yr + n);
+      const int n = col(c, i);
+      yv[c][i] = u32x4_t{0u, 0u, 0u, 0u};
+      if (c < chunks && (served || copied) && n < p.N) yv[c][i] = *reinterpret_cast<const u32x4_t*>(yr + n);
     }
+
+  u32x4_t vf[BF ? 2 : 1][NF];
+#pragma unroll
+  for (int f = 0; f < NF; ++f) {
+#pragma unroll
+    for (int i = 0; i < LE; ++i) v[f][i] = row.a >= 0 ? v[f][i] : 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (BF) {
+        const bf16_t h0 = f32_to_bf16(v[f][2 * i]), h1 = f32_to_bf16(v[f][2 * i + 1]);
+        vf[0][f][i] = (uint32_t)h0 | ((uint32_t)h1 << 16);
+        vf[BF ? 1 : 0][f][i] = (uint32_t)f32_to_bf16(v[f][2 * i] - bf16_to_f32(h0)) |
+                               ((uint32_t)f32_to_bf16(v[f][2 * i + 1] - bf16_to_f32(h1)) << 16);
+      } else {
+        vf[0][f][i] = __float_as_uint(v[f][i]);
+      }
+    }
+  }
+
+  u32x4_t bv[DEPTH][4][NF];
+  auto load_b = [&](u32x4_t (&b)[4][NF], int pair, int c) {
+    const int rank = __builtin_amdgcn_readlane(prank, pair);
+    const T* const bm = (const T*)p.b + ((size_t)__builtin_amdgcn_readlane(pa, pair) * p.G +
+                                         __builtin_amdgcn_readlane(pg, pair)) * (size_t)p.N * p.R;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int n = n_beg + 64 * c + 32 * (j >> 1) + 8 * (l16 >> 2) + 4 * (j & 1) + (l16 & 3);
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+        const int ch = (4 * f + lg) * LE;
+        b[j][f] = u32x4_t{0u, 0u, 0u, 0u};
+        if (ch < rank && n < p.N) b[j][f] = *reinterpret_cast<const u32x4_t*>(bm + (size_t)n * p.R + ch);
+      }
+    }
+  };
+  // chunk by chunk (its rows of y are registers), the pairs of each in turn
+  const int items = np * chunks;
+#pragma unroll
+  for (int d = 0; d < DEPTH; ++d)
+    if (d < items) load_b(bv[d], d % np, d / np);
+#pragma unroll
+  for (int c = 0; c < CM; ++c) {
+    if (c >= chunks) break;
     f32x4_t acc[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    uint32_t todo = all;
-    while (todo) {
-      const int first = __builtin_ctz(todo);
-      const int a = __shfl(row.a, first, 64), g = __shfl(row.g, first, 64);
-      const bool mine = row.a == a && row.g == g;
-      todo &= ~(uint32_t)__ballot(mine);
-      const int rank = adapt_rank(p, a);
-      const T* const bm = (const T*)p.b + ((size_t)a * p.G + g) * (size_t)p.N * p.R;
-      f32x4_t t[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) t[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int st = 0; st < STEPS; ++st) {
-        const int left = bch[st] < 0 ? 0 : rank - bch[st] * LE;  // ranks of the chunk that exist
+    for (int pair = 0; pair < np; ++pair) {
+      const int it = c * np + pair, rank = __builtin_amdgcn_readlane(prank, pair);
+      const bool mine = row.a == __builtin_amdgcn_readlane(pa, pair) && row.g == __builtin_amdgcn_readlane(pg, pair);
+      auto step = [&](u32x4_t (&b)[4][NF]) {
+        f32x4_t t[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int n = n0 + 16 * (l16 >> 2) + 4 * j + (l16 & 3);
-          u32x4_t bv = {0u, 0u, 0u, 0u};
-          if (left > 0 && n < p.N) bv = *reinterpret_cast<const u32x4_t*>(bm + (size_t)n * p.R + bch[st] * LE);
-          if (left < LE) {  // what lies behind the rank may be anything
+          t[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if constexpr (BF) bv[i] &= (2 * i < left ? 0xffffu : 0u) | (2 * i + 1 < left ? 0xffff0000u : 0u);
-              else bv[i] = i < left ? bv[i] : 0u;
+          for (int f = 0; f < NF; ++f) {
+            const int left = rank - (4 * f + lg) * LE;  // ranks of the piece that exist
+            u32x4_t w = b[j][f];
+            if (left > 0 && left < LE) {  // what lies behind the rank may be anything
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if constexpr (BF) w[i] &= (2 * i < left ? 0xffffu : 0u) | (2 * i + 1 < left ? 0xffff0000u : 0u);
+                else w[i] = i < left ? w[i] : 0u;
+              }
             }
+            t[j] = mma16<T>(w, vf[0][f], t[j]);
+            if constexpr (BF) t[j] = mma16<T>(w, vf[1][f], t[j]);
           }
-          t[j] = mma16<T>(bv, vf[st], t[j]);
         }
-      }
+        if (it + DEPTH < items) load_b(b, (it + DEPTH) % np, (it + DEPTH) / np);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (mine) acc[j] = t[j];
+        for (int j = 0; j < 4; ++j)
+          if (mine) acc[j] = t[j];
+      };
+      // the item's slot, as a compile-time index
+#pragma unroll
+      for (int d = 0; d < DEPTH; ++d)
+        if (it % DEPTH == d) step(bv[d]);
     }
-    // acc[j][e]: column n0 + 16 * lg + 4 * j + e of row l16
-    const bool write = row.live && !(inplace && row.a < 0);
+    // acc[j][e]: column 32 (j / 2) + 8 lg + 4 (j % 2) + e of row l16
 #pragma unroll
     for (int i = 0; i < YV; ++i) {
-      const int n = n0 + 16 * lg + i * LE;
-      if (!write || n >= p.N) continue;
-      u32x4_t o = yv[i];
-      if (row.a >= 0) {
+      const int n = col(c, i);
+      u32x4_t o;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          if constexpr (BF) {
-            const int c = i * LE + 2 * w;
-            o[w] = (uint32_t)f32_to_bf16(__uint_as_float(yv[i][w] << 16) + acc[c >> 2][c & 3]) |
-                   ((uint32_t)f32_to_bf16(__uint_as_float(yv[i][w] & 0xffff0000u) + acc[(c + 1) >> 2][(c + 1) & 3]) << 16);
-          } else {
-            const int c = i * LE + w;
-            o[w] = __float_as_uint(__uint_as_float(yv[i][w]) + acc[c >> 2][c & 3]);
-          }
+      for (int w = 0; w < 4; ++w) {
+        if constexpr (BF) {
+          const f32x4_t& q = acc[2 * i + (w >> 1)];
+          o[w] = (uint32_t)f32_to_bf16(__uint_as_float(yv[c][i][w] << 16) + q[2 * (w & 1)]) |
+                 ((uint32_t)f32_to_bf16(__uint_as_float(yv[c][i][w] & 0xffff0000u) + q[2 * (w & 1) + 1]) << 16);
+        } else {
+          o[w] = __float_as_uint(__uint_as_float(yv[c][i][w]) + acc[i][w]);
         }
       }
-      *reinterpret_cast<u32x4_t*>(outr + n) = o;
+      if (copied) o = yv[c][i];
+      if ((served || copied) && n < p.N) *reinterpret_cast<u32x4_t*>(outr + n) = o;
     }
   }
 }
+
+// Shares of a window's pairs: 1 where the windows fill the chip, more where they
+// are few.
+static int pair_shares(int waves) { return max(1, min(4, 4096 / max(1, waves))); }
 
 int adapt_splits(int rows, int K, int elt) {
   const int windows = max(1, (rows + AW - 1) / AW);
   const int steps = (K * elt + 63) / 64;
-  return max(1, min(min(8, (512 + windows - 1) / windows), steps / 16));
+  return max(1, min(min(8, (1024 + windows - 1) / windows), steps / 16));
 }
 
 template <typename T>
 static void launch_adapt_t(const AdaptArgs& p, float* part, int S, hipStream_t st) {
   const int windows = (p.rows + AW - 1) / AW;
-  const int pieces = max(1, min((p.N + 255) / 256, (2048 + windows - 1) / windows));
-  const int cols = ((p.N + pieces * 4 - 1) / (pieces * 4) + 63) / 64 * 64;
-  const dim3 ge(windows, (p.N + 4 * cols - 1) / (4 * cols));
-#define MOE_ADAPT(RT)                                                                                          \
+  const int n64 = (p.N + 63) / 64;
+  const int chunks = max(1, min(4, (int)((long long)windows * n64 / 4096)));
+  const int pieces = (n64 + 4 * chunks - 1) / (4 * chunks);
+  const dim3 gs(windows, S, pair_shares(4 * windows * S)), ge(windows, pieces, pair_shares(4 * windows * pieces));
+#define MOE_ADAPT(RT, NF)                                                                                      \
   do {                                                                                                         \
-    hipLaunchKernelGGL((adapt_shrink_kernel<T, RT>), dim3(windows, S), dim3(256), 0, st, p, part);             \
-    hipLaunchKernelGGL((adapt_expand_kernel<T, RT>), ge, dim3(256), 0, st, p, (const float*)part, S, cols);    \
+    hipLaunchKernelGGL((adapt_shrink_kernel<T, RT>), gs, dim3(256), 0, st, p, part);                           \
+    hipLaunchKernelGGL((adapt_expand_kernel<T, NF>), ge, dim3(256), 0, st, p, (const float*)part, S, chunks);  \
   } while (0)
   const int rt = (p.R + 15) / 16;
-  if (rt == 1) MOE_ADAPT(1);
-  else if (rt == 2) MOE_ADAPT(2);
-  else if (rt <= 4) MOE_ADAPT(4);
-  else MOE_ADAPT(8);
+  constexpr bool BF = sizeof(T) == 2;
+  if (rt == 1) MOE_ADAPT(1, 1);
+  else if (rt == 2) MOE_ADAPT(2, BF ? 1 : 2);
+  else if (rt <= 4) MOE_ADAPT(4, BF ? 2 : 4);
+  else MOE_ADAPT(8, BF ? 4 : 8);
 #undef MOE_ADAPT
 }
 
