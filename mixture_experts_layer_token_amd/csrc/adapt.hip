@@ -2,11 +2,10 @@
 // belongs to a token, the token to an adapter a (none if its id is outside
 // [0, L)), and, behind the router, the row to an expert g:
 //   out[r] = y[r] + scale[a] * B[a][g] (A[a][g] x[r])
-// with v = A x summed in float32 over the whole K and never rounded to the
+// with v = scale * A x summed in float32 over the whole K and never rounded to the
 // element type: in bf16 the second product takes v as the sum of two bf16 values
 // (v and its remainder: 16 bits of v survive, so its error, 2^-17, stays far
-// below the rounding of the output, 2^-9), which fill the K lanes of the same
-// matrix instruction that a rank of 16 would leave half empty.
+// below the rounding of the output, 2^-9).
 //
 // Both kernels take windows of 16 rows in the order of the batch, the rows of
 // one matrix instruction.  A window's distinct (adapter, expert) pairs are run
@@ -24,26 +23,28 @@ namespace {
 constexpr int AW = 16;      // rows of a window
 constexpr int MAX_G = 1024;
 
-// What lane l of a wave knows of row r = 16 * window + l % 16.
+// What a lane knows of one row.
 struct AdaptRow {
-  int a, g;      // adapter (-1: none) and expert
-  long long x;   // row of x
-  bool live;     // the row exists
+  int a, g, rank;  // adapter (-1: none), expert, rank
+  float scale;
+  int x;           // row of x
+  bool live;       // the row exists
 };
 
-// `off`: G + 1 offsets in LDS (G > 1 or given), already staged.
+// `off`: G + 1 offsets in LDS (if there are groups), already staged.  Every load
+// has an address in range and none waits behind a branch.
 __device__ __forceinline__ AdaptRow adapt_row(const AdaptArgs& p, int r, const int32_t* off) {
-  AdaptRow o{-1, 0, 0, false};
-  const int count = p.expert_off ? min(off[p.G], p.rows) : p.rows;
-  if (r >= count) return o;
-  o.live = true;
-  const int tok = p.row_tok ? p.row_tok[r] : r;
-  int xr = r;
-  if (p.x_rows) xr = p.x_rows[r];
-  o.x = xr;
-  if (tok < 0 || tok >= p.T || xr < 0 || xr >= p.x_count) return o;
-  const int a = p.ids[tok];
-  if (a < 0 || a >= p.L) return o;
+  AdaptRow o{-1, 0, 0, 1.0f, 0, false};
+  const int rc = min(r, p.rows - 1);
+  const int tok = p.row_tok ? p.row_tok[rc] : rc;
+  const int xr = p.x_rows ? p.x_rows[rc] : rc;
+  o.live = r < (p.expert_off ? min(off[p.G], p.rows) : p.rows);
+  if (p.T == 0) return o;
+  const int a = p.ids[min(max(tok, 0), p.T - 1)];
+  const int ac = min(max(a, 0), p.L - 1);
+  const int rank = p.ranks ? p.ranks[ac] : p.R;
+  const float scale = p.scales ? p.scales[ac] : 1.0f;
+  if (!o.live || tok < 0 || tok >= p.T || xr < 0 || xr >= p.x_count || a != ac) return o;
   if (p.expert_off) {  // the last g with off[g] <= r
     int lo = 0, hi = p.G;
     while (hi - lo > 1) {
@@ -54,6 +55,9 @@ __device__ __forceinline__ AdaptRow adapt_row(const AdaptArgs& p, int r, const i
     o.g = lo;
   }
   o.a = a;
+  o.x = xr;
+  o.rank = min(max(rank, 0), p.R);
+  o.scale = scale;
   return o;
 }
 
@@ -61,11 +65,6 @@ __device__ __forceinline__ void stage_offsets(const AdaptArgs& p, int32_t* off) 
   if (!p.expert_off) return;
   for (int i = threadIdx.x; i <= p.G; i += blockDim.x) off[i] = p.expert_off[i];
   __syncthreads();
-}
-
-__device__ __forceinline__ int adapt_rank(const AdaptArgs& p, int a) {
-  const int r = p.ranks ? p.ranks[a] : p.R;
-  return r < 0 ? 0 : (r > p.R ? p.R : r);
 }
 
 template <typename T>
@@ -79,55 +78,59 @@ __device__ __forceinline__ f32x4_t mma16(const u32x4_t& a, const u32x4_t& b, f32
   }
 }
 
-}  // namespace
-
-// The distinct (adapter, expert) pairs of a window, as seen by every lane of a wave:
-// f(rows, a, g, rank, mine) for each z-th of Z of them, in the order of their first
-// rows.  `rank`: the lane's row's adapter's.
+// The distinct (adapter, expert) pairs of a window, of which lane l holds row
+// l % 16 (a < 0: none): f(rows, first) for each z-th of Z of them, in the order of
+// their first rows.
 template <class F>
-__device__ __forceinline__ void for_pairs(const AdaptRow& row, int rank, int z, int Z, F f) {
-  uint32_t todo = (uint32_t)__ballot(row.a >= 0) & 0xffffu;
+__device__ __forceinline__ void for_pairs(int a, int g, int z, int Z, F f) {
+  uint32_t todo = (uint32_t)__ballot(a >= 0) & 0xffffu;
   for (int i = 0; todo; ++i) {
     const int first = __builtin_ctz(todo);
-    const int a = __builtin_amdgcn_readlane(row.a, first), g = __builtin_amdgcn_readlane(row.g, first);
-    const bool mine = row.a == a && row.g == g;
-    const uint32_t rows = (uint32_t)__ballot(mine) & 0xffffu;
+    const uint32_t rows = todo & (uint32_t)__ballot(a == __builtin_amdgcn_readlane(a, first) &&
+                                                    g == __builtin_amdgcn_readlane(g, first));
     todo &= ~rows;
-    if (i % Z == z) f(rows, a, g, __builtin_amdgcn_readlane(rank, first), mine);
+    if (i % Z == z) f(rows, first);
   }
 }
 
-// v[r][:] = scale A[a][g] x[r], partial over slice blockIdx.y of K: part[s][r][R],
-// 0 behind the adapter's rank.
-// The workgroup's four waves take quarters of the slice and are added in wave
-// order.  A lane's 16 bytes of x row l % 16 and of A row l % 16 hold the same K.
-// blockIdx.z takes every Z-th pair of the window: where windows are few (decode)
-// and hold many adapters, their latencies pass side by side.
+}  // namespace
+
+// v[r][:] = scale A[a][g] x[r], 0 behind the adapter's rank: float [rows][R], or in
+// bf16 two arrays [rows][R], v rounded and its remainder rounded.  The workgroup's
+// waves take equal parts of K and are added in wave order, so that a batch of one
+// window is as parallel as its K is long.  A lane's 16 bytes of x row l % 16 and of
+// A row l % 16 hold the same K.  blockIdx.y takes every Z-th pair of the window:
+// where windows are few (decode) and hold many adapters, their latencies pass side
+// by side.
 template <typename T, int RT>
-__global__ __launch_bounds__(256) void adapt_shrink_kernel(AdaptArgs p, float* __restrict__ part) {
+__global__ __launch_bounds__(1024) void adapt_shrink_kernel(AdaptArgs p, void* __restrict__ vout) {
   constexpr int LE = 16 / (int)sizeof(T);
   constexpr int KS = 4 * LE;  // K of one step (four lane groups)
+  constexpr int LD = 16 * RT + 1;
   __shared__ int32_t off[MAX_G + 1];
-  __shared__ float red[4][AW][16 * RT + 1], scale[AW];
+  __shared__ float scale[AW];
+  extern __shared__ float red[];  // [waves][AW][LD]
   stage_offsets(p, off);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, lg = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), nw = blockDim.x >> 6;
+  const int l16 = lane & 15, lg = lane >> 4;
   const AdaptRow row = adapt_row(p, (int)blockIdx.x * AW + l16, off);
-  const int steps = (p.K + KS - 1) / KS, nq = gridDim.y * 4, q = blockIdx.y * 4 + wave;
-  const int s0 = (int)((long long)steps * q / nq), s1 = (int)((long long)steps * (q + 1) / nq);
+  const int steps = (p.K + KS - 1) / KS;
+  const int s0 = steps * wave / nw, s1 = steps * (wave + 1) / nw;
   f32x4_t acc[RT];
 #pragma unroll
   for (int i = 0; i < RT; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   const T* const xr = (const T*)p.x + (size_t)row.x * p.K;
   uint32_t done = 0;  // rows that this workgroup computes
-  const int my_rank = row.a >= 0 ? adapt_rank(p, row.a) : 0;
-  const float my_scale = row.a >= 0 && p.scales ? p.scales[row.a] : 1.0f;
-  for_pairs(row, my_rank, blockIdx.z, gridDim.z, [&](uint32_t rows, int a, int g, int rank, bool mine) {
+  for_pairs(row.a, row.g, blockIdx.y, gridDim.y, [&](uint32_t rows, int first) {
     done |= rows;
-    const T* const am = (const T*)p.a + ((size_t)a * p.G + g) * (size_t)p.R * p.K;
+    const int rank = __builtin_amdgcn_readlane(row.rank, first);
+    const bool mine = (rows >> l16) & 1u;
+    const T* const am = (const T*)p.a + ((size_t)__builtin_amdgcn_readlane(row.a, first) * p.G +
+                                         __builtin_amdgcn_readlane(row.g, first)) * (size_t)p.R * p.K;
     f32x4_t t[RT];
 #pragma unroll
     for (int i = 0; i < RT; ++i) t[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    constexpr int U = RT <= 2 ? 8 : (RT <= 4 ? 4 : 2);  // steps in flight
+    constexpr int U = RT <= 2 ? 4 : 2;  // steps in flight
     for (int s = s0; s < s1; s += U) {
       u32x4_t xv[U], av[U][RT];
 #pragma unroll
@@ -154,226 +157,225 @@ __global__ __launch_bounds__(256) void adapt_shrink_kernel(AdaptArgs p, float* _
       for (int r = 0; r < 4; ++r)
         if ((rows >> (4 * lg + r)) & 1u) acc[i][r] = t[i][r];
   });
-  if (!done) return;  // the same for the four waves
-  if (threadIdx.x < AW) scale[threadIdx.x] = my_scale;
+  if (!done) return;  // the same for all waves
+  if (threadIdx.x < AW) scale[threadIdx.x] = row.scale;
   // acc[i][r] is row 4 * lg + r, rank 16 * i + l16
 #pragma unroll
   for (int i = 0; i < RT; ++i)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) red[wave][4 * lg + r][16 * i + l16] = acc[i][r];
+    for (int r = 0; r < 4; ++r) red[(wave * AW + 4 * lg + r) * LD + 16 * i + l16] = acc[i][r];
   __syncthreads();
-  float* const out = part + ((size_t)blockIdx.y * p.rows + (size_t)blockIdx.x * AW) * p.R;
-  for (int i = threadIdx.x; i < AW * p.R; i += 256) {
-    const int r = i / p.R, c = i % p.R;
-    if ((done >> r) & 1u) out[i] = scale[r] * ((red[0][r][c] + red[1][r][c]) + (red[2][r][c] + red[3][r][c]));
+  for (int i = threadIdx.x; i < AW * p.R; i += blockDim.x) {
+    const int r = i / p.R, c = i - r * p.R;
+    if (!((done >> r) & 1u)) continue;
+    float v = red[r * LD + c];
+    for (int w = 1; w < nw; ++w) v += red[(w * AW + r) * LD + c];
+    v *= scale[r];
+    const size_t at = (size_t)blockIdx.x * AW * p.R + i;
+    if constexpr (sizeof(T) == 2) {
+      const bf16_t hi = f32_to_bf16(v);
+      ((bf16_t*)vout)[at] = hi;
+      ((bf16_t*)vout)[(size_t)p.rows * p.R + at] = f32_to_bf16(v - bf16_to_f32(hi));
+    } else {
+      ((float*)vout)[at] = v;
+    }
   }
 }
 
-// out[r] = y[r] + B v: a wave takes up to 4 chunks of 64 columns of a window, for
-// every Z-th of its pairs.  The matrix instruction's rows are the columns of y:
-// row i of tile j is column 32 (j / 2) + 8 (i / 4) + 4 (j % 2) + i % 4 of the
-// chunk, so that a lane ends with runs of 8 columns of one row and four lanes with
-// 64 contiguous bytes of it (bf16).  A fragment of B holds 4 * LE ranks (lane
-// group lg: LE of them); bf16 multiplies it with v and with its remainder.  A wave
-// has little to compute and much to wait for: all its rows of y are requested
-// first, and B of the next DEPTH (pair, chunk) items while one is multiplied.
+// out[r] = y[r] + B v: a wave takes 64 columns of up to 8 windows, B of the pair at
+// hand in registers.  The matrix instruction's rows are the columns of y: in bf16
+// row i of tile j is column 32 (j / 2) + 8 (i / 4) + 4 (j % 2) + i % 4 of the 64, so
+// that a lane ends with runs of 8 columns of one row.  A fragment of B holds 4 * LE ranks (lane group lg: LE of
+// them); bf16 multiplies it with v and with its remainder.
+//
+// A wave has little to compute and much to wait for: what it needs of its rows is
+// read once, y and v of the next D windows are in flight while one is multiplied,
+// from addresses that depend on nothing (so that the waits count loads instead of
+// draining them).  B of a pair is loaded when it changes.
 template <typename T, int NF>
-__global__ __launch_bounds__(256) void adapt_expand_kernel(AdaptArgs p, const float* __restrict__ part, int S,
-                                                           int chunks) {
+__global__ __launch_bounds__(256, NF == 1 ? 4 : (NF <= 4 ? 2 : 1)) void adapt_expand_kernel(AdaptArgs p, const T* __restrict__ vin, int wpw) {
   constexpr int LE = 16 / (int)sizeof(T);
   constexpr bool BF = sizeof(T) == 2;
-  constexpr int CM = 4;                                    // chunks of 64 columns at most
-  constexpr int YV = BF ? 2 : 4;                           // 16-byte pieces of a lane's 16 columns
-  constexpr int DEPTH = NF == 1 ? 4 : (NF == 2 ? 2 : 1);   // items of B in registers
+  constexpr int YV = BF ? 2 : 4;                  // 16-byte pieces of a lane's 16 columns
+  constexpr int NV = BF ? 2 : 1;                  // v and its remainder
+  constexpr int D = 2;
   __shared__ int32_t off[MAX_G + 1];
   stage_offsets(p, off);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, lg = lane >> 4;
-  const int r = (int)blockIdx.x * AW + l16;
-  const int n_beg = ((int)blockIdx.y * 4 + wave) * chunks * 64;
-  if (n_beg >= p.N) return;
+  const int windows = (p.rows + AW - 1) / AW;
+  const int n0 = ((int)blockIdx.x * 4 + wave) * 64;
+  const int w0 = blockIdx.y * wpw, w1 = min(w0 + wpw, windows);
+  if (n0 >= p.N) return;
   const bool inplace = p.y == p.out;
-  // this lane's ranks: LE from (4 f + lg) LE on, f < NF; parts of rows without an
-  // adapter were not written: they are read and left out
-  float v[NF][LE];
-#pragma unroll
-  for (int f = 0; f < NF; ++f)
-#pragma unroll
-    for (int i = 0; i < LE; ++i) v[f][i] = 0.f;
-  if (r < p.rows) {
-    for (int s = 0; s < S; ++s) {
-#pragma unroll
-      for (int f = 0; f < NF; ++f) {
-        const int c = (4 * f + lg) * LE;
-        if (c < p.R) {
-          const float4* src = reinterpret_cast<const float4*>(part + ((size_t)s * p.rows + r) * p.R + c);
-#pragma unroll
-          for (int i = 0; i < LE / 4; ++i) {
-            const float4 q = src[i];
-            v[f][4 * i] += q.x;
-            v[f][4 * i + 1] += q.y;
-            v[f][4 * i + 2] += q.z;
-            v[f][4 * i + 3] += q.w;
-          }
-        }
-      }
-    }
-  }
-  const AdaptRow row = adapt_row(p, r, off);
-  const int my_rank = row.a >= 0 ? adapt_rank(p, row.a) : 0;
-  // the wave's pairs, one in each of the first lanes
-  int pa = 0, pg = 0, prank = 0, np = 0;
-  bool served = false;
-  for_pairs(row, my_rank, blockIdx.z, gridDim.z, [&](uint32_t, int a, int g, int rank, bool mine) {
-    if (lane == np) {
-      pa = a;
-      pg = g;
-      prank = rank;
-    }
-    served |= mine;
-    ++np;
-  });
-  // rows without an adapter are copied
-  const bool copied = blockIdx.z == 0 && !inplace && row.live && row.a < 0;
+  const int nchunk = p.R / LE;
 
-  const T* const yr = (const T*)p.y + (size_t)r * p.N;
-  T* const outr = (T*)p.out + (size_t)r * p.N;
-  // column of piece i of a lane's share of chunk c
-  auto col = [&](int c, int i) {
-    return n_beg + 64 * c + (BF ? 32 * i + 8 * lg : 32 * (i >> 1) + 8 * lg + 4 * (i & 1));
+  // the lane's pieces of y: row ar[i] of the window from column cc[i] on, and its
+  // ranks (those that do not exist: the last ones)
+  int ar[YV], cc[YV], cv[NF];
+#pragma unroll
+  for (int i = 0; i < YV; ++i) {
+    ar[i] = BF ? (l16 & 7) + 8 * i : l16;
+    cc[i] = n0 + (BF ? 32 * (l16 >> 3) + 8 * lg : 16 * i + 4 * lg);
+  }
+#pragma unroll
+  for (int f = 0; f < NF; ++f) cv[f] = min(4 * f + lg, nchunk - 1) * LE;
+  u32x4_t yv[D][YV], vf[D][NV][NF];
+  auto load_window = [&](u32x4_t (&y)[YV], u32x4_t (&v)[NV][NF], int w) {
+    const int wc = min(w, windows - 1), last = p.rows - 1 - wc * AW, rl = min(l16, last);
+    const T* const yb = (const T*)p.y + (size_t)wc * AW * p.N;
+    const T* const vb = vin + (size_t)wc * AW * p.R;
+#pragma unroll
+    for (int i = 0; i < YV; ++i)
+      y[i] = *reinterpret_cast<const u32x4_t*>(yb + (uint32_t)(min(ar[i], last) * p.N + min(cc[i], p.N - LE)));
+#pragma unroll
+    for (int e = 0; e < NV; ++e)
+#pragma unroll
+      for (int f = 0; f < NF; ++f)
+        v[e][f] = *reinterpret_cast<const u32x4_t*>(vb + (size_t)e * p.rows * p.R + (uint32_t)(rl * p.R + cv[f]));
   };
-  u32x4_t yv[CM][YV];
 #pragma unroll
-  for (int c = 0; c < CM; ++c)
+  for (int d = 0; d < D; ++d) load_window(yv[d], vf[d], w0 + d);
+  // the wave's rows, two a lane: row 16 w0 + lane and 64 further
+  int ra[2], rg[2], rr[2], rlive = 0;
 #pragma unroll
-    for (int i = 0; i < YV; ++i) {
-      const int n = col(c, i);
-      yv[c][i] = u32x4_t{0u, 0u, 0u, 0u};
-      if (c < chunks && (served || copied) && n < p.N) yv[c][i] = *reinterpret_cast<const u32x4_t*>(yr + n);
-    }
-
-  u32x4_t vf[BF ? 2 : 1][NF];
-#pragma unroll
-  for (int f = 0; f < NF; ++f) {
-#pragma unroll
-    for (int i = 0; i < LE; ++i) v[f][i] = row.a >= 0 ? v[f][i] : 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (BF) {
-        const bf16_t h0 = f32_to_bf16(v[f][2 * i]), h1 = f32_to_bf16(v[f][2 * i + 1]);
-        vf[0][f][i] = (uint32_t)h0 | ((uint32_t)h1 << 16);
-        vf[BF ? 1 : 0][f][i] = (uint32_t)f32_to_bf16(v[f][2 * i] - bf16_to_f32(h0)) |
-                               ((uint32_t)f32_to_bf16(v[f][2 * i + 1] - bf16_to_f32(h1)) << 16);
-      } else {
-        vf[0][f][i] = __float_as_uint(v[f][i]);
-      }
-    }
+  for (int h = 0; h < 2; ++h) {
+    const AdaptRow row = adapt_row(p, w0 * AW + 64 * h + lane, off);
+    ra[h] = row.a;
+    rg[h] = row.g;
+    rr[h] = row.rank;
+    rlive |= row.live ? 1 << h : 0;
   }
 
-  u32x4_t bv[DEPTH][4][NF];
-  auto load_b = [&](u32x4_t (&b)[4][NF], int pair, int c) {
-    const int rank = __builtin_amdgcn_readlane(prank, pair);
-    const T* const bm = (const T*)p.b + ((size_t)__builtin_amdgcn_readlane(pa, pair) * p.G +
-                                         __builtin_amdgcn_readlane(pg, pair)) * (size_t)p.N * p.R;
+  auto load_b = [&](u32x4_t (&b)[4][NF], int a, int g) {
+    const T* const bm = (const T*)p.b + ((size_t)a * p.G + g) * (size_t)p.N * p.R;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int n = n_beg + 64 * c + 32 * (j >> 1) + 8 * (l16 >> 2) + 4 * (j & 1) + (l16 & 3);
+      const int i = BF ? 32 * (j >> 1) + 8 * (l16 >> 2) + 4 * (j & 1) + (l16 & 3) : 16 * j + l16;
+      const int n = min(n0 + i, p.N - 1);
+#pragma unroll
+      for (int f = 0; f < NF; ++f) b[j][f] = *reinterpret_cast<const u32x4_t*>(bm + (uint32_t)(n * p.R + cv[f]));
+    }
+  };
+  // t = B v of one pair; what lies behind its rank may be anything and is not used
+  auto product = [&](const u32x4_t (&b)[4][NF], const u32x4_t (&v)[NV][NF], int rank, f32x4_t (&t)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      t[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int f = 0; f < NF; ++f) {
-        const int ch = (4 * f + lg) * LE;
-        b[j][f] = u32x4_t{0u, 0u, 0u, 0u};
-        if (ch < rank && n < p.N) b[j][f] = *reinterpret_cast<const u32x4_t*>(bm + (size_t)n * p.R + ch);
+        const int left = rank - (4 * f + lg) * LE;  // ranks of the piece that exist
+        u32x4_t w = b[j][f];
+        if (left < LE) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (BF) w[i] &= (2 * i < left ? 0xffffu : 0u) | (2 * i + 1 < left ? 0xffff0000u : 0u);
+            else w[i] = i < left ? w[i] : 0u;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < NV; ++e) t[j] = mma16<T>(w, v[e][f], t[j]);
       }
     }
   };
-  // chunk by chunk (its rows of y are registers), the pairs of each in turn
-  const int items = np * chunks;
+  u32x4_t bv[4][NF];
+  int ba = -1, bg = -1;  // the pair in bv
+  auto window = [&](const u32x4_t (&y)[YV], u32x4_t (&v)[NV][NF], int w) {
+    const int i = (w - w0) * AW, h = i >> 6, src = (i & 63) + l16;
+    const int a = __shfl(h ? ra[1] : ra[0], src, 64), g = __shfl(h ? rg[1] : rg[0], src, 64);
+    const int rank = __shfl(h ? rr[1] : rr[0], src, 64);
+    const bool live = (__shfl(rlive, src, 64) >> h) & 1;
+    // v of rows without an adapter was not written
 #pragma unroll
-  for (int d = 0; d < DEPTH; ++d)
-    if (d < items) load_b(bv[d], d % np, d / np);
+    for (int e = 0; e < NV; ++e)
 #pragma unroll
-  for (int c = 0; c < CM; ++c) {
-    if (c >= chunks) break;
+      for (int f = 0; f < NF; ++f)
+        if (a < 0 || (4 * f + lg) * LE >= p.R) v[e][f] = u32x4_t{0u, 0u, 0u, 0u};
     f32x4_t acc[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    for (int pair = 0; pair < np; ++pair) {
-      const int it = c * np + pair, rank = __builtin_amdgcn_readlane(prank, pair);
-      const bool mine = row.a == __builtin_amdgcn_readlane(pa, pair) && row.g == __builtin_amdgcn_readlane(pg, pair);
-      auto step = [&](u32x4_t (&b)[4][NF]) {
-        f32x4_t t[4];
+    uint32_t served = 0;
+    for_pairs(a, g, blockIdx.z, gridDim.z, [&](uint32_t rows, int first) {
+      const int pa = __builtin_amdgcn_readlane(a, first), pg = __builtin_amdgcn_readlane(g, first);
+      if (pa != ba || pg != bg) load_b(bv, pa, pg);
+      ba = pa;
+      bg = pg;
+      f32x4_t t[4];
+      product(bv, v, __builtin_amdgcn_readlane(rank, first), t);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          t[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < 4; ++j)
+        if ((rows >> l16) & 1u) acc[j] = t[j];
+      served |= rows;
+    });
+    // rows without an adapter are copied
+    if (blockIdx.z == 0 && !inplace) served |= (uint32_t)__ballot(live && a < 0) & 0xffffu;
+    if (!served) return;
+    // acc[j][e]: column n0 + (bf16: 32 (j / 2) + 8 lg + 4 (j % 2), float: 16 j + 4 lg) + e of row l16
+    u32x4_t o[YV];
+    if constexpr (BF) {
+      // to whole 128-byte lines: lanes l16 and l16 ^ 8 have half a line each of two
+      // rows and swap one, so that a load or store covers 8 rows x 128 bytes
+      auto swap = [&](const u32x4_t& lo, const u32x4_t& hi, u32x4_t& a0, u32x4_t& a1) {
 #pragma unroll
-          for (int f = 0; f < NF; ++f) {
-            const int left = rank - (4 * f + lg) * LE;  // ranks of the piece that exist
-            u32x4_t w = b[j][f];
-            if (left > 0 && left < LE) {  // what lies behind the rank may be anything
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if constexpr (BF) w[i] &= (2 * i < left ? 0xffffu : 0u) | (2 * i + 1 < left ? 0xffff0000u : 0u);
-                else w[i] = i < left ? w[i] : 0u;
-              }
-            }
-            t[j] = mma16<T>(w, vf[0][f], t[j]);
-            if constexpr (BF) t[j] = mma16<T>(w, vf[1][f], t[j]);
-          }
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t send = l16 < 8 ? hi[q] : lo[q];
+          const uint32_t got = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)send, 0x128, 0xf, 0xf, false);  // row_ror 8
+          a0[q] = l16 < 8 ? lo[q] : got;
+          a1[q] = l16 < 8 ? got : hi[q];
         }
-        if (it + DEPTH < items) load_b(b, (it + DEPTH) % np, (it + DEPTH) / np);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (mine) acc[j] = t[j];
       };
-      // the item's slot, as a compile-time index
+      u32x4_t m[2], t[2];
+      swap(y[0], y[1], m[0], m[1]);
 #pragma unroll
-      for (int d = 0; d < DEPTH; ++d)
-        if (it % DEPTH == d) step(bv[d]);
-    }
-    // acc[j][e]: column 32 (j / 2) + 8 lg + 4 (j % 2) + e of row l16
+      for (int i2 = 0; i2 < 2; ++i2)
 #pragma unroll
-    for (int i = 0; i < YV; ++i) {
-      const int n = col(c, i);
-      u32x4_t o;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        if constexpr (BF) {
-          const f32x4_t& q = acc[2 * i + (w >> 1)];
-          o[w] = (uint32_t)f32_to_bf16(__uint_as_float(yv[c][i][w] << 16) + q[2 * (w & 1)]) |
-                 ((uint32_t)f32_to_bf16(__uint_as_float(yv[c][i][w] & 0xffff0000u) + q[2 * (w & 1) + 1]) << 16);
-        } else {
-          o[w] = __float_as_uint(__uint_as_float(yv[c][i][w]) + acc[i][w]);
+        for (int q = 0; q < 4; ++q) {
+          const f32x4_t& c = acc[2 * i2 + (q >> 1)];
+          t[i2][q] = a < 0 ? m[i2][q]
+                           : (uint32_t)f32_to_bf16(__uint_as_float(m[i2][q] << 16) + c[2 * (q & 1)]) |
+                                 ((uint32_t)f32_to_bf16(__uint_as_float(m[i2][q] & 0xffff0000u) + c[2 * (q & 1) + 1]) << 16);
         }
-      }
-      if (copied) o = yv[c][i];
-      if ((served || copied) && n < p.N) *reinterpret_cast<u32x4_t*>(outr + n) = o;
+      swap(t[0], t[1], o[0], o[1]);
+    } else {
+#pragma unroll
+      for (int i2 = 0; i2 < YV; ++i2)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          o[i2][q] = a < 0 ? y[i2][q] : __float_as_uint(__uint_as_float(y[i2][q]) + acc[i2][q]);
+    }
+    T* const ob = (T*)p.out + (size_t)w * AW * p.N;
+#pragma unroll
+    for (int i2 = 0; i2 < YV; ++i2)
+      if (((served >> ar[i2]) & 1u) && cc[i2] < p.N) *reinterpret_cast<u32x4_t*>(ob + (uint32_t)(ar[i2] * p.N + cc[i2])) = o[i2];
+  };
+  for (int w = w0; w < w1; w += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      if (w + d < w1) window(yv[d], vf[d], w + d);
+      load_window(yv[d], vf[d], w + d + D);
     }
   }
 }
 
-// Shares of a window's pairs: 1 where the windows fill the chip, more where they
-// are few.
-static int pair_shares(int waves) { return max(1, min(4, 4096 / max(1, waves))); }
-
-int adapt_splits(int rows, int K, int elt) {
-  const int windows = max(1, (rows + AW - 1) / AW);
-  const int steps = (K * elt + 63) / 64;
-  return max(1, min(min(8, (1024 + windows - 1) / windows), steps / 16));
-}
-
 template <typename T>
-static void launch_adapt_t(const AdaptArgs& p, float* part, int S, hipStream_t st) {
+static void launch_adapt_t(const AdaptArgs& p, void* v, hipStream_t st) {
   const int windows = (p.rows + AW - 1) / AW;
-  const int n64 = (p.N + 63) / 64;
-  const int chunks = max(1, min(4, (int)((long long)windows * n64 / 4096)));
-  const int pieces = (n64 + 4 * chunks - 1) / (4 * chunks);
-  const dim3 gs(windows, S, pair_shares(4 * windows * S)), ge(windows, pieces, pair_shares(4 * windows * pieces));
-#define MOE_ADAPT(RT, NF)                                                                                      \
-  do {                                                                                                         \
-    hipLaunchKernelGGL((adapt_shrink_kernel<T, RT>), gs, dim3(256), 0, st, p, part);                           \
-    hipLaunchKernelGGL((adapt_expand_kernel<T, NF>), ge, dim3(256), 0, st, p, (const float*)part, S, chunks);  \
+  const int cols = (p.N + 255) / 256;  // workgroups across the columns
+  // windows of a wave: one while the waves are few, up to 8
+  const int wpw = max(1, min(8, (int)((long long)windows * cols * 4 / 4096)));
+  const int splits = (windows + wpw - 1) / wpw;
+  // shares of a window's pairs: 1 where the windows fill the chip, more where few
+  const int ze = max(1, min(4, 4096 / (cols * 4 * splits)));
+  const int rt = (p.R + 15) / 16, rtp = rt <= 2 ? rt : (rt <= 4 ? 4 : 8);
+  const int steps = (p.K * (int)sizeof(T) + 63) / 64;
+  const int nw = max(1, min(rtp <= 2 ? 16 : 32 / rtp, steps / 4));
+  const int zs = max(1, min(16, 1024 / windows / nw));
+  const size_t lds = (size_t)nw * AW * (16 * rtp + 1) * sizeof(float);
+#define MOE_ADAPT(RT, NF)                                                                                       \
+  do {                                                                                                          \
+    hipLaunchKernelGGL((adapt_shrink_kernel<T, RT>), dim3(windows, zs), dim3(64 * nw), lds, st, p, v);          \
+    hipLaunchKernelGGL((adapt_expand_kernel<T, NF>), dim3(cols, splits, ze), dim3(256), 0, st, p, (const T*)v, wpw); \
   } while (0)
-  const int rt = (p.R + 15) / 16;
   constexpr bool BF = sizeof(T) == 2;
   if (rt == 1) MOE_ADAPT(1, 1);
   else if (rt == 2) MOE_ADAPT(2, BF ? 1 : 2);
@@ -382,10 +384,10 @@ static void launch_adapt_t(const AdaptArgs& p, float* part, int S, hipStream_t s
 #undef MOE_ADAPT
 }
 
-hipError_t launch_adapt(int dtype, const AdaptArgs& p, float* part, int S, hipStream_t st) {
+hipError_t launch_adapt(int dtype, const AdaptArgs& p, void* v, hipStream_t st) {
   if (p.rows == 0) return hipSuccess;
-  if (dtype == DT_BF16) launch_adapt_t<bf16_t>(p, part, S, st);
-  else launch_adapt_t<float>(p, part, S, st);
+  if (dtype == DT_BF16) launch_adapt_t<bf16_t>(p, v, st);
+  else launch_adapt_t<float>(p, v, st);
   return hipGetLastError();
 }
 

@@ -226,9 +226,8 @@ struct AdaptArgs {
   const int32_t *ranks;       // [L] (null: R)
   const float* scales;        // [L] (null: 1)
 };
-// Slices of K of the first product (partials part[S][rows][R], float).
-int adapt_splits(int rows, int K, int elt);
-hipError_t launch_adapt(int dtype, const AdaptArgs& p, float* part, int S, hipStream_t st);
+// v: scratch of rows * R floats (the first product).
+hipError_t launch_adapt(int dtype, const AdaptArgs& p, void* v, hipStream_t st);
 
 // moe_abi.cpp -- the forward of moe_forward over a caller-chosen scratch
 // region.  own_regions: `ws` holds only the forward's own regions

@@ -538,17 +538,13 @@ static moe_status check_adapter(const moe_adapter_desc* ad) {
   return MOE_OK;
 }
 
-static float* plan_adapt(const moe_adapter_desc& a, Carver& c, int* splits) {
-  *splits = adapt_splits(a.rows, a.K, a.dtype == MOE_BF16 ? 2 : 4);
-  return c.take<float>((size_t)*splits * a.rows * a.R);
-}
+static void* plan_adapt(const moe_adapter_desc& a, Carver& c) { return c.take<float>((size_t)a.rows * a.R); }
 
 moe_status moe_adapt_workspace_size(const moe_adapter_desc* ad, size_t* bytes) {
   MOE_TRY(check_adapter(ad));
   if (!bytes) return MOE_ERR_NULL;
   Carver c(nullptr);
-  int s;
-  plan_adapt(*ad, c, &s);
+  plan_adapt(*ad, c);
   *bytes = c.total();
   return MOE_OK;
 }
@@ -577,11 +573,10 @@ moe_status moe_adapt(const moe_adapter_desc* ad, const void* x, const int32_t* x
   if (!ws || ws_bytes < need) return MOE_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return MOE_ERR_ALIGN;
   Carver c(ws);
-  int splits;
-  float* part = plan_adapt(d, c, &splits);
+  void* v = plan_adapt(d, c);
   const AdaptArgs p{d.rows, d.T, d.K, d.N, d.R, d.L, d.G, x_count, x, a, b, y_in, y_out, adapter_ids, row_tok,
                     x_rows, expert_off, ranks, scales};
-  return launched(launch_adapt(d.dtype, p, part, splits, static_cast<hipStream_t>(stream)));
+  return launched(launch_adapt(d.dtype, p, v, static_cast<hipStream_t>(stream)));
 }
 
 moe_status moe_permute(const moe_desc* desc, const int32_t* tok_off, const int32_t* topk_ids,
