@@ -109,56 +109,103 @@ __global__ __launch_bounds__(1024) void adapt_shrink_kernel(AdaptArgs p, void* _
   constexpr int LD = 16 * RT + 1;
   __shared__ int32_t off[MAX_G + 1];
   __shared__ float scale[AW];
+  __shared__ int32_t ranks[AW];
   extern __shared__ float red[];  // [waves][AW][LD]
   stage_offsets(p, off);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), nw = blockDim.x >> 6;
   const int l16 = lane & 15, lg = lane >> 4;
-  const AdaptRow row = adapt_row(p, (int)blockIdx.x * AW + l16, off);
+  const int r = (int)blockIdx.x * AW + l16;
   const int steps = (p.K + KS - 1) / KS;
   const int s0 = steps * wave / nw, s1 = steps * (wave + 1) / nw;
+  constexpr int U = RT <= 2 ? 4 : 2;  // steps in flight
+  // x of the first steps, before anything is known of its adapter: every row's
+  const int xr = p.x_rows ? min(max(p.x_rows[min(r, p.rows - 1)], 0), p.x_count - 1) : min(r, p.rows - 1);
+  const T* const xb = (const T*)p.x + (size_t)xr * p.K;
+  auto load_x = [&](u32x4_t (&x)[U], int s) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u] = *reinterpret_cast<const u32x4_t*>(xb + min((s + u) * KS + lg * LE, p.K - LE));
+  };
+  u32x4_t xv[U], av[U][RT];
+  if (p.x_count > 0) load_x(xv, s0);
+  const AdaptRow row = adapt_row(p, r, off);
+  // the workgroup's pairs, one in each of the first lanes
+  int pa = 0, pg = 0, np = 0;
+  uint32_t prows = 0, done = 0;
+  for_pairs(row.a, row.g, blockIdx.y, gridDim.y, [&](uint32_t rows, int first) {
+    const int a = __builtin_amdgcn_readlane(row.a, first), g = __builtin_amdgcn_readlane(row.g, first);
+    if (lane == np) {
+      pa = a;
+      pg = g;
+      prows = rows;
+    }
+    done |= rows;
+    ++np;
+  });
+  auto load_a = [&](u32x4_t (&m)[U][RT], int pair, int s) {
+    const T* const am = (const T*)p.a + ((size_t)__builtin_amdgcn_readlane(pa, pair) * p.G +
+                                         __builtin_amdgcn_readlane(pg, pair)) * (size_t)p.R * p.K;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = min((s + u) * KS + lg * LE, p.K - LE);
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+        m[u][i] = *reinterpret_cast<const u32x4_t*>(am + (uint32_t)(min(16 * i + l16, p.R - 1) * p.K + k));
+    }
+  };
   f32x4_t acc[RT];
 #pragma unroll
   for (int i = 0; i < RT; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const T* const xr = (const T*)p.x + (size_t)row.x * p.K;
-  uint32_t done = 0;  // rows that this workgroup computes
-  for_pairs(row.a, row.g, blockIdx.y, gridDim.y, [&](uint32_t rows, int first) {
-    done |= rows;
-    const int rank = __builtin_amdgcn_readlane(row.rank, first);
-    const bool mine = (rows >> l16) & 1u;
-    const T* const am = (const T*)p.a + ((size_t)__builtin_amdgcn_readlane(row.a, first) * p.G +
-                                         __builtin_amdgcn_readlane(row.g, first)) * (size_t)p.R * p.K;
-    f32x4_t t[RT];
+  if (np) load_a(av, 0, s0);
+  for (int s = s0; np && s < s1; s += U) {
+    const bool more = s + U < s1;
+    u32x4_t xn[U];
 #pragma unroll
-    for (int i = 0; i < RT; ++i) t[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    constexpr int U = RT <= 2 ? 4 : 2;  // steps in flight
-    for (int s = s0; s < s1; s += U) {
-      u32x4_t xv[U], av[U][RT];
+    for (int u = 0; u < U; ++u) xn[u] = xv[u];
+    if (more) load_x(xn, s + U);
+    // steps behind the wave's part, and K behind the end: zeros on both sides
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int k = (s + u) * KS + lg * LE;
-        const bool in = s + u < s1 && k < p.K;
-        xv[u] = u32x4_t{0u, 0u, 0u, 0u};
-        if (in && mine) xv[u] = *reinterpret_cast<const u32x4_t*>(xr + k);
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          av[u][i] = u32x4_t{0u, 0u, 0u, 0u};
-          if (in && 16 * i + l16 < rank)
-            av[u][i] = *reinterpret_cast<const u32x4_t*>(am + (size_t)(16 * i + l16) * p.K + k);
-        }
-      }
+    for (int u = 0; u < U; ++u)
+      if (s + u >= s1 || (s + u) * KS + lg * LE >= p.K) xv[u] = u32x4_t{0u, 0u, 0u, 0u};
+    for (int q = 0; q < np; ++q) {
+      u32x4_t an[U][RT];  // A of the next pair, or of the first one's next steps
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int i = 0; i < RT; ++i) t[i] = mma16<T>(xv[u], av[u][i], t[i]);
+        for (int i = 0; i < RT; ++i) an[u][i] = av[u][i];
+      if (q + 1 < np || more) load_a(an, q + 1 < np ? q + 1 : 0, q + 1 < np ? s : s + U);
+      const uint32_t rows = (uint32_t)__builtin_amdgcn_readlane((int)prows, q);
+      f32x4_t t[RT];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) t[i] = acc[i];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool out = s + u >= s1 || (s + u) * KS + lg * LE >= p.K;
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          u32x4_t m = av[u][i];
+          if (out) m = u32x4_t{0u, 0u, 0u, 0u};
+          t[i] = mma16<T>(xv[u], m, t[i]);
+        }
+      }
+      // a row's sum takes its own pair's product only
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if ((rows >> (4 * lg + j)) & 1u) acc[i][j] = t[i][j];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < RT; ++i) av[u][i] = an[u][i];
     }
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if ((rows >> (4 * lg + r)) & 1u) acc[i][r] = t[i][r];
-  });
+    for (int u = 0; u < U; ++u) xv[u] = xn[u];
+  }
   if (!done) return;  // the same for all waves
-  if (threadIdx.x < AW) scale[threadIdx.x] = row.scale;
+  if (threadIdx.x < AW) {
+    scale[threadIdx.x] = row.scale;
+    ranks[threadIdx.x] = row.rank;
+  }
   // acc[i][r] is row 4 * lg + r, rank 16 * i + l16
 #pragma unroll
   for (int i = 0; i < RT; ++i)
@@ -170,7 +217,7 @@ __global__ __launch_bounds__(1024) void adapt_shrink_kernel(AdaptArgs p, void* _
     if (!((done >> r) & 1u)) continue;
     float v = red[r * LD + c];
     for (int w = 1; w < nw; ++w) v += red[(w * AW + r) * LD + c];
-    v *= scale[r];
+    v = c < ranks[r] ? v * scale[r] : 0.f;  // A behind the rank may be anything
     const size_t at = (size_t)blockIdx.x * AW * p.R + i;
     if constexpr (sizeof(T) == 2) {
       const bf16_t hi = f32_to_bf16(v);
@@ -369,7 +416,7 @@ static void launch_adapt_t(const AdaptArgs& p, void* v, hipStream_t st) {
   const int rt = (p.R + 15) / 16, rtp = rt <= 2 ? rt : (rt <= 4 ? 4 : 8);
   const int steps = (p.K * (int)sizeof(T) + 63) / 64;
   const int nw = max(1, min(rtp <= 2 ? 16 : 32 / rtp, steps / 4));
-  const int zs = max(1, min(16, 1024 / windows / nw));
+  const int zs = max(1, min(16, 2048 / (windows * nw)));
   const size_t lds = (size_t)nw * AW * (16 * rtp + 1) * sizeof(float);
 #define MOE_ADAPT(RT, NF)                                                                                       \
   do {                                                                                                          \
