@@ -210,8 +210,9 @@ struct NormRow {
   void *resid_out, *x_out;
 };
 hipError_t launch_norm(int dtype, const void* y, const NormRow& n, int T, hipStream_t st);
+// cap: rows of yp and entries of wts and inv_perm (offsets and rows behind it are ignored).
 hipError_t launch_combine_norm(int dtype, const void* yp, const void* ysh, const int32_t* tok_off, const float* wts,
-                               const int32_t* inv_perm, const NormRow& n, int T, hipStream_t st);
+                               const int32_t* inv_perm, int cap, const NormRow& n, int T, hipStream_t st);
 
 // adapt.hip -- low-rank adapters: out[r] = y[r] + scales[a] * B[a][g] (A[a][g] x[r]).
 struct AdaptArgs {

@@ -524,7 +524,7 @@ moe_status moe_combine_norm(const moe_desc* desc, const moe_norm_desc* nd, const
   for (const void* o : {(const void*)resid_out, (const void*)x_out})
     if (overlap(y_perm, a_cap(d) * d.d * elt_size(d), o, bytes) || overlap(y_shared, bytes, o, bytes))
       return MOE_ERR_SHAPE;
-  return launched(launch_combine_norm(d.dtype, y_perm, y_shared, tok_off, topk_w, inv_perm, row, d.T,
+  return launched(launch_combine_norm(d.dtype, y_perm, y_shared, tok_off, topk_w, inv_perm, (int)a_cap(d), row, d.T,
                                       static_cast<hipStream_t>(stream)));
 }
 

@@ -66,32 +66,46 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 template <typename T, int CH, bool VEC>
 struct RowIo {
   static constexpr int LE = 16 / (int)sizeof(T);
+  // One operand's chunks as they were read; elements that are not there are 0.
+  struct Part {
+    u32x4_t v[CH];
+    __device__ __forceinline__ float get(int q, int i) const {
+      if constexpr (sizeof(T) == 2) return __uint_as_float(i & 1 ? v[q][i >> 1] & 0xffff0000u : v[q][i >> 1] << 16);
+      else return __uint_as_float(v[q][i]);
+    }
+  };
   int d;
-  __device__ __forceinline__ bool has(int q, int i) const {
-    return VEC ? (int)(threadIdx.x + blockDim.x * q) * LE < d : (int)(threadIdx.x + blockDim.x * (LE * q + i)) < d;
-  }
   __device__ __forceinline__ int at(int q, int i) const {
     return VEC ? (int)(threadIdx.x + blockDim.x * q) * LE + i : (int)(threadIdx.x + blockDim.x * (LE * q + i));
   }
-  // Elements of the row that are not there read as 0.
-  __device__ __forceinline__ void load(const T* p, float (&f)[CH][LE]) const {
+  __device__ __forceinline__ bool has(int q, int i) const { return at(q, VEC ? 0 : i) < d; }
+  template <bool NT = false>
+  __device__ __forceinline__ void read(const void* base, size_t first, Part& f) const {
+    const T* const p = (const T*)base + first;
 #pragma unroll
     for (int q = 0; q < CH; ++q) {
+      f.v[q] = u32x4_t{0u, 0u, 0u, 0u};
       if constexpr (VEC) {
-        u32x4_t v = {0u, 0u, 0u, 0u};
-        if (has(q, 0)) v = *reinterpret_cast<const u32x4_t*>(p + at(q, 0));
-        unpack16<T>(v, f[q]);
+        const u32x4_t* const c = reinterpret_cast<const u32x4_t*>(p + at(q, 0));
+        if (has(q, 0)) f.v[q] = NT ? __builtin_nontemporal_load(c) : *c;
       } else {
 #pragma unroll
-        for (int i = 0; i < LE; ++i) f[q][i] = has(q, i) ? Elt<T>::to_f32(p[at(q, i)]) : 0.f;
+        for (int i = 0; i < LE; ++i)
+          if (has(q, i)) {
+            if constexpr (sizeof(T) == 2) f.v[q][i >> 1] |= (uint32_t)p[at(q, i)] << (16 * (i & 1));
+            else f.v[q][i] = __float_as_uint(p[at(q, i)]);
+          }
       }
     }
   }
-  __device__ __forceinline__ void store(T* p, const float (&f)[CH][LE]) const {
+  // Non-temporal: the row's next reader is another kernel (8,192 x 2,048 bf16,
+  // four rows of traffic a token: 37 -> 30 us).
+  __device__ __forceinline__ void write(void* base, size_t first, const float (&f)[CH][LE]) const {
+    T* const p = (T*)base + first;
 #pragma unroll
     for (int q = 0; q < CH; ++q) {
       if constexpr (VEC) {
-        if (has(q, 0)) *reinterpret_cast<u32x4_t*>(p + at(q, 0)) = pack16<T>(f[q]);
+        if (has(q, 0)) __builtin_nontemporal_store(pack16<T>(f[q]), reinterpret_cast<u32x4_t*>(p + at(q, 0)));
       } else {
 #pragma unroll
         for (int i = 0; i < LE; ++i)
@@ -100,10 +114,8 @@ struct RowIo {
     }
   }
   // v = norm(v)
-  __device__ __forceinline__ void norm(float (&v)[CH][LE], const NormRow& n, const T* w, const T* b, float* red) const {
-    float wv[CH][LE], bv[CH][LE];
-    if (w) load(w, wv);
-    if (b) load(b, bv);
+  __device__ __forceinline__ void norm(float (&v)[CH][LE], const NormRow& n, bool has_w, const Part& w, bool has_b,
+                                       const Part& b, float* red) const {
     if (n.layer) {
       float s = 0.f;
 #pragma unroll
@@ -127,24 +139,47 @@ struct RowIo {
 #pragma unroll
       for (int i = 0; i < LE; ++i) {
         float o = v[q][i] * rs;
-        if (w) o *= n.w_offset + wv[q][i];
-        if (b) o += bv[q][i];
+        if (has_w) o *= n.w_offset + w.get(q, i);
+        if (has_b) o += b.get(q, i);
         v[q][i] = o;
       }
   }
 };
 
+// The row's operands.  EARLY (short rows, where there are registers for it): all of
+// them are requested at once, before anything is known of y, so that their
+// latencies pass together; otherwise each before its use.
+template <typename T, int CH, bool VEC, bool EARLY_>
+struct RowParts {
+  static constexpr bool EARLY = EARLY_;
+  typename RowIo<T, CH, VEC>::Part resid, post_w, post_b, gate, pre_w, pre_b;
+  template <bool NT>
+  __device__ __forceinline__ void early(const RowIo<T, CH, VEC>& io, const NormRow& n, size_t row) {
+    if (n.resid) io.template read<NT>(n.resid, row, resid);
+    if constexpr (EARLY) {
+      if (n.has_y && n.post && n.post_w) io.read(n.post_w, 0, post_w);
+      if (n.has_y && n.post && n.post_b) io.read(n.post_b, 0, post_b);
+      if (n.gate_mode >= MOE_GATE_CHANNEL && n.gate_mode != MOE_GATE_TOKEN)
+        io.read(n.gate, n.gate_mode == MOE_GATE_FULL ? row : 0, gate);
+      if (n.x_out && n.pre_w) io.read(n.pre_w, 0, pre_w);
+      if (n.x_out && n.pre_b) io.read(n.pre_b, 0, pre_b);
+    }
+  }
+};
+
 // The chain behind y (v in: y, float32).  resid, y and the outputs may be the
 // same buffers: a thread writes only elements that it alone has read before.
-template <typename T, int CH, bool VEC>
+template <typename T, int CH, bool VEC, bool EARLY>
 __device__ __forceinline__ void norm_chain(float (&v)[CH][16 / sizeof(T)], const RowIo<T, CH, VEC>& io,
-                                           const NormRow& n, int t, float* red) {
+                                           const NormRow& n, RowParts<T, CH, VEC, EARLY>& o, int t, float* red) {
   constexpr int LE = 16 / (int)sizeof(T);
   const size_t row = (size_t)t * io.d;
-  float rv[CH][LE];
-  if (n.resid) io.load((const T*)n.resid + row, rv);
   if (n.has_y) {
-    if (n.post) io.norm(v, n, (const T*)n.post_w, (const T*)n.post_b, red);
+    if (n.post) {
+      if (!EARLY && n.post_w) io.read(n.post_w, 0, o.post_w);
+      if (!EARLY && n.post_b) io.read(n.post_b, 0, o.post_b);
+      io.norm(v, n, n.post_w != nullptr, o.post_w, n.post_b != nullptr, o.post_b, red);
+    }
     if (n.gate_mode == MOE_GATE_TOKEN) {
       const float g = Elt<T>::to_f32(((const T*)n.gate)[t]);
 #pragma unroll
@@ -152,55 +187,67 @@ __device__ __forceinline__ void norm_chain(float (&v)[CH][16 / sizeof(T)], const
 #pragma unroll
         for (int i = 0; i < LE; ++i) v[q][i] *= g;
     } else if (n.gate_mode != MOE_GATE_NONE) {
-      float g[CH][LE];
-      io.load((const T*)n.gate + (n.gate_mode == MOE_GATE_FULL ? row : 0), g);
+      if (!EARLY) io.read(n.gate, n.gate_mode == MOE_GATE_FULL ? row : 0, o.gate);
 #pragma unroll
       for (int q = 0; q < CH; ++q)
 #pragma unroll
-        for (int i = 0; i < LE; ++i) v[q][i] *= g[q][i];
+        for (int i = 0; i < LE; ++i) v[q][i] *= o.gate.get(q, i);
     }
 #pragma unroll
     for (int q = 0; q < CH; ++q)
 #pragma unroll
-      for (int i = 0; i < LE; ++i) v[q][i] = n.resid ? fmaf(n.alpha, v[q][i], rv[q][i]) : n.alpha * v[q][i];
+      for (int i = 0; i < LE; ++i) v[q][i] = n.resid ? fmaf(n.alpha, v[q][i], o.resid.get(q, i)) : n.alpha * v[q][i];
   } else {
 #pragma unroll
     for (int q = 0; q < CH; ++q)
 #pragma unroll
-      for (int i = 0; i < LE; ++i) v[q][i] = rv[q][i];
+      for (int i = 0; i < LE; ++i) v[q][i] = o.resid.get(q, i);
   }
-  if (n.resid_out) io.store((T*)n.resid_out + row, v);
+  if (n.resid_out) io.write(n.resid_out, row, v);
   if (n.x_out) {
-    // the elements past the row must not count: y * gate + resid is 0 there
-    io.norm(v, n, (const T*)n.pre_w, (const T*)n.pre_b, red);
-    io.store((T*)n.x_out + row, v);
+    // elements past the row do not count: they are 0 here
+    if (!EARLY && n.pre_w) io.read(n.pre_w, 0, o.pre_w);
+    if (!EARLY && n.pre_b) io.read(n.pre_b, 0, o.pre_b);
+    io.norm(v, n, n.pre_w != nullptr, o.pre_w, n.pre_b != nullptr, o.pre_b, red);
+    io.write(n.x_out, row, v);
   }
 }
 
 template <typename T, int CH, bool VEC>
-__global__ __launch_bounds__(1024) void norm_kernel(const T* y, NormRow n) {
+__global__ __launch_bounds__(CH <= 2 ? 512 : 1024) void norm_kernel(const T* y, NormRow n) {
   constexpr int LE = 16 / (int)sizeof(T);
   __shared__ float red[16];
   const RowIo<T, CH, VEC> io{n.d};
   const int t = blockIdx.x;
   float v[CH][LE];
-  if (n.has_y) io.load(y + (size_t)t * n.d, v);
-  norm_chain<T, CH, VEC>(v, io, n, t, red);
+  typename RowIo<T, CH, VEC>::Part yp;
+  RowParts<T, CH, VEC, (CH <= 2)> o;
+  if (n.has_y) io.read(y, (size_t)t * n.d, yp);
+  o.template early<false>(io, n, (size_t)t * n.d);
+#pragma unroll
+  for (int q = 0; q < CH; ++q)
+#pragma unroll
+    for (int i = 0; i < LE; ++i) v[q][i] = n.has_y ? yp.get(q, i) : 0.f;
+  norm_chain(v, io, n, o, t, red);
 }
 
 // The combine of combine.hip (same order of the same fused multiply-adds),
 // kept in float32 and followed by the chain above.  The rows of CBN
 // assignments are requested together.
 template <typename T, int CH, int CBN>
-__global__ __launch_bounds__(1024) void combine_norm_kernel(const T* __restrict__ yp, const T* __restrict__ ysh,
+__global__ __launch_bounds__(CH <= 2 ? 512 : 1024) void combine_norm_kernel(const T* __restrict__ yp, const T* __restrict__ ysh,
                                                             const int32_t* __restrict__ tok_off,
                                                             const float* __restrict__ wts,
-                                                            const int32_t* __restrict__ inv_perm, NormRow n) {
+                                                            const int32_t* __restrict__ inv_perm, int cap, NormRow n) {
   constexpr int LE = 16 / (int)sizeof(T);
   __shared__ float red[16];
   const RowIo<T, CH, true> io{n.d};
   const int t = blockIdx.x;
-  const int a0 = tok_off[t], a1 = tok_off[t + 1];
+  const int a0 = max(tok_off[t], 0), a1 = min(tok_off[t + 1], cap);
+  // resid is read past the caches like the rows of Y; with y_shared read so as well
+  // the call is slower (4,096 x 7,168, k in {4, 8}: 114 against 119 us)
+  RowParts<T, CH, true, CH == 1> o;
+  o.template early<true>(io, n, (size_t)t * n.d);
   float v[CH][LE];
 #pragma unroll
   for (int q = 0; q < CH; ++q)
@@ -208,39 +255,43 @@ __global__ __launch_bounds__(1024) void combine_norm_kernel(const T* __restrict_
     for (int i = 0; i < LE; ++i) v[q][i] = 0.f;
   for (int b = a0; b < a1; b += CBN) {
     u32x4_t r[CBN][CH];
+    float w[CBN];
+    int p[CBN];
 #pragma unroll
     for (int j = 0; j < CBN; ++j) {
-      const int p = b + j < a1 ? inv_perm[b + j] : -1;
+      p[j] = inv_perm[min(b + j, a1 - 1)];
+      w[j] = wts[min(b + j, a1 - 1)];
+      if (b + j >= a1 || p[j] >= cap) p[j] = -1;
+    }
+#pragma unroll
+    for (int j = 0; j < CBN; ++j)
 #pragma unroll
       for (int q = 0; q < CH; ++q) {
         r[j][q] = u32x4_t{0u, 0u, 0u, 0u};
-        if (p >= 0 && io.has(q, 0))
-          r[j][q] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(yp + (size_t)p * n.d + io.at(q, 0)));
+        if (p[j] >= 0 && io.has(q, 0))
+          r[j][q] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(yp + (size_t)p[j] * n.d + io.at(q, 0)));
       }
-    }
 #pragma unroll
     for (int j = 0; j < CBN; ++j) {
-      if (b + j < a1 && inv_perm[b + j] >= 0) {
-        const float w = wts[b + j];
+      if (p[j] < 0) continue;
 #pragma unroll
-        for (int q = 0; q < CH; ++q) {
-          float f[LE];
-          unpack16<T>(r[j][q], f);
+      for (int q = 0; q < CH; ++q) {
+        float f[LE];
+        unpack16<T>(r[j][q], f);
 #pragma unroll
-          for (int i = 0; i < LE; ++i) v[q][i] = fmaf(w, f[i], v[q][i]);
-        }
+        for (int i = 0; i < LE; ++i) v[q][i] = fmaf(w[j], f[i], v[q][i]);
       }
     }
   }
   if (ysh) {
-    float f[CH][LE];
-    io.load(ysh + (size_t)t * n.d, f);
+    typename RowIo<T, CH, true>::Part sh;
+    io.read(ysh, (size_t)t * n.d, sh);
 #pragma unroll
     for (int q = 0; q < CH; ++q)
 #pragma unroll
-      for (int i = 0; i < LE; ++i) v[q][i] += f[q][i];
+      for (int i = 0; i < LE; ++i) v[q][i] += sh.get(q, i);
   }
-  norm_chain<T, CH, true>(v, io, n, t, red);
+  norm_chain(v, io, n, o, t, red);
 }
 
 // Threads of a row: enough for CH chunks each, in whole waves.
@@ -273,12 +324,12 @@ hipError_t launch_norm(int dtype, const void* y, const NormRow& n, int T, hipStr
 
 template <typename T>
 static void launch_combine_norm_t(const T* yp, const T* ysh, const int32_t* tok_off, const float* wts,
-                                  const int32_t* inv_perm, const NormRow& n, int T_, hipStream_t st) {
+                                  const int32_t* inv_perm, int cap, const NormRow& n, int T_, hipStream_t st) {
   constexpr int LE = 16 / (int)sizeof(T);
   const int nch = n.d / LE;
 #define MOE_CNORM(CH, CBN)                                                                                          \
   hipLaunchKernelGGL((combine_norm_kernel<T, CH, CBN>), dim3(T_), dim3(row_threads(nch, CH)), 0, st, yp, ysh, tok_off, \
-                     wts, inv_perm, n)
+                     wts, inv_perm, cap, n)
   if (nch <= 512) MOE_CNORM(1, 8);
   else if (nch <= 1024) MOE_CNORM(2, 8);
   else if (nch <= 4096) MOE_CNORM(4, 4);
@@ -288,12 +339,12 @@ static void launch_combine_norm_t(const T* yp, const T* ysh, const int32_t* tok_
 }
 
 hipError_t launch_combine_norm(int dtype, const void* yp, const void* ysh, const int32_t* tok_off, const float* wts,
-                               const int32_t* inv_perm, const NormRow& n, int T, hipStream_t st) {
+                               const int32_t* inv_perm, int cap, const NormRow& n, int T, hipStream_t st) {
   if (T == 0) return hipSuccess;
   if (dtype == DT_BF16)
-    launch_combine_norm_t<bf16_t>((const bf16_t*)yp, (const bf16_t*)ysh, tok_off, wts, inv_perm, n, T, st);
+    launch_combine_norm_t<bf16_t>((const bf16_t*)yp, (const bf16_t*)ysh, tok_off, wts, inv_perm, cap, n, T, st);
   else
-    launch_combine_norm_t<float>((const float*)yp, (const float*)ysh, tok_off, wts, inv_perm, n, T, st);
+    launch_combine_norm_t<float>((const float*)yp, (const float*)ysh, tok_off, wts, inv_perm, cap, n, T, st);
   return hipGetLastError();
 }
 
