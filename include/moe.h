@@ -554,9 +554,11 @@ moe_status moe_forward(const moe_desc* desc, const void* x, const void* w_router
  *                k_max <= topk_group * E / n_group (else MOE_ERR_SHAPE)
  *   select_bias  float [E], or NULL for none
  *   others       as in moe_route; budgets follow desc->k_policy; desc->router:
- *                AUTO, FLOAT64 or SCREENED (same ids under each; the weights of
- *                SCREENED and of AUTO's large bf16 batches are those of logits
- *                within 2e-6 of sum |x_i w_i| / sqrt(d))
+ *                AUTO, FLOAT64 or SCREENED.  The ids are the same under each.  With
+ *                SCREENED, and with AUTO for bf16 when T * E * d >= 2^30, a weight
+ *                comes from a logit whose products are summed 64 at a time in
+ *                float32 and further in float64, unless its order was in doubt (a
+ *                softmax with select_bias always takes FLOAT64)
  *   ws           scratch of moe_workspace_size(MOE_OP_ROUTE_GROUPED) bytes
  * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED (rule values, or
  * MOE_ROUTER_FUSED), MOE_ERR_ALIGN, MOE_ERR_WORKSPACE, MOE_ERR_LAUNCH.
@@ -645,7 +647,7 @@ moe_status moe_combine_norm(const moe_desc* desc, const moe_norm_desc* nd, const
  *   y_in, y_out  ELT [rows][N]; the same buffer (in place) or not overlapping,
  *                and y_out overlaps neither x, a nor b
  *   ws           scratch of moe_adapt_workspace_size bytes
- * Ranges: 0 <= rows, T; K and N multiples of 8 up to 65536; R a multiple of 8 up
+ * Ranges: 0 <= rows <= 2^22, T >= 0; K and N multiples of 8 up to 65536; R a multiple of 8 up
  * to 128; 1 <= L <= 65536; 1 <= G <= 1024.  Any ELT buffer: 16-byte aligned.
  * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE (ranges, overlap), MOE_ERR_UNSUPPORTED
  * (dtype), MOE_ERR_ALIGN, MOE_ERR_WORKSPACE, MOE_ERR_LAUNCH.

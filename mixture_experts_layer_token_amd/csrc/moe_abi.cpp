@@ -532,7 +532,7 @@ static moe_status check_adapter(const moe_adapter_desc* ad) {
   if (!ad) return MOE_ERR_NULL;
   const moe_adapter_desc& a = *ad;
   if (a.dtype != MOE_F32 && a.dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
-  if (a.T < 0 || a.rows < 0 || a.rows > (1 << 30) || a.L < 1 || a.L > 65536 || a.G < 1 || a.G > 1024) return MOE_ERR_SHAPE;
+  if (a.T < 0 || a.rows < 0 || a.rows > (1 << 22) || a.L < 1 || a.L > 65536 || a.G < 1 || a.G > 1024) return MOE_ERR_SHAPE;
   if (a.K < 8 || a.K > 65536 || a.K % 8 || a.N < 8 || a.N > 65536 || a.N % 8) return MOE_ERR_SHAPE;
   if (a.R < 8 || a.R > 128 || a.R % 8) return MOE_ERR_SHAPE;
   return MOE_OK;

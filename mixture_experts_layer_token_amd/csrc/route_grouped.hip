@@ -12,7 +12,6 @@
 // with id -1 and weight 0, which moe_permute and moe_combine skip.
 #include "common.h"
 #include "launch.h"
-#include "screen.h"
 #include "select.h"
 
 #include <type_traits>
@@ -480,11 +479,9 @@ struct ScreenIn {
   int d;
 };
 
-// LDS words (8 bytes) of one wave: keys; logits; experts and places of the
-// chosen; with SCREEN the exact sums' shares, the sums and their experts.
-__host__ __device__ constexpr int rg_words(int E, bool screen) {
-  return 3 * E + (screen ? SEL_GRP * 64 + E + (E + 1) / 2 : 0);
-}
+// LDS words (8 bytes) of one wave: keys (between passes: exact sums); logits;
+// experts and places of the chosen; with SCREEN the experts of the exact sums.
+__host__ __device__ constexpr int rg_words(int E, bool screen) { return 3 * E + (screen ? (E + 1) / 2 : 0); }
 
 __device__ __forceinline__ uint64_t to_key(double c) { return score_key(c); }
 __device__ __forceinline__ uint32_t to_key(float c) { return score_key32(c); }
@@ -521,6 +518,59 @@ __device__ __forceinline__ K kth_key(const K (&key)[KPL], int k, int* got) {
   }
   *got = g;
   return v;
+}
+
+// Exact dot products of the token's row x with n rows (row_of(c), c < n): exact
+// products, float64 sums, sink(c, sum) on every lane with the sum.  Two rows at a
+// time against one reading of x, four steps of 512 elements in flight; the lanes
+// are added by DPP.  (At 4,096 tokens, d = 7168, the tokens with open decisions end
+// last: 48 us for this kernel with one row after the other and LDS sums, or with
+// four rows, whose registers spill; 38 us so.)
+template <class RowOf, class Sink>
+__device__ __forceinline__ void wave_dots(const bf16_t* __restrict__ x, int d, int n, RowOf row_of, Sink sink) {
+  constexpr int CB = 2, RING = 4;
+  const int lane = threadIdx.x & 63;
+  const int steps = (d + 511) / 512;
+#pragma unroll 1
+  for (int c0 = 0; c0 < n; c0 += CB) {
+    const bf16_t* row[CB];
+#pragma unroll
+    for (int c = 0; c < CB; ++c) row[c] = row_of(min(c0 + c, n - 1));
+    u32x4_t xv[RING], wv[RING][CB];
+    double acc[CB] = {};
+    auto load = [&](int q, int s) {
+      const uint32_t off = (uint32_t)min(s * 512 + 8 * lane, d - 8);
+      xv[q] = *reinterpret_cast<const u32x4_t*>(x + off);
+#pragma unroll
+      for (int c = 0; c < CB; ++c) wv[q][c] = *reinterpret_cast<const u32x4_t*>(row[c] + off);
+    };
+#pragma unroll
+    for (int q = 0; q < RING; ++q) load(q, q);
+#pragma unroll 1
+    for (int s0 = 0; s0 < steps; s0 += RING) {
+#pragma unroll
+      for (int q = 0; q < RING; ++q) {
+        const bool in = (s0 + q) * 512 + 8 * lane < d;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t xw = in ? xv[q][i] : 0u;
+          const double x0 = (double)__uint_as_float(xw << 16), x1 = (double)__uint_as_float(xw & 0xffff0000u);
+#pragma unroll
+          for (int c = 0; c < CB; ++c) {
+            const uint32_t ww = in ? wv[q][c][i] : 0u;
+            acc[c] = fma(x0, (double)__uint_as_float(ww << 16), acc[c]);
+            acc[c] = fma(x1, (double)__uint_as_float(ww & 0xffff0000u), acc[c]);
+          }
+        }
+        load(q, s0 + q + RING);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < CB; ++c) {
+      const double v = wave_sum(acc[c]);
+      if (c0 + c < n) sink(c0 + c, v);
+    }
+  }
 }
 
 // What the selection of a token keeps between its passes, by slot s of a lane
@@ -761,7 +811,7 @@ __device__ __forceinline__ int route_pass(const double (&l)[KPL], const float (&
 }
 
 template <int KPL, bool SCREEN>
-__global__ __launch_bounds__(256) void route_grouped_kernel(const double* __restrict__ part, int S, ScreenIn in,
+__global__ __launch_bounds__(256, KPL <= 4 ? 4 : 1) void route_grouped_kernel(const double* __restrict__ part, int S, ScreenIn in,
                                                             const float* __restrict__ bias,
                                                             const float* __restrict__ sel_bias,
                                                             const int32_t* __restrict__ tok_off, int T_, int E,
@@ -867,8 +917,8 @@ __global__ __launch_bounds__(256) void route_grouped_kernel(const double* __rest
     }
     all = false;
     if constexpr (SCREEN) {  // exact logits of the marked slots
-      int32_t* const list = reinterpret_cast<int32_t*>(lds + 4 * E + SEL_GRP * 64);
-      double* const val = reinterpret_cast<double*>(lds + 3 * E + SEL_GRP * 64);
+      int32_t* const list = reinterpret_cast<int32_t*>(lds + 3 * E);
+      double* const val = reinterpret_cast<double*>(lds);
       const uint64_t below = (1ull << lane) - 1ull;
       int n = 0, at[KPL];
 #pragma unroll
@@ -880,9 +930,13 @@ __global__ __launch_bounds__(256) void route_grouped_kernel(const double* __rest
         n += __popcll(b);
       }
       wave_sync();
-      exact_dots<2, false, SEL_GRP>(
-          in.x + (size_t)t * in.d, in.d, n, [&](int c) { return in.w + (size_t)list[c] * in.d; },
-          reinterpret_cast<double*>(lds + 3 * E), [&](int c, double v) { val[c] = v; });
+      wave_dots(
+          in.x + (size_t)t * in.d, in.d, n,
+          [&](int c) { return in.w + (size_t)__builtin_amdgcn_readfirstlane(list[c]) * in.d; },
+          [&](int c, double v) {
+            if (lane == 0) val[c] = v;
+          });
+      wave_sync();
 #pragma unroll
       for (int s = 0; s < KPL; ++s)
         if ((m.mark >> s) & 1u) l[s] = (double)(float)(val[at[s]] + (double)bs[s]);

@@ -174,7 +174,7 @@ def _ad(**kw):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(dtype=5), 3), (dict(T=-1), 2), (dict(rows=-1), 2), (dict(K=4), 2), (dict(K=65544), 2), (dict(K=65), 2),
+    (dict(dtype=5), 3), (dict(T=-1), 2), (dict(rows=-1), 2), (dict(T=1 << 23, rows=(1 << 22) + 1), 2), (dict(K=4), 2), (dict(K=65544), 2), (dict(K=65), 2),
     (dict(N=12), 2), (dict(R=4), 2), (dict(R=12), 2), (dict(R=136), 2), (dict(L=0), 2), (dict(G=0), 2),
     (dict(G=1025), 2), (dict(T=15), 2), (dict(G=2), 1), ({}, 4)])
 def test_adapt_refuses(kw, code):
