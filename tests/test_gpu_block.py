@@ -57,9 +57,18 @@ def _route(x, w, k, k_max, rule, *, rb=None, sb=None, scale=1.0, router="auto", 
     return off.cpu().numpy(), ids.cpu().numpy(), to_f64(wts), int(status)
 
 
-def _spread(x, w):
-    """How far a logit of the large bf16 batches may be from its float64 sum."""
-    return 2e-6 * np.sqrt(x.shape[1]) * np.abs(to_f64(x)).max() * np.abs(to_f64(w)).max() if x.dtype == torch.bfloat16 else 0.0
+def _weight_bound(x, w, ref_w, off):
+    """Relative error a weight may have: two roundings (its logit's, its own; exp and
+    the divisions are float64), and in bf16, where the logits may come from sums of
+    64 products in float32, twice the logit's error: at most 66 * 2^-23 (64 additions
+    that may truncate, second-order terms) + 2^-24 (a stored slice) of sum |x_i w_i|
+    <= |x| |w|; a sigmoid or a softmax moves by at most that factor, and so does the
+    sum it is divided by."""
+    r = np.zeros(len(off) - 1)
+    if x.dtype == torch.bfloat16:
+        r = (66 * 2.0 ** -23 + 2.0 ** -24) * np.linalg.norm(to_f64(x), axis=1) * np.linalg.norm(to_f64(w), axis=1).max()
+    r = np.repeat(r, np.diff(off))
+    return np.abs(ref_w) * (2 * EPS + 2.02 * np.expm1(r)) + 1e-38
 
 
 def _check_route(x, w, k, k_max, rb=None, sb=None, scale=1.0, router="auto", policy="exact", **kw):
@@ -71,9 +80,7 @@ def _check_route(x, w, k, k_max, rb=None, sb=None, scale=1.0, router="auto", pol
     assert status == bad
     np.testing.assert_array_equal(off, ref["tok_off"])
     np.testing.assert_array_equal(ids[:A], ref["ids"])
-    # one rounding of the weight to float32 and of its logit; exp and the
-    # division in float64; a score moves by at most its logit's error
-    np.testing.assert_allclose(wts[:A], ref["w"], rtol=2 * EPS + 2 * _spread(x, w), atol=1e-38)
+    assert (np.abs(wts[:A] - ref["w"]) <= _weight_bound(x, w, ref["w"], ref["tok_off"])).all()
     assert (ids[A:] == -7).all() and (wts[A:] == -7.0).all()
     return ref
 
@@ -189,7 +196,29 @@ def test_route_grouped_routers_agree(T, d, E, rule):
     b = _route(x, w, k, min(8, E // 8 * 3), moe.make_route_rule(**RULES[rule]), router="screened", **kw)
     np.testing.assert_array_equal(a[0], b[0])
     np.testing.assert_array_equal(a[1], b[1])
-    np.testing.assert_allclose(a[2], b[2], rtol=2 * EPS + 2 * _spread(x, w))
+    A = int(a[0][-1])
+    assert (np.abs(a[2][:A] - b[2][:A]) <= 2 * _weight_bound(x, w, a[2][:A], a[0])).all()
+
+
+@pytest.mark.parametrize("T,d,E,k_max,rule", [(4200, 1024, 256, 8, 0), (900, 8192, 160, 8, 0), (2100, 2048, 272, 70, 3),
+                                              (1100, 1024, 1024, 9, 2)])
+def test_route_grouped_large_batches(T, d, E, k_max, rule):
+    """AUTO's matrix-instruction logits (T * E * d >= 2^30) against the oracle: scaled
+    tokens (wide and narrow radius), equal and nearly equal experts, some out of service."""
+    g = _gen(T + E)
+    x, w = _randn(g, T, d, dtype=torch.bfloat16), _randn(g, E, d, dtype=torch.bfloat16, std=d ** -0.5)
+    x[::7] *= 8
+    x[1::7] *= 2.0 ** -6
+    x[5] = 0
+    w[E // 3] = w[0]
+    w[E // 2] = w[2]
+    w[E // 2, 5] += 2.0 ** -9
+    k = torch.randint(0, k_max + 1, (T,), generator=g, device=DEV, dtype=torch.int32)
+    sb = None
+    if RULES[rule]["score"] == "sigmoid":
+        sb = (torch.rand(E, generator=g, device=DEV) - 0.5) * 0.1
+        sb[7] = -math.inf
+    _check_route(x, w, k, k_max, sb=sb, scale=2.5, **RULES[rule])
 
 
 # ---------------------------------------------------------------------- norms
@@ -422,7 +451,9 @@ def _adapt_ref(t, dtype):
     (100, 256, 512, 64, 40, 1, 1, False, "random"), (300, 128, 2056, 40, 6, 1, 1, False, "runs"),
     (64, 128, 128, 16, 3, 1, 1, False, "none"), (50, 256, 128, 16, 3, 9, 4, False, "random"),
     (40, 128, 256, 32, 4, 64, 6, True, "random"), (9, 1000, 24, 8, 2, 1024, 3, False, "random"),
-    (70, 64, 64, 16, 6, 1, 1, True, "random"), (5, 4096, 64, 72, 2, 3, 2, False, "one")])
+    (70, 64, 64, 16, 6, 1, 1, True, "random"), (5, 4096, 64, 72, 2, 3, 2, False, "one"),
+    (8200, 72, 1032, 16, 5, 1, 1, False, "random"), (33000, 16, 1032, 8, 3, 1, 1, False, "runs"),
+    (2100, 40, 264, 24, 3, 5, 5, True, "random"), (20, 7168, 512, 96, 2, 1, 1, False, "random")])
 def test_adapt(dtype, T, K, N, R, L, G, k_max, mapped, order):
     t = _adapt_case(T + K + R, dtype, T, K, N, R, L, G, k_max, mapped, order)
     ref, bound = _adapt_ref(t, dtype)
