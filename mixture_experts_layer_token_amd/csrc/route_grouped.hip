@@ -119,6 +119,12 @@ __device__ __forceinline__ void merge2(K& a1, K& a2, K b1, K b2) {
 // long as both operands have the same).  The four waves of a workgroup take
 // quarters of the slice and are added in wave order; slices are added by the
 // selection kernel.  One more slice (z = S) holds the token-offset scan.
+// Bound by the f64 matrix rate (a loop of these instructions alone reaches 70
+// TFLOP/s): 128 tokens x 7168 x 256 take 14 us against 6.7 us at that rate (the
+// rest is the first loads and the sum over the waves), 4,096 tokens 269 us against
+// 215 (float32 batches; bf16 ones take the kernel below), one token 4 us.  The
+// split-K kernel of the plain router, vector float64 through LDS, takes 24 us for
+// one token and 750 us for 4,096.
 typedef double f64x4_t __attribute__((ext_vector_type(4)));
 
 template <typename T>
@@ -269,6 +275,11 @@ hipError_t launch_logits_f64(int dtype, const void* x, const void* w, const int3
 // slices are stored in float32).  One float32 sum over a slice of 1,792 would
 // leave 28 times as much.  The norms'
 // squares are summed beside the products, by the slices: xn[S][T], wn[S][E].
+// 4,096 tokens x 7168 x 256: 41 us, against 12 us for reading x at 4.9 TB/s and 12
+// us of bf16 products at 1,200 TFLOP/s.  It moves 290 MB from the L2 into LDS (a
+// workgroup re-reads its 256 router rows for every 64 tokens) and stores 17 MB of
+// slices; its last 7 us are the scan, whose workgroup finds no CU before the tiles
+// end.
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 constexpr int RG_NW = 8, RG_TOK = 64, RG_EXP = 256, RG_STG = 3;
 constexpr int RG_XB = RG_TOK * 128, RG_SB = RG_XB + RG_EXP * 128;  // 8 KB + 32 KB a stage
@@ -469,10 +480,13 @@ hipError_t launch_logits_tile(const void* x, const void* w, const int32_t* k, in
 // terms: it scales all scores alike, so the order needs select_bias to be absent
 // (the host takes float64 logits otherwise, and the pass starts in float64).
 //
-// A wave that runs alone waits above all for its instructions: the code of the
-// common pass is short, reductions go by DPP, loops over the chosen broadcast by
-// readlane.  One token, 256 experts in 8 groups: 10.7 -> 6.1 us for this kernel
-// against the same steps in float64 with shuffles and unrolled loops.
+// What bounds it: instructions.  A token takes some 1,750 vector and 1,200 scalar
+// ones (counters, 4,096 tokens, 256 experts in 8 groups), 13 us of issue for the
+// batch; its waves are resident at once, three quarters end after 16 us, and the
+// tokens with open decisions (one in six) end last: 38 us.  A few tokens take 9-11
+// us, of which a wave that runs alone spends most waiting for its own instructions,
+// so the common pass is short, reductions go by DPP and the chosen are compared in
+// pairs of lanes.
 struct ScreenIn {
   const bf16_t *x, *w;
   const float *part, *xn, *wn;
