@@ -466,7 +466,7 @@ hipError_t launch_logits_tile(const void* x, const void* w, const int32_t* k, in
 // result stands.  The radius is that of the logits (SCREEN: they come from
 // logits_tile_kernel and may be off by r, so a sigmoid by r / 4, a softmax by a
 // factor within exp(+-2 r); nothing for exact ones) plus what float32 rounds off,
-// 2^-20 of the largest score and key.  What is closer is looked at again:
+// 2^-20 of the largest score and of the values compared.  What is closer is looked at again:
 //  - inexact logits are computed exactly: of the groups whose value is within two
 //    radii of the last one kept or the first one dropped, the experts that may be
 //    among the counted ones (every other group is certainly kept or dropped);
@@ -656,17 +656,19 @@ __device__ __forceinline__ int route_pass(const double (&l)[KPL], const float (&
     key[s] = (m.there >> s) & 1u ? to_key(c) : 0;
     if constexpr (F32) {
       // float32: a few roundings of the score, |a| half steps of the exponent's
-      // argument, one of the key
+      // argument
       const float a = fminf(fabsf((float)(softmax ? l[s] - topd : l[s])), 1e4f);
-      unit = fmaxf(unit, key[s] ? sc * (1.f + 0.125f * a) + fabsf(c) : 0.f);
+      unit = fmaxf(unit, key[s] ? sc * (1.f + 0.125f * a) : 0.f);
     }
   }
-  // two radii: of exact logits, and of inexact ones (expm1(2 rl) <= 2.2 rl)
+  // two radii: of exact logits, and of inexact ones (expm1(2 rl) <= 2.2 rl); in
+  // float32 a comparison adds what rounding the two values themselves may do, so
+  // that one very large bias does not blur the others
   const F r0 = F32 ? tiny * wave_max(unit) + (F)0x1p-120 : (F)0;
   const F r1 = r0 + (F)(softmax ? 4.5 * rl * (double)inv : 0.51 * rl);
+  auto far = [&](F a, F b, F mag, F r) { return F32 ? fabs(a - b) > r + tiny * mag : fabs(a - b) > r; };
   auto apart = [&](F a, F b, bool both_exact) {  // certainly in order
-    const F r = both_exact ? r0 : r1;
-    return F32 || !both_exact ? fabs(a - b) > r : true;
+    return F32 || !both_exact ? far(a, b, (F)(fabs(a) + fabs(b)), both_exact ? r0 : r1) : true;
   };
 
   if (rule.topk_group < rule.n_group) {
@@ -709,24 +711,32 @@ __device__ __forceinline__ int route_pass(const double (&l)[KPL], const float (&
     for (int off = 1; off < lpg; off <<= 1) rank += __shfl_xor(rank, off, 64);
     wave_sync();
     const uint64_t ml = __ballot(mine && rank == rule.topk_group - 1), mf = __ballot(mine && rank == rule.topk_group);
-    const K vl = key_lane(val, __builtin_ctzll(ml)), vf = key_lane(val, __builtin_ctzll(mf));
+    // a float32 sum beyond the type's lowest value says nothing of the group
+    if (F32 && __ballot(mine && m1 != 0 && val == 0)) return 2;
+    const int ll = __builtin_ctzll(ml), lf = __builtin_ctzll(mf);
+    const K vl = key_lane(val, ll), vf = key_lane(val, lf);
     const F z = rule.top2 ? (F)2 : (F)1;
+    // what the rounding of a group's value goes by: the keys that are added
+    const F mag = (F)(fabs(m1 ? to_score(m1) : (F)0) + fabs(rule.top2 && m2 ? to_score(m2) : (F)0));
+    const F magl = to_score(key_lane(to_key(mag), ll)), magf = to_score(key_lane(to_key(mag), lf));
     // a group without experts in service is last, whatever the scores
-    if (vf != 0 && !(to_score(vl) - to_score(vf) > z * r1 + r0)) {
+    if (vf != 0 && !far(to_score(vl), to_score(vf), magl + magf, z * r1 + r0)) {
       const F v = to_score(val);
-      const bool zone = mine && val != 0 && (!(fabs(v - to_score(vl)) > z * r1 + r0) ||
-                                             !(fabs(v - to_score(vf)) > z * r1 + r0));
+      const bool zone = mine && val != 0 && (!far(v, to_score(vl), mag + magl, z * r1 + r0) ||
+                                             !far(v, to_score(vf), mag + magf, z * r1 + r0));
       const uint64_t zones = __ballot(zone);
       const K second = rule.top2 && m2 ? m2 : m1;
       m.mark = 0;
 #pragma unroll
       for (int s = 0; s < KPL; ++s) {
         const K sec = shfl_key(second, first[s]);
-        if (key[s] != 0 && ((zones >> first[s]) & 1ull) && !(to_score(sec) - to_score(key[s]) > r1)) m.mark |= 1u << s;
+        if (key[s] != 0 && ((zones >> first[s]) & 1ull) && !(to_score(sec) > to_score(key[s]) &&
+              far(to_score(sec), to_score(key[s]), (F)(fabs(to_score(sec)) + fabs(to_score(key[s]))), r1)))
+          m.mark |= 1u << s;
       }
       m.mark &= ~m.exact;
       if (__ballot(m.mark != 0)) return 1;
-      if (F32 && !(to_score(vl) - to_score(vf) > (z + 1) * r0)) return 2;
+      if (F32 && !far(to_score(vl), to_score(vf), magl + magf, (z + 1) * r0)) return 2;
     }
     const uint64_t in_kept = __ballot(mine && rank < rule.topk_group);
 #pragma unroll
@@ -747,9 +757,9 @@ __device__ __forceinline__ int route_pass(const double (&l)[KPL], const float (&
   uint32_t near = 0, near0 = 0, above = 0;
 #pragma unroll
   for (int s = 0; s < KPL; ++s) {
-    const F dist = fabs(to_score(key[s]) - pv);
-    if (key[s] != 0 && !(dist > r1)) near |= 1u << s;
-    if (F32 && key[s] != 0 && !(dist > r0)) near0 |= 1u << s;
+    const F c = to_score(key[s]), m2 = (F)(fabs(c) + fabs(pv));
+    if (key[s] != 0 && !far(c, pv, m2, r1)) near |= 1u << s;
+    if (F32 && key[s] != 0 && !far(c, pv, m2, r0)) near0 |= 1u << s;
     if (key[s] >= v) above |= 1u << s;
   }
   m.mark = 0;

@@ -162,6 +162,27 @@ def test_route_grouped_values_that_are_no_numbers():
             assert (ids2[16:20] == -1).all()
 
 
+@pytest.mark.parametrize("router", ["float64", "screened"])
+@pytest.mark.parametrize("low", [-3.4028234663852886e38, -1e4, -3.0])
+def test_route_grouped_large_biases(router, low):
+    """Experts pushed away by the type's lowest value or a smaller constant: alone, in a
+    whole group, against each other (the sum of two is below float32), and biases so
+    large that a float32 key would lose the scores."""
+    g = _gen(17)
+    x, w = _randn(g, 40, 512, dtype=torch.bfloat16), _randn(g, 64, 512, dtype=torch.bfloat16, std=512 ** -0.5)
+    k = torch.randint(0, 9, (40,), generator=g, device=DEV, dtype=torch.int32)
+    for away in ([0, 9, 63], list(range(8, 24)) + [3], list(range(64)), list(range(5, 64))):
+        sb = (torch.rand(64, generator=g, device=DEV) - 0.5) * 0.1
+        sb[away] = low
+        for gs in ("top2", "max"):
+            _check_route(x, w, k, 8, sb=sb, router=router, score="sigmoid", n_group=8, topk_group=3, group_score=gs,
+                         renorm=True)
+        _check_route(x, w, k, 8, sb=sb, router=router, score="softmax", n_group=8, topk_group=3, group_score="top2",
+                     renorm=False)
+    sb = torch.full((64,), 1e4, device=DEV) + (torch.rand(64, generator=g, device=DEV) * 1e-2)
+    _check_route(x, w, k, 8, sb=sb, router=router, **RULES[0])
+
+
 @pytest.mark.parametrize("T", [0, 1])
 def test_route_grouped_empty(T):
     x, w = torch.zeros(T, 128, device=DEV), torch.zeros(8, 128, device=DEV)
