@@ -555,7 +555,7 @@ moe_status moe_forward(const moe_desc* desc, const void* x, const void* w_router
  *   select_bias  float [E], or NULL for none
  *   others       as in moe_route; budgets follow desc->k_policy; desc->router:
  *                AUTO, FLOAT64 or SCREENED.  The ids are the same under each.  With
- *                SCREENED, and with AUTO for bf16 when T * E * d >= 2^30, a weight
+ *                SCREENED, and with AUTO for bf16 when T * E * d >= 3 * 2^28, a weight
  *                comes from a logit whose products are summed 64 at a time in
  *                float32 and further in float64, unless its order was in doubt (a
  *                softmax with select_bias always takes FLOAT64)

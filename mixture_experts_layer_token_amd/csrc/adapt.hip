@@ -17,7 +17,7 @@
 // Bound by memory in prefill (4,096 rows, 2,048 -> 7,168, rank 32, 8 adapters: 15 us
 // for the first product, 37 us for the second, which reads and writes 117 MB, a copy
 // in the same shape taking 30), by latency in decode (128 rows, 32 adapters: 8.5 +
-// 12 us; 1,150 permuted rows of 128 experts, 4 adapters: 10 + 18 us).
+// 11 us; 1,150 permuted rows of 128 experts, 4 adapters: 10 + 17 us).
 #include "common.h"
 #include "launch.h"
 
@@ -244,8 +244,13 @@ __global__ __launch_bounds__(1024) void adapt_shrink_kernel(AdaptArgs p, void* _
 // read once, y and v of the next D windows are in flight while one is multiplied,
 // from addresses that depend on nothing (so that the waits count loads instead of
 // draining them).  B of a pair is loaded when it changes.
-template <typename T, int NF>
-__global__ __launch_bounds__(256, NF == 1 ? 4 : (NF <= 4 ? 2 : 1)) void adapt_expand_kernel(AdaptArgs p, const T* __restrict__ vin, int wpw) {
+//
+// AHEAD: B of a window's next pair is requested while one is multiplied; taken where
+// the waves are few, which is where windows hold many pairs, up to the rank whose
+// fragments fit the registers (128 rows, 32 adapters: 21.2 -> 20.0 us a call with two
+// shares of a window's pairs; 1,150 permuted rows, 128 x 4 adapters: 27.5 -> 26.8).
+template <typename T, int NF, bool AHEAD>
+__global__ __launch_bounds__(256, NF == 1 && !AHEAD ? 4 : (NF <= 4 ? 2 : 1)) void adapt_expand_kernel(AdaptArgs p, const T* __restrict__ vin, int wpw) {
   constexpr int LE = 16 / (int)sizeof(T);
   constexpr bool BF = sizeof(T) == 2;
   constexpr int YV = BF ? 2 : 4;                  // 16-byte pieces of a lane's 16 columns
@@ -347,18 +352,49 @@ __global__ __launch_bounds__(256, NF == 1 ? 4 : (NF <= 4 ? 2 : 1)) void adapt_ex
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     uint32_t served = 0;
-    for_pairs(a, g, blockIdx.z, gridDim.z, [&](uint32_t rows, int first) {
-      const int pa = __builtin_amdgcn_readlane(a, first), pg = __builtin_amdgcn_readlane(g, first);
-      if (pa != ba || pg != bg) load_b(bv, pa, pg);
-      ba = pa;
-      bg = pg;
+    auto multiply = [&](uint32_t rows, int first) {
       f32x4_t t[4];
       product(bv, v, __builtin_amdgcn_readlane(rank, first), t);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if ((rows >> l16) & 1u) acc[j] = t[j];
-      served |= rows;
-    });
+    };
+    if constexpr (AHEAD) {
+      // the pairs, one in each of the first lanes
+      int firsts = 0, n = 0;
+      uint32_t prows = 0;
+      for_pairs(a, g, blockIdx.z, gridDim.z, [&](uint32_t rows, int first) {
+        if (lane == n) {
+          firsts = first;
+          prows = rows;
+        }
+        served |= rows;
+        ++n;
+      });
+      u32x4_t bn[4][NF];
+      auto load_pair = [&](u32x4_t (&to)[4][NF], int q) {
+        const int first = __builtin_amdgcn_readlane(firsts, q);
+        load_b(to, __builtin_amdgcn_readlane(a, first), __builtin_amdgcn_readlane(g, first));
+      };
+      if (n) load_pair(bv, 0);
+      for (int q = 0; q < n; ++q) {
+        load_pair(bn, min(q + 1, n - 1));
+        multiply((uint32_t)__builtin_amdgcn_readlane((int)prows, q), __builtin_amdgcn_readlane(firsts, q));
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int f = 0; f < NF; ++f) bv[j][f] = bn[j][f];
+      }
+    } else {
+      for_pairs(a, g, blockIdx.z, gridDim.z, [&](uint32_t rows, int first) {
+        const int pa = __builtin_amdgcn_readlane(a, first), pg = __builtin_amdgcn_readlane(g, first);
+        if (pa != ba || pg != bg) load_b(bv, pa, pg);
+        ba = pa;
+        bg = pg;
+        multiply(rows, first);
+        served |= rows;
+      });
+    }
     // rows without an adapter are copied
     if (blockIdx.z == 0 && !inplace) served |= (uint32_t)__ballot(live && a < 0) & 0xffffu;
     if (!served) return;
@@ -416,8 +452,10 @@ static void launch_adapt_t(const AdaptArgs& p, void* v, hipStream_t st) {
   // windows of a wave: one while the waves are few, up to 8
   const int wpw = max(1, min(8, (int)((long long)windows * cols * 4 / 4096)));
   const int splits = (windows + wpw - 1) / wpw;
-  // shares of a window's pairs: 1 where the windows fill the chip, more where few
-  const int ze = max(1, min(4, 4096 / (cols * 4 * splits)));
+  // shares of a window's pairs: 1 where the windows fill the chip, 2 where they are
+  // few (128 rows, us a call: 21.9 with 1, 20.0 with 2, 20.7 with 3, 21.6 with 4)
+  const int ze = max(1, min(2, 4096 / (cols * 4 * splits)));
+  const bool ahead = wpw == 1;
   const int rt = (p.R + 15) / 16, rtp = rt <= 2 ? rt : (rt <= 4 ? 4 : 8);
   const int steps = (p.K * (int)sizeof(T) + 63) / 64;
   const int nw = max(1, min(rtp <= 2 ? 16 : 32 / rtp, steps / 4));
@@ -426,7 +464,12 @@ static void launch_adapt_t(const AdaptArgs& p, void* v, hipStream_t st) {
 #define MOE_ADAPT(RT, NF)                                                                                       \
   do {                                                                                                          \
     hipLaunchKernelGGL((adapt_shrink_kernel<T, RT>), dim3(windows, zs), dim3(64 * nw), lds, st, p, v);          \
-    hipLaunchKernelGGL((adapt_expand_kernel<T, NF>), dim3(cols, splits, ze), dim3(256), 0, st, p, (const T*)v, wpw); \
+    if (ahead)                                                                                                  \
+      hipLaunchKernelGGL((adapt_expand_kernel<T, NF, ((NF) <= 2)>), dim3(cols, splits, ze), dim3(256), 0, st, p,  \
+                         (const T*)v, wpw);                                                                     \
+    else                                                                                                        \
+      hipLaunchKernelGGL((adapt_expand_kernel<T, NF, false>), dim3(cols, splits, ze), dim3(256), 0, st, p,      \
+                         (const T*)v, wpw);                                                                     \
   } while (0)
   constexpr bool BF = sizeof(T) == 2;
   if (rt == 1) MOE_ADAPT(1, 1);

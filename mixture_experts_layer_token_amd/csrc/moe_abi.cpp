@@ -187,9 +187,12 @@ void plan_path(const moe_desc& d, Carver& c, PathWs& w) {
 // Grouped routing: float64 partial logits, or for large bf16 batches those of
 // the bf16 matrix instructions with the squared norms that bound their error.
 struct GroupedWs { double* part; int splits; float *approx, *xn, *wn; int tile_splits; };
+// AUTO takes the latter from T * E * d = 3 * 2^28 on (us a call, float64 against bf16:
+// 7168 x 256 experts, 256 tokens 37 / 52, 512 tokens 62 / 59, 1,024 tokens 91 / 59;
+// 2048 x 512, 512 tokens 46 / 51, 1,024 tokens 64 / 51; 4096 x 64, 2,048 tokens 37 / 38).
 bool grouped_tile(const moe_desc& d) {
   if (d.router == MOE_ROUTER_SCREENED) return true;
-  return d.router == MOE_ROUTER_AUTO && d.dtype == MOE_BF16 && (double)d.T * d.E * d.d >= 1073741824.0;
+  return d.router == MOE_ROUTER_AUTO && d.dtype == MOE_BF16 && (double)d.T * d.E * d.d >= 805306368.0;
 }
 void plan_grouped(const moe_desc& d, Carver& c, GroupedWs& w) {
   // the two ways share the region: which one runs depends on the rule as well
