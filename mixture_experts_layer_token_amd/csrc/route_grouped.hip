@@ -150,14 +150,17 @@ __global__ __launch_bounds__(256) void logits_f64_kernel(const T* __restrict__ x
   __shared__ double red[4 * TT * LD];
   const int S = gridDim.z - 1;
   if ((int)blockIdx.z == S) {
-    if (blockIdx.x == 0 && blockIdx.y == 0) {
+    if (blockIdx.x == 0) {
       int32_t* sc = reinterpret_cast<int32_t*>(red);
       token_offsets_block<256>(k, T_, k_max, pol, tok_off, status, sc, sc + 8);
     }
     return;
   }
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, lg = lane >> 4;
-  const int e0 = blockIdx.x * TE, t0 = blockIdx.y * TT;
+  // expert tiles of a token tile next to each other (one grid dimension: no limit
+  // on the tokens)
+  const int ntile = (E + TE - 1) / TE;
+  const int e0 = (blockIdx.x % ntile) * TE, t0 = (blockIdx.x / ntile) * TT;
   const int steps = d / KS, nq = S * 4, q = blockIdx.z * 4 + wave;
   const int s0 = (int)((long long)steps * q / nq), s1 = (int)((long long)steps * (q + 1) / nq);
   const T* wr[ME];
@@ -238,7 +241,7 @@ static void launch_logits_f64_t(const T* x, const T* w, const int32_t* k, int T_
                                 hipStream_t st) {
 #define MOE_LF(ME, NT)                                                                                             \
   hipLaunchKernelGGL((logits_f64_kernel<T, ME, NT>),                                                               \
-                     dim3((E + 16 * ME - 1) / (16 * ME), max(1, (T_ + 16 * NT - 1) / (16 * NT)), S + 1), dim3(256), 0, \
+                     dim3(((E + 16 * ME - 1) / (16 * ME)) * ((T_ + 16 * NT - 1) / (16 * NT)), 1, S + 1), dim3(256), 0, \
                      st, x, w, T_, d, E, part, k, k_max, pol, tok_off, status)
   switch (T_ == 0 ? -1 : f64_tile(T_, E)) {
     case -1:  // the token scan alone
