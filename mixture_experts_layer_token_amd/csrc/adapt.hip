@@ -225,9 +225,12 @@ __global__ __launch_bounds__(1024) void adapt_shrink_kernel(AdaptArgs p, void* _
     v = c < ranks[r] ? v * scale[r] : 0.f;  // A behind the rank may be anything
     const size_t at = (size_t)blockIdx.x * AW * p.R + i;
     if constexpr (sizeof(T) == 2) {
-      const bf16_t hi = f32_to_bf16(v);
+      // a finite v behind bf16's largest value keeps it and leaves the rest to the
+      // remainder; an infinity has none (inf - inf is no number)
+      const bool finite = fabsf(v) < INFINITY;
+      const bf16_t hi = f32_to_bf16(finite ? fminf(fmaxf(v, -0x1.fep127f), 0x1.fep127f) : v);
       ((bf16_t*)vout)[at] = hi;
-      ((bf16_t*)vout)[(size_t)p.rows * p.R + at] = f32_to_bf16(v - bf16_to_f32(hi));
+      ((bf16_t*)vout)[(size_t)p.rows * p.R + at] = finite ? f32_to_bf16(v - bf16_to_f32(hi)) : (bf16_t)0;
     } else {
       ((float*)vout)[at] = v;
     }
@@ -250,7 +253,7 @@ __global__ __launch_bounds__(1024) void adapt_shrink_kernel(AdaptArgs p, void* _
 // fragments fit the registers (128 rows, 32 adapters: 21.2 -> 20.0 us a call with two
 // shares of a window's pairs; 1,150 permuted rows, 128 x 4 adapters: 27.5 -> 26.8).
 template <typename T, int NF, bool AHEAD>
-__global__ __launch_bounds__(256, NF == 1 && !AHEAD ? 4 : (NF <= 4 ? 2 : 1)) void adapt_expand_kernel(AdaptArgs p, const T* __restrict__ vin, int wpw) {
+__global__ __launch_bounds__(256, NF == 1 && !AHEAD ? 4 : (NF == 2 && !AHEAD ? 3 : (NF <= 4 ? 2 : 1))) void adapt_expand_kernel(AdaptArgs p, const T* __restrict__ vin, int wpw) {
   constexpr int LE = 16 / (int)sizeof(T);
   constexpr bool BF = sizeof(T) == 2;
   constexpr int YV = BF ? 2 : 4;                  // 16-byte pieces of a lane's 16 columns
@@ -398,6 +401,20 @@ __global__ __launch_bounds__(256, NF == 1 && !AHEAD ? 4 : (NF <= 4 ? 2 : 1)) voi
     // rows without an adapter are copied
     if (blockIdx.z == 0 && !inplace) served |= (uint32_t)__ballot(live && a < 0) & 0xffffu;
     if (!served) return;
+    // an infinity in B meets v's value and its remainder, which may be 0 or of the other
+    // sign: rows with a sum that is not finite are left to the end (where it is cheapest
+    // in registers: 4,096 rows, 2,048 -> 7,168: 52.7 -> 53.1 us a call with it)
+    uint32_t odd = 0;
+    if constexpr (BF) {
+      float zero = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) zero = fmaf(acc[j][e], 0.f, zero);
+      const uint64_t b = __ballot(zero != zero);
+      odd = (uint32_t)(b | (b >> 16) | (b >> 32) | (b >> 48)) & 0xffffu;
+      served &= ~odd;
+    }
     // acc[j][e]: column n0 + (bf16: 32 (j / 2) + 8 lg + 4 (j % 2), float: 16 j + 4 lg) + e of row l16
     u32x4_t o[YV];
     if constexpr (BF) {
@@ -435,6 +452,22 @@ __global__ __launch_bounds__(256, NF == 1 && !AHEAD ? 4 : (NF <= 4 ? 2 : 1)) voi
 #pragma unroll
     for (int i2 = 0; i2 < YV; ++i2)
       if (((served >> ar[i2]) & 1u) && cc[i2] < p.N) *reinterpret_cast<u32x4_t*>(ob + (uint32_t)(ar[i2] * p.N + cc[i2])) = o[i2];
+    // ... and summed from value and remainder together, a lane a column of the row
+    if constexpr (BF) {
+      for (; odd; odd &= odd - 1) {
+        const int r = __builtin_ctz(odd), n = n0 + lane, rk = __builtin_amdgcn_readlane(rank, r);
+        if (n >= p.N) continue;
+        const T* const bm = (const T*)p.b + (((size_t)__builtin_amdgcn_readlane(a, r) * p.G +
+                                              __builtin_amdgcn_readlane(g, r)) * p.N + n) * (size_t)p.R;
+        const T* const vr = vin + ((size_t)w * AW + r) * p.R;
+        float s = 0.f;
+#pragma unroll 1
+        for (int k = 0; k < rk; ++k)
+          s = fmaf(bf16_to_f32(vr[k]) + bf16_to_f32(vr[(size_t)p.rows * p.R + k]), bf16_to_f32(bm[k]), s);
+        const size_t at = ((size_t)w * AW + r) * p.N + n;
+        ((T*)p.out)[at] = f32_to_bf16(bf16_to_f32(((const T*)p.y)[at]) + s);
+      }
+    }
   };
   for (int w = w0; w < w1; w += D) {
 #pragma unroll

@@ -1,0 +1,60 @@
+"""Edges of the operators around the layer on the GPU.  Tolerances as in
+test_gpu_block.py."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests.test_gpu_block import DEV, DT, _adapt, _adapt_ref, _gen, _randn
+from workloads import to_f64
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------- adapters
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,N,R", [(16, 72, 8), (40, 264, 24), (33, 136, 64), (32, 200, 128), (9000, 1032, 16),
+                                   (9000, 1032, 128)])
+def test_adapt_products_that_are_infinite(dtype, T, N, R):
+    """An infinite or very large A x and infinite entries of B give what the
+    definition gives: infinities of the product's sign, NaN only where it has one."""
+    g = _gen(T + N)
+    dt, K = DT[dtype], 64
+    t = dict(x=_randn(g, T, K, dtype=dt), a=_randn(g, 3, 1, R, K, dtype=dt, std=K ** -0.5),
+             b=_randn(g, 3, 1, N, R, dtype=dt), ranks=torch.tensor([1, 1, R], dtype=torch.int32, device=DEV),
+             scales=torch.tensor([1.0, 0.5, -2.0], device=DEV),
+             adapter_ids=torch.full((T,), 2, dtype=torch.int32, device=DEV), row_tok=None, x_rows=None,
+             expert_off=None, y=_randn(g, T, N, dtype=dt))
+    for at in (0, T - 16):
+        ids, x = t["adapter_ids"][at:at + 16], t["x"][at:at + 16]
+        ids[:10] = 0
+        ids[10:12] = 1
+        x[0, 5], x[1, 5] = math.inf, -math.inf
+        # A x = 2^127 (2 - 2^-7) + 2^120 3/4: finite, above half a step behind bf16's largest value
+        x[2] = 0
+        x[2, 0], x[2, 1] = 2.0 ** 127 * (2 - 2.0 ** -7), 2.0 ** 120 * 0.75
+        x[3] = -x[2]
+        x[4], x[5] = 0, 0
+        x[4, 0] = 1.5                              # A x is a bf16 value: no remainder
+        x[5, 0], x[5, 1] = 1.0, 2.0 ** -8 * 1.75   # rounded up: a remainder of the other sign
+        x[6], x[7] = -x[5], 0
+        x[7, 0], x[7, 1] = 1.0, 2.0 ** -8 * 0.5
+    t["a"][0, 0, 0] = 0
+    t["a"][0, 0, 0, :2] = 1.0
+    t["a"][0, 0, 0, 5] = 0.25
+    t["b"][0, 0, :, 0] *= 2.0 ** -30
+    t["b"][0, 0, 3, 0], t["b"][0, 0, 4, 0], t["b"][0, 0, N - 1, 0] = math.inf, -math.inf, math.inf
+    t["b"][0, 0, 6, 0] = 0
+    t["b"][1, 0, 5, 0] = -math.inf
+    t["b"][2, 0, 7, R - 1], t["b"][2, 0, 9, 2] = math.inf, -math.inf
+    with np.errstate(invalid="ignore"):
+        ref, bound = _adapt_ref(t, dtype)
+    assert np.isnan(ref[0, 6]) and np.isposinf(ref[5, 3]) and np.isneginf(ref[6, 3]) and np.isfinite(ref[2, 0])
+    got = to_f64(_adapt(t, torch.empty_like(t["y"]), dtype, T))
+    sure = np.isfinite(ref)
+    np.testing.assert_array_equal(got[~sure], ref[~sure])
+    assert (np.abs(got[sure] - ref[sure]) <= bound[sure]).all()
+    y = t["y"].clone()
+    np.testing.assert_array_equal(to_f64(_adapt({**t, "y": y}, y, dtype, T)), got)
