@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_block import DEV, DT, _adapt, _adapt_ref, _gen, _randn
+from tests.test_gpu_block import DEV, DT, RULES, _adapt, _adapt_ref, _check_route, _gen, _randn
 from workloads import to_f64
 
 pytestmark = pytest.mark.gpu
@@ -58,3 +58,28 @@ def test_adapt_products_that_are_infinite(dtype, T, N, R):
     assert (np.abs(got[sure] - ref[sure]) <= bound[sure]).all()
     y = t["y"].clone()
     np.testing.assert_array_equal(to_f64(_adapt({**t, "y": y}, y, dtype, T)), got)
+
+
+# ------------------------------------------------------------ grouped routing
+
+@pytest.mark.parametrize("rule", [0, 1, 3])
+@pytest.mark.parametrize("xs,ws", [(0, 0), (-75, 58), (-80, 58), (58, -80), (-66, 0), (-110, 40)])
+def test_route_grouped_scales_at_the_ends_of_float32(rule, xs, ws):
+    """Tokens or router rows whose squares are below float32, with the others so
+    large that the products are not: equal experts are ordered by their exact logits all
+    the same."""
+    g = _gen(41)
+    T, d, E = 96, 512, 64
+    x, w = _randn(g, T, d, dtype=torch.bfloat16), _randn(g, E, d, dtype=torch.bfloat16)
+    # in each 64 values x reads the same from behind and w is its own negative from
+    # behind, so that these products add to 0 (and to float32 roundings); the small
+    # rest, eight in the middle, is the logit, the same for both experts of a pair
+    flip = torch.arange(d, device=DEV).view(-1, 64).flip(1).reshape(-1)
+    at = torch.arange(d, device=DEV) % 64
+    x, w = torch.where(at < 32, x, x[:, flip]), torch.where(at < 32, w, -w[:, flip])
+    rest = (at >= 28) & (at < 36)
+    w[:, rest] = _randn(g, E, d // 8, dtype=torch.bfloat16, std=2.0 ** -9)
+    w[E // 2:, rest] = w[:E // 2, rest]
+    x, w = x * 2.0 ** xs, w * 2.0 ** ws
+    k = torch.full((T,), 8, dtype=torch.int32, device=DEV)
+    _check_route(x, w, k, 8, router="screened", **RULES[rule])
