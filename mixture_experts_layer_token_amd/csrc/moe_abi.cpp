@@ -208,6 +208,19 @@ void plan_grouped(const moe_desc& d, Carver& c, GroupedWs& w) {
   w.wn = p ? w.xn + nx : nullptr;
 }
 
+// What moe_forward asks of its workspace: its own regions, and as much as folding
+// and path routing need (a caller may have stored this size).
+size_t forward_need(const moe_desc& d) {
+  Carver c(nullptr), f(nullptr), p(nullptr);
+  FwdWs w;
+  plan_forward(d, c, w);
+  FoldScratch fw;
+  plan_fold(d, f, fw);
+  PathWs pw;
+  plan_path(d, p, pw);
+  return std::max({c.total(), f.total(), p.total()});
+}
+
 size_t ws_size(const moe_desc& d, int op) {
   Carver c(nullptr);
   switch (op) {
@@ -218,18 +231,10 @@ size_t ws_size(const moe_desc& d, int op) {
     case MOE_OP_FOLD: { FoldScratch w; plan_fold(d, c, w); break; }
     case MOE_OP_PATH: { PathWs w; plan_path(d, c, w); break; }
     case MOE_OP_ROUTE_GROUPED: { GroupedWs w; plan_grouped(d, c, w); break; }
-    default: {  // the forward's own regions; large enough for every other op
-      FwdWs w;
-      plan_forward(d, c, w);
-      Carver f(nullptr), p(nullptr);
-      FoldScratch fw;
-      plan_fold(d, f, fw);
-      PathWs pw;
-      plan_path(d, p, pw);
-      Carver g(nullptr);
-      GroupedWs gw;
-      plan_grouped(d, g, gw);
-      return std::max({c.total(), f.total(), p.total(), g.total()});
+    default: {  // MOE_OP_FORWARD: large enough for every op
+      GroupedWs w;
+      plan_grouped(d, c, w);
+      return std::max(forward_need(d), c.total());
     }
   }
   return c.total();
@@ -246,12 +251,14 @@ moe_status launched(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_LA
     if (s_ != MOE_OK) return s_;                   \
   } while (0)
 
-moe_status check_ws(const moe_desc& d, int op, const void* ws, size_t ws_bytes) {
-  const size_t need = ws_size(d, op);
+moe_status check_ws_need(size_t need, const void* ws, size_t ws_bytes) {
   if (need == 0) return MOE_OK;
   if (!ws || ws_bytes < need) return MOE_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return MOE_ERR_ALIGN;
   return MOE_OK;
+}
+moe_status check_ws(const moe_desc& d, int op, const void* ws, size_t ws_bytes) {
+  return check_ws_need(ws_size(d, op), ws, ws_bytes);
 }
 
 moe_status path_ok(const moe_desc& d) {
@@ -937,7 +944,7 @@ moe_status forward_impl(const moe_desc* desc, const void* x, const void* w_route
     if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return MOE_ERR_ALIGN;
     if (forward_scratch_bytes(d) > ws_bytes) return MOE_ERR_SCRATCH;
   } else {
-    MOE_TRY(check_ws(d, MOE_OP_FORWARD, ws, ws_bytes));
+    MOE_TRY(check_ws_need(forward_need(d), ws, ws_bytes));
   }
   Carver c(ws);
   FwdWs fw;
