@@ -664,7 +664,9 @@ class BlockLayer:
     routing, the permutation, the expert FFN, per-request adapters on the experts'
     down projections (and on the always-on expert's), and the combine fused with
     the norm behind the block, its gate, the residual and the next norm.
-    ``run`` only launches (no allocation), so it can be captured in a graph."""
+    ``run`` only launches (no allocation), so it can be captured in a graph.  All of
+    its steps run on the layer's GPU, whichever is current, on ``stream`` or that
+    GPU's current stream; runs of one layer share its buffers and must not overlap."""
 
     def __init__(self, desc: moe_desc, rule: moe_route_rule, before: moe_norm_desc, behind: moe_norm_desc, *,
                  adapters: int = 0, shared_adapters: int = 0, rank: int = 16, device="cuda"):
@@ -709,6 +711,10 @@ class BlockLayer:
         if shared_adapters:
             self.adapt_shared = make_adapter_desc(T, T, desc.I_shared, d, rank, shared_adapters, 1, dtype=dtype)
             self.ws_adapt_sh = alloc_adapt_workspace(self.adapt_shared, device)
+        if self.x.is_cuda and not torch.cuda.is_current_stream_capturing():
+            # run's stream may be another: what is written here, and what still uses the
+            # memory that the buffers came from, is done before it
+            torch.cuda.current_stream(self.x.device).synchronize()
 
     def run(self, y, resid, pre_w, w_router, select_bias, k, w_gate, w_up, w_down, resid_out, x_out, *, shared=None,
             before_post_w=None, before_gate=None, behind_post_w=None, behind_gate=None, next_w=None, router_bias=None,
@@ -721,33 +727,41 @@ class BlockLayer:
             raise ValueError("the descriptor has a shared expert: pass its weights")
         if (adapters is None) != (self.adapt is None) or (shared_adapters is None) != (self.adapt_shared is None):
             raise ValueError("adapters: pass what the layer was made for")
-        moe_norm(self.before, y, resid, before_post_w, None, before_gate, pre_w, None,
-                 None if y is None else self.resid, self.x, stream)
-        mid = resid if y is None else self.resid
-        moe_route_grouped(d, self.rule, self.x, w_router, router_bias, select_bias, k, self.tok_off, self.ids, self.w,
-                          self.status, self.ws_route, stream)
-        moe_permute(d, self.tok_off, self.ids, self.counts, self.eoff, self.ptok, self.psrc, self.inv, self.nact,
-                    self.ws_perm, stream)
         sh = shared if shared is not None else (None, None, None)
-        if adapters is None and shared_adapters is None:
-            moe_ffn(d, self.x, w_gate, w_up, w_down, *sh, self.eoff, self.ptok, self.y, self.y_sh, self.ws_ffn, stream)
-        else:
-            h = self.h
-            moe_ffn_plan(d, self.eoff, self.ws_ffn, stream)
-            moe_ffn_gateup(d, self.x, w_gate, w_up, self.eoff, self.ptok, h, self.ws_ffn, stream)
-            moe_ffn_down(d, h, w_down, self.eoff, self.y, self.ws_ffn, stream)
-            if adapters is not None:
-                a, b, ranks, scales, ids = adapters
-                moe_adapt(self.adapt, h, None, a, b, ranks, scales, ids, self.ptok, self.eoff, self.y, self.y,
-                          self.ws_adapt, stream)
-            if d.I_shared:
-                moe_ffn_plan(self.sh, self.sh_eoff, self.ws_sh, stream)
-                moe_ffn_gateup(self.sh, self.x, sh[0], sh[1], self.sh_eoff, self.sh_tok, self.h_sh, self.ws_sh, stream)
-                moe_ffn_down(self.sh, self.h_sh, sh[2], self.sh_eoff, self.y_sh, self.ws_sh, stream)
-            if shared_adapters is not None:
-                a, b, ranks, scales, ids = shared_adapters
-                moe_adapt(self.adapt_shared, self.h_sh, None, a, b, ranks, scales, ids, None, None, self.y_sh,
-                          self.y_sh, self.ws_adapt_sh, stream)
-        moe_combine_norm(d, self.behind, self.y, self.y_sh, self.tok_off, self.w, self.inv, mid, behind_post_w, None,
-                         behind_gate, next_w, None, resid_out, x_out, stream)
+        device = self.x.device
+        for name, t in zip(("w_gate", "w_up", "w_down", "shared[0]", "shared[1]", "shared[2]"),
+                           (w_gate, w_up, w_down, *sh)):
+            if isinstance(t, torch.Tensor) and t.device != device:
+                raise ValueError(f"{name}: on {t.device}, the layer is on {device}")
+        with torch.cuda.device(device):
+            if stream is None:
+                stream = torch.cuda.current_stream(device)
+            moe_norm(self.before, y, resid, before_post_w, None, before_gate, pre_w, None,
+                     None if y is None else self.resid, self.x, stream)
+            mid = resid if y is None else self.resid
+            moe_route_grouped(d, self.rule, self.x, w_router, router_bias, select_bias, k, self.tok_off, self.ids, self.w,
+                              self.status, self.ws_route, stream)
+            moe_permute(d, self.tok_off, self.ids, self.counts, self.eoff, self.ptok, self.psrc, self.inv, self.nact,
+                        self.ws_perm, stream)
+            if adapters is None and shared_adapters is None:
+                moe_ffn(d, self.x, w_gate, w_up, w_down, *sh, self.eoff, self.ptok, self.y, self.y_sh, self.ws_ffn, stream)
+            else:
+                h = self.h
+                moe_ffn_plan(d, self.eoff, self.ws_ffn, stream)
+                moe_ffn_gateup(d, self.x, w_gate, w_up, self.eoff, self.ptok, h, self.ws_ffn, stream)
+                moe_ffn_down(d, h, w_down, self.eoff, self.y, self.ws_ffn, stream)
+                if adapters is not None:
+                    a, b, ranks, scales, ids = adapters
+                    moe_adapt(self.adapt, h, None, a, b, ranks, scales, ids, self.ptok, self.eoff, self.y, self.y,
+                              self.ws_adapt, stream)
+                if d.I_shared:
+                    moe_ffn_plan(self.sh, self.sh_eoff, self.ws_sh, stream)
+                    moe_ffn_gateup(self.sh, self.x, sh[0], sh[1], self.sh_eoff, self.sh_tok, self.h_sh, self.ws_sh, stream)
+                    moe_ffn_down(self.sh, self.h_sh, sh[2], self.sh_eoff, self.y_sh, self.ws_sh, stream)
+                if shared_adapters is not None:
+                    a, b, ranks, scales, ids = shared_adapters
+                    moe_adapt(self.adapt_shared, self.h_sh, None, a, b, ranks, scales, ids, None, None, self.y_sh,
+                              self.y_sh, self.ws_adapt_sh, stream)
+            moe_combine_norm(d, self.behind, self.y, self.y_sh, self.tok_off, self.w, self.inv, mid, behind_post_w, None,
+                             behind_gate, next_w, None, resid_out, x_out, stream)
         return resid_out, x_out

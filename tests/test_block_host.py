@@ -3,6 +3,7 @@ devices and streams.  No GPU needed: nothing is launched."""
 import ctypes
 
 import pytest
+import torch
 
 import mixture_experts_layer_token_amd as moe
 from mixture_experts_layer_token_amd import _lib
@@ -33,3 +34,65 @@ def test_forward_asks_for_no_more_than_it_uses(shape, need):
     assert call(need) == 5
     if need < sizes[moe.MOE_OP_FORWARD]:
         assert call(need - 256) == 4
+
+
+class _Devices:
+    """Stands in for torch.cuda's current device and streams, and for the steps of a
+    BlockLayer: notes the device that is current and the stream of each step."""
+
+    STEPS = ("moe_norm", "moe_route_grouped", "moe_permute", "moe_ffn", "moe_ffn_plan", "moe_ffn_gateup", "moe_ffn_down",
+             "moe_adapt", "moe_combine_norm")
+
+    def __init__(self, monkeypatch):
+        self.current, self.calls, outer = [], [], self
+
+        class device:
+            def __init__(self, d):
+                self.d = d
+
+            def __enter__(self):
+                outer.current.append(self.d)
+
+            def __exit__(self, *exc):
+                outer.current.pop()
+
+        monkeypatch.setattr(torch.cuda, "device", device)
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: ("stream", d))
+        for name in self.STEPS:
+            monkeypatch.setattr(moe, name, lambda *a, _n=name: self.calls.append((_n, a, list(self.current))))
+
+
+def _block(adapters=0, shared_adapters=0, T=6, d=128, **kw):
+    desc = moe.make_desc(T, d, 8, 128, 2, I_shared=128)
+    layer = moe.BlockLayer(desc, moe.make_route_rule(), moe.make_norm_desc(T, d), moe.make_norm_desc(T, d), rank=8,
+                           adapters=adapters, shared_adapters=shared_adapters, device="cpu")
+    z = torch.zeros(1)
+    ad = lambda n: (z,) * 5 if n else None
+    args = dict(y=z, resid=z, pre_w=z, w_router=z, select_bias=None, k=z, w_gate=z, w_up=z, w_down=z, resid_out=z, x_out=z,
+                shared=(z, z, z), adapters=ad(adapters), shared_adapters=ad(shared_adapters))
+    return layer, {**args, **kw}
+
+
+@pytest.mark.parametrize("adapters,shared_adapters", [(0, 0), (3, 0), (0, 2), (3, 2)])
+@pytest.mark.parametrize("stream", [None, "own"])
+def test_block_layer_runs_all_steps_on_one_device_and_stream(monkeypatch, adapters, shared_adapters, stream):
+    layer, args = _block(adapters, shared_adapters)
+    dev = _Devices(monkeypatch)
+    layer.run(**args, stream=stream)
+    here = layer.x.device
+    assert [c[0] for c in dev.calls[:3]] == ["moe_norm", "moe_route_grouped", "moe_permute"]
+    assert dev.calls[-1][0] == "moe_combine_norm"
+    for name, a, current in dev.calls:
+        assert a[-1] == (stream or ("stream", here)), name
+        assert current == [here], name
+
+
+@pytest.mark.parametrize("name", ["w_gate", "w_up", "w_down", "shared"])
+def test_block_layer_refuses_weights_elsewhere(monkeypatch, name):
+    layer, args = _block()
+    dev = _Devices(monkeypatch)
+    far = torch.zeros(1, device="meta")
+    args[name] = (args["w_up"], far, far) if name == "shared" else far
+    with pytest.raises(ValueError, match="on meta, the layer is on cpu"):
+        layer.run(**args)
+    assert not dev.calls

@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+import mixture_experts_layer_token_amd as moe
 from tests.test_gpu_block import DEV, DT, RULES, _adapt, _adapt_ref, _check_route, _gen, _randn
 from workloads import to_f64
 
@@ -83,3 +84,47 @@ def test_route_grouped_scales_at_the_ends_of_float32(rule, xs, ws):
     x, w = x * 2.0 ** xs, w * 2.0 ** ws
     k = torch.full((T,), 8, dtype=torch.int32, device=DEV)
     _check_route(x, w, k, 8, router="screened", **RULES[rule])
+
+
+# ----------------------------------------------------------------- BlockLayer
+
+def _block_case(g, T, d, E, I, Is, k_max, L, R):
+    bf = torch.bfloat16
+    stack = lambda G, K: (_randn(g, L, G, R, K, dtype=bf, std=K ** -0.5), _randn(g, L, G, d, R, dtype=bf, std=0.2), None,
+                          None, torch.randint(-1, L, (T,), generator=g, device=DEV, dtype=torch.int32))
+    return dict(y=_randn(g, T, d, dtype=bf), resid=_randn(g, T, d, dtype=bf), pre_w=_randn(g, d, dtype=bf),
+                w_router=_randn(g, E, d, dtype=bf, std=d ** -0.5), select_bias=None,
+                k=torch.randint(0, k_max + 1, (T,), generator=g, device=DEV, dtype=torch.int32),
+                w_gate=_randn(g, E, I, d, dtype=bf, std=d ** -0.5), w_up=_randn(g, E, I, d, dtype=bf, std=d ** -0.5),
+                w_down=_randn(g, E, d, I, dtype=bf, std=I ** -0.5),
+                shared=[_randn(g, Is, d, dtype=bf, std=d ** -0.5), _randn(g, Is, d, dtype=bf, std=d ** -0.5),
+                        _randn(g, d, Is, dtype=bf, std=Is ** -0.5)],
+                adapters=stack(E, I), shared_adapters=stack(1, Is))
+
+
+def test_block_layer_made_and_run_on_other_streams():
+    """A layer made on a busy stream and run on another, given or current, has what it
+    needs; the results are those of a layer made and run on the default stream."""
+    g = _gen(61)
+    T, d, E, I, Is, k_max, L, R = 700, 256, 16, 128, 256, 4, 3, 8
+    args = _block_case(g, T, d, E, I, Is, k_max, L, R)
+    make = lambda: moe.BlockLayer(moe.make_desc(T, d, E, I, k_max, I_shared=Is), moe.make_route_rule(),
+                                  moe.make_norm_desc(T, d), moe.make_norm_desc(T, d, post=True), adapters=L,
+                                  shared_adapters=L, rank=R, device=DEV)
+    out = lambda: [torch.zeros(T, d, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    want = make().run(**args, resid_out=(o := out())[0], x_out=o[1])
+    torch.cuda.synchronize()
+    busy, side = torch.cuda.Stream(), torch.cuda.Stream()
+    for given in (True, False):
+        got = out()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(busy):
+            torch.cuda._sleep(20_000_000)
+            layer = make()
+        if given:
+            layer.run(**args, resid_out=got[0], x_out=got[1], stream=side)
+        else:
+            with torch.cuda.stream(side):
+                layer.run(**args, resid_out=got[0], x_out=got[1])
+        side.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
