@@ -16,8 +16,8 @@
 // four rows of traffic a token, 29 us (4.6 TB/s; a copy of 2 GiB reaches 4.9), the
 // combine of 4,096 x 7,168 with k in {4, 8} 114 us (5.1 TB/s).  Few rows are bound
 // by latency: one row of 7,168 4.6 us, 128 rows behind their combine 10 us (offsets,
-// rows, two reductions, one after the other).  CH chunks a thread: as few as make
-// a row at most 512 threads (one wave with four chunks of 2,048 columns took 94 us
+// rows, two reductions, one after the other).  CH chunks a thread: as few as make a
+// row of up to 1,024 chunks at most 512 threads, a wider one at most 1,024 (one wave with four chunks of 2,048 columns took 94 us
 // where one chunk a thread takes 29, its loads waiting for one another).
 #include "common.h"
 #include "launch.h"
@@ -64,6 +64,12 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   __syncthreads();
   return s;
 }
+
+// The workgroup's row.  A launch holds less than 2^32 threads a dimension, so the
+// rows go on in y (2^21 rows of at most 1024 threads each).
+constexpr int ROWS_X = 1 << 21;
+__device__ __forceinline__ int block_row() { return (int)(blockIdx.y * gridDim.x + blockIdx.x); }
+dim3 row_grid(int T) { return dim3(min(T, ROWS_X), (T - 1) / ROWS_X + 1); }
 
 }  // namespace
 
@@ -222,11 +228,12 @@ __device__ __forceinline__ void norm_chain(float (&v)[CH][16 / sizeof(T)], const
 }
 
 template <typename T, int CH, bool VEC>
-__global__ __launch_bounds__(CH <= 2 ? 512 : 1024) void norm_kernel(const T* y, NormRow n) {
+__global__ __launch_bounds__(CH <= 2 ? 512 : 1024) void norm_kernel(const T* y, NormRow n, int T_) {
   constexpr int LE = 16 / (int)sizeof(T);
   __shared__ float red[16];
   const RowIo<T, CH, VEC> io{n.d};
-  const int t = blockIdx.x;
+  const int t = block_row();
+  if (t >= T_) return;
   float v[CH][LE];
   typename RowIo<T, CH, VEC>::Part yp;
   RowParts<T, CH, VEC, (CH <= 2)> o;
@@ -246,11 +253,13 @@ template <typename T, int CH, int CBN>
 __global__ __launch_bounds__(CH <= 2 ? 512 : 1024) void combine_norm_kernel(const T* __restrict__ yp, const T* __restrict__ ysh,
                                                             const int32_t* __restrict__ tok_off,
                                                             const float* __restrict__ wts,
-                                                            const int32_t* __restrict__ inv_perm, int cap, NormRow n) {
+                                                            const int32_t* __restrict__ inv_perm, int cap, NormRow n,
+                                                            int T_) {
   constexpr int LE = 16 / (int)sizeof(T);
   __shared__ float red[16];
   const RowIo<T, CH, true> io{n.d};
-  const int t = blockIdx.x;
+  const int t = block_row();
+  if (t >= T_) return;
   const int a0 = max(tok_off[t], 0), a1 = min(tok_off[t + 1], cap);
   // resid is read past the caches like the rows of Y; with y_shared read so as well
   // the call is slower (4,096 x 7,168, k in {4, 8}: 114 against 119 us)
@@ -312,8 +321,10 @@ static void launch_norm_t(const T* y, const NormRow& n, int T_, hipStream_t st) 
   const bool vec = n.d % LE == 0;
 #define MOE_NORM(CH)                                                                                              \
   do {                                                                                                            \
-    if (vec) hipLaunchKernelGGL((norm_kernel<T, CH, true>), dim3(T_), dim3(row_threads(nch, CH)), 0, st, y, n);   \
-    else hipLaunchKernelGGL((norm_kernel<T, CH, false>), dim3(T_), dim3(row_threads(nch, CH)), 0, st, y, n);      \
+    if (vec)                                                                                                      \
+      hipLaunchKernelGGL((norm_kernel<T, CH, true>), row_grid(T_), dim3(row_threads(nch, CH)), 0, st, y, n, T_);  \
+    else                                                                                                          \
+      hipLaunchKernelGGL((norm_kernel<T, CH, false>), row_grid(T_), dim3(row_threads(nch, CH)), 0, st, y, n, T_); \
   } while (0)
   if (nch <= 512) MOE_NORM(1);
   else if (nch <= 1024) MOE_NORM(2);
@@ -336,8 +347,8 @@ static void launch_combine_norm_t(const T* yp, const T* ysh, const int32_t* tok_
   constexpr int LE = 16 / (int)sizeof(T);
   const int nch = n.d / LE;
 #define MOE_CNORM(CH, CBN)                                                                                          \
-  hipLaunchKernelGGL((combine_norm_kernel<T, CH, CBN>), dim3(T_), dim3(row_threads(nch, CH)), 0, st, yp, ysh, tok_off, \
-                     wts, inv_perm, cap, n)
+  hipLaunchKernelGGL((combine_norm_kernel<T, CH, CBN>), row_grid(T_), dim3(row_threads(nch, CH)), 0, st, yp, ysh,     \
+                     tok_off, wts, inv_perm, cap, n, T_)
   if (nch <= 512) MOE_CNORM(1, 8);
   else if (nch <= 1024) MOE_CNORM(2, 8);
   else if (nch <= 4096) MOE_CNORM(4, 4);

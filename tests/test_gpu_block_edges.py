@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import mixture_experts_layer_token_amd as moe
-from tests.test_gpu_block import DEV, DT, RULES, _adapt, _adapt_ref, _check_route, _gen, _randn
+from tests.test_gpu_block import DEV, DT, EPS, RULES, U, _adapt, _adapt_ref, _check_route, _gen, _randn
 from workloads import to_f64
 
 pytestmark = pytest.mark.gpu
@@ -84,6 +84,41 @@ def test_route_grouped_scales_at_the_ends_of_float32(rule, xs, ws):
     x, w = x * 2.0 ** xs, w * 2.0 ** ws
     k = torch.full((T,), 8, dtype=torch.int32, device=DEV)
     _check_route(x, w, k, 8, router="screened", **RULES[rule])
+
+
+# ---------------------------------------- more rows than one grid dimension holds
+
+MANY = 2 ** 26 + 3  # workgroups of 64 threads: 2^32 threads and some
+
+
+def test_norm_of_many_rows():
+    y = torch.empty(MANY, 8, dtype=torch.bfloat16, device=DEV)
+    y.normal_(generator=_gen(51))
+    w = _randn(_gen(52), 8, dtype=torch.bfloat16)
+    x = torch.full_like(y, 7.0)
+    moe.moe_norm(moe.make_norm_desc(MANY, 8), None, y, None, None, None, w, None, None, x)
+    for lo in range(0, MANY, 1 << 24):
+        v = y[lo:lo + (1 << 24)].double()
+        ref = v * torch.rsqrt((v * v).mean(1, keepdim=True) + 1e-6) * w.double()
+        # 24 roundings on any path of eight values, the rounding to bf16
+        bound = ref.abs() * (24 * EPS + U["bf16"] * 1.01) + 1e-40
+        assert ((x[lo:lo + (1 << 24)].double() - ref).abs() <= bound).all()
+
+
+def test_combine_norm_of_many_rows():
+    T, d = MANY, 128
+    yp = torch.empty(T, d, dtype=torch.bfloat16, device=DEV)
+    yp.normal_(generator=_gen(53))
+    off = torch.arange(T + 1, dtype=torch.int32, device=DEV)
+    inv = torch.arange(T, dtype=torch.int32, device=DEV).flip(0).contiguous()
+    wts = torch.rand(T, generator=_gen(54), device=DEV)
+    r = torch.full_like(yp, 7.0)
+    moe.moe_combine_norm(moe.make_desc(T, d, 1, 128, 1), moe.make_norm_desc(T, d), yp, None, off, wts, inv, None, None,
+                         None, None, None, None, r, None)
+    for lo in range(0, T, 1 << 22):
+        n = min(1 << 22, T - lo)
+        ref = wts[lo:lo + n, None].double() * yp[T - lo - n:T - lo].flip(0).double()
+        assert ((r[lo:lo + n].double() - ref).abs() <= ref.abs() * (2 * EPS + U["bf16"] * 1.01) + 1e-40).all()
 
 
 # ----------------------------------------------------------------- BlockLayer
