@@ -190,7 +190,9 @@ struct GroupedWs { double* part; int splits; float *approx, *xn, *wn; int tile_s
 // AUTO takes the latter from T * E * d = 3 * 2^28 on (us a call, float64 against bf16:
 // 7168 x 256 experts, 256 tokens 37 / 52, 512 tokens 62 / 59, 1,024 tokens 91 / 59;
 // 2048 x 512, 512 tokens 46 / 51, 1,024 tokens 64 / 51; 4096 x 64, 2,048 tokens 37 / 38).
+// Its grid holds 2^28 tokens; larger batches take float64.
 bool grouped_tile(const moe_desc& d) {
+  if (d.T > 1 << 28) return false;
   if (d.router == MOE_ROUTER_SCREENED) return true;
   return d.router == MOE_ROUTER_AUTO && d.dtype == MOE_BF16 && (double)d.T * d.E * d.d >= 805306368.0;
 }

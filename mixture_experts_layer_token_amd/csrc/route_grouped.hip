@@ -20,6 +20,12 @@ namespace moe {
 
 namespace {
 
+// Workgroups of at most 256 threads in x and, behind 2^23 of them, in y: a launch
+// holds less than 2^32 threads a dimension.
+constexpr int BLOCKS_X = 1 << 23;
+dim3 grid_of(int blocks, int z = 1) { return dim3(min(blocks, BLOCKS_X), (blocks - 1) / BLOCKS_X + 1, z); }
+__device__ __forceinline__ int grid_block() { return (int)(blockIdx.y * gridDim.x + blockIdx.x); }
+
 // Order-preserving image of a float64 key; 0 marks an expert that cannot be
 // chosen (out of service, or in a group that is not kept).
 __device__ __forceinline__ uint64_t score_key(double c) {
@@ -150,17 +156,17 @@ __global__ __launch_bounds__(256) void logits_f64_kernel(const T* __restrict__ x
   __shared__ double red[4 * TT * LD];
   const int S = gridDim.z - 1;
   if ((int)blockIdx.z == S) {
-    if (blockIdx.x == 0) {
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
       int32_t* sc = reinterpret_cast<int32_t*>(red);
       token_offsets_block<256>(k, T_, k_max, pol, tok_off, status, sc, sc + 8);
     }
     return;
   }
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, lg = lane >> 4;
-  // expert tiles of a token tile next to each other (one grid dimension: no limit
-  // on the tokens)
-  const int ntile = (E + TE - 1) / TE;
-  const int e0 = (blockIdx.x % ntile) * TE, t0 = (blockIdx.x / ntile) * TT;
+  // expert tiles of a token tile next to each other
+  const int ntile = (E + TE - 1) / TE, tile = grid_block();
+  const int e0 = (tile % ntile) * TE, t0 = (tile / ntile) * TT;
+  if (t0 >= T_) return;  // the same for the whole workgroup
   const int steps = d / KS, nq = S * 4, q = blockIdx.z * 4 + wave;
   const int s0 = (int)((long long)steps * q / nq), s1 = (int)((long long)steps * (q + 1) / nq);
   const T* wr[ME];
@@ -241,7 +247,7 @@ static void launch_logits_f64_t(const T* x, const T* w, const int32_t* k, int T_
                                 hipStream_t st) {
 #define MOE_LF(ME, NT)                                                                                             \
   hipLaunchKernelGGL((logits_f64_kernel<T, ME, NT>),                                                               \
-                     dim3(((E + 16 * ME - 1) / (16 * ME)) * ((T_ + 16 * NT - 1) / (16 * NT)), 1, S + 1), dim3(256), 0, \
+                     grid_of(((E + 16 * ME - 1) / (16 * ME)) * ((T_ + 16 * NT - 1) / (16 * NT)), S + 1), dim3(256), 0,  \
                      st, x, w, T_, d, E, part, k, k_max, pol, tok_off, status)
   switch (T_ == 0 ? -1 : f64_tile(T_, E)) {
     case -1:  // the token scan alone
@@ -848,7 +854,7 @@ __global__ __launch_bounds__(256, KPL <= 4 ? 4 : 1) void route_grouped_kernel(co
   extern __shared__ uint64_t rg_lds[];
   // wv is uniform: with it in a scalar register so are the token and its addresses
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int t = blockIdx.x * (blockDim.x >> 6) + wv;
+  const int t = grid_block() * (int)(blockDim.x >> 6) + wv;
   if (t >= T_) return;
   uint64_t* const lds = rg_lds + (size_t)wv * rg_words(E, SCREEN);
   double* const ls = reinterpret_cast<double*>(lds + E);
@@ -1013,7 +1019,7 @@ static hipError_t launch_rg(const double* part, int S, const ScreenIn& in, const
   // waves of a workgroup: as many as 64 KB of LDS hold, at most four
   const size_t per = (size_t)rg_words(E, SCREEN) * sizeof(uint64_t);
   const int nw = (int)max((size_t)1, min((size_t)4, (size_t)65536 / per));
-  const dim3 grid((T + nw - 1) / nw);
+  const dim3 grid = grid_of((T + nw - 1) / nw);
 #define MOE_RG(KPL)                                                                                               \
   hipLaunchKernelGGL((route_grouped_kernel<KPL, SCREEN>), grid, dim3(64 * nw), per * nw, st, part, S, in, bias,   \
                      sel_bias, tok_off, T, E, rule, scale, ids, wts)

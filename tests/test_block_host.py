@@ -96,3 +96,10 @@ def test_block_layer_refuses_weights_elsewhere(monkeypatch, name):
     with pytest.raises(ValueError, match="on meta, the layer is on cpu"):
         layer.run(**args)
     assert not dev.calls
+
+
+def test_grouped_routing_of_more_tokens_than_the_screened_grid_holds():
+    size = lambda T, router: _size(moe.make_desc(T, 128, 2, 128, 1, router=router), moe.MOE_OP_ROUTE_GROUPED)
+    # the tile kernel adds the squared norms to half the bytes of float64 slices
+    T = (1 << 28) + 64
+    assert size(T, "screened") == size(T, "float64") == T * 2 * 8

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import mixture_experts_layer_token_amd as moe
-from tests.test_gpu_block import DEV, DT, EPS, RULES, U, _adapt, _adapt_ref, _check_route, _gen, _randn
+from tests.test_gpu_block import DEV, DT, EPS, RULES, U, _adapt, _adapt_ref, _check_route, _gen, _randn, _route
 from workloads import to_f64
 
 pytestmark = pytest.mark.gpu
@@ -119,6 +119,31 @@ def test_combine_norm_of_many_rows():
         n = min(1 << 22, T - lo)
         ref = wts[lo:lo + n, None].double() * yp[T - lo - n:T - lo].flip(0).double()
         assert ((r[lo:lo + n].double() - ref).abs() <= ref.abs() * (2 * EPS + U["bf16"] * 1.01) + 1e-40).all()
+
+
+@pytest.mark.parametrize("router", ["float64", "screened"])
+def test_route_grouped_of_many_tokens(router):
+    T, d, E = MANY, 128, 8
+    x = torch.empty(T, d, dtype=torch.bfloat16, device=DEV)
+    x.normal_(generator=_gen(55))
+    w = _randn(_gen(56), E, d, dtype=torch.bfloat16, std=d ** -0.5)
+    k = torch.ones(T, dtype=torch.int32, device=DEV)
+    desc = moe.make_desc(T, d, E, 128, 1, router=router)
+    off = torch.empty(T + 1, dtype=torch.int32, device=DEV)
+    ids = torch.full((T,), -7, dtype=torch.int32, device=DEV)
+    wts = torch.full((T,), -7.0, device=DEV)
+    st = torch.empty(1, dtype=torch.int32, device=DEV)
+    rule = moe.make_route_rule(renorm=False)
+    moe.moe_route_grouped(desc, rule, x, w, None, None, k, off, ids, wts, st,
+                          moe.alloc_workspace(desc, moe.MOE_OP_ROUTE_GROUPED, DEV))
+    assert torch.equal(off, torch.arange(T + 1, dtype=torch.int32, device=DEV)) and int(st) == 0
+    assert int(ids.min()) >= 0 and int(ids.max()) < E
+    for lo in (0, 2 ** 25 - 50, 2 ** 26 - 50, T - 100):
+        part = x[lo:lo + 100].contiguous()
+        _, want, ww, _ = _route(part, w, k[:100], 1, rule, router="float64")
+        np.testing.assert_array_equal(ids[lo:lo + 100].cpu().numpy(), want)
+        # |x| |w| is below 14 * 1.5: radius 1.7e-4, twice
+        np.testing.assert_allclose(to_f64(wts[lo:lo + 100]), ww, rtol=4e-4)
 
 
 # ----------------------------------------------------------------- BlockLayer
