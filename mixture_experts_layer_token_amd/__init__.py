@@ -718,8 +718,11 @@ class BlockLayer:
 
     def run(self, y, resid, pre_w, w_router, select_bias, k, w_gate, w_up, w_down, resid_out, x_out, *, shared=None,
             before_post_w=None, before_gate=None, behind_post_w=None, behind_gate=None, next_w=None, router_bias=None,
-            adapters=None, shared_adapters=None, stream=None):
+            adapters=None, shared_adapters=None, stream=None, before_post_b=None, pre_b=None, behind_post_b=None,
+            next_b=None):
         """y: the attention block's output (None: resid is normed as it is).
+        *_w, *_b: weight and bias of the norm of y, the norm before the block (pre), the
+        norm behind it and the next block's (next), each None for none.
         adapters: (a, b, ranks, scales, adapter_ids) of moe_adapt with a [L, E, R, I]
         and b [L, E, d, R]; shared_adapters the same with one expert."""
         d = self.desc
@@ -736,7 +739,7 @@ class BlockLayer:
         with torch.cuda.device(device):
             if stream is None:
                 stream = torch.cuda.current_stream(device)
-            moe_norm(self.before, y, resid, before_post_w, None, before_gate, pre_w, None,
+            moe_norm(self.before, y, resid, before_post_w, before_post_b, before_gate, pre_w, pre_b,
                      None if y is None else self.resid, self.x, stream)
             mid = resid if y is None else self.resid
             moe_route_grouped(d, self.rule, self.x, w_router, router_bias, select_bias, k, self.tok_off, self.ids, self.w,
@@ -762,6 +765,6 @@ class BlockLayer:
                     a, b, ranks, scales, ids = shared_adapters
                     moe_adapt(self.adapt_shared, self.h_sh, None, a, b, ranks, scales, ids, None, None, self.y_sh,
                               self.y_sh, self.ws_adapt_sh, stream)
-            moe_combine_norm(d, self.behind, self.y, self.y_sh, self.tok_off, self.w, self.inv, mid, behind_post_w, None,
-                             behind_gate, next_w, None, resid_out, x_out, stream)
+            moe_combine_norm(d, self.behind, self.y, self.y_sh, self.tok_off, self.w, self.inv, mid, behind_post_w,
+                             behind_post_b, behind_gate, next_w, next_b, resid_out, x_out, stream)
         return resid_out, x_out

@@ -87,6 +87,15 @@ def test_block_layer_runs_all_steps_on_one_device_and_stream(monkeypatch, adapte
         assert current == [here], name
 
 
+def test_block_layer_passes_norm_biases(monkeypatch):
+    layer, args = _block()
+    dev = _Devices(monkeypatch)
+    layer.run(**args, before_post_w="w0", before_post_b="b0", pre_b="b1", behind_post_w="w2", behind_post_b="b2",
+              next_w="w3", next_b="b3")
+    assert dev.calls[0][1][3:8] == ("w0", "b0", None, args["pre_w"], "b1")
+    assert dev.calls[-1][1][8:13] == ("w2", "b2", None, "w3", "b3")
+
+
 @pytest.mark.parametrize("name", ["w_gate", "w_up", "w_down", "shared"])
 def test_block_layer_refuses_weights_elsewhere(monkeypatch, name):
     layer, args = _block()

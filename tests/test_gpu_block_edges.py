@@ -188,3 +188,26 @@ def test_block_layer_made_and_run_on_other_streams():
                 layer.run(**args, resid_out=got[0], x_out=got[1])
         side.synchronize()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_block_layer_with_layer_norms_and_biases():
+    """Weights and biases of all four norms reach their step: the layer's buffers and
+    outputs have the bits of the single calls on the same inputs."""
+    g = _gen(62)
+    T, d, E, I, k_max = 50, 256, 8, 128, 3
+    args = {**_block_case(g, T, d, E, I, 128, k_max, 1, 8), "shared": None, "adapters": None, "shared_adapters": None}
+    desc = moe.make_desc(T, d, E, I, k_max)
+    before = moe.make_norm_desc(T, d, kind="layer", post=True, gate="token")
+    behind = moe.make_norm_desc(T, d, kind="layer", post=True, gate="channel", alpha=0.5)
+    layer = moe.BlockLayer(desc, moe.make_route_rule(), before, behind, device=DEV)
+    vec = {n: _randn(g, d, dtype=torch.bfloat16) for n in (
+        "pre_w", "pre_b", "before_post_w", "before_post_b", "behind_post_w", "behind_post_b", "next_w", "next_b")}
+    g1, g2 = _randn(g, T, dtype=torch.bfloat16), _randn(g, d, dtype=torch.bfloat16)
+    r, x, r1, x1 = (torch.zeros(T, d, dtype=torch.bfloat16, device=DEV) for _ in range(4))
+    layer.run(**{**args, **vec}, before_gate=g1, behind_gate=g2, resid_out=r, x_out=x)
+    moe.moe_norm(before, args["y"], args["resid"], vec["before_post_w"], vec["before_post_b"], g1, vec["pre_w"],
+                 vec["pre_b"], r1, x1)
+    assert torch.equal(layer.resid, r1) and torch.equal(layer.x, x1)
+    moe.moe_combine_norm(desc, behind, layer.y, None, layer.tok_off, layer.w, layer.inv, layer.resid, vec["behind_post_w"],
+                         vec["behind_post_b"], g2, vec["next_w"], vec["next_b"], r1, x1)
+    assert torch.equal(r, r1) and torch.equal(x, x1)
