@@ -674,6 +674,9 @@ class BlockLayer:
         T, d, E, I, km = desc.T, desc.d, desc.E, desc.I, desc.k_max
         if shared_adapters and not desc.I_shared:
             raise ValueError("shared_adapters: the descriptor has no shared expert")
+        for name, nd in (("before", before), ("behind", behind)):
+            if (nd.T, nd.d, nd.dtype) != (desc.T, desc.d, desc.dtype):
+                raise ValueError(f"{name}: its T, d and dtype must be the layer's")
         dtype = _ELT[desc.dtype]
         i32 = dict(dtype=torch.int32, device=device)
         A = max(T * km, 1)

@@ -112,3 +112,14 @@ def test_grouped_routing_of_more_tokens_than_the_screened_grid_holds():
     # the tile kernel adds the squared norms to half the bytes of float64 slices
     T = (1 << 28) + 64
     assert size(T, "screened") == size(T, "float64") == T * 2 * 8
+
+
+@pytest.mark.parametrize("which", ["before", "behind"])
+@pytest.mark.parametrize("kw", [dict(T=5), dict(T=7), dict(d=256), dict(dtype=torch.float32)])
+def test_block_layer_refuses_norms_of_other_shapes(which, kw):
+    """Fewer rows in the norm before the block would leave the rest of its input as it was."""
+    shape = dict(T=6, d=128, dtype=torch.bfloat16)
+    nd = {"before": moe.make_norm_desc(**shape), "behind": moe.make_norm_desc(**shape)}
+    nd[which] = moe.make_norm_desc(**{**shape, **kw})
+    with pytest.raises(ValueError, match=which):
+        moe.BlockLayer(moe.make_desc(6, 128, 8, 128, 2), moe.make_route_rule(), nd["before"], nd["behind"], device="cpu")
