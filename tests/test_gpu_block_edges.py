@@ -1,5 +1,6 @@
 """Edges of the operators around the layer on the GPU.  Tolerances as in
-test_gpu_block.py."""
+test_gpu_block.py.  AUTO takes the screened routing of bf16 batches from T * E * d =
+3 * 2^28 on."""
 import math
 
 import numpy as np
@@ -84,6 +85,79 @@ def test_route_grouped_scales_at_the_ends_of_float32(rule, xs, ws):
     x, w = x * 2.0 ** xs, w * 2.0 ** ws
     k = torch.full((T,), 8, dtype=torch.int32, device=DEV)
     _check_route(x, w, k, 8, router="screened", **RULES[rule])
+
+
+def _wide_tokens(g, T, d, E):
+    """Ordinary tokens, tokens of a norm in the thousands whose logits stay small (the
+    large part meets pairs w, -w), and tokens of a norm that saturates the scores."""
+    x, w = _randn(g, T, d, dtype=torch.bfloat16), _randn(g, E, d, dtype=torch.bfloat16, std=(d // 2) ** -0.5)
+    w[:, 1:d // 2:2] = -w[:, 0:d // 2:2]
+    x[:, 1:d // 2:2] = x[:, 0:d // 2:2]
+    x[1::4, :d // 2] *= 2.0 ** 10
+    x[2::8] *= 2.0 ** 9
+    w[E // 3] = w[0]
+    w[E // 2] = w[2]
+    w[E // 2, d - 1] *= 1 + 2.0 ** -7
+    return x, w
+
+
+@pytest.mark.parametrize("rule", range(len(RULES)))
+@pytest.mark.parametrize("T,d,E", [(70, 2048, 256), (37, 1024, 40), (21, 2048, 320), (19, 1024, 1024), (65, 4096, 128)])
+def test_route_grouped_every_logit_exact(rule, T, d, E):
+    """Tokens whose logits are too uncertain to screen (|x| |w| 8e-6 > 1/16) between
+    ordinary ones."""
+    g = _gen(T + E)
+    x, w = _wide_tokens(g, T, d, E)
+    radius = 66 * 2.0 ** -23 * torch.linalg.vector_norm(x.double(), dim=1) * torch.linalg.vector_norm(w.double(), dim=1).max()
+    assert (radius > 0.1).sum() >= T // 4 and (radius < 0.03).sum() >= T // 2
+    k = torch.randint(0, 6, (T,), generator=g, device=DEV, dtype=torch.int32)
+    sb = None if RULES[rule]["score"] == "softmax" else (torch.rand(E, generator=g, device=DEV) - 0.5) * 0.1
+    _check_route(x, w, k, 5, sb=sb, scale=2.5, router="screened", **RULES[rule])
+    # every logit exact for a -inf router bias too
+    rb = torch.zeros(E, device=DEV)
+    rb[E // 4], rb[E - 1] = -math.inf, -math.inf
+    _check_route(x, w, k, 5, sb=sb, rb=rb, router="screened", **RULES[rule])
+
+
+@pytest.mark.parametrize("rule", range(len(RULES)))
+@pytest.mark.parametrize("E", [64, 256, 320, 1024])
+def test_route_grouped_screened_values_that_are_no_numbers(rule, E):
+    """bf16 tokens and router rows with NaN or infinities: the screened router's ids are
+    the float64 one's, and ordinary tokens keep theirs."""
+    g = _gen(E)
+    T, d = 40, 512
+    x, w = _randn(g, T, d, dtype=torch.bfloat16), _randn(g, E, d, dtype=torch.bfloat16, std=d ** -0.5)
+    k = torch.full((T,), 5, dtype=torch.int32, device=DEV)
+    x[3, 9], x[8, 500], x[13, 0], x[13, 1] = math.nan, math.inf, math.inf, -math.inf
+    x[20] = math.inf
+    x[30, 4] = 3.3e38
+    for bad_row in (False, True):
+        if bad_row:
+            w[5, 7], w[E - 2, 8] = math.nan, math.inf
+        a, b = (_route(x, w, k, 5, moe.make_route_rule(**RULES[rule]), scale=2.5, router=r) for r in ("float64", "screened"))
+        np.testing.assert_array_equal(a[0], b[0])
+        np.testing.assert_array_equal(a[1], b[1])
+        # radius of the ordinary tokens: 8e-6 * 23 * 1.3, twice, and both sides' roundings
+        np.testing.assert_allclose(a[2], b[2], rtol=6e-4, atol=1e-38)
+        assert (b[1][15:20] == -1).all()  # a NaN in the token leaves no score a number
+
+
+@pytest.mark.parametrize("dtype,T,d,E,router,bias,rule", [
+    ("f32", 4099, 256, 250, "auto", True, 4), ("f32", 2113, 384, 264, "auto", False, 2),
+    ("bf16", 2100, 256, 272, "float64", True, 0), ("bf16", 4099, 1024, 256, "auto", True, 3),
+    ("bf16", 1090, 768, 1000, "float64", False, 1), ("f32", 16385, 128, 8, "float64", True, 1)])
+def test_route_grouped_large_batches_in_float64(dtype, T, d, E, router, bias, rule):
+    """The 32 x 64 tiles of the float64 logits (from 256 tiles on), at sizes off the tile."""
+    g = _gen(T + E)
+    rule = (RULES + [dict(score="sigmoid", n_group=5, topk_group=2, group_score="top2", renorm=True)])[rule]
+    assert -(-T // 64) * -(-E // 32) >= 256
+    x, w = _randn(g, T, d, dtype=DT[dtype]), _randn(g, E, d, dtype=DT[dtype], std=d ** -0.5)
+    w[E // 3], w[E - 1] = w[0], w[2]
+    k = torch.randint(0, 7, (T,), generator=g, device=DEV, dtype=torch.int32)
+    sb = (torch.rand(E, generator=g, device=DEV) - 0.5) * 0.1 if bias else None
+    if bias:
+        sb[1] = -math.inf
+    _check_route(x, w, k, 6, sb=sb, scale=2.5, router=router, **rule)
 
 
 # ---------------------------------------- more rows than one grid dimension holds
