@@ -17,10 +17,15 @@
 // combine of 4,096 x 7,168 with k in {4, 8} 114 us (5.1 TB/s).  Few rows are bound
 // by latency: one row of 7,168 4.6 us, 128 rows behind their combine 10 us (offsets,
 // rows, two reductions, one after the other).  CH chunks a thread: as few as make a
-// row of up to 1,024 chunks at most 512 threads, a wider one at most 1,024 (one wave with four chunks of 2,048 columns took 94 us
-// where one chunk a thread takes 29, its loads waiting for one another).
+// row of up to 1,024 chunks at most 512 threads, a wider one at most 1,024 (one wave
+// with four chunks of 2,048 columns took 94 us where one chunk a thread takes 29, its
+// loads waiting for one another).  Eight and sixteen chunks (rows of more than 32,768
+// bf16, 16,384 float32) do not fit the registers of 1,024 threads and spill: 512 rows
+// of 65,536 bf16 213 us, a quarter of the copy's rate.
 #include "common.h"
 #include "launch.h"
+
+#include <type_traits>
 
 namespace moe {
 
@@ -64,12 +69,6 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   __syncthreads();
   return s;
 }
-
-// The workgroup's row.  A launch holds less than 2^32 threads a dimension, so the
-// rows go on in y (2^21 rows of at most 1024 threads each).
-constexpr int ROWS_X = 1 << 21;
-__device__ __forceinline__ int block_row() { return (int)(blockIdx.y * gridDim.x + blockIdx.x); }
-dim3 row_grid(int T) { return dim3(min(T, ROWS_X), (T - 1) / ROWS_X + 1); }
 
 }  // namespace
 
@@ -228,12 +227,11 @@ __device__ __forceinline__ void norm_chain(float (&v)[CH][16 / sizeof(T)], const
 }
 
 template <typename T, int CH, bool VEC>
-__global__ __launch_bounds__(CH <= 2 ? 512 : 1024) void norm_kernel(const T* y, NormRow n, int T_) {
+__global__ __launch_bounds__(CH <= 2 ? 512 : 1024) void norm_kernel(const T* y, NormRow n) {
   constexpr int LE = 16 / (int)sizeof(T);
   __shared__ float red[16];
   const RowIo<T, CH, VEC> io{n.d};
-  const int t = block_row();
-  if (t >= T_) return;
+  const int t = blockIdx.x;
   float v[CH][LE];
   typename RowIo<T, CH, VEC>::Part yp;
   RowParts<T, CH, VEC, (CH <= 2)> o;
@@ -253,13 +251,11 @@ template <typename T, int CH, int CBN>
 __global__ __launch_bounds__(CH <= 2 ? 512 : 1024) void combine_norm_kernel(const T* __restrict__ yp, const T* __restrict__ ysh,
                                                             const int32_t* __restrict__ tok_off,
                                                             const float* __restrict__ wts,
-                                                            const int32_t* __restrict__ inv_perm, int cap, NormRow n,
-                                                            int T_) {
+                                                            const int32_t* __restrict__ inv_perm, int cap, NormRow n) {
   constexpr int LE = 16 / (int)sizeof(T);
   __shared__ float red[16];
   const RowIo<T, CH, true> io{n.d};
-  const int t = block_row();
-  if (t >= T_) return;
+  const int t = blockIdx.x;
   const int a0 = max(tok_off[t], 0), a1 = min(tok_off[t + 1], cap);
   // resid is read past the caches like the rows of Y; with y_shared read so as well
   // the call is slower (4,096 x 7,168, k in {4, 8}: 114 against 119 us)
@@ -311,6 +307,26 @@ __global__ __launch_bounds__(CH <= 2 ? 512 : 1024) void combine_norm_kernel(cons
   norm_chain(v, io, n, o, t, red);
 }
 
+// A launch holds less than 2^32 threads (and the runtime does not refuse more): at
+// most ROWS rows of up to 1,024 threads each.  Larger batches take several launches,
+// the operands moved on (with the row in a second grid dimension instead, the widest
+// rows spill more and take a fifth longer).
+constexpr int ROWS = 1 << 21;
+template <typename T>
+static T* past(T* p, size_t elements, size_t size) {
+  using C = std::conditional_t<std::is_const_v<T>, const char, char>;
+  return p ? (T*)((C*)p + elements * size) : nullptr;
+}
+static NormRow past_rows(NormRow n, int t0, size_t size) {
+  const size_t e = (size_t)t0 * n.d;
+  n.resid = past(n.resid, e, size);
+  n.resid_out = past(n.resid_out, e, size);
+  n.x_out = past(n.x_out, e, size);
+  if (n.gate_mode == MOE_GATE_TOKEN) n.gate = past(n.gate, t0, size);
+  if (n.gate_mode == MOE_GATE_FULL) n.gate = past(n.gate, e, size);
+  return n;
+}
+
 // Threads of a row: enough for CH chunks each, in whole waves.
 static int row_threads(int nch, int ch) { return ((nch + ch - 1) / ch + 63) / 64 * 64; }
 
@@ -321,10 +337,8 @@ static void launch_norm_t(const T* y, const NormRow& n, int T_, hipStream_t st) 
   const bool vec = n.d % LE == 0;
 #define MOE_NORM(CH)                                                                                              \
   do {                                                                                                            \
-    if (vec)                                                                                                      \
-      hipLaunchKernelGGL((norm_kernel<T, CH, true>), row_grid(T_), dim3(row_threads(nch, CH)), 0, st, y, n, T_);  \
-    else                                                                                                          \
-      hipLaunchKernelGGL((norm_kernel<T, CH, false>), row_grid(T_), dim3(row_threads(nch, CH)), 0, st, y, n, T_); \
+    if (vec) hipLaunchKernelGGL((norm_kernel<T, CH, true>), dim3(T_), dim3(row_threads(nch, CH)), 0, st, y, n);   \
+    else hipLaunchKernelGGL((norm_kernel<T, CH, false>), dim3(T_), dim3(row_threads(nch, CH)), 0, st, y, n);      \
   } while (0)
   if (nch <= 512) MOE_NORM(1);
   else if (nch <= 1024) MOE_NORM(2);
@@ -335,10 +349,16 @@ static void launch_norm_t(const T* y, const NormRow& n, int T_, hipStream_t st) 
 }
 
 hipError_t launch_norm(int dtype, const void* y, const NormRow& n, int T, hipStream_t st) {
-  if (T == 0) return hipSuccess;
-  if (dtype == DT_BF16) launch_norm_t<bf16_t>((const bf16_t*)y, n, T, st);
-  else launch_norm_t<float>((const float*)y, n, T, st);
-  return hipGetLastError();
+  const size_t size = dtype == DT_BF16 ? 2 : 4;
+  for (int t0 = 0; t0 < T; t0 += min(ROWS, T - t0)) {
+    const NormRow r = past_rows(n, t0, size);
+    const void* const yr = past(y, (size_t)t0 * n.d, size);
+    if (dtype == DT_BF16) launch_norm_t<bf16_t>((const bf16_t*)yr, r, min(ROWS, T - t0), st);
+    else launch_norm_t<float>((const float*)yr, r, min(ROWS, T - t0), st);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <typename T>
@@ -347,8 +367,8 @@ static void launch_combine_norm_t(const T* yp, const T* ysh, const int32_t* tok_
   constexpr int LE = 16 / (int)sizeof(T);
   const int nch = n.d / LE;
 #define MOE_CNORM(CH, CBN)                                                                                          \
-  hipLaunchKernelGGL((combine_norm_kernel<T, CH, CBN>), row_grid(T_), dim3(row_threads(nch, CH)), 0, st, yp, ysh,     \
-                     tok_off, wts, inv_perm, cap, n, T_)
+  hipLaunchKernelGGL((combine_norm_kernel<T, CH, CBN>), dim3(T_), dim3(row_threads(nch, CH)), 0, st, yp, ysh, tok_off, \
+                     wts, inv_perm, cap, n)
   if (nch <= 512) MOE_CNORM(1, 8);
   else if (nch <= 1024) MOE_CNORM(2, 8);
   else if (nch <= 4096) MOE_CNORM(4, 4);
@@ -359,12 +379,19 @@ static void launch_combine_norm_t(const T* yp, const T* ysh, const int32_t* tok_
 
 hipError_t launch_combine_norm(int dtype, const void* yp, const void* ysh, const int32_t* tok_off, const float* wts,
                                const int32_t* inv_perm, int cap, const NormRow& n, int T, hipStream_t st) {
-  if (T == 0) return hipSuccess;
-  if (dtype == DT_BF16)
-    launch_combine_norm_t<bf16_t>((const bf16_t*)yp, (const bf16_t*)ysh, tok_off, wts, inv_perm, cap, n, T, st);
-  else
-    launch_combine_norm_t<float>((const float*)yp, (const float*)ysh, tok_off, wts, inv_perm, cap, n, T, st);
-  return hipGetLastError();
+  const size_t size = dtype == DT_BF16 ? 2 : 4;
+  for (int t0 = 0; t0 < T; t0 += min(ROWS, T - t0)) {
+    const NormRow r = past_rows(n, t0, size);
+    const void* const yr = past(ysh, (size_t)t0 * n.d, size);
+    const int rows = min(ROWS, T - t0);
+    if (dtype == DT_BF16)
+      launch_combine_norm_t<bf16_t>((const bf16_t*)yp, (const bf16_t*)yr, tok_off + t0, wts, inv_perm, cap, r, rows, st);
+    else
+      launch_combine_norm_t<float>((const float*)yp, (const float*)yr, tok_off + t0, wts, inv_perm, cap, r, rows, st);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace moe
