@@ -113,10 +113,24 @@ def test_route_grouped_every_logit_exact(rule, T, d, E):
     k = torch.randint(0, 6, (T,), generator=g, device=DEV, dtype=torch.int32)
     sb = None if RULES[rule]["score"] == "softmax" else (torch.rand(E, generator=g, device=DEV) - 0.5) * 0.1
     _check_route(x, w, k, 5, sb=sb, scale=2.5, router="screened", **RULES[rule])
-    # every logit exact for a -inf router bias too
-    rb = torch.zeros(E, device=DEV)
-    rb[E // 4], rb[E - 1] = -math.inf, -math.inf
-    _check_route(x, w, k, 5, sb=sb, rb=rb, router="screened", **RULES[rule])
+
+
+@pytest.mark.parametrize("rule", range(len(RULES)))
+@pytest.mark.parametrize("router,T,d,E", [("screened", 70, 2048, 256), ("screened", 33, 1024, 1024), ("float64", 40, 512, 64),
+                                          ("auto", 3100, 1024, 256)])
+def test_route_grouped_router_biases_that_are_not_finite(rule, router, T, d, E):
+    """-inf: score 0, of all experts too; +inf: score 1 (a softmax has none then); NaN: out
+    of service; ordinary and wide tokens."""
+    g = _gen(T + E)
+    x, w = _wide_tokens(g, T, d, E)
+    k = torch.randint(0, 6, (T,), generator=g, device=DEV, dtype=torch.int32)
+    sb = None if RULES[rule]["score"] == "softmax" else (torch.rand(E, generator=g, device=DEV) - 0.5) * 0.1
+    for bias in ({E // 4: -math.inf, E - 1: -math.inf}, {E // 4: math.inf}, {1: math.nan, 3: -math.inf},
+                 dict.fromkeys(range(E), -math.inf), dict.fromkeys(range(3, E), -math.inf)):
+        rb = torch.zeros(E, device=DEV)
+        rb[list(bias)] = torch.tensor(list(bias.values()), device=DEV)
+        with np.errstate(invalid="ignore"):
+            _check_route(x, w, k, 5, sb=sb, rb=rb, router=router, **RULES[rule])
 
 
 @pytest.mark.parametrize("rule", range(len(RULES)))
