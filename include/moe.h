@@ -79,8 +79,10 @@ typedef enum {
   MOE_PATH_GEMM = 2     /* LDS-tiled grouped GEMM on MFMA (compute-bound prefill) */
 } moe_path;
 
-/* Router algorithm.  Both produce identical ids, order and weights (the
- * routing contract below); they differ only in cost. */
+/* Router algorithm.  In moe_route all produce identical ids, order and weights
+ * (the routing contract below); they differ only in cost.  moe_route_grouped
+ * has its own algorithms behind these values, with the same ids under each but
+ * not the same last bits of the weights; its rules stand there. */
 typedef enum {
   MOE_ROUTER_AUTO = 0,      /* screened for bf16 when T * E * d >= 2^30; else fused when
                                T <= 1024, E <= 256 and E * d <= 2^16; else float64 */
@@ -268,9 +270,10 @@ moe_status moe_route(const moe_desc* desc, const void* x, const void* w_router,
  *   perm_tok      int32 [T*k_max] out: token of sorted row p
  *   perm_src      int32 [T*k_max] out: assignment index tok_off[t]+j of sorted row p
  *   inv_perm      int32 [T*k_max] out: sorted row of assignment a; -1 for an
- *                 assignment whose expert id is outside [0, E) (never
- *                 produced by moe_route: such an entry gets no row, is not
- *                 counted, and moe_combine skips it)
+ *                 assignment whose expert id is outside [0, E): such an
+ *                 entry gets no row, is not counted, and moe_combine skips it
+ *                 (moe_route never produces one; moe_route_grouped does where
+ *                 a token has fewer experts to choose from than its budget)
  *   n_active      int32 [1] out: experts with at least one assignment
  *                 (the activated experts whose weights a batch loads; METRO
  *                 reading notes, arXiv 2512.09277, Q1)
@@ -557,8 +560,15 @@ moe_status moe_forward(const moe_desc* desc, const void* x, const void* w_router
  *                AUTO, FLOAT64 or SCREENED.  The ids are the same under each.  With
  *                SCREENED, and with AUTO for bf16 when T * E * d >= 3 * 2^28, a weight
  *                comes from a logit whose products are summed 64 at a time in
- *                float32 and further in float64, unless its order was in doubt (a
- *                softmax with select_bias always takes FLOAT64)
+ *                float32 and further in float64, unless its order was in doubt: that
+ *                logit is off by at most 8e-6 |x| max |w_e| (the weight, measured, by
+ *                3e-8 of itself), and a token's weight may differ in its last bits from
+ *                the one it has in another batch.
+ *                FLOAT64 sums every logit in float64.  It serves a softmax with
+ *                select_bias and batches of more than 2^28 tokens under any router.
+ *                Tokens of |x| max |w_e| above some 7,900, or with a value that is
+ *                no number, have all their logits summed exactly one after the other
+ *                (a batch of such tokens takes five times as long as with FLOAT64)
  *   ws           scratch of moe_workspace_size(MOE_OP_ROUTE_GROUPED) bytes
  * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED (rule values, or
  * MOE_ROUTER_FUSED), MOE_ERR_ALIGN, MOE_ERR_WORKSPACE, MOE_ERR_LAUNCH.
@@ -628,7 +638,8 @@ moe_status moe_combine_norm(const moe_desc* desc, const moe_norm_desc* nd, const
  * expert_off[g+1]-1; 0 without groups),
  *   y_out[r] = y_in[r] + scales[a] * B[a][g] (A[a][g] x[x_rows[r]])
  * over the first ranks[a] ranks, both products summed in float32, one rounding
- * to ELT.  A row without adapter (id outside [0, L), token outside [0, T) or x
+ * to ELT; in bf16 the second product takes scales[a] * (A x) as two bf16 values,
+ * itself rounded and the remainder (2^-17 of it is lost).  A row without adapter (id outside [0, L), token outside [0, T) or x
  * row out of range) keeps y_in's bits.  With expert_off, rows from
  * expert_off[G] on are left as they were.
  * The rows may be a batch's tokens (a dense projection: the always-on expert,

@@ -17,7 +17,12 @@
 // Bound by memory in prefill (4,096 rows, 2,048 -> 7,168, rank 32, 8 adapters: 15 us
 // for the first product, 37 us for the second, which reads and writes 117 MB, a copy
 // in the same shape taking 30), by latency in decode (128 rows, 32 adapters: 8.5 +
-// 11 us; 1,150 permuted rows of 128 experts, 4 adapters: 10 + 17 us).
+// 11 us; 1,150 permuted rows of 128 experts, 4 adapters: 10 + 17 us).  Where windows of
+// a large batch hold many pairs it is bound by their products (4,096 rows of 32 mixed
+// adapters, rank 16: 157 us; 32,768 permuted rows of 128 experts, 8 mixed adapters, 768
+// -> 2,048: 248 us).  Ranks above 64 spill in the first product (up to 199 registers):
+// rank 128 takes 103 us for 128 rows, 173 for 4,096 rows of 8 adapters (rank 64: 40 and
+// 67).  float32: 30 us for 128 rows, 93 for 4,096 (2,048 -> 7,168, rank 16 and 32).
 #include "common.h"
 #include "launch.h"
 
@@ -486,7 +491,8 @@ static void launch_adapt_t(const AdaptArgs& p, void* v, hipStream_t st) {
   const int wpw = max(1, min(8, (int)((long long)windows * cols * 4 / 4096)));
   const int splits = (windows + wpw - 1) / wpw;
   // shares of a window's pairs: 1 where the windows fill the chip, 2 where they are
-  // few (128 rows, us a call: 21.9 with 1, 20.0 with 2, 20.7 with 3, 21.6 with 4)
+  // few (128 rows of 32 adapters, the one shape measured, us a call: 21.9 with 1, 20.0
+  // with 2, 20.7 with 3, 21.6 with 4)
   const int ze = max(1, min(2, 4096 / (cols * 4 * splits)));
   const bool ahead = wpw == 1;
   const int rt = (p.R + 15) / 16, rtp = rt <= 2 ? rt : (rt <= 4 ? 4 : 8);

@@ -112,7 +112,11 @@ struct RowIo {
     }
   }
   // Non-temporal: the row's next reader is another kernel (8,192 x 2,048 bf16,
-  // four rows of traffic a token: 37 -> 30 us).
+  // four rows of traffic a token: 33 -> 27 us for the norm alone).  With the kernel
+  // that reads x behind it, us a pair, cached against non-temporal: the router at
+  // 1 x 7168 22.2 / 22.3, 8,192 x 2,048 93.9 / 96.4, 4,096 x 7168 158.8 / 157.5; the
+  // experts' gate/up at 1 x 7168 43.6 / 43.6, 8,192 x 2,048 500 / 499, 4,096 x 7168
+  // 386 / 350.
   __device__ __forceinline__ void write(void* base, size_t first, const float (&f)[CH][LE]) const {
     T* const p = (T*)base + first;
 #pragma unroll
