@@ -607,7 +607,7 @@ moe_status moe_route_grouped(const moe_desc* desc, const moe_route_rule* rule, c
  * alpha and w_offset finite.
  *
  * moe_combine_norm: the same with y = moe_combine's sum in float32 (not
- * rounded), in one launch.  T, d and dtype come from desc and must equal nd's;
+ * rounded), in one launch (one for every 2^21 tokens, as moe_norm).  T, d and dtype come from desc and must equal nd's;
  * y_perm and y_shared must not overlap the outputs.
  * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED (dtype, kind or gate
  * mode), MOE_ERR_ALIGN, MOE_ERR_LAUNCH.

@@ -253,6 +253,9 @@ __global__ __launch_bounds__(1024) void adapt_shrink_kernel(AdaptArgs p, void* _
 // from addresses that depend on nothing (so that the waits count loads instead of
 // draining them).  B of a pair is loaded when it changes.
 //
+// Waves a SIMD: as many as the registers of a form allow without spilling (NF = 2 is
+// held to three, which it misses by six registers of its own accord).
+//
 // AHEAD: B of a window's next pair is requested while one is multiplied; taken where
 // the waves are few, which is where windows hold many pairs, up to the rank whose
 // fragments fit the registers (128 rows, 32 adapters: 21.2 -> 20.0 us a call with two

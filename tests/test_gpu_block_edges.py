@@ -8,7 +8,8 @@ import pytest
 import torch
 
 import mixture_experts_layer_token_amd as moe
-from tests.test_gpu_block import DEV, DT, EPS, RULES, U, _adapt, _adapt_ref, _check_route, _gen, _randn, _route
+from tests.test_gpu_block import (DEV, DT, EPS, RULES, U, _adapt, _adapt_ref, _check_route, _gen, _norm_case, _randn,
+                                  _route)
 from workloads import to_f64
 
 pytestmark = pytest.mark.gpu
@@ -207,6 +208,48 @@ def test_combine_norm_of_many_rows():
         n = min(1 << 22, T - lo)
         ref = wts[lo:lo + n, None].double() * yp[T - lo - n:T - lo].flip(0).double()
         assert ((r[lo:lo + n].double() - ref).abs() <= ref.abs() * (2 * EPS + U["bf16"] * 1.01) + 1e-40).all()
+
+
+@pytest.mark.parametrize("gate", ["channel", "token", "full"])
+@pytest.mark.parametrize("d", [16, 9])
+def test_norm_operands_of_many_rows(gate, d):
+    """Every operand of the rows behind the first launch's 2^21: the bits of a call on
+    those rows alone."""
+    T, n = (1 << 21) + 5, 9
+    t = _norm_case(57 + d, "bf16", T, d, "layer", True, gate, True)
+    out = [torch.full_like(t["y"], 7.0) for _ in range(2)]
+    call = lambda T, t, o: moe.moe_norm(
+        moe.make_norm_desc(T, d, kind="layer", post=True, gate=gate, alpha=0.5), t["y"], t["resid"], t["post_w"],
+        t["post_b"], t["gate"], t["pre_w"], t["pre_b"], *o)
+    call(T, t, out)
+    rows = {k: v[-n:].clone() if v is not None and (k in ("y", "resid") or (k == "gate" and gate != "channel")) else v
+            for k, v in t.items()}
+    last = [torch.empty_like(rows["y"]) for _ in range(2)]
+    call(n, rows, last)
+    for a, b in zip(out, last):
+        assert torch.equal(a[-n:], b)
+
+
+@pytest.mark.parametrize("gate", ["none", "token", "full"])
+def test_combine_norm_operands_of_many_rows(gate):
+    T, d, n = (1 << 21) + 5, 128, 9
+    t = _norm_case(58, "bf16", T, d, "rms", True, gate, False)
+    g = _gen(59)
+    off = torch.arange(T + 1, dtype=torch.int32, device=DEV)
+    inv = torch.randperm(T, generator=g, device=DEV).int()
+    wts, yp, ysh = torch.rand(T, generator=g, device=DEV), t.pop("y"), _randn(g, T, d, dtype=torch.bfloat16)
+    call = lambda T, yp, ysh, off, wts, inv, resid, gt, o: moe.moe_combine_norm(
+        moe.make_desc(T, d, 1, 128, 1), moe.make_norm_desc(T, d, post=True, gate=gate), yp, ysh, off, wts, inv, resid,
+        t["post_w"], None, gt, t["pre_w"], None, *o)
+    out = [torch.full_like(ysh, 7.0) for _ in range(2)]
+    call(T, yp, ysh, off, wts, inv, t["resid"], t["gate"], out)
+    last = [torch.empty(n, d, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    own = yp[inv[-n:].long()].contiguous()
+    c = lambda v: None if v is None else v[-n:].clone()
+    call(n, own, c(ysh), off[:n + 1].clone(), c(wts), torch.arange(n, dtype=torch.int32, device=DEV), c(t["resid"]),
+         c(t["gate"]), last)
+    for a, b in zip(out, last):
+        assert torch.equal(a[-n:], b)
 
 
 @pytest.mark.parametrize("router", ["float64", "screened"])
