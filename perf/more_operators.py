@@ -1,0 +1,408 @@
+"""Operators for a few tokens: the whole layer in two launches, and 4-bit weights with group scales.
+
+Each case is one call as a serving program makes it when few requests are live.
+With ``own`` false ``run`` computes the operator in elementary torch operations,
+in 32 bits (router logits in 64, as the routing contract asks); with ``own`` true
+it calls the library.
+
+4-bit weights stand in the state as checkpoints hold them: codes uint8
+[..., N, K/2] (element 2j in the low half of byte j), scales [..., N, groups] and
+zero points uint8 [..., N, groups] (or none: 8); a value is scale * (code - zero).
+"""
+import math
+
+import torch
+
+own = False
+
+_DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+# --------------------------------------------------------------------- cases
+
+def listed():
+    return [
+        # one request's next token through a 128-expert layer
+        dict(name="layer_token", op="layer", dtype="bf16", T=1, d=2048, E=128, I=768, Is=0, k="8", k_max=8,
+             group=0, zeros=False, layout="blocked", bias=False),
+        # a small float32 layer, every column of the few-token tile in use
+        dict(name="layer_small_f32", op="layer", dtype="f32", T=16, d=256, E=8, I=512, Is=0, k="2", k_max=2,
+             group=0, zeros=False, layout="rowmajor", bias=True),
+        # four requests with their own budgets through a 256-expert layer with an always-on expert
+        dict(name="layer_wide", op="layer", dtype="bf16", T=4, d=7168, E=256, I=2048, Is=2048, k="4 8", k_max=8,
+             group=0, zeros=False, layout="rowmajor", bias=False),
+        # sixteen requests over narrow sub-experts with large and with no budgets
+        dict(name="layer_subexperts", op="layer", dtype="bf16", T=16, d=2048, E=256, I=384, Is=0, k="0 8 16 32",
+             k_max=32, group=0, zeros=False, layout="blocked", bias=False),
+        # the first layer and the wide one with 4-bit experts
+        dict(name="layer_q4_token", op="layer", dtype="bf16", T=1, d=2048, E=128, I=768, Is=0, k="8", k_max=8,
+             group=128, zeros=False, layout="rowmajor", bias=False),
+        dict(name="layer_q4_wide", op="layer", dtype="bf16", T=8, d=7168, E=256, I=2048, Is=2048, k="4 8", k_max=8,
+             group=64, zeros=True, layout="rowmajor", bias=False),
+        # two requests behind a router of another kind, large experts
+        dict(name="experts_large", op="experts", dtype="bf16", T=2, d=4096, E=8, I=14336, Is=0, k="2", k_max=2,
+             group=0, zeros=False, layout="blocked", holes=False),
+        # odd sizes, 4-bit experts beside float32 activations, slots that the router left without an expert
+        dict(name="experts_q4_f32", op="experts", dtype="f32", T=5, d=1152, E=61, I=640, Is=384, k="0 3 6", k_max=6,
+             group=32, zeros=True, layout="rowmajor", holes=True),
+        # one token through a projection
+        dict(name="linear_token", op="linear", dtype="bf16", rows=1, K=7168, N=2048, group=128, zeros=False),
+        # a few requests' logits over a vocabulary of odd size
+        dict(name="linear_vocab", op="linear", dtype="bf16", rows=24, K=4096, N=50257, group=64, zeros=True),
+        # quantising a stack of experts when it is loaded, and back for a large batch
+        dict(name="pack_stack", op="pack", dtype="bf16", G=8, N=14336, K=4096, group=128, zeros=False),
+        dict(name="pack_odd_f32", op="pack", dtype="f32", G=3, N=1531, K=1000, group=32, zeros=True),
+    ]
+
+
+def _log_int(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    while True:  # nothing larger than the listed cases
+        c = _draw(rng)
+        w = work(c)
+        if max(w["bytes"], w["flops"] / 50) < 2e9:
+            return c
+
+
+def _draw(rng):
+    op = rng.choice(["layer", "layer", "experts", "linear", "pack"])
+    dtype = rng.choice(["bf16", "bf16", "f32"])
+    group, zeros = rng.choice([32, 64, 128]), rng.random() < 0.5
+    if op in ("layer", "experts"):
+        d, I = 128 * _log_int(rng, 1, 56), 128 * _log_int(rng, 1, 32)
+        E = _log_int(rng, 2, max(2, min(320, (1 << 31) // (3 * d * I))))
+        k_max = rng.randint(1, min(E, rng.choice([4, 8, 24])))
+        c = dict(op=op, dtype=dtype, T=_log_int(rng, 1, 16), d=d, E=E, I=I,
+                 Is=rng.choice([0, 0, I, 128 * rng.randint(1, 16)]), k="%d %d" % (rng.randint(0, k_max), k_max),
+                 k_max=k_max, group=rng.choice([0, 0, group]), zeros=zeros,
+                 layout=rng.choice(["rowmajor", "blocked"]))
+        if c["group"]:
+            c["layout"] = "rowmajor"
+        else:
+            c["zeros"] = False
+        c["bias" if op == "layer" else "holes"] = rng.random() < 0.4
+        return c
+    if op == "linear":
+        K, N = 8 * _log_int(rng, 8, 1792), _log_int(rng, 48, 65536)
+        return dict(op=op, dtype=dtype, rows=_log_int(rng, 1, 64 if dtype == "bf16" else 16), K=K, N=N, group=group,
+                    zeros=zeros)
+    K, N = 8 * _log_int(rng, 8, 1024), _log_int(rng, 16, 16384)
+    return dict(op=op, dtype=dtype, G=_log_int(rng, 1, max(1, min(64, (1 << 28) // (K * N)))), N=N, K=K, group=group,
+                zeros=zeros)
+
+
+def _choices(c):
+    """The budgets that requests of the case ask for."""
+    return [int(v) for v in c["k"].split()]
+
+
+def _groups(K, group):
+    return -(-K // group)
+
+
+def _weight_bytes(c, s, N, K):
+    if not c["group"]:
+        return N * K * s
+    return N * K // 2 + N * _groups(K, c["group"]) * (s + c["zeros"])
+
+
+def work(case):
+    c, s = case, 2 if case["dtype"] == "bf16" else 4
+    if c["op"] == "linear":
+        return {"bytes": _weight_bytes(c, s, c["N"], c["K"]) + c["rows"] * (c["K"] + c["N"]) * s,
+                "flops": 2 * c["rows"] * c["K"] * c["N"]}
+    if c["op"] == "pack":  # in and back: the weights read and written, the codes and scales written and read
+        n = c["G"] * c["N"] * c["K"]
+        return {"bytes": 2 * n * s + 2 * c["G"] * _weight_bytes(c, s, c["N"], c["K"]), "flops": 6 * n}
+    T, d, E, ks = c["T"], c["d"], c["E"], _choices(c)
+    A = T * sum(ks) / len(ks)
+    used = E * (1 - math.prod(1 - k / E for k in (ks * T)[:T]))
+    per = 2 * _weight_bytes(c, s, c["I"], d) + _weight_bytes(c, s, d, c["I"])
+    sh = 2 * _weight_bytes(c, s, c["Is"], d) + _weight_bytes(c, s, d, c["Is"]) if c["Is"] else 0
+    router = E * d * s if c["op"] == "layer" else 8 * A
+    return {"bytes": used * per + sh + router + 2 * T * d * s,
+            "flops": 6 * d * (A * c["I"] + T * c["Is"]) + (2 * T * E * d if c["op"] == "layer" else 0)}
+
+
+# -------------------------------------------------------------------- inputs
+
+def _codes(gen, shape, K, c, std):
+    """A 4-bit weight of shape [*shape, K]: its codes, scales and zero points."""
+    dt, ng = _DT[c["dtype"]], _groups(K, c["group"])
+    q = torch.randint(0, 256, (*shape, K // 2), generator=gen, device="cuda", dtype=torch.uint8)
+    s = ((torch.rand(*shape, ng, generator=gen, device="cuda") + 0.5) * (std / 4.8)).to(dt)
+    z = torch.randint(6, 10, (*shape, ng), generator=gen, device="cuda", dtype=torch.uint8) if c["zeros"] else None
+    return q, s, z
+
+
+def _weight(gen, shape, K, c, std):
+    if c["group"]:
+        return _codes(gen, shape, K, c, std)
+    w = torch.empty(*shape, K, dtype=_DT[c["dtype"]], device="cuda")
+    return w.normal_(0.0, std, generator=gen)
+
+
+def prepare(case, seed):
+    c, dt = case, _DT[case["dtype"]]
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    randn = lambda *n, std=1.0: (torch.randn(*n, generator=gen, device="cuda") * std).to(dt)
+    s = {"c": c}
+    if c["op"] == "linear":
+        s["x"] = randn(c["rows"], c["K"])
+        s["w"] = _codes(gen, (c["N"],), c["K"], c, c["K"] ** -0.5)
+        s["out"] = torch.empty(c["rows"], c["N"], dtype=dt, device="cuda")
+        return s
+    if c["op"] == "pack":
+        s["w"] = randn(c["G"], c["N"], c["K"], std=c["K"] ** -0.5)
+        s["out"] = torch.empty_like(s["w"])
+        return s
+    T, d, E, I, Is = c["T"], c["d"], c["E"], c["I"], c["Is"]
+    s["x"] = randn(T, d)
+    s["gate"], s["up"] = (_weight(gen, (E, I), d, c, d ** -0.5) for _ in range(2))
+    s["down"] = _weight(gen, (E, d), I, c, I ** -0.5)
+    if Is:
+        s["s_gate"], s["s_up"] = (_weight(gen, (Is,), d, c, d ** -0.5) for _ in range(2))
+        s["s_down"] = _weight(gen, (d,), Is, c, Is ** -0.5)
+    ks = torch.tensor(_choices(c), dtype=torch.int32, device="cuda")
+    s["k"] = ks[torch.randint(0, len(ks), (T,), generator=gen, device="cuda")]
+    s["out"] = torch.empty(T, d, dtype=dt, device="cuda")
+    s["stats"] = torch.zeros(E + 2, dtype=torch.int32, device="cuda")
+    s["status"] = torch.zeros(1, dtype=torch.int32, device="cuda")
+    if c["op"] == "layer":
+        s["router"] = randn(E, d, std=d ** -0.5)
+        s["bias"] = torch.randn(E, generator=gen, device="cuda") * 0.5 if c["bias"] else None
+        return s
+    # routes as a router leaves them: distinct experts of a token from its offset on
+    s["tok_off"] = torch.zeros(T + 1, dtype=torch.int32, device="cuda")
+    s["tok_off"][1:] = torch.cumsum(s["k"], 0)
+    order = torch.rand(T, E, generator=gen, device="cuda").argsort(1).int()
+    use = torch.arange(E, device="cuda") < s["k"][:, None]
+    ids = order[use]
+    if c["holes"]:
+        ids = torch.where(torch.rand(len(ids), generator=gen, device="cuda") < 0.2, -1, ids)
+    s["ids"] = torch.full((T * c["k_max"],), -1, dtype=torch.int32, device="cuda")
+    s["ids"][:len(ids)] = ids
+    s["wts"] = torch.rand(T * c["k_max"], generator=gen, device="cuda") / max(c["k_max"], 1)
+    return s
+
+
+# ---------------------------------------------------------------- plain forms
+
+def _values(w, c, at=None):
+    """A weight, or its matrices `at`, in float32."""
+    if not c["group"]:
+        return (w if at is None else w[at]).float()
+    q, s, z = (t if t is None or at is None else t[at] for t in w)
+    q = torch.stack([q & 15, q >> 4], -1).flatten(-2).float()
+    wide = lambda t: t.float().repeat_interleave(c["group"], -1)[..., :q.shape[-1]]
+    return wide(s) * (q - (8.0 if z is None else wide(z)))
+
+
+def _plain_routes(s):
+    """Per token: experts by logit (ties to the lower index) and weights, k_max of them."""
+    c = s["c"]
+    j = torch.arange(c["k_max"], device=s["x"].device)
+    use = j < s["k"][:, None]
+    if c["op"] == "experts":
+        at = (s["tok_off"][:-1, None].long() + j).clamp(max=s["ids"].numel() - 1)
+        ids = s["ids"][at].long()
+        use &= ids >= 0
+        return ids.clamp(min=0), torch.where(use, s["wts"][at], 0.0), use
+    l = s["x"].double() @ s["router"].double().t()
+    if s["bias"] is not None:
+        l = l + s["bias"].double()
+    best = torch.sort(l.float(), dim=1, descending=True, stable=True)
+    l, ids = best.values[:, :c["k_max"]], best.indices[:, :c["k_max"]]
+    p = torch.where(use, torch.exp(l - l[:, :1]), 0.0)
+    return ids, p / p.sum(1, keepdim=True).clamp(min=1e-30), use
+
+
+def _plain_swiglu(x, wg, wu, wd):
+    """One token through n experts: [n, I, d], [n, I, d], [n, d, I] -> [n, d]."""
+    g, u = torch.matmul(wg, x), torch.matmul(wu, x)
+    return torch.matmul(wd, (g * torch.sigmoid(g) * u)[..., None])[..., 0]
+
+
+def _plain_layer(s):
+    c = s["c"]
+    ids, wts, use = _plain_routes(s)
+    x = s["x"].float()
+    rows = []
+    for t in range(c["T"]):
+        y = _plain_swiglu(x[t], *(_values(s[n], c, ids[t]) for n in ("gate", "up", "down")))
+        rows.append((wts[t, :, None] * y).sum(0))
+    out = torch.stack(rows)
+    if c["Is"]:
+        wg, wu, wd = (_values(s[n], c) for n in ("s_gate", "s_up", "s_down"))
+        g = x @ wg.t()
+        out = out + (g * torch.sigmoid(g) * (x @ wu.t())) @ wd.t()
+    out = out.to(s["x"].dtype)
+    if c["op"] == "experts":
+        return out
+    counts = torch.zeros(c["E"], dtype=torch.int32, device=ids.device)
+    counts.index_add_(0, ids.flatten(), use.int().flatten())
+    return out, torch.cat([counts, (counts > 0).sum().int()[None], counts.sum().int()[None]])
+
+
+def _plain_pack(s):
+    c, w = s["c"], s["w"]
+    g, K = c["group"], c["K"]
+    pad = _groups(K, g) * g - K
+    v = torch.nn.functional.pad(w.double(), (0, pad)).unflatten(-1, (-1, g))
+    if c["zeros"]:
+        lo, hi = v.amin(-1).clamp(max=0.0), v.amax(-1).clamp(min=0.0)
+        sc = ((hi - lo) / 15.0).to(w.dtype)
+        one = torch.where(sc == 0, 1.0, sc.double())
+        z = torch.round(-lo / one).clamp(0, 15)
+        low = 0
+    else:
+        sc = (v.abs().amax(-1) / 7.0).to(w.dtype)
+        one = torch.where(sc == 0, 1.0, sc.double())
+        z = torch.full_like(one, 8.0)
+        low = 1
+    q = torch.where(sc[..., None] == 0, z[..., None], torch.round(v / one[..., None]) + z[..., None]).clamp(low, 15)
+    vals = (sc.float()[..., None] * (q - z[..., None]).float()).flatten(-2)[..., :K]
+    return vals.to(w.dtype), sc, z.to(torch.uint8) if c["zeros"] else None
+
+
+# ----------------------------------------------------------------------- run
+
+def _handle(s):
+    """What a program keeps between calls: descriptors, workspaces, laid-out weights."""
+    if "handle" in s:
+        return s["handle"]
+    import mixture_experts_layer_token_amd as moe
+    c, dt = s["c"], _DT[s["c"]["dtype"]]
+    if c["op"] == "linear":
+        s["handle"] = (moe, moe.q4_tile(*s["w"], group=c["group"]))
+    elif c["op"] == "pack":
+        q = moe.alloc_q4(c["G"], c["N"], c["K"], group=c["group"], zeros=c["zeros"], dtype=dt)
+        s["handle"] = (moe, q)
+    else:
+        desc = moe.make_desc(c["T"], c["d"], c["E"], c["I"], c["k_max"], I_shared=c["Is"], dtype=dt,
+                             weight_layout=c["layout"])
+        names = ("gate", "up", "down", "s_gate", "s_up", "s_down")
+        lay = (lambda w: moe.q4_tile(*w, group=c["group"])) if c["group"] else (
+            moe.pack_weights if c["layout"] == "blocked" else lambda w: w)
+        s["handle"] = (moe, desc, [lay(s[n]) if n in s else None for n in names],
+                       moe.alloc_workspace(desc, moe.MOE_OP_FEW))
+    return s["handle"]
+
+
+def _own(s):
+    c, h = s["c"], _handle(s)
+    moe = h[0]
+    if c["op"] == "linear":
+        moe.moe_q4_linear(h[1], s["x"], s["out"])
+        return s["out"]
+    if c["op"] == "pack":
+        moe.moe_q4_pack(s["w"], h[1])
+        moe.moe_q4_unpack(h[1], s["out"])
+        # scales and zero points as [G, N, groups], the order the plain form has them in
+        sc = h[1].scales.transpose(1, 2)[:, :c["N"]]
+        return s["out"], sc, h[1].zeros.transpose(1, 2)[:, :c["N"]] if c["zeros"] else None
+    if c["op"] == "layer":
+        moe.moe_forward_few(h[1], s["x"], s["router"], s["bias"], s["k"], *h[2], s["out"], s["stats"], s["status"],
+                            h[3])
+        return s["out"], s["stats"]
+    moe.moe_experts_few(h[1], s["x"], s["tok_off"], s["ids"], s["wts"], *h[2], s["out"], h[3])
+    return s["out"]
+
+
+def run(state):
+    if own:
+        return _own(state)
+    op = state["c"]["op"]
+    if op == "linear":
+        return (state["x"].float() @ _values(state["w"], state["c"]).t()).to(state["x"].dtype)
+    if op == "pack":
+        return _plain_pack(state)
+    return _plain_layer(state)
+
+
+# --------------------------------------------------- the definitions, 64 bits
+
+def _wide(w, c, e=None):
+    """One matrix of a weight in float64, element by element of its definition."""
+    if not c["group"]:
+        return (w if e is None else w[e]).double()
+    q, s, z = (t if t is None or e is None else t[e] for t in w)
+    N, K = q.shape[0], 2 * q.shape[1]
+    out = torch.empty(N, K, dtype=torch.float64, device=q.device)
+    out[:, 0::2], out[:, 1::2] = (q % 16).double(), (q // 16).double()
+    for g in range(s.shape[1]):
+        cols = slice(g * c["group"], min(K, (g + 1) * c["group"]))
+        out[:, cols] -= 8.0 if z is None else z[:, g, None].double()
+        out[:, cols] *= s[:, g, None].double()
+    return out
+
+
+def _exact_ffn(x, wg, wu, wd):
+    g = x @ wg.T
+    return (g / (1.0 + torch.exp(-g)) * (x @ wu.T)) @ wd.T
+
+
+def _exact_layer(c, s):
+    T, x = c["T"], s["x"].double()
+    chosen = []  # (token, expert, weight)
+    if c["op"] == "layer":
+        logit = torch.mm(s["router"].double(), x.T)
+        if s["bias"] is not None:
+            logit += s["bias"].double()[:, None]
+        logit = logit.float().double().cpu()
+        for t in range(T):
+            l = logit[:, t].tolist()
+            best = sorted(range(c["E"]), key=lambda e: (-l[e], e))[:int(s["k"][t])]
+            total = math.fsum(math.exp(l[e] - l[best[0]]) for e in best)
+            chosen += [(t, e, math.exp(l[e] - l[best[0]]) / total) for e in best]
+    else:
+        off, ids, wts = s["tok_off"].tolist(), s["ids"].tolist(), s["wts"].double().tolist()
+        chosen = [(t, ids[a], wts[a]) for t in range(T) for a in range(off[t], off[t + 1]) if ids[a] >= 0]
+    out = torch.zeros(T, c["d"], dtype=torch.float64, device=x.device)
+    if c["Is"]:
+        out += _exact_ffn(x, *(_wide(s[n], c) for n in ("s_gate", "s_up", "s_down")))
+    counts = [0] * c["E"]
+    for e in sorted({e for _, e, _ in chosen}):
+        mine = [(t, w) for t, f, w in chosen if f == e]
+        counts[e] = len(mine)
+        y = _exact_ffn(x[[t for t, _ in mine]], *(_wide(s[n], c, e) for n in ("gate", "up", "down")))
+        for row, (t, w) in zip(y, mine):
+            out[t] += w * row
+    if c["op"] == "experts":
+        return out
+    return out, torch.tensor(counts + [sum(n > 0 for n in counts), sum(counts)], dtype=torch.int32)
+
+
+def _exact_pack(c, s):
+    w, g = s["w"], c["group"]
+    ng = _groups(c["K"], g)
+    vals = torch.empty(w.shape, dtype=torch.float64, device=w.device)
+    scales = torch.empty(*w.shape[:2], ng, dtype=w.dtype, device=w.device)
+    zeros = torch.empty(*w.shape[:2], ng, dtype=torch.uint8, device=w.device)
+    for i in range(ng):
+        v = w[..., i * g:(i + 1) * g].double()
+        if c["zeros"]:
+            lo, hi = torch.clamp(v.min(-1).values, max=0), torch.clamp(v.max(-1).values, min=0)
+            sc = ((hi - lo) / 15).to(w.dtype)
+        else:
+            lo, sc = None, (v.abs().max(-1).values / 7).to(w.dtype)
+        d = sc.double()
+        d[d == 0] = math.inf  # a group of zeros: every quotient is 0
+        z = torch.clamp(torch.round(-lo / d), 0, 15) if c["zeros"] else torch.full_like(d, 8.0)
+        q = torch.clamp(torch.round(v / d[..., None]) + z[..., None], 0 if c["zeros"] else 1, 15)
+        # a value is rounded to the weights' type: it has more bits than that
+        vals[..., i * g:(i + 1) * g] = sc.double()[..., None] * (q - z[..., None])
+        scales[..., i], zeros[..., i] = sc, z.to(torch.uint8)
+    return vals, scales, zeros if c["zeros"] else None
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    if case["op"] == "linear":
+        return s["x"].double() @ _wide(s["w"], case).T
+    if case["op"] == "pack":
+        return _exact_pack(case, s)
+    return _exact_layer(case, s)
