@@ -118,7 +118,8 @@ typedef enum {
   MOE_OP_FORWARD = 4,
   MOE_OP_FOLD = 5,
   MOE_OP_PATH = 6,  /* moe_path_route and moe_path_sources */
-  MOE_OP_ROUTE_GROUPED = 7
+  MOE_OP_ROUTE_GROUPED = 7,
+  MOE_OP_FEW = 8    /* moe_forward_few and moe_experts_few */
 } moe_op;
 
 /* Expert scores of moe_route_grouped. */
@@ -678,6 +679,103 @@ moe_status moe_adapt(const moe_adapter_desc* ad, const void* x, const int32_t* x
                      const int32_t* ranks, const float* scales, const int32_t* adapter_ids, const int32_t* row_tok,
                      const int32_t* expert_off, const void* y_in, void* y_out, void* ws, size_t ws_bytes,
                      moe_stream_t stream);
+
+/*
+ * 4-bit weights with group scales.  A stack of G matrices [N][K] is stored as
+ *   W[n][k] = s[n][k / group] * (q[n][k] - z[n][k / group]),   q in 0..15,
+ * z = 8 without zero points.  Storage (the library's own order; sizes from
+ * moe_q4_bytes; every buffer 16-byte aligned):
+ *   codes   per matrix ceil(N/16) x ceil(K/128) tiles of 1 KB, tile (nb, kb) at
+ *           (nb * ceil(K/128) + kb) KB.  Code (n, k) of a tile (both from its corner)
+ *           sits in the 32-bit word ((k / 8 % 4) * 16 + n) * 4 + k / 32 at bit
+ *           4 * (k % 8 / 2) + 16 * (k % 2).  Codes outside the matrix: any
+ *   scales  ELT [G][ceil(K/128) * 128 / group][Np], Np = N rounded up to 16;
+ *           0 outside the matrix
+ *   zeros   uint8 of the same shape, values 0..15, or NULL for z = 8
+ *
+ * moe_q4_pack: quantises w, ELT [G][N][K].  Per row and group (the last one may
+ * be short):
+ *   without zero points  s = ELT(max |w| / 7), q = 8 + clamp(rne(w / s), -7, 7)
+ *   with                 lo, hi = the group's range widened to hold 0,
+ *                        s = ELT((hi - lo) / 15), z = clamp(rne(-lo / s), 0, 15),
+ *                        q = clamp(rne(w / s) + z, 0, 15)
+ * with the stored s and the exact quotient (rne: to nearest, ties to even); s = 0
+ * gives q = z (z = 0 with zero points), a value that is not finite s = NaN.
+ * moe_q4_tile: re-lays codes uint8 [G][N][K/2] (input 2j in the low half of byte
+ * j), scales ELT [G][N][ceil(K/group)] and zeros uint8 of that shape.
+ * moe_q4_unpack: w = ELT(s * (q - z)), ELT [G][N][K].
+ * moe_q4_linear (G = 1): y[r][n] = sum_k x[r][k] W[n][k] for x ELT [rows][K], y
+ * ELT [rows][N]; exact products and float32 sums, scaled per group, one rounding
+ * to ELT.  Made for few rows (decode): the weights are read once for every 16.
+ * Values that are not finite stay in their own row's and column's outputs, which are
+ * then summed again one by one (slow).
+ *
+ * Ranges: 0 <= G < 2^20; 1 <= N <= 262144; K a multiple of 8, 8 <= K <= 65536;
+ * group 32, 64 or 128; zeros 0 or 1; 0 <= rows <= 65536.  Outputs must not overlap
+ * inputs.
+ * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED (dtype, group, zeros),
+ * MOE_ERR_ALIGN, MOE_ERR_LAUNCH.
+ */
+typedef struct moe_q4_desc {
+  int32_t G, N, K;
+  int32_t group;  /* inputs of a scale */
+  int32_t zeros;  /* 1: with zero points */
+  int32_t dtype;  /* moe_dtype of the scales and of w, x and y */
+} moe_q4_desc;
+
+moe_status moe_q4_bytes(const moe_q4_desc* qd, size_t* codes, size_t* scales, size_t* zeros);
+moe_status moe_q4_pack(const moe_q4_desc* qd, const void* w, void* codes, void* scales, void* zeros,
+                       moe_stream_t stream);
+moe_status moe_q4_tile(const moe_q4_desc* qd, const void* codes_rm, const void* scales_rm, const void* zeros_rm,
+                       void* codes, void* scales, void* zeros, moe_stream_t stream);
+moe_status moe_q4_unpack(const moe_q4_desc* qd, const void* codes, const void* scales, const void* zeros, void* w,
+                         moe_stream_t stream);
+moe_status moe_q4_linear(const moe_q4_desc* qd, int32_t rows, const void* x, const void* codes, const void* scales,
+                         const void* zeros, void* y, moe_stream_t stream);
+
+/*
+ * The whole layer for a few tokens (0 <= T <= MOE_FEW_MAX_T, k_max <= 64):
+ * moe_forward's function without the permutation and the combine.  The ids are
+ * moe_route's; H keeps the routing weight, w_t * SiLU(x . w_gate) * (x . w_up),
+ * rounded once to ELT, and the down products of all experts are summed in float32
+ * and rounded once.  desc->path and desc->router are not consulted.  Values that are
+ * not finite stay with the tokens that they belong to (outputs that are not finite are
+ * summed again one by one, which is slow).
+ *   q4     NULL: the weights are ELT in desc->weight_layout, as in moe_forward.
+ *          Otherwise the six weight arguments are the codes of moe_q4_pack /
+ *          moe_q4_tile (stacks [E][I][d], [E][I][d], [E][d][I], and one matrix each
+ *          for the always-on expert) and q4 names their group and their scales and
+ *          zero points in the same order (zeros: all NULL, or none of those in use);
+ *          float32 H is then kept whole
+ *   others as in moe_forward; out must not overlap the inputs
+ *   ws     scratch of moe_workspace_size(MOE_OP_FEW) bytes
+ *
+ * moe_experts_few: the same behind routes that are given (moe_route_grouped,
+ * moe_fold, moe_proxy_route or the caller's): out[t] = sum over token t's routes of
+ * topk_w * expert output (+ the always-on expert), instead of moe_permute, moe_ffn
+ * and moe_combine.  An id outside [0, E) adds nothing; an expert that a token
+ * names twice gets both weights.
+ *   tok_off int32 [T+1], topk_ids int32 [T*k_max], topk_w float [T*k_max]: moe_route's
+ *   CSR, at most k_max routes a token (offsets outside [0, T*k_max] are cut off)
+ * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE (T or k_max too large, too), MOE_ERR_UNSUPPORTED,
+ * MOE_ERR_ALIGN, MOE_ERR_WORKSPACE, MOE_ERR_LAUNCH.
+ */
+#define MOE_FEW_MAX_T 16
+typedef struct moe_few_q4 {
+  int32_t group;
+  const void* scales[6];  /* gate, up, down, and the always-on expert's */
+  const void* zeros[6];
+} moe_few_q4;
+
+moe_status moe_forward_few(const moe_desc* desc, const void* x, const void* w_router, const float* router_bias,
+                           const int32_t* k, const void* w_gate, const void* w_up, const void* w_down,
+                           const void* ws_gate, const void* ws_up, const void* ws_down, const moe_few_q4* q4,
+                           void* out, int32_t* stats, int32_t* dev_status, void* ws, size_t ws_bytes,
+                           moe_stream_t stream);
+moe_status moe_experts_few(const moe_desc* desc, const void* x, const int32_t* tok_off, const int32_t* topk_ids,
+                           const float* topk_w, const void* w_gate, const void* w_up, const void* w_down,
+                           const void* ws_gate, const void* ws_up, const void* ws_down, const moe_few_q4* q4,
+                           void* out, void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /*
  * Streaming-read probe (measurement only, not a step of the layer): reads

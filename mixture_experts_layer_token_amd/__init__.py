@@ -17,9 +17,10 @@ from ._lib import (MOE_BF16, MOE_DEV_BAD_K, MOE_F32, MOE_OP_COMBINE, MOE_OP_FFN,
                    MOE_OP_FORWARD, MOE_OP_PERMUTE, MOE_OP_ROUTE, MOE_PATH_AUTO, MOE_PATH_GEMM,
                    MOE_PATH_STREAM, MOE_ROUTER_AUTO, MOE_ROUTER_FLOAT64, MOE_ROUTER_SCREENED, MOE_ROUTER_FUSED, MOE_K_EXACT,
                    MOE_K_BATCH_MAX, MOE_K_ROUND_UP, MOE_OP_FOLD, MOE_OP_PATH, MOE_FOLD_TOKEN, MOE_FOLD_POOL,
-                   MOE_W_ROWMAJOR, MOE_W_BLOCKED64, MOE_OP_ROUTE_GROUPED, MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX,
+                   MOE_W_ROWMAJOR, MOE_W_BLOCKED64, MOE_OP_FEW, MOE_OP_ROUTE_GROUPED, MOE_FEW_MAX_T, MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX,
                    MOE_GROUP_MAX, MOE_GROUP_TOP2, MOE_NORM_RMS, MOE_NORM_LAYER, MOE_GATE_NONE, MOE_GATE_CHANNEL,
-                   MOE_GATE_TOKEN, MOE_GATE_FULL, moe_adapter_desc, moe_desc, moe_norm_desc, moe_route_rule)
+                   MOE_GATE_TOKEN, MOE_GATE_FULL, moe_adapter_desc, moe_desc, moe_few_q4, moe_norm_desc,
+                   moe_q4_desc, moe_route_rule)
 
 __all__ = [
     "MoeError", "make_desc", "pack_weights", "workspace_size", "resolve_path", "alloc_workspace", "moe_route", "moe_permute",
@@ -31,6 +32,8 @@ __all__ = [
     "library_path",
     "make_route_rule", "moe_route_grouped", "make_norm_desc", "moe_norm", "moe_combine_norm", "make_adapter_desc",
     "adapt_workspace_size", "alloc_adapt_workspace", "moe_adapt", "BlockLayer",
+    "Q4Weight", "alloc_q4", "q4_pack", "q4_tile", "moe_q4_pack", "moe_q4_tile", "moe_q4_unpack", "moe_q4_linear",
+    "moe_forward_few", "moe_experts_few",
 ]
 
 _DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
@@ -656,6 +659,149 @@ def moe_adapt(ad, x, x_rows, a, b, ranks, scales, adapter_ids, row_tok, expert_o
           p(ranks, "ranks", _I32, ad.L), p(scales, "scales", _F32, ad.L), p(adapter_ids, "adapter_ids", _I32, T),
           p(row_tok, "row_tok", _I32, rows), p(expert_off, "expert_off", _I32, ad.G + 1),
           p(y_in, "y_in", el, rows * ad.N), p(y_out, "y_out", el, rows * ad.N), p(ws, "ws"), _nbytes(ws))
+
+
+class Q4Weight:
+    """A stack of G matrices [N, K] in 4 bits with group scales, in the library's order
+    (include/moe.h): codes uint8, scales [G, groups, Np] of the element type (Np: N
+    rounded up to 16) and zero points uint8 of that shape, or None."""
+
+    __slots__ = ("desc", "codes", "scales", "zeros")
+
+    def __init__(self, desc: moe_q4_desc, codes: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.Tensor]):
+        self.desc, self.codes, self.scales, self.zeros = desc, codes, scales, zeros
+
+    def __repr__(self):
+        d = self.desc
+        return f"Q4Weight(G={d.G}, N={d.N}, K={d.K}, group={d.group}, zeros={bool(d.zeros)}, dtype={_ELT[d.dtype]})"
+
+
+def alloc_q4(G: int, N: int, K: int, *, group: int = 128, zeros: bool = False, dtype=torch.bfloat16,
+             device="cuda") -> Q4Weight:
+    """An unwritten Q4Weight, for moe_q4_pack or moe_q4_tile."""
+    qd = moe_q4_desc(G, N, K, group, int(bool(zeros)), _DTYPES[dtype])
+    n = [ctypes.c_size_t(0) for _ in range(3)]
+    _check("moe_q4_bytes", _lib.load().moe_q4_bytes(ctypes.byref(qd), *(ctypes.byref(v) for v in n)))
+    shape = (G, -(-K // 128) * 128 // group, -(-N // 16) * 16)
+    codes = torch.empty(n[0].value, dtype=torch.uint8, device=device)
+    return Q4Weight(qd, codes, torch.empty(shape, dtype=dtype, device=device),
+                    torch.empty(shape, dtype=torch.uint8, device=device) if zeros else None)
+
+
+def _q4_args(p, q: Q4Weight, name: str):
+    d = q.desc
+    n = d.G * (-(-d.K // 128) * 128 // d.group) * (-(-d.N // 16) * 16)
+    return (p(q.codes, name + ".codes", torch.uint8, d.G * -(-d.N // 16) * -(-d.K // 128) * 1024),
+            p(q.scales, name + ".scales", _ELT[d.dtype], n), p(q.zeros, name + ".zeros", torch.uint8, n))
+
+
+def moe_q4_pack(w, q: Q4Weight, stream=None) -> None:
+    """Quantises w [G, N, K] into q."""
+    d, p = q.desc, _Args()
+    p.run("moe_q4_pack", stream, d, p(w, "w", _ELT[d.dtype], d.G * d.N * d.K), *_q4_args(p, q, "q"))
+
+
+def q4_pack(w: torch.Tensor, *, group: int = 128, zeros: bool = False, stream=None) -> Q4Weight:
+    """w ([G, N, K] or [N, K]) quantised to 4 bits: per row and `group` inputs one scale,
+    and one zero point with `zeros` (else the codes are symmetric around 8)."""
+    if w.dim() not in (2, 3) or not w.is_contiguous():
+        raise ValueError("q4_pack expects a contiguous [G, N, K] or [N, K] tensor")
+    q = alloc_q4(w.shape[0] if w.dim() == 3 else 1, *w.shape[-2:], group=group, zeros=zeros, dtype=w.dtype,
+                 device=w.device)
+    moe_q4_pack(w, q, stream)
+    return q
+
+
+def moe_q4_tile(codes, scales, zeros, q: Q4Weight, stream=None) -> None:
+    """Re-lays row-major codes uint8 [G, N, K/2] (input 2j in the low half of byte j), scales
+    [G, N, groups] and zeros uint8 [G, N, groups] (or None) into q."""
+    d, p = q.desc, _Args()
+    n = d.G * d.N * -(-d.K // d.group)
+    p.run("moe_q4_tile", stream, d, p(codes, "codes", torch.uint8, d.G * d.N * d.K // 2),
+          p(scales, "scales", _ELT[d.dtype], n), p(zeros, "zeros", torch.uint8, n), *_q4_args(p, q, "q"))
+
+
+def q4_tile(codes: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.Tensor] = None, *, group: int = 128,
+            stream=None) -> Q4Weight:
+    """A Q4Weight of row-major codes ([G, N, K/2] or [N, K/2]), scales and zero points."""
+    if codes.dim() not in (2, 3):
+        raise ValueError("q4_tile expects codes [G, N, K/2] or [N, K/2]")
+    K = 2 * codes.shape[-1]
+    shape = (*codes.shape[:-1], -(-K // group))
+    for name, t in (("scales", scales), ("zeros", zeros)):
+        if t is not None and tuple(t.shape) != shape:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    q = alloc_q4(codes.shape[0] if codes.dim() == 3 else 1, codes.shape[-2], K, group=group, zeros=zeros is not None,
+                 dtype=scales.dtype, device=codes.device)
+    moe_q4_tile(codes, scales, zeros, q, stream)
+    return q
+
+
+def moe_q4_unpack(q: Q4Weight, w, stream=None) -> None:
+    """w [G, N, K] = q's values, rounded once to the element type."""
+    d, p = q.desc, _Args()
+    p.run("moe_q4_unpack", stream, d, *_q4_args(p, q, "q"), p(w, "w", _ELT[d.dtype], d.G * d.N * d.K))
+
+
+def moe_q4_linear(q: Q4Weight, x, y, stream=None) -> None:
+    """y [rows, N] = x [rows, K] times the transpose of q (one matrix), for few rows."""
+    d, p = q.desc, _Args()
+    if x.dim() != 2 or x.shape[1] != d.K:
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected [rows, {d.K}]")
+    rows, el = x.shape[0], _ELT[d.dtype]
+    a = p(x, "x", el)
+    p.run("moe_q4_linear", stream, d, rows, a, *_q4_args(p, q, "q"), p(y, "y", el, rows * d.N))
+
+
+def _few_weights(p, desc, weights):
+    """Addresses of the six weight arguments, and the moe_few_q4 of 4-bit ones."""
+    d, E, I, Is, el = desc.d, desc.E, desc.I, desc.I_shared, _ELT[desc.dtype]
+    names = ("w_gate", "w_up", "w_down", "ws_gate", "ws_up", "ws_down")
+    shapes = ((E, I, d), (E, I, d), (E, d, I), (1, Is, d), (1, Is, d), (1, d, Is))
+    if not isinstance(weights[0], Q4Weight):
+        return [p(w, n, el, s[0] * s[1] * s[2]) for w, n, s in zip(weights, names, shapes)], None
+    q4, out = moe_few_q4(), []
+    first = weights[0].desc
+    q4.group = first.group
+    for i, (w, n, s) in enumerate(zip(weights, names, shapes)):
+        if w is None:
+            out.append(None)
+            continue
+        if not isinstance(w, Q4Weight):
+            raise TypeError(f"{n}: expected a Q4Weight beside w_gate's")
+        qd = w.desc
+        if (qd.G, qd.N, qd.K) != s:
+            raise ValueError(f"{n}: {w!r}, expected G, N, K = {s}")
+        if (qd.group, qd.zeros, qd.dtype) != (first.group, first.zeros, desc.dtype):
+            raise ValueError(f"{n}: {w!r}, its group, zero points and dtype must be the layer's")
+        codes, q4.scales[i], q4.zeros[i] = _q4_args(p, w, n)
+        out.append(codes)
+    return out, q4
+
+
+def moe_forward_few(desc, x, w_router, router_bias, k, w_gate, w_up, w_down, ws_gate, ws_up, ws_down, out, stats,
+                    dev_status, ws, stream=None) -> None:
+    """moe_forward for at most MOE_FEW_MAX_T tokens, without permutation and combine.  The
+    six weights are tensors (in desc's weight layout) or all Q4Weight.
+    ws: alloc_workspace(desc, MOE_OP_FEW)."""
+    T, d, E, el, p = desc.T, desc.d, desc.E, _ELT[desc.dtype], _Args()
+    xp = p(x, "x", el, T * d)
+    w, q4 = _few_weights(p, desc, (w_gate, w_up, w_down, ws_gate, ws_up, ws_down))
+    p.run("moe_forward_few", stream, desc, xp, p(w_router, "w_router", el, E * d),
+          p(router_bias, "router_bias", _F32, E), p(k, "k", _I32, T), *w, q4, p(out, "out", el, T * d),
+          p(stats, "stats", _I32, E + 2), p(dev_status, "dev_status", _I32, 1), p(ws, "ws"), _nbytes(ws))
+
+
+def moe_experts_few(desc, x, tok_off, topk_ids, topk_w, w_gate, w_up, w_down, ws_gate, ws_up, ws_down, out, ws,
+                    stream=None) -> None:
+    """The experts (and the always-on one) of at most MOE_FEW_MAX_T tokens behind given
+    routes, combined: instead of moe_permute, moe_ffn and moe_combine.  Weights and ws as
+    in moe_forward_few."""
+    T, A, el, p = desc.T, desc.T * desc.k_max, _ELT[desc.dtype], _Args()
+    xp = p(x, "x", el, T * desc.d)
+    w, q4 = _few_weights(p, desc, (w_gate, w_up, w_down, ws_gate, ws_up, ws_down))
+    p.run("moe_experts_few", stream, desc, xp, p(tok_off, "tok_off", _I32, T + 1), p(topk_ids, "topk_ids", _I32, A),
+          p(topk_w, "topk_w", _F32, A), *w, q4, p(out, "out", el, T * desc.d), p(ws, "ws"), _nbytes(ws))
 
 
 class BlockLayer:

@@ -15,7 +15,8 @@ MOE_PATH_AUTO, MOE_PATH_STREAM, MOE_PATH_GEMM = 0, 1, 2
 MOE_ROUTER_AUTO, MOE_ROUTER_FLOAT64, MOE_ROUTER_SCREENED, MOE_ROUTER_FUSED = 0, 1, 2, 3
 MOE_K_EXACT, MOE_K_BATCH_MAX, MOE_K_ROUND_UP = 0, 1, 2
 MOE_OP_ROUTE, MOE_OP_PERMUTE, MOE_OP_FFN, MOE_OP_COMBINE, MOE_OP_FORWARD, MOE_OP_FOLD, MOE_OP_PATH = 0, 1, 2, 3, 4, 5, 6
-MOE_OP_ROUTE_GROUPED = 7
+MOE_OP_ROUTE_GROUPED, MOE_OP_FEW = 7, 8
+MOE_FEW_MAX_T = 16
 MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX = 0, 1
 MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
 MOE_NORM_RMS, MOE_NORM_LAYER = 0, 1
@@ -52,8 +53,17 @@ class moe_adapter_desc(ctypes.Structure):
                 ("G", c_i32), ("dtype", c_i32)]
 
 
+class moe_q4_desc(ctypes.Structure):
+    _fields_ = [("G", c_i32), ("N", c_i32), ("K", c_i32), ("group", c_i32), ("zeros", c_i32), ("dtype", c_i32)]
+
+
+class moe_few_q4(ctypes.Structure):
+    _fields_ = [("group", c_i32), ("scales", c_ptr * 6), ("zeros", c_ptr * 6)]
+
+
 _P = ctypes.POINTER(moe_desc)
 _PR, _PN, _PA = (ctypes.POINTER(s) for s in (moe_route_rule, moe_norm_desc, moe_adapter_desc))
+_PQ, _PF = ctypes.POINTER(moe_q4_desc), ctypes.POINTER(moe_few_q4)
 
 # name -> argument types (return type is int: moe_status), as in include/moe.h
 SIGNATURES = {
@@ -91,6 +101,13 @@ SIGNATURES = {
     "moe_combine_norm": [_P, _PN, *[c_ptr] * 13, c_ptr],
     "moe_adapt_workspace_size": [_PA, ctypes.POINTER(c_size)],
     "moe_adapt": [_PA, *[c_ptr] * 12, c_size, c_ptr],
+    "moe_q4_bytes": [_PQ, *[ctypes.POINTER(c_size)] * 3],
+    "moe_q4_pack": [_PQ, *[c_ptr] * 5],
+    "moe_q4_tile": [_PQ, *[c_ptr] * 7],
+    "moe_q4_unpack": [_PQ, *[c_ptr] * 5],
+    "moe_q4_linear": [_PQ, c_i32, *[c_ptr] * 6],
+    "moe_forward_few": [_P, *[c_ptr] * 10, _PF, *[c_ptr] * 4, c_size, c_ptr],
+    "moe_experts_few": [_P, *[c_ptr] * 10, _PF, *[c_ptr] * 2, c_size, c_ptr],
     "moe_status_str": [c_i32],
 }
 

@@ -230,6 +230,43 @@ struct AdaptArgs {
 // v: scratch of rows * R floats (the first product).
 hipError_t launch_adapt(int dtype, const AdaptArgs& p, void* v, hipStream_t st);
 
+// few.hip -- the whole layer for at most MOE_FEW_MAX_T tokens.
+struct FewLaunch {
+  int T, d, E, I, Is, k_max, dtype, blocked;
+  float scale;
+  BudgetPolicy pol;
+  const void* x;
+  const void* w_router;                // null: the routes are given
+  const float* bias;
+  const int32_t* k;
+  const int32_t *in_off, *in_ids;      // given routes
+  const float* in_w;
+  int group;                           // 0: element weights; else inputs of a scale
+  const void *w[6], *scales[6], *zeros[6];  // gate, up, down, and the always-on expert's
+  // scratch
+  double* part;                        // [S][T][E]
+  int S;
+  int32_t *tok_off, *status;           // [T + 1], [1] (the caller's status, if any)
+  int32_t *head, *expert, *mask, *row; // the list of chosen experts
+  float* wt;                           // [T][E]
+  void* h;                             // few_h_bytes
+  int32_t* stats;
+  void* out;
+};
+size_t few_h_bytes(int dtype, int q4, int T, int k_max, int I, int Is);
+hipError_t launch_few(const FewLaunch& a, hipStream_t st);
+
+// q4.hip -- 4-bit weights (rowtile.h has the order of the codes).
+// Codes per byte pair, row-major [G][N][K / 2] -> tiles; scales and zeros [G][N][groups] -> [G][groups][Np].
+struct Q4Shape { int G, N, K, group, dtype; };
+hipError_t launch_q4_pack(const Q4Shape& s, const void* w, void* codes, void* scales, void* zeros, hipStream_t st);
+hipError_t launch_q4_tile(const Q4Shape& s, const void* codes_rm, const void* scales_rm, const void* zeros_rm,
+                          void* codes, void* scales, void* zeros, hipStream_t st);
+hipError_t launch_q4_unpack(const Q4Shape& s, const void* codes, const void* scales, const void* zeros, void* w,
+                            hipStream_t st);
+hipError_t launch_q4_linear(const Q4Shape& s, int rows, const void* x, const void* codes, const void* scales,
+                            const void* zeros, void* y, hipStream_t st);
+
 // moe_abi.cpp -- the forward of moe_forward over a caller-chosen scratch
 // region.  own_regions: `ws` holds only the forward's own regions
 // (forward_scratch_bytes), as the no-allocation entry point supplies;

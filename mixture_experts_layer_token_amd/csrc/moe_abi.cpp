@@ -210,6 +210,27 @@ void plan_grouped(const moe_desc& d, Carver& c, GroupedWs& w) {
   w.wn = p ? w.xn + nx : nullptr;
 }
 
+// The few-token layer: partial logits, the list of chosen experts and their
+// intermediate rows (of the wider of float32's forms: the weights' kind is not in the
+// descriptor).
+struct FewWs { double* part; int splits; int32_t *tok_off, *status, *head, *expert, *mask, *row; float* wt; void* h; };
+moe_status few_ok(const moe_desc& d) {
+  return d.T > MOE_FEW_MAX_T || d.k_max > 64 ? MOE_ERR_SHAPE : MOE_OK;
+}
+void plan_few(const moe_desc& d, Carver& c, FewWs& w) {
+  const size_t cap = std::min<size_t>(d.E, a_cap(d));
+  w.splits = logits_f64_splits(d.T, d.d, d.E, d.dtype);
+  w.part = c.take<double>((size_t)w.splits * d.T * d.E);
+  w.tok_off = c.take<int32_t>((size_t)d.T + 1);
+  w.status = c.take<int32_t>(1);
+  w.head = c.take<int32_t>(2);
+  w.expert = c.take<int32_t>(cap);
+  w.mask = c.take<int32_t>(cap);
+  w.row = c.take<int32_t>(cap);
+  w.wt = c.take<float>((size_t)d.T * d.E);
+  w.h = c.take_bytes(few_h_bytes(d.dtype, 1, d.T, d.k_max, d.I, d.I_shared));
+}
+
 // What moe_forward asks of its workspace: its own regions, and as much as folding
 // and path routing need (a caller may have stored this size).
 size_t forward_need(const moe_desc& d) {
@@ -233,10 +254,14 @@ size_t ws_size(const moe_desc& d, int op) {
     case MOE_OP_FOLD: { FoldScratch w; plan_fold(d, c, w); break; }
     case MOE_OP_PATH: { PathWs w; plan_path(d, c, w); break; }
     case MOE_OP_ROUTE_GROUPED: { GroupedWs w; plan_grouped(d, c, w); break; }
+    case MOE_OP_FEW: { FewWs w; plan_few(d, c, w); break; }
     default: {  // MOE_OP_FORWARD: large enough for every op
       GroupedWs w;
       plan_grouped(d, c, w);
-      return std::max(forward_need(d), c.total());
+      Carver f(nullptr);
+      FewWs fw;
+      if (few_ok(d) == MOE_OK) plan_few(d, f, fw);
+      return std::max({forward_need(d), c.total(), f.total()});
     }
   }
   return c.total();
@@ -375,7 +400,8 @@ extern "C" {
 moe_status moe_workspace_size(const moe_desc* desc, int32_t op, size_t* bytes) {
   MOE_TRY(check_desc(desc));
   if (!bytes) return MOE_ERR_NULL;
-  if (op < MOE_OP_ROUTE || op > MOE_OP_ROUTE_GROUPED) return MOE_ERR_UNSUPPORTED;
+  if (op < MOE_OP_ROUTE || op > MOE_OP_FEW) return MOE_ERR_UNSUPPORTED;
+  if (op == MOE_OP_FEW) MOE_TRY(few_ok(*desc));
   *bytes = ws_size(*desc, op);
   return MOE_OK;
 }
@@ -886,6 +912,184 @@ moe_status moe_forward(const moe_desc* desc, const void* x, const void* w_router
                        int32_t* dev_status, void* ws, size_t ws_bytes, moe_stream_t stream) {
   return moe::forward_impl(desc, x, w_router, router_bias, k, w_gate, w_up, w_down, ws_gate, ws_up, ws_down, out,
                            stats, dev_status, ws, ws_bytes, stream, false);
+}
+
+static moe_status check_q4(const moe_q4_desc* qd) {
+  if (!qd) return MOE_ERR_NULL;
+  const moe_q4_desc& q = *qd;
+  if (q.dtype != MOE_F32 && q.dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (q.group != 32 && q.group != 64 && q.group != 128) return MOE_ERR_UNSUPPORTED;
+  if (q.zeros != 0 && q.zeros != 1) return MOE_ERR_UNSUPPORTED;
+  if (q.G < 0 || q.G >= 1 << 20 || q.N < 1 || q.N > 262144 || q.K < 8 || q.K > 65536 || q.K % 8) return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+struct Q4Bytes { size_t w, codes, scales, zeros; };
+static Q4Bytes q4_sizes(const moe_q4_desc& q) {
+  const size_t nt = (q.N + 15) / 16, kt = (q.K + 127) / 128, ng = kt * (128 / q.group), s = q.dtype == MOE_BF16 ? 2 : 4;
+  return {(size_t)q.G * q.N * q.K * s, (size_t)q.G * nt * kt * 1024, (size_t)q.G * ng * nt * 16 * s,
+          q.zeros ? (size_t)q.G * ng * nt * 16 : 0};
+}
+static Q4Shape q4_shape(const moe_q4_desc& q) { return Q4Shape{q.G, q.N, q.K, q.group, q.dtype}; }
+static bool disjoint(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x + na <= y || y + nb <= x;
+}
+// Codes, scales and zero points of a call: there, aligned, zero points as the descriptor says.
+static moe_status q4_operand(const moe_q4_desc& q, const void* codes, const void* scales, const void* zeros) {
+  if (!codes || !scales || (q.zeros && !zeros)) return MOE_ERR_NULL;
+  if (!q.zeros && zeros) return MOE_ERR_UNSUPPORTED;
+  if (!aligned16(codes) || !aligned16(scales) || !aligned16(zeros)) return MOE_ERR_ALIGN;
+  return MOE_OK;
+}
+
+moe_status moe_q4_bytes(const moe_q4_desc* qd, size_t* codes, size_t* scales, size_t* zeros) {
+  MOE_TRY(check_q4(qd));
+  if (!codes || !scales || !zeros) return MOE_ERR_NULL;
+  const Q4Bytes b = q4_sizes(*qd);
+  *codes = b.codes;
+  *scales = b.scales;
+  *zeros = b.zeros;
+  return MOE_OK;
+}
+
+moe_status moe_q4_pack(const moe_q4_desc* qd, const void* w, void* codes, void* scales, void* zeros,
+                       moe_stream_t stream) {
+  MOE_TRY(check_q4(qd));
+  const moe_q4_desc& q = *qd;
+  if (q.G == 0) return MOE_OK;
+  if (!w) return MOE_ERR_NULL;
+  MOE_TRY(q4_operand(q, codes, scales, zeros));
+  if (!aligned16(w)) return MOE_ERR_ALIGN;
+  const Q4Bytes b = q4_sizes(q);
+  if (!disjoint(w, b.w, codes, b.codes) || !disjoint(w, b.w, scales, b.scales) ||
+      (zeros && !disjoint(w, b.w, zeros, b.zeros)))
+    return MOE_ERR_SHAPE;
+  return launched(launch_q4_pack(q4_shape(q), w, codes, scales, zeros, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_q4_tile(const moe_q4_desc* qd, const void* codes_rm, const void* scales_rm, const void* zeros_rm,
+                       void* codes, void* scales, void* zeros, moe_stream_t stream) {
+  MOE_TRY(check_q4(qd));
+  const moe_q4_desc& q = *qd;
+  if (q.G == 0) return MOE_OK;
+  MOE_TRY(q4_operand(q, codes_rm, scales_rm, zeros_rm));
+  MOE_TRY(q4_operand(q, codes, scales, zeros));
+  const Q4Bytes b = q4_sizes(q);
+  const size_t ng = (size_t)(q.K + q.group - 1) / q.group, s = q.dtype == MOE_BF16 ? 2 : 4;
+  const size_t n = (size_t)q.G * q.N;
+  const void* in[3] = {codes_rm, scales_rm, zeros_rm};
+  const size_t in_b[3] = {n * q.K / 2, n * ng * s, q.zeros ? n * ng : 0};
+  void* out[3] = {codes, scales, zeros};
+  const size_t out_b[3] = {b.codes, b.scales, b.zeros};
+  for (int i = 0; i < 3; ++i)
+    for (int o = 0; o < 3; ++o)
+      if (in[i] && out[o] && !disjoint(in[i], in_b[i], out[o], out_b[o])) return MOE_ERR_SHAPE;
+  return launched(launch_q4_tile(q4_shape(q), codes_rm, scales_rm, zeros_rm, codes, scales, zeros,
+                                 static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_q4_unpack(const moe_q4_desc* qd, const void* codes, const void* scales, const void* zeros, void* w,
+                         moe_stream_t stream) {
+  MOE_TRY(check_q4(qd));
+  const moe_q4_desc& q = *qd;
+  if (q.G == 0) return MOE_OK;
+  if (!w) return MOE_ERR_NULL;
+  MOE_TRY(q4_operand(q, codes, scales, zeros));
+  if (!aligned16(w)) return MOE_ERR_ALIGN;
+  const Q4Bytes b = q4_sizes(q);
+  if (!disjoint(w, b.w, codes, b.codes) || !disjoint(w, b.w, scales, b.scales) ||
+      (zeros && !disjoint(w, b.w, zeros, b.zeros)))
+    return MOE_ERR_SHAPE;
+  return launched(launch_q4_unpack(q4_shape(q), codes, scales, zeros, w, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_q4_linear(const moe_q4_desc* qd, int32_t rows, const void* x, const void* codes, const void* scales,
+                         const void* zeros, void* y, moe_stream_t stream) {
+  MOE_TRY(check_q4(qd));
+  const moe_q4_desc& q = *qd;
+  if (q.G != 1 || rows < 0 || rows > 65536) return MOE_ERR_SHAPE;
+  if (rows == 0) return MOE_OK;
+  if (!x || !y) return MOE_ERR_NULL;
+  MOE_TRY(q4_operand(q, codes, scales, zeros));
+  if (!aligned16(x) || !aligned16(y)) return MOE_ERR_ALIGN;
+  const Q4Bytes b = q4_sizes(q);
+  const size_t s = q.dtype == MOE_BF16 ? 2 : 4, ny = (size_t)rows * q.N * s;
+  if (!disjoint(y, ny, x, (size_t)rows * q.K * s) || !disjoint(y, ny, codes, b.codes) ||
+      !disjoint(y, ny, scales, b.scales) || (zeros && !disjoint(y, ny, zeros, b.zeros)))
+    return MOE_ERR_SHAPE;
+  return launched(launch_q4_linear(q4_shape(q), rows, x, codes, scales, zeros, y, static_cast<hipStream_t>(stream)));
+}
+
+// The operands that the two few-token entry points share.
+static moe_status few_operands(const moe_desc& d, const void* x, const void* const (&w)[6], const moe_few_q4* q4,
+                               void* out, void* ws, size_t ws_bytes, FewLaunch& a) {
+  MOE_TRY(few_ok(d));
+  const int n = d.I_shared ? 6 : 3;
+  if (!tok_ptr(d, x) || !tok_ptr(d, out)) return MOE_ERR_NULL;
+  for (int i = 0; i < n; ++i)
+    if (!w[i]) return MOE_ERR_NULL;
+  if (!aligned16(x) || !aligned16(out)) return MOE_ERR_ALIGN;
+  if (q4 && q4->group != 32 && q4->group != 64 && q4->group != 128) return MOE_ERR_UNSUPPORTED;
+  const size_t out_b = (size_t)d.T * d.d * elt_size(d);
+  if (out_b && !disjoint(out, out_b, x, out_b)) return MOE_ERR_SHAPE;
+  for (int i = 0; i < n; ++i) {
+    if (!aligned16(w[i])) return MOE_ERR_ALIGN;
+    a.w[i] = w[i];
+    if (!q4) continue;
+    if (!q4->scales[i]) return MOE_ERR_NULL;
+    if (!q4->zeros[i] != !q4->zeros[0]) return MOE_ERR_NULL;
+    if (!aligned16(q4->scales[i]) || !aligned16(q4->zeros[i])) return MOE_ERR_ALIGN;
+    a.scales[i] = q4->scales[i];
+    a.zeros[i] = q4->zeros[i];
+  }
+  a.group = q4 ? q4->group : 0;
+  MOE_TRY(check_ws(d, MOE_OP_FEW, ws, ws_bytes));
+  Carver c(ws);
+  FewWs fw;
+  plan_few(d, c, fw);
+  a.T = d.T, a.d = d.d, a.E = d.E, a.I = d.I, a.Is = d.I_shared, a.k_max = d.k_max, a.dtype = d.dtype;
+  a.blocked = d.weight_layout;
+  a.scale = d.routed_scale;
+  a.pol = budget(d);
+  a.x = x;
+  a.out = out;
+  a.part = fw.part, a.S = fw.splits, a.tok_off = fw.tok_off, a.status = fw.status;
+  a.head = fw.head, a.expert = fw.expert, a.mask = fw.mask, a.row = fw.row, a.wt = fw.wt, a.h = fw.h;
+  return MOE_OK;
+}
+
+moe_status moe_forward_few(const moe_desc* desc, const void* x, const void* w_router, const float* router_bias,
+                           const int32_t* k, const void* w_gate, const void* w_up, const void* w_down,
+                           const void* ws_gate, const void* ws_up, const void* ws_down, const moe_few_q4* q4,
+                           void* out, int32_t* stats, int32_t* dev_status, void* ws, size_t ws_bytes,
+                           moe_stream_t stream) {
+  MOE_TRY(check_desc(desc));
+  const moe_desc& d = *desc;
+  if (!w_router || !tok_ptr(d, k)) return MOE_ERR_NULL;
+  if (!aligned16(w_router)) return MOE_ERR_ALIGN;
+  FewLaunch a{};
+  MOE_TRY(few_operands(d, x, {w_gate, w_up, w_down, ws_gate, ws_up, ws_down}, q4, out, ws, ws_bytes, a));
+  a.w_router = w_router;
+  a.bias = router_bias;
+  a.k = k;
+  a.stats = stats;
+  if (dev_status) a.status = dev_status;
+  return launched(launch_few(a, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_experts_few(const moe_desc* desc, const void* x, const int32_t* tok_off, const int32_t* topk_ids,
+                           const float* topk_w, const void* w_gate, const void* w_up, const void* w_down,
+                           const void* ws_gate, const void* ws_up, const void* ws_down, const moe_few_q4* q4,
+                           void* out, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  MOE_TRY(check_desc(desc));
+  const moe_desc& d = *desc;
+  if (!tok_ptr(d, tok_off) || !tok_ptr(d, topk_ids) || !tok_ptr(d, topk_w)) return MOE_ERR_NULL;
+  FewLaunch a{};
+  MOE_TRY(few_operands(d, x, {w_gate, w_up, w_down, ws_gate, ws_up, ws_down}, q4, out, ws, ws_bytes, a));
+  a.in_off = tok_off;
+  a.in_ids = topk_ids;
+  a.in_w = topk_w;
+  return launched(launch_few(a, static_cast<hipStream_t>(stream)));
 }
 
 moe_status moe_probe_read(const void* src, size_t bytes, int32_t nontemporal, int32_t* sink, moe_stream_t stream) {

@@ -1,0 +1,305 @@
+// 4-bit weights with group scales: quantising, re-laying, widening, and the product
+// with few rows (moe_q4_pack, moe_q4_tile, moe_q4_unpack, moe_q4_linear).  rowtile.h
+// has the order of the codes and the product's arithmetic.
+#include "common.h"
+#include "launch.h"
+#include "rowtile.h"
+
+namespace moe {
+
+// ------------------------------------------------------------------- quantising
+// A group of GROUP inputs of a row has the scale
+//   s = ELT(max |w| / 7), codes 8 + rne(w / s)               without zero points
+//   s = ELT((hi - lo) / 15), z = rne(-lo / s), codes z + rne(w / s)   with,
+// lo and hi the group's range with 0 in it, codes held in [1, 15] or [0, 15].  The
+// codes are those of the stored scale; rne takes the exact quotient, ties to even.
+// The quotient's float32 value decides unless it lies within an ulp or so of a tie,
+// where the exact remainder does: w - (j + 1/2) s is exact in float64 (24-bit w,
+// 4-bit times 24-bit product).
+// A group whose values are all 0 (or whose scale rounds to 0) has scale 0; one with a
+// value that is no finite number has scale NaN.
+
+__device__ __forceinline__ float q4_round(float w, float s) {
+  const float q = w / s;
+  const float r = rintf(q);
+  // near a tie the float32 quotient may lie on the wrong side of it, or on it
+  if (fabsf(fabsf(q - r) - 0.5f) > 1e-5f) return r;
+  const float j = floorf(q);
+  const double d = (double)w - (double)s * ((double)j + 0.5);
+  if (d > 0.0) return j + 1.f;
+  if (d < 0.0) return j;
+  return (((int)j) & 1) ? j + 1.f : j;
+}
+
+// One thread quantises the 8 inputs of one code word; the GROUP / 8 threads of a group
+// agree on its range by shuffles.  A workgroup takes 16 rows x 128 inputs (256 threads:
+// row tid / 16, word tid % 16) and writes the codes through LDS in the tile's order.
+template <typename T, int GROUP, bool ZEROS>
+__global__ __launch_bounds__(256) void q4_pack_kernel(const T* __restrict__ w, int G, int N, int K, int kt_n, int nt_n,
+                                                      uint32_t* __restrict__ codes, T* __restrict__ scales,
+                                                      uint8_t* __restrict__ zeros) {
+  __shared__ uint32_t buf[256];
+  constexpr int NG = Q4_K / GROUP;
+  const int tid = threadIdx.x, r = tid >> 4, c = tid & 15;
+  const int kt = blockIdx.x % kt_n, nt = blockIdx.x / kt_n;
+  const int n = nt * TILE_N + r, k = kt * Q4_K + 8 * c;
+  const int Np = nt_n * TILE_N;
+  for (int g = blockIdx.y; g < G; g += gridDim.y) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.f;
+    const bool in = n < N && k < K;
+    if (in) {
+      const T* p = w + ((size_t)g * N + n) * K + k;
+#pragma unroll
+      for (int h = 0; h < (int)sizeof(T) / 2; ++h) {
+        const u32x4_t u = *reinterpret_cast<const u32x4_t*>(p + h * (16 / sizeof(T)));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (sizeof(T) == 2) {
+            v[2 * i] = __uint_as_float(u[i] << 16);
+            v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+          } else {
+            v[4 * h + i] = __uint_as_float(u[i]);
+          }
+        }
+      }
+    }
+    float lo = 0.f, hi = 0.f;
+    int bad = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      lo = fminf(lo, v[j]);
+      hi = fmaxf(hi, v[j]);
+      bad |= !(fabsf(v[j]) < INFINITY);
+    }
+#pragma unroll
+    for (int o = 1; o < GROUP / 8; o <<= 1) {
+      lo = fminf(lo, __shfl_xor(lo, o, 64));
+      hi = fmaxf(hi, __shfl_xor(hi, o, 64));
+      bad |= __shfl_xor(bad, o, 64);
+    }
+    const double range = ZEROS ? ((double)hi - (double)lo) / 15.0 : (double)fmaxf(hi, -lo) / 7.0;
+    const T st = Elt<T>::from_f32(bad ? __uint_as_float(0x7fc00000u) : (float)range);
+    const float s = Elt<T>::to_f32(st);
+    const bool live = s > 0.f && s < INFINITY;
+    const float z = ZEROS ? (live ? fminf(fmaxf(q4_round(-lo, s), 0.f), 15.f) : 0.f) : 8.f;
+    uint32_t word = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float q = z;
+      if (live) q = fminf(fmaxf(q4_round(v[j], s) + z, ZEROS ? 0.f : 1.f), 15.f);
+      word |= (uint32_t)q << (4 * (j >> 1) + 16 * (j & 1));
+    }
+    // word c of row r: instruction c / 4, lane group c % 4
+    buf[((c & 3) * 16 + r) * 4 + (c >> 2)] = word;
+    if ((c & (GROUP / 8 - 1)) == 0) {
+      const size_t o = (((size_t)g * kt_n + kt) * NG + c / (GROUP / 8)) * Np + n;
+      scales[o] = n < N ? st : T(0);
+      if (ZEROS) zeros[o] = (uint8_t)z;
+    }
+    __syncthreads();
+    codes[(((size_t)g * nt_n + nt) * kt_n + kt) * 256 + tid] = buf[tid];
+    __syncthreads();
+  }
+}
+
+// Re-lays row-major codes (input 2 j in the low half of byte j), scales and zero points
+// [G][N][groups]: one thread a code word, as above.
+template <typename T, int GROUP, bool ZEROS>
+__global__ __launch_bounds__(256) void q4_tile_kernel(const uint8_t* __restrict__ src, const T* __restrict__ s_in,
+                                                      const uint8_t* __restrict__ z_in, int G, int N, int K, int kt_n,
+                                                      int nt_n, uint32_t* __restrict__ codes, T* __restrict__ scales,
+                                                      uint8_t* __restrict__ zeros) {
+  __shared__ uint32_t buf[256];
+  constexpr int NG = Q4_K / GROUP;
+  const int tid = threadIdx.x, r = tid >> 4, c = tid & 15;
+  const int kt = blockIdx.x % kt_n, nt = blockIdx.x / kt_n;
+  const int n = nt * TILE_N + r, k = kt * Q4_K + 8 * c;
+  const int Np = nt_n * TILE_N, ng = ceil_div(K, GROUP);
+  for (int g = blockIdx.y; g < G; g += gridDim.y) {
+    uint32_t u = 0;
+    if (n < N && k < K) u = *reinterpret_cast<const uint32_t*>(src + (((size_t)g * N + n) * K + k) / 2);
+    uint32_t word = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) word |= ((u >> (4 * j)) & 15u) << (4 * (j >> 1) + 16 * (j & 1));
+    buf[((c & 3) * 16 + r) * 4 + (c >> 2)] = word;
+    if ((c & (GROUP / 8 - 1)) == 0) {
+      const int gi = kt * NG + c / (GROUP / 8);
+      const size_t o = ((size_t)g * kt_n * NG + gi) * Np + n, i = ((size_t)g * N + n) * ng + gi;
+      const bool in = n < N && gi < ng;
+      scales[o] = in ? s_in[i] : T(0);
+      if (ZEROS) zeros[o] = in ? z_in[i] : 0;
+    }
+    __syncthreads();
+    codes[(((size_t)g * nt_n + nt) * kt_n + kt) * 256 + tid] = buf[tid];
+    __syncthreads();
+  }
+}
+
+// The values s (q - z), rounded once to the element type.
+template <typename T, int GROUP, bool ZEROS>
+__global__ __launch_bounds__(256) void q4_unpack_kernel(const uint32_t* __restrict__ codes,
+                                                        const T* __restrict__ scales,
+                                                        const uint8_t* __restrict__ zeros, int G, int N, int K,
+                                                        int kt_n, int nt_n, T* __restrict__ w) {
+  __shared__ uint32_t buf[256];
+  constexpr int NG = Q4_K / GROUP;
+  const int tid = threadIdx.x, r = tid >> 4, c = tid & 15;
+  const int kt = blockIdx.x % kt_n, nt = blockIdx.x / kt_n;
+  const int n = nt * TILE_N + r, k = kt * Q4_K + 8 * c;
+  const int Np = nt_n * TILE_N;
+  for (int g = blockIdx.y; g < G; g += gridDim.y) {
+    buf[tid] = codes[(((size_t)g * nt_n + nt) * kt_n + kt) * 256 + tid];
+    const size_t o = (((size_t)g * kt_n + kt) * NG + c / (GROUP / 8)) * Np + n;
+    const float s = Elt<T>::to_f32(scales[o]);
+    const int z = ZEROS ? zeros[o] : 8;
+    __syncthreads();
+    if (n < N && k < K) {
+      const uint32_t word = buf[((c & 3) * 16 + r) * 4 + (c >> 2)];
+      f32x4_t v[2];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        v[j >> 2][j & 3] = s * (float)((int)((word >> (4 * (j >> 1) + 16 * (j & 1))) & 15u) - z);
+      T* p = w + ((size_t)g * N + n) * K + k;
+      store_row4(p, v[0]);
+      store_row4(p + 4, v[1]);
+    }
+    __syncthreads();
+  }
+}
+
+// -------------------------------------------------------------- few-row product
+// y[r][n] = sum_k x[r][k] W[n][k].  A workgroup takes 16 outputs of up to 16 rows, its
+// waves a share of K each, and adds their sums in LDS.  (More rows: one more pass over
+// the weights for each 16, which the caches hold for all but the widest.)
+constexpr int QL_NW = 8;
+
+template <class Op>
+__global__ __launch_bounds__(64 * QL_NW) void q4_linear_kernel(const typename Op::elt* __restrict__ x, RowWeights w,
+                                                               int rows, int N, int K,
+                                                               typename Op::elt* __restrict__ y) {
+  typedef typename Op::elt T;
+  __shared__ f32x4_t red[QL_NW * 64];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, col = lane & 15;
+  const int n0 = blockIdx.x * TILE_N, row = blockIdx.y * 16 + col;
+  const int steps = ceil_div(K, Q4_K);
+  const int beg = steps * wave / QL_NW, end = steps * (wave + 1) / QL_NW;
+  const T* xrow = x + (size_t)(row < rows ? row : 0) * K;
+  const typename Op::Src src = Op::tile(w, 0, n0, N, K, 0);
+  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+  for (int s = beg; s < end; ++s) {
+    const typename Op::W v = Op::load(src, s);
+    typename Op::X xv = Op::load_x(xrow, s, K);
+    if (row >= rows) Op::clear(xv);
+    Op::finish_x(xv);
+    Op::mma(acc, v, xv);
+  }
+  red[wave * 64 + lane] = acc;
+  __syncthreads();
+  if (wave > 0) return;
+  f32x4_t v = red[lane];
+#pragma unroll
+  for (int q = 1; q < QL_NW; ++q) v += red[q * 64 + lane];
+  redo_not_finite(v, row < rows, [&](int r, int c) {
+    const T* xr = x + (size_t)(blockIdx.y * 16 + c) * K;
+    const int n = min(n0 + r, N - 1);
+    return wave_dot(K, [&](int k) { return Elt<T>::to_f32(xr[k]) * Op::value(w, 0, n, k, N, K, 0); });
+  });
+  if (row < rows) {
+    T* p = y + (size_t)row * N + n0 + 4 * (lane >> 4);
+    const int left = N - n0 - 4 * (lane >> 4);
+    if (left >= 4 && (N & 3) == 0) {
+      store_row4(p, v);
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (r < left) p[r] = Elt<T>::from_f32(v[r]);
+    }
+  }
+}
+
+// -------------------------------------------------------------------- launches
+
+#define MOE_Q4_GROUP(CALL, G)               \
+  do {                                      \
+    if (zeros) CALL(G, true); else CALL(G, false); \
+  } while (0)
+#define MOE_Q4_ALL(CALL)                        \
+  do {                                          \
+    if (s.group == 32) MOE_Q4_GROUP(CALL, 32);  \
+    else if (s.group == 64) MOE_Q4_GROUP(CALL, 64); \
+    else MOE_Q4_GROUP(CALL, 128);               \
+  } while (0)
+
+template <typename T>
+static void pack_t(const Q4Shape& s, const void* w, void* codes, void* scales, void* zeros, hipStream_t st) {
+  const int kt = ceil_div(s.K, Q4_K), nt = ceil_div(s.N, TILE_N);
+#define MOE_CALL(GR_, ZP_)                                                                                          \
+  hipLaunchKernelGGL((q4_pack_kernel<T, GR_, ZP_>), dim3((uint32_t)kt * nt, min(s.G, 65535)), dim3(256), 0, st, (const T*)w, s.G, s.N, s.K, \
+                     kt, nt, (uint32_t*)codes, (T*)scales, (uint8_t*)zeros)
+  MOE_Q4_ALL(MOE_CALL);
+#undef MOE_CALL
+}
+template <typename T>
+static void tile_t(const Q4Shape& s, const void* c_rm, const void* s_rm, const void* z_rm, void* codes, void* scales,
+                   void* zeros, hipStream_t st) {
+  const int kt = ceil_div(s.K, Q4_K), nt = ceil_div(s.N, TILE_N);
+#define MOE_CALL(GR_, ZP_)                                                                                          \
+  hipLaunchKernelGGL((q4_tile_kernel<T, GR_, ZP_>), dim3((uint32_t)kt * nt, min(s.G, 65535)), dim3(256), 0, st, (const uint8_t*)c_rm, \
+                     (const T*)s_rm, (const uint8_t*)z_rm, s.G, s.N, s.K, kt, nt, (uint32_t*)codes, (T*)scales,      \
+                     (uint8_t*)zeros)
+  MOE_Q4_ALL(MOE_CALL);
+#undef MOE_CALL
+}
+template <typename T>
+static void unpack_t(const Q4Shape& s, const void* codes, const void* scales, const void* zeros, void* w,
+                     hipStream_t st) {
+  const int kt = ceil_div(s.K, Q4_K), nt = ceil_div(s.N, TILE_N);
+#define MOE_CALL(GR_, ZP_)                                                                                          \
+  hipLaunchKernelGGL((q4_unpack_kernel<T, GR_, ZP_>), dim3((uint32_t)kt * nt, min(s.G, 65535)), dim3(256), 0, st,              \
+                     (const uint32_t*)codes, (const T*)scales, (const uint8_t*)zeros, s.G, s.N, s.K, kt, nt, (T*)w)
+  MOE_Q4_ALL(MOE_CALL);
+#undef MOE_CALL
+}
+template <typename T>
+static void linear_t(const Q4Shape& s, int rows, const void* x, const void* codes, const void* scales,
+                     const void* zeros, void* y, hipStream_t st) {
+  const RowWeights w{codes, scales, static_cast<const uint8_t*>(zeros)};
+  const dim3 grid(ceil_div(s.N, TILE_N), ceil_div(rows, 16));
+#define MOE_CALL(GR_, ZP_)                                                                                           \
+  hipLaunchKernelGGL((q4_linear_kernel<Q4Op<T, GR_, ZP_>>), grid, dim3(64 * QL_NW), 0, st, (const T*)x, w, rows, s.N, \
+                     s.K, (T*)y)
+  MOE_Q4_ALL(MOE_CALL);
+#undef MOE_CALL
+}
+
+hipError_t launch_q4_pack(const Q4Shape& s, const void* w, void* codes, void* scales, void* zeros, hipStream_t st) {
+  if (s.G == 0) return hipSuccess;
+  if (s.dtype == DT_BF16) pack_t<bf16_t>(s, w, codes, scales, zeros, st);
+  else pack_t<float>(s, w, codes, scales, zeros, st);
+  return hipGetLastError();
+}
+hipError_t launch_q4_tile(const Q4Shape& s, const void* c_rm, const void* s_rm, const void* z_rm, void* codes,
+                          void* scales, void* zeros, hipStream_t st) {
+  if (s.G == 0) return hipSuccess;
+  if (s.dtype == DT_BF16) tile_t<bf16_t>(s, c_rm, s_rm, z_rm, codes, scales, zeros, st);
+  else tile_t<float>(s, c_rm, s_rm, z_rm, codes, scales, zeros, st);
+  return hipGetLastError();
+}
+hipError_t launch_q4_unpack(const Q4Shape& s, const void* codes, const void* scales, const void* zeros, void* w,
+                            hipStream_t st) {
+  if (s.G == 0) return hipSuccess;
+  if (s.dtype == DT_BF16) unpack_t<bf16_t>(s, codes, scales, zeros, w, st);
+  else unpack_t<float>(s, codes, scales, zeros, w, st);
+  return hipGetLastError();
+}
+hipError_t launch_q4_linear(const Q4Shape& s, int rows, const void* x, const void* codes, const void* scales,
+                            const void* zeros, void* y, hipStream_t st) {
+  if (rows == 0) return hipSuccess;
+  if (s.dtype == DT_BF16) linear_t<bf16_t>(s, rows, x, codes, scales, zeros, y, st);
+  else linear_t<float>(s, rows, x, codes, scales, zeros, y, st);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -1,0 +1,318 @@
+// Few activation rows against streamed weights: operands of 16-row weight tiles.
+//
+// A wave multiplies a tile of 16 weight rows with up to 16 activation rows by
+// 16x16 matrix instructions whose A side is the weights (row lane % 16) and whose
+// B side the activations (column lane % 16); the result holds rows 4 * (lane / 16)
+// + r of column lane % 16.  With few rows the weights' bytes are the time, so an
+// operand's `W` is what one lane loads of a tile for one step of K, `X` the
+// matching activations:
+//
+//   DenseOp<bf16>   64 of K: two 16-byte loads, 2 instructions
+//   DenseOp<float>  32 of K: two 16-byte loads, 8 instructions
+//   Q4Op            128 of K: one 16-byte load of codes and the groups' scales
+//
+// 4-bit weights.  W[n][k] = s (q - z) with one scale s (and zero point z) for a
+// row's group of GROUP inputs.  A code becomes the bf16 value 16 + q without
+// arithmetic: bf16 numbers from 16 to 32 are 1/8 apart, so 0x4180 + 8 q is 16 + q.
+// The matrix instruction sums x (16 + q) over a group, exact products in float32,
+// and the group ends with  acc += s (sum - (16 + z) sum x),  sum x from the same
+// instruction with ones for weights.  (The usual base 128 would lose three more
+// bits to the difference.)  Two mask-and-or operations and shifts for two codes,
+// where a conversion of each would cost four.
+// float32 activations are cut into three bf16 parts of 8 bits each, which hold all
+// 24 bits, and run as three instructions: the float32 matrix instruction takes
+// four times the time of all three.
+//
+// Order of the codes: 1 KB per 16 rows x 128 inputs, lane l's 16 bytes at 16 l:
+// row l % 16, word i (of 4) inputs 32 i + 8 (l / 16) + 0..7, input 2 j in bits 4 j
+// and input 2 j + 1 in bits 16 + 4 j, which the masks above take apart in place.
+// A wave reads a whole tile step as 1 KB in a row.
+#pragma once
+
+#include "common.h"
+
+namespace moe {
+
+constexpr int TILE_N = 16;
+constexpr int Q4_K = 128;                         // inputs of a code tile
+constexpr uint32_t BF16_ONES = 0x3f803f80u;       // two bf16 ones
+
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+
+// A weight matrix stack as a kernel takes it: row-major, blocked, or codes.
+struct RowWeights {
+  const void* w;       // elements, or codes
+  const void* scales;  // ELT [groups][Np]
+  const uint8_t* zeros;  // [groups][Np], null: 8
+};
+
+__host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// Four consecutive elements of a row (8- or 16-byte aligned).
+__device__ __forceinline__ void store_row4(bf16_t* p, f32x4_t v) {
+  u32x2_t o;
+  o.x = (uint32_t)f32_to_bf16(v[0]) | ((uint32_t)f32_to_bf16(v[1]) << 16);
+  o.y = (uint32_t)f32_to_bf16(v[2]) | ((uint32_t)f32_to_bf16(v[3]) << 16);
+  *reinterpret_cast<u32x2_t*>(p) = o;
+}
+__device__ __forceinline__ void store_row4(float* p, f32x4_t v) { *reinterpret_cast<f32x4_t*>(p) = v; }
+
+// Three bf16 parts of a float32 that add up to it (each cut off after 8 bits); a
+// value that is not finite stays whole in the first.
+__device__ __forceinline__ void split3(float f, uint32_t& a, uint32_t& b, uint32_t& c) {
+  const uint32_t u = __float_as_uint(f);
+  const bool fin = (u & 0x7f800000u) != 0x7f800000u;
+  a = fin ? u & 0xffff0000u : (u | ((u & 0x007fffffu) ? 0x00400000u : 0u)) & 0xffff0000u;
+  const float r = fin ? f - __uint_as_float(a) : 0.f;
+  b = __float_as_uint(r) & 0xffff0000u;
+  c = __float_as_uint(r - __uint_as_float(b)) & 0xffff0000u;
+}
+
+template <typename T>
+struct DenseOp {
+  typedef T elt;
+  typedef T hid;                                  // element of the intermediate rows
+  static constexpr int KS = 128 / sizeof(T);      // of K per step
+  static constexpr int LE = 16 / sizeof(T);
+  static constexpr int PLANES = 1;
+  static constexpr bool Q4 = false;
+  struct W { u32x4_t v[2]; };
+  struct X { u32x4_t v[2]; };
+  struct Src { const T* p; int kstr; };
+
+  // Tile of rows n0 .. n0 + 15 of matrix `mat` of a stack of [N][K].
+  __device__ __forceinline__ static Src tile(const RowWeights& m, int mat, int n0, int N, int K, int blocked) {
+    const int lane = threadIdx.x & 63;
+    const T* w = static_cast<const T*>(m.w) + (size_t)mat * N * K;
+    return Src{w + w_offset<T>(n0 + (lane & 15), (lane >> 4) * LE, K, blocked), w_kstep<T>(blocked)};
+  }
+  __device__ __forceinline__ static W load(const Src& s, int step) {
+    const T* p = s.p + (size_t)step * s.kstr;
+    return W{{*reinterpret_cast<const u32x4_t*>(p), *reinterpret_cast<const u32x4_t*>(p + 4 * LE)}};
+  }
+  // Activations of a step: `row` is the lane's row (any row it may read if it has none).
+  __device__ __forceinline__ static X load_x(const T* row, int step) {
+    const T* p = row + step * KS + ((threadIdx.x & 63) >> 4) * LE;
+    return X{{*reinterpret_cast<const u32x4_t*>(p), *reinterpret_cast<const u32x4_t*>(p + 4 * LE)}};
+  }
+  __device__ __forceinline__ static X load_h(const hid* row, size_t, int step) { return load_x(row, step); }
+  __device__ __forceinline__ static void clear(X& x) { x.v[0] = x.v[1] = u32x4_t{0, 0, 0, 0}; }
+  __device__ __forceinline__ static void finish_x(X&) {}
+  __device__ __forceinline__ static void mma(f32x4_t& acc, const W& w, const X& x) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if constexpr (sizeof(T) == 2) {
+        acc = Mfma<bf16_t>::step(w.v[i], x.v[i], acc);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc = mfma_f32_4(__uint_as_float(w.v[i][j]), __uint_as_float(x.v[i][j]), acc);
+      }
+    }
+  }
+  // One element, and one of an intermediate row.
+  __device__ __forceinline__ static float value(const RowWeights& m, int mat, int n, int k, int N, int K, int blocked) {
+    return Elt<T>::to_f32(static_cast<const T*>(m.w)[(size_t)mat * N * K + w_offset<T>(n, k, K, blocked)]);
+  }
+  __device__ __forceinline__ static float h_value(const hid* row, size_t, int k) { return Elt<T>::to_f32(row[k]); }
+  // Four intermediate values (one rounding to the element type, as moe_ffn keeps H).
+  __device__ __forceinline__ static void store_h(hid* p, size_t, f32x4_t v) { store_row4(p, v); }
+};
+
+template <typename T, int GROUP, bool ZEROS>
+struct Q4Op {
+  typedef T elt;
+  typedef bf16_t hid;                             // float32: three planes of it
+  static constexpr int KS = Q4_K;
+  static constexpr int PLANES = sizeof(T) == 2 ? 1 : 3;
+  static constexpr bool Q4 = true;
+  static constexpr int NG = Q4_K / GROUP;         // groups of a step
+  static constexpr int PER = 4 / NG;              // instructions of a group
+  struct W {
+    u32x4_t q;
+    u32x2_t s2[sizeof(T) == 2 ? NG : 1];          // four rows' scales, bf16
+    f32x4_t s4[sizeof(T) == 2 ? 1 : NG];          // or float32
+    uint32_t z[ZEROS ? NG : 1];
+  };
+  struct X { u32x4_t v[PLANES][4]; float sum[NG]; };
+  struct Src { const u32x4_t* q; const T* s; const uint8_t* z; int Np; };
+
+  __device__ __forceinline__ static Src tile(const RowWeights& m, int mat, int n0, int N, int K, int) {
+    const int lane = threadIdx.x & 63, kt = ceil_div(K, Q4_K), nt = ceil_div(N, TILE_N), Np = nt * TILE_N;
+    const size_t g = (size_t)mat * kt * NG * Np + n0 + 4 * (lane >> 4);
+    return Src{static_cast<const u32x4_t*>(m.w) + ((size_t)mat * nt + n0 / TILE_N) * kt * 64 + lane,
+               static_cast<const T*>(m.scales) + g, ZEROS ? m.zeros + g : nullptr, Np};
+  }
+  __device__ __forceinline__ static W load(const Src& s, int step) {
+    W w;
+    w.q = s.q[(size_t)step * 64];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const size_t o = (size_t)(step * NG + g) * s.Np;
+      if constexpr (sizeof(T) == 2) w.s2[g] = *reinterpret_cast<const u32x2_t*>(s.s + o);
+      else w.s4[g] = *reinterpret_cast<const f32x4_t*>(s.s + o);
+      if constexpr (ZEROS) w.z[g] = *reinterpret_cast<const uint32_t*>(s.z + o);
+    }
+    return w;
+  }
+  __device__ __forceinline__ static void set3(X& x, int i, const f32x4_t& a, const f32x4_t& b) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t l[3], h[3];
+      split3(j < 2 ? a[2 * j] : b[2 * j - 4], l[0], l[1], l[2]);
+      split3(j < 2 ? a[2 * j + 1] : b[2 * j - 3], h[0], h[1], h[2]);
+#pragma unroll
+      for (int p = 0; p < PLANES; ++p) x.v[p][i][j] = (l[p] >> 16) | h[p];
+    }
+  }
+  __device__ __forceinline__ static X load_x(const T* row, int step) {
+    return load_x(row, step, 1 << 30);
+  }
+  // Inputs from K on read as zero (K a multiple of 8).
+  __device__ __forceinline__ static X load_x(const T* row, int step, int K) {
+    X x;
+    const int k0 = step * KS + 8 * ((threadIdx.x & 63) >> 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = k0 + 32 * i;
+      const T* p = row + (k < K ? k : 0);
+      if constexpr (sizeof(T) == 2) {
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(p);
+        x.v[0][i] = k < K ? v : u32x4_t{0, 0, 0, 0};
+      } else {
+        f32x4_t a = *reinterpret_cast<const f32x4_t*>(p), b = *reinterpret_cast<const f32x4_t*>(p + 4);
+        if (k >= K) a = b = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        set3(x, i, a, b);
+      }
+    }
+    return x;
+  }
+  // Plane p of an intermediate row lies `plane` elements behind plane p - 1.
+  __device__ __forceinline__ static X load_h(const hid* row, size_t plane, int step) {
+    X x;
+    const hid* p0 = row + step * KS + 8 * ((threadIdx.x & 63) >> 4);
+#pragma unroll
+    for (int p = 0; p < PLANES; ++p)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x.v[p][i] = *reinterpret_cast<const u32x4_t*>(p0 + p * plane + 32 * i);
+    return x;
+  }
+  __device__ __forceinline__ static void clear(X& x) {
+#pragma unroll
+    for (int p = 0; p < PLANES; ++p)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x.v[p][i] = u32x4_t{0, 0, 0, 0};
+  }
+  // The groups' sums of x, in every lane of its column.
+  __device__ __forceinline__ static void finish_x(X& x) {
+    const u32x4_t one = {BF16_ONES, BF16_ONES, BF16_ONES, BF16_ONES};
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      f32x4_t a = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = g * PER; i < (g + 1) * PER; ++i)
+#pragma unroll
+        for (int p = PLANES - 1; p >= 0; --p) a = Mfma<bf16_t>::step(one, x.v[p][i], a);
+      x.sum[g] = a[0];
+    }
+  }
+  // A word's eight codes as bf16 values 16 + q.
+  __device__ __forceinline__ static u32x4_t widen(uint32_t q) {
+    return u32x4_t{((q << 3) & 0x00780078u) | 0x41804180u, ((q >> 1) & 0x00780078u) | 0x41804180u,
+                   ((q >> 5) & 0x00780078u) | 0x41804180u, ((q >> 9) & 0x00780078u) | 0x41804180u};
+  }
+  __device__ __forceinline__ static void mma(f32x4_t& acc, const W& w, const X& x) {
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      f32x4_t a = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = g * PER; i < (g + 1) * PER; ++i) {
+        const u32x4_t b = widen(w.q[i]);
+#pragma unroll
+        for (int p = PLANES - 1; p >= 0; --p) a = Mfma<bf16_t>::step(b, x.v[p][i], a);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float s;
+        if constexpr (sizeof(T) == 2) {
+          const uint32_t u = w.s2[g][r >> 1];
+          s = __uint_as_float((r & 1) ? u & 0xffff0000u : u << 16);
+        } else {
+          s = w.s4[g][r];
+        }
+        const float z = ZEROS ? 16.f + (float)((w.z[g] >> (8 * r)) & 0xffu) : 24.f;
+        acc[r] = fmaf(s, fmaf(-z, x.sum[g], a[r]), acc[r]);
+      }
+    }
+  }
+  __device__ __forceinline__ static float value(const RowWeights& m, int mat, int n, int k, int N, int K, int) {
+    const int kt = ceil_div(K, Q4_K), nt = ceil_div(N, TILE_N), c = k % Q4_K;
+    const uint32_t* w = static_cast<const uint32_t*>(m.w) + (((size_t)mat * nt + n / TILE_N) * kt + k / Q4_K) * 256;
+    const uint32_t q = w[((c / 8 % 4) * 16 + n % TILE_N) * 4 + c / 32] >> (4 * (c % 8 / 2) + 16 * (c & 1));
+    const size_t g = ((size_t)mat * kt * NG + k / GROUP) * (nt * TILE_N) + n;
+    return Elt<T>::to_f32(static_cast<const T*>(m.scales)[g]) * (float)((int)(q & 15u) - (ZEROS ? (int)m.zeros[g] : 8));
+  }
+  __device__ __forceinline__ static float h_value(const hid* row, size_t plane, int k) {
+    float v = 0.f;
+#pragma unroll
+    for (int p = PLANES - 1; p >= 0; --p) v += bf16_to_f32(row[p * plane + k]);
+    return v;
+  }
+  __device__ __forceinline__ static void store_h(hid* p, size_t plane, f32x4_t v) {
+    if constexpr (PLANES == 1) {
+      store_row4(p, v);
+    } else {
+      uint32_t a[4], b[4], c[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) split3(v[r], a[r], b[r], c[r]);
+      *reinterpret_cast<u32x2_t*>(p) = u32x2_t{(a[0] >> 16) | a[1], (a[2] >> 16) | a[3]};
+      *reinterpret_cast<u32x2_t*>(p + plane) = u32x2_t{(b[0] >> 16) | b[1], (b[2] >> 16) | b[3]};
+      *reinterpret_cast<u32x2_t*>(p + 2 * plane) = u32x2_t{(c[0] >> 16) | c[1], (c[2] >> 16) | c[3]};
+    }
+  }
+};
+
+// ---- sums that are not finite ----
+// A matrix instruction multiplies every column with every row: an infinity or NaN among
+// the weights turns the zeros of tokens that have no part in them into NaN, and the
+// codes' difference turns an infinite activation into one.  An output that is not finite
+// is therefore summed again from its own products alone, by a whole wave.
+__device__ __forceinline__ bool not_finite(float v) { return !(fabsf(v) < INFINITY); }
+
+// Sum over k < K of f(k), the same in every lane.
+template <class F>
+__device__ __forceinline__ float wave_dot(int K, F f) {
+  float s = 0.f;
+  for (int k = threadIdx.x & 63; k < K; k += 64) s += f(k);
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o, 64);
+  return s;
+}
+
+// Replaces the values of a tile that are not finite (in lanes with `mine`) by
+// f(row of the tile, column).
+template <class F>
+__device__ __forceinline__ void redo_not_finite(f32x4_t& v, bool mine, F f) {
+  bool bad = false;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) bad |= not_finite(v[r]);
+  uint64_t todo = __ballot(bad && mine);
+  while (todo) {
+    const int l = __builtin_ctzll(todo);
+    todo &= todo - 1;
+    const bool own = (int)(threadIdx.x & 63) == l;
+#pragma unroll 1
+    for (int r = 0; r < 4; ++r) {
+      const float old = __shfl(r == 0 ? v[0] : r == 1 ? v[1] : r == 2 ? v[2] : v[3], l, 64);
+      if (!not_finite(old)) continue;
+      const float s = f(4 * (l >> 4) + r, l & 15);
+      if (own) {
+        if (r == 0) v[0] = s;
+        if (r == 1) v[1] = s;
+        if (r == 2) v[2] = s;
+        if (r == 3) v[3] = s;
+      }
+    }
+  }
+}
+
+}  // namespace moe
