@@ -3,19 +3,24 @@
 // With so few tokens the time is that of the chosen experts' weights and of the
 // launches, so nothing is permuted: every chosen expert's weight tile is multiplied
 // with all tokens at once (one 16-column matrix instruction, rowtile.h) and only the
-// tokens that chose it are kept.
+// tokens that chose it are kept.  Three launches:
 //
-//   logits   float64 partial logits (route_grouped.hip)
-//   select   one workgroup: per token the top k_t and their weights (select.h), then
-//            the list of the experts that some token chose, ascending, with the mask
-//            of its tokens, their weights and its first intermediate row
-//   gate/up  H[row][i] = w_t * SiLU(x_t . Wg_i) * (x_t . Wu_i), one row for each
-//            (expert, token) of the list and one per token for the always-on expert
+//   logits   float64 partial logits (given routes: none)
+//   gate/up  every workgroup: per token the top k_t and their weights, then the list of
+//            the experts that some token chose, ascending, all in LDS; then
+//            H[row][i] = w * SiLU(x_t . Wg_i) * (x_t . Wu_i), with row and w those of the
+//            token's choice of the expert (row t k_max + j for its j-th) and a row per
+//            token for the always-on expert
 //   down     out[t] = sum over the list of H . Wd: one workgroup owns 16 outputs of
 //            all tokens and sums over every expert, so there is no combine
 //
 // The routing weight is applied to H in float32 before its one rounding to the
 // element type, so that the down products of all experts share their accumulators.
+//
+// The code is kept short on purpose: a launch begins with a cold instruction cache, and a
+// 64-byte line of straight code costs some 0.1 us to fetch (a down kernel unrolled over a
+// ring of 8 steps took 16 us for one token where 4 took 11).  Loops are rolled unless their
+// loads must be in flight together.
 #include "common.h"
 #include "launch.h"
 #include "rowtile.h"
@@ -23,419 +28,761 @@
 
 namespace moe {
 
-constexpr int FEW_NW = 8;                 // waves of a workgroup, each a share of K
-constexpr int FEW_NT = 64 * FEW_NW;
-constexpr int FEW_SEL_NT = 1024;          // one wave per token
+constexpr int FEW_T = MOE_FEW_MAX_T;
+constexpr int FEW_S = 8;                  // slices of the partial logits
 
-// The list as the kernels read it (device memory).
-struct FewList {
-  int32_t* head;    // [0] experts of the list, [1] rows
-  int32_t* expert;  // [cap]
-  int32_t* mask;    // [cap] tokens, bit t
-  int32_t* row;     // [cap] first row of H
-  float* w;         // [T][E] weights, where a mask has its bit
-};
-
-// The list of the experts that some token chose, from mask[e] in LDS.
-template <int NT>
-__device__ void few_list(const uint32_t* mask, int E, const FewList& L, int32_t* stats, int32_t* wsum) {
-  const int tid = threadIdx.x, per = (E + NT - 1) / NT;
-  int act = 0, rows = 0;
-  for (int j = 0; j < per; ++j) {
-    const int e = tid * per + j;
-    const uint32_t m = e < E ? mask[e] : 0;
-    act += m != 0;
-    rows += __popc(m);
-  }
-  const int ia = block_scan_incl<NT>(act, wsum), ir = block_scan_incl<NT>(rows, wsum);
-  int at = ia - act, row = ir - rows;
-  for (int j = 0; j < per; ++j) {
-    const int e = tid * per + j;
-    if (e >= E) break;
-    const uint32_t m = mask[e];
-    if (stats) stats[e] = __popc(m);
-    if (!m) continue;
-    L.expert[at] = e;
-    L.mask[at] = (int32_t)m;
-    L.row[at] = row;
-    ++at;
-    row += __popc(m);
-  }
-  if (tid == NT - 1) {
-    L.head[0] = ia;
-    L.head[1] = ir;
-    if (stats) {
-      stats[E] = ia;
-      stats[E + 1] = ir;
-    }
-  }
-}
-
-// KPL logits a lane (E <= 64 * KPL).
-template <int KPL>
-__global__ __launch_bounds__(FEW_SEL_NT) void few_select_kernel(const double* __restrict__ part, int S,
-                                                                const float* __restrict__ bias,
-                                                                const int32_t* __restrict__ tok_off, int T, int E,
-                                                                int k_max, float scale, FewList L, int32_t* stats) {
-  extern __shared__ uint64_t few_smem[];
-  __shared__ int32_t wsum[FEW_SEL_NT / 64];
-  const int tid = threadIdx.x, t = tid >> 6, lane = tid & 63;
-  uint32_t* mask = reinterpret_cast<uint32_t*>(few_smem);
-  uint64_t* scratch = few_smem + (E + 1) / 2 + (size_t)t * (k_max + 1);
-  float* wts = reinterpret_cast<float*>(few_smem + (E + 1) / 2 + (size_t)T * (k_max + 1)) + t * k_max;
-  for (int e = tid; e < E; e += FEW_SEL_NT) mask[e] = 0;
-  __syncthreads();
-  if (t < T) {
-    const int kt = tok_off[t + 1] - tok_off[t];
-    uint32_t key[KPL];
-#pragma unroll
-    for (int s = 0; s < KPL; ++s) {
-      const int e = lane + 64 * s;
-      key[s] = 0;
-      if (e < E) {
-        double l = 0.0;
-#pragma unroll 1
-        for (int q = 0; q < S; ++q) l += part[((size_t)q * T + t) * E + e];
-        if (bias) l += (double)bias[e];
-        key[s] = logit_key((float)l);
-      }
-    }
-    if (kt > 0) {
-      int pos[KPL];
-#pragma unroll
-      for (int s = 0; s < KPL; ++s) pos[s] = -1;
-      wave_topk_softmax_emit<KPL>(key, kt, scale, [&](int j, int s) { pos[s] = j; }, wts, scratch);
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-#pragma unroll
-      for (int s = 0; s < KPL; ++s)
-        if (pos[s] >= 0) {
-          const int e = lane + 64 * s;
-          L.w[t * E + e] = wts[pos[s]];
-          atomicOr(&mask[e], 1u << t);
-        }
-    }
-  }
-  __syncthreads();
-  few_list<FEW_SEL_NT>(mask, E, L, stats, wsum);
-}
-
-// The list from given routes.  An expert that a token names twice counts once with
-// both weights; ids outside [0, E) are skipped; offsets outside the arrays are cut.
-__global__ __launch_bounds__(FEW_SEL_NT) void few_routes_kernel(const int32_t* __restrict__ tok_off,
-                                                                const int32_t* __restrict__ ids,
-                                                                const float* __restrict__ w, int T, int E, int k_max,
-                                                                FewList L) {
-  extern __shared__ uint64_t few_smem[];
-  __shared__ int32_t wsum[FEW_SEL_NT / 64];
-  const int tid = threadIdx.x, t = tid >> 6, lane = tid & 63;
-  uint32_t* mask = reinterpret_cast<uint32_t*>(few_smem);
-  for (int e = tid; e < E; e += FEW_SEL_NT) mask[e] = 0;
-  __syncthreads();
-  if (t < T) {
-    const int cap = T * k_max;
-    const int beg = min(max(tok_off[t], 0), cap), n = min(min(max(tok_off[t + 1], beg), cap) - beg, k_max);
-    const int id = lane < n ? ids[beg + lane] : -1;
-    const float mine = lane < n ? w[beg + lane] : 0.f;
-    bool first = id >= 0 && id < E;
-    float sum = 0.f;
-    for (int j = 0; j < n; ++j) {  // k_max <= 64: one entry a lane
-      const int other = __shfl(id, j, 64);
-      const float wj = __shfl(mine, j, 64);
-      if (other == id) {
-        sum += wj;
-        if (j < lane) first = false;
-      }
-    }
-    if (first) {
-      L.w[t * E + id] = sum;
-      atomicOr(&mask[id], 1u << t);
-    }
-  }
-  __syncthreads();
-  few_list<FEW_SEL_NT>(mask, E, L, nullptr, wsum);
-}
-
-// What the FFN kernels take.
-struct FewFfn {
-  int T, d, E, I, Is, blocked;
+// What the launches take.
+struct FewArgs {
+  int T, d, E, I, Is, k_max, blocked;
+  int stride;               // workgroups of the gate/up launch
+  int hw;                   // width of a row of H: max(I, Is)
+  int zero_row;             // rows: T k_max choices, T of the always-on expert, one of zeros
+  // routing: partial logits, or given routes (part null)
+  BudgetPolicy pol;
+  float scale;
+  const double* part;
+  const float* bias;
+  const int32_t* k;
+  const int32_t *off, *ids;
+  const float* wts;
+  int32_t *stats, *status;
+  int32_t* n_list;          // the list for the down launch: its length,
+  int32_t* expert;          // the experts,
+  uint32_t* rows;           // and their tokens' rows [.][16] (16 bits each)
   const void* x;
-  RowWeights w[6];  // gate, up, down, and the always-on expert's
-  FewList L;
-  void* h;          // rows of width max(I, Is), in planes
-  size_t plane;     // elements of a plane
-  int hw;           // width of an intermediate row
+  void* h;                  // in planes
+  size_t plane;             // elements of a plane
   void* out;
+  RowWeights w[6];          // gate, up, down, and the always-on expert's
 };
+// a or b, by value: a reference to either would put both into memory.
+__device__ __forceinline__ RowWeights pick(bool first, RowWeights a, RowWeights b) {
+  return RowWeights{first ? a.w : b.w, first ? a.scales : b.scales, first ? a.zeros : b.zeros};
+}
 
-// Sum of the waves' accumulators of one tile, by one wave.
-__device__ __forceinline__ f32x4_t few_sum(const f32x4_t* red) {
+// The list of chosen experts, in LDS.
+struct FewList {
+  // while it is made (in the place of what the products need later)
+  uint32_t* keys;   // [T][E]
+  uint32_t* mask;   // [E] tokens of an expert, bit t
+  uint32_t* all;    // [E][8] as rows, of every expert
+  // what stays
+  int32_t* expert;  // [min(E, T k_max)] ascending
+  uint32_t* rows;   // [min(E, T k_max)][8] rows of H of its tokens, 16 bits each; zero_row: none
+  float* w;         // [T k_max] weight of a choice
+};
+__host__ __device__ __forceinline__ int few_scratch_words(int T, int E) { return ((T + 9) * E + 3) & ~3; }
+__host__ __device__ __forceinline__ int few_kept_words(int T, int E, int k_max) {
+  return 9 * min(E, T * k_max) + T * k_max;
+}
+__device__ __forceinline__ FewList few_carve(uint32_t* scratch, uint32_t* kept, int T, int E, int k_max) {
+  const int cap = min(E, T * k_max);
+  FewList L;
+  L.keys = scratch;
+  L.mask = scratch + T * E;
+  L.all = L.mask + E;
+  L.expert = reinterpret_cast<int32_t*>(kept);
+  L.rows = kept + cap;
+  L.w = reinterpret_cast<float*>(kept + 9 * cap);
+  return L;
+}
+__device__ __forceinline__ int few_row(const FewList& L, int idx, int t) {
+  return reinterpret_cast<const uint16_t*>(L.rows)[idx * FEW_T + t];
+}
+
+// Largest of one value per lane, in every lane: row shifts, then the rows' last lanes
+// passed on, which leaves the maximum in lane 63.
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+#define MOE_DPP_MAX(ctrl, rows) \
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, rows, 0xf, false))
+  MOE_DPP_MAX(0x111, 0xf);  // row_shr:1, 2, 4, 8
+  MOE_DPP_MAX(0x112, 0xf);
+  MOE_DPP_MAX(0x114, 0xf);
+  MOE_DPP_MAX(0x118, 0xf);
+  MOE_DPP_MAX(0x142, 0xa);  // row_bcast:15, 31
+  MOE_DPP_MAX(0x143, 0xc);
+#undef MOE_DPP_MAX
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+// A token's choice from its keys (E <= 64 KPL), by one wave: the largest key kt times,
+// ties to the lowest expert (select.h's keys and order; its radix search takes fewer steps
+// from some 20 experts a token on, but many times the code).  Lane j ends with the j-th
+// choice (kt <= 64) and its logit.
+template <int KPL>
+__device__ __forceinline__ void few_choose(const uint32_t* keys, int E, int kt, int& mine, float& logit) {
   const int lane = threadIdx.x & 63;
-  f32x4_t v = red[lane];
+  uint32_t key[KPL];
 #pragma unroll
-  for (int w = 1; w < FEW_NW; ++w) v += red[w * 64 + lane];
+  for (int s = 0; s < KPL; ++s) key[s] = lane + 64 * s < E ? keys[lane + 64 * s] : 0;  // 0: none, or chosen
+#pragma unroll 1
+  for (int j = 0; j < kt; ++j) {
+    uint32_t m = key[0];
+#pragma unroll
+    for (int s = 1; s < KPL; ++s) m = max(m, key[s]);
+    m = wave_max_u32(m);
+    int e = 0;
+#pragma unroll
+    for (int s = KPL - 1; s >= 0; --s) {
+      const uint64_t has = __ballot(key[s] == m);
+      e = has ? 64 * s + __builtin_ctzll(has) : e;
+    }
+#pragma unroll
+    for (int s = 0; s < KPL; ++s) key[s] = e == lane + 64 * s ? 0 : key[s];
+    mine = lane == j ? e : mine;
+    logit = lane == j ? key_logit(m) : logit;
+  }
+}
+
+// The list, by a whole workgroup; every workgroup builds the same one, and the first
+// stores it for the down launch.  Returns the number of experts.
+template <int NT>
+__device__ __forceinline__ int few_list(const FewArgs& p, const FewList& L) {
+  constexpr int NW = NT / 64;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const bool first = blockIdx.x == 0;
+  const uint32_t none = (uint32_t)p.zero_row * 0x10001u;
+  int v = 0;
+  if (p.part) {
+    v = lane < p.T ? p.k[lane] : 0;
+#pragma unroll 1
+    for (int i = tid; i < p.T * p.E; i += NT) {
+      const int e = i % p.E;
+      double part[FEW_S];
+#pragma unroll
+      for (int q = 0; q < FEW_S; ++q) part[q] = p.part[(size_t)q * (p.T * p.E) + i];
+      double l = 0.0;
+      const float b = p.bias ? p.bias[e] : 0.f;
+#pragma unroll
+      for (int q = 0; q < FEW_S; ++q) l += part[q];
+      if (p.bias) l += (double)b;
+      L.keys[i] = max(logit_key((float)l), 1u);
+    }
+  }
+#pragma unroll 1
+  for (int i = tid; i < 9 * p.E; i += NT) L.mask[i] = i < p.E ? 0 : none;  // and the rows behind them
+  __syncthreads();
+  int exec = 0;
+  if (p.part) {
+    const bool ok = budget_valid(v, p.k_max);
+    const int kb = p.pol.policy == K_BATCH_MAX ? (int)wave_max_u32(ok ? (uint32_t)v : 0u) : 0;
+    exec = lane < p.T ? budget_exec(v, p.k_max, p.pol, kb) : 0;
+    const bool bad = __ballot(!ok) != 0;
+    if (first && p.status && tid == 0) p.status[0] = bad ? MOE_DEV_BAD_K_BIT : 0;
+  }
+#pragma unroll 1
+  for (int t = wave; t < p.T; t += NW) {
+    int e = -1;
+    float w = 0.f;
+    if (p.part) {
+      const int kt = __builtin_amdgcn_readlane(exec, t);
+      if (p.E <= 256) few_choose<4>(L.keys + t * p.E, p.E, kt, e, w);
+      else few_choose<16>(L.keys + t * p.E, p.E, kt, e, w);
+      const float ex = e >= 0 ? expf(w - __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(w)))) : 0.f;
+      float sum = ex;
+#pragma unroll 1
+      for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 64);
+      w = ex * (p.scale / sum);
+    } else {
+      // Given routes (k_max <= 64: one entry a lane).  An expert that the token names twice
+      // counts once with both weights; ids outside [0, E) are skipped; offsets outside the
+      // arrays are cut.
+      const int cap = p.T * p.k_max;
+      const int beg = min(max(p.off[t], 0), cap), n = min(min(max(p.off[t + 1], beg), cap) - beg, p.k_max);
+      const int id = lane < n ? p.ids[beg + lane] : -1;
+      const float mine = lane < n ? p.wts[beg + lane] : 0.f;
+      e = id >= 0 && id < p.E ? id : -1;
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        const bool same = __shfl(id, j, 64) == id;
+        const float wj = __shfl(mine, j, 64);
+        w += same ? wj : 0.f;
+        if (same && j < lane) e = -1;
+      }
+    }
+    if (e >= 0) {
+      L.w[t * p.k_max + lane] = w;
+      reinterpret_cast<uint16_t*>(L.all)[e * FEW_T + t] = (uint16_t)(t * p.k_max + lane);
+      atomicOr(&L.mask[e], 1u << t);
+    }
+  }
+  __syncthreads();
+  // a wave lists the experts of every NW-th chunk of 64, and counts what lies before them
+  // itself
+  int base = 0, rows = 0;
+#pragma unroll 1
+  for (int c = 0; 64 * c < p.E; ++c) {
+    const int e = 64 * c + lane;
+    const uint32_t m = e < p.E ? L.mask[e] : 0;
+    const uint64_t act = __ballot(m != 0);
+    if (c % NW == wave && m) {
+      const int at = base + __popcll(act & ((1ull << lane) - 1ull));
+      L.expert[at] = e;
+      if (first) p.expert[at] = e;
+    }
+    if (first && wave == 0 && p.stats) {
+      if (e < p.E) p.stats[e] = __popc(m);
+      rows += __popc(m);
+    }
+    base += __popcll(act);
+  }
+  if (first && wave == 0) {
+    if (lane == 0) p.n_list[0] = base;
+    if (p.stats) {
+#pragma unroll 1
+      for (int o = 32; o >= 1; o >>= 1) rows += __shfl_xor(rows, o, 64);
+      if (lane == 0) {
+        p.stats[p.E] = base;
+        p.stats[p.E + 1] = rows;
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int i = tid; i < base * 8; i += NT) {
+    const uint32_t r = L.all[L.expert[i >> 3] * 8 + (i & 7)];
+    L.rows[i] = r;
+    if (first) p.rows[i] = r;
+  }
+  __syncthreads();
+  return base;
+}
+
+// The waves' accumulators of a tile in LDS, [waves][64 lanes][4]; the sum of output n (of
+// 16) for token t, in wave order.
+template <int NW>
+__device__ __forceinline__ float few_sum(const f32x4_t* red, int n, int t) {
+  const float* r = reinterpret_cast<const float*>(red) + ((n >> 2) * 16 + t) * 4 + (n & 3);
+  float v = 0.f;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) v += r[w * 256];
   return v;
 }
 
-// Gate and up: a workgroup takes 16 intermediate columns of one expert at a time, its
-// waves a share of d each, whose activations stay in registers from tile to tile when
-// XS steps a wave cover d.
-template <class Op, int XS, int NB>
-__global__ __launch_bounds__(FEW_NT) void few_gateup_kernel(FewFfn p) {
-  __shared__ f32x4_t red[2][2][FEW_NW * 64];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int col = lane & 15;
-  typedef typename Op::elt T;
-  static_assert((2 * XS) % NB == 0, "the ring repeats with the tiles");
-  const int n_list = p.L.head[0], n_rows = p.L.head[1];
-  const int ci = p.I / TILE_N, cs = p.Is / TILE_N;
-  const int n_items = n_list * ci + cs;
-  const int steps = p.d / Op::KS;
-  const int chunks = ceil_div(steps, FEW_NW * XS);
-  const T* xrow = static_cast<const T*>(p.x) + (size_t)(col < p.T ? col : 0) * p.d;
+// Rows of zeros for the tokens without a part in an expert.
+template <class Op, int NT>
+__device__ __forceinline__ void few_zero_row(const FewArgs& p) {
+  typename Op::hid* const h = static_cast<typename Op::hid*>(p.h);
+#pragma unroll 1
+  for (int q = 0; q < Op::PLANES; ++q)
+#pragma unroll 1
+    for (int i = threadIdx.x; i < p.hw; i += NT) h[q * p.plane + (size_t)p.zero_row * p.hw + i] = 0;
+}
 
-  struct Tiles { typename Op::Src a[2]; };
-  auto tiles_of = [&](int item) {
-    const bool sh = item >= n_list * ci;
-    const int idx = sh ? 0 : item / ci, n0 = (sh ? item - n_list * ci : item % ci) * TILE_N;
-    const int mat = sh ? 0 : p.L.expert[idx], N = sh ? p.Is : p.I;
-    Tiles t;
+// H of one value of an item: output j of the tile, token t.
+template <class Op>
+__device__ __forceinline__ void few_store_h(const FewArgs& p, const FewList& L, bool sh, int idx, int n, int t, float g,
+                                            float u, int row) {
+  const float rw = sh ? 1.f : L.w[row];
+  Op::store_h(static_cast<typename Op::hid*>(p.h) + (size_t)row * p.hw + n, p.plane, rw * (silu(g) * u));
+}
+
+// ---- element weights ----
+// A wave streams its share of K through a ring of its own in LDS: copies of whole 128-byte
+// lines straight from memory, past the caches (weights are read once), NB steps of 16 rows
+// x 128 bytes ahead and on into the workgroup's next item, the activations of a step beside
+// its weights.  So the loop is short, needs no barrier, and its loads may carry the
+// non-temporal hint, which would fetch lines twice that two register loads take by halves
+// (reads of 2 GiB: 7.2 TB/s with it, 6.4 without).
+constexpr int FEW_RW = 8;                 // waves of a workgroup
+constexpr int FEW_RT = 64 * FEW_RW;
+
+// One 1 KB copy: eight rows of 128 bytes, lane l to 16 l.
+template <int AUX>
+__device__ __forceinline__ void few_copy(const void* base, uint32_t lane_off, char* lds) {
+  __builtin_amdgcn_global_load_lds((gbl_ptr_t)(static_cast<const char*>(base) + lane_off), (lds_ptr_t)lds, 16, 0, AUX);
+}
+// Row (0..7) and byte of a lane in copy q of a 16-row tile, its chunks swizzled as lds_off
+// reads them.
+__device__ __forceinline__ int few_copy_row(int q) { return 8 * q + ((int)(threadIdx.x & 63) >> 3); }
+__device__ __forceinline__ uint32_t few_copy_byte(int q) {
+  return 16 * ((threadIdx.x & 7) ^ lds_swz(few_copy_row(q)));
+}
+__device__ __forceinline__ void few_barrier() {
+  lgkm_wait0();
+  compiler_fence();
+  __builtin_amdgcn_s_barrier();
+  compiler_fence();
+}
+
+// A step's operand from LDS.
+template <typename T>
+__device__ __forceinline__ typename DenseOp<T>::W few_frag(const char* tile) {
+  const int lane = threadIdx.x & 63;
+  typename DenseOp<T>::W w;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) t.a[h] = Op::tile(p.w[h + (sh ? 3 : 0)], mat, n0, N, p.d, p.blocked);
-    return t;
+  for (int i = 0; i < 2; ++i) w.v[i] = *reinterpret_cast<const u32x4_t*>(tile + lds_off(lane & 15, (lane >> 4) + 4 * i));
+  return w;
+}
+
+// Gate and up: a workgroup takes every p.stride-th item, 16 intermediate columns of one
+// expert.  XQ: copies of the activations, 1 for up to 8 tokens.
+template <typename T, int NB, int XQ>
+__global__ __launch_bounds__(FEW_RT) void few_gateup_dense_kernel(FewArgs p) {
+  typedef DenseOp<T> Op;
+  constexpr int SLOT = 4096 + 1024 * XQ, PER = 4 + XQ;
+  extern __shared__ char few_ring[];  // the rings (the list's scratch before), the waves' sums, the list
+  const RowWeights wg = p.w[0], wu = p.w[1], sg = p.w[3], su = p.w[4];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int ring_bytes = max(FEW_RW * NB * SLOT, few_scratch_words(p.T, p.E) * 4);
+  f32x4_t* const red = reinterpret_cast<f32x4_t*>(few_ring + ring_bytes);
+  const FewList L = few_carve(reinterpret_cast<uint32_t*>(few_ring), reinterpret_cast<uint32_t*>(red + 2 * FEW_RT), p.T,
+                              p.E, p.k_max);
+  const int n_list = few_list<FEW_RT>(p, L);
+  if (blockIdx.x == 0) few_zero_row<Op, FEW_RT>(p);
+  const int ci = p.I / TILE_N, routed = n_list * ci;
+  const int n_items = routed + p.Is / TILE_N;
+  const int steps = p.d / Op::KS, kstr = w_kstep<T>(p.blocked) * (int)sizeof(T);
+  const int beg = steps * wave / FEW_RW, end = steps * (wave + 1) / FEW_RW;
+  const int pitch = (p.blocked ? Op::KS : p.d) * (int)sizeof(T);
+  uint32_t woff[2], xoff[XQ];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) woff[q] = (uint32_t)few_copy_row(q) * pitch + few_copy_byte(q);
+#pragma unroll
+  for (int q = 0; q < XQ; ++q)  // rows behind the last token repeat it; their sums are not used
+    xoff[q] = (uint32_t)min(few_copy_row(q), p.T - 1) * p.d * (uint32_t)sizeof(T) + few_copy_byte(q);
+  char* const ring = few_ring + wave * NB * SLOT;
+
+  // requests: a step of the item `want`; behind the last item its last step again
+  int want = blockIdx.x, rs = beg;
+  const char *rg = nullptr, *ru = nullptr;
+  auto seek = [&]() {
+    const bool sh = want >= routed;
+    const int idx = sh ? 0 : (int)((uint32_t)want / (uint32_t)ci);
+    const int n0 = (sh ? want - routed : want - idx * ci) * TILE_N, N = sh ? p.Is : p.I;
+    const int mat = sh ? 0 : __builtin_amdgcn_readfirstlane(L.expert[idx]);
+    const size_t o = ((size_t)mat * N * p.d + Op::corner(n0, p.d, p.blocked)) * sizeof(T);
+    rg = static_cast<const char*>(sh ? sg.w : wg.w) + o;
+    ru = static_cast<const char*>(sh ? su.w : wu.w) + o;
   };
+  auto request = [&](int slot) {
+    char* const to = ring + slot * SLOT;
+    const size_t o = (size_t)rs * kstr;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      few_copy<2>(rg + o, woff[q], to + 1024 * q);
+      few_copy<2>(ru + o, woff[q], to + 2048 + 1024 * q);
+    }
+#pragma unroll
+    for (int q = 0; q < XQ; ++q) few_copy<0>(static_cast<const char*>(p.x) + rs * 128, xoff[q], to + 4096 + 1024 * q);
+    if (rs + 1 < end) {
+      ++rs;
+    } else if (want + p.stride < n_items) {
+      want += p.stride;
+      rs = beg;
+      seek();
+    }
+  };
+  const bool live = beg < end && want < n_items;
+  if (live) {
+    seek();
+#pragma unroll 1
+    for (int i = 0; i < NB; ++i) request(i);
+  }
+  int slot = 0;
+#pragma unroll 1
+  for (int item = blockIdx.x; item < n_items; item += p.stride) {
+    f32x4_t ga = {0.f, 0.f, 0.f, 0.f}, ua = ga;
+#pragma unroll 1
+    for (int s = beg; s < end; ++s) {
+      vm_wait<PER * (NB - 1)>();
+      compiler_fence();
+      const char* const from = ring + slot * SLOT;
+      const typename Op::W gw = few_frag<T>(from), uw = few_frag<T>(from + 2048), xw = few_frag<T>(from + 4096);
+      lgkm_wait0();  // read before the slot is filled again
+      compiler_fence();
+      request(slot);
+      slot = slot + 1 == NB ? 0 : slot + 1;
+      const typename Op::X x{{xw.v[0], xw.v[1]}};
+      Op::mma(ga, gw, x);
+      Op::mma(ua, uw, x);
+    }
+    red[wave * 64 + lane] = ga;
+    red[FEW_RT + wave * 64 + lane] = ua;
+    few_barrier();
+    if (wave < 4) {
+      const bool sh = item >= routed;
+      const int idx = sh ? 0 : (int)((uint32_t)item / (uint32_t)ci);
+      const int n0 = (sh ? item - routed : item - idx * ci) * TILE_N;
+      const int j = tid & 15, t = tid >> 4;
+      const float g = few_sum<FEW_RW>(red, j, t), u = few_sum<FEW_RW>(red + FEW_RT, j, t);
+      const int row = sh ? p.T * p.k_max + t : few_row(L, idx, t);
+      if (t < p.T && row != p.zero_row) few_store_h<Op>(p, L, sh, idx, n0 + j, t, g, u, row);
+    }
+    few_barrier();
+  }
+  vm_wait<0>();  // no copy into LDS outlives the workgroup
+}
 
-  int item = blockIdx.x;
-  if (item >= n_items) return;
-  typename Op::X x[XS];
-  int par = 0;
-  for (; item < n_items; item += gridDim.x, par ^= 1) {
-    const Tiles cur = tiles_of(item);
-    f32x4_t acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-    for (int c = 0; c < chunks; ++c) {
-      const int c0 = (int)((long long)steps * c / chunks), c1 = (int)((long long)steps * (c + 1) / chunks);
-      const int beg = c0 + (c1 - c0) * wave / FEW_NW, n = c0 + (c1 - c0) * (wave + 1) / FEW_NW - beg;
-      if (chunks > 1 || item == (int)blockIdx.x) {
+// The list that the gate/up launch stored, into LDS: experts, and their tokens' rows.
+template <int NT>
+__device__ __forceinline__ int few_load_list(const FewArgs& p, uint32_t* to) {
+  const int cap = min(p.E, p.T * p.k_max);
+#pragma unroll 1
+  for (int i = threadIdx.x; i < 9 * cap; i += NT)  // what lies behind the list is not used
+    to[i] = i < cap ? (uint32_t)p.expert[i] : p.rows[i - cap];
+  return __builtin_amdgcn_readfirstlane(p.n_list[0]);
+}
+
+// An output that is not finite, from its own token's products alone.
+template <class Op>
+__device__ __forceinline__ float few_down_again(const FewArgs& p, const int32_t* l_expert, const uint16_t* row_of,
+                                                int n_list, int n, int t) {
+  float sum = 0.f;
+#pragma unroll 1
+  for (int i = 0; i <= n_list; ++i) {
+    const bool sh = i == n_list;
+    if (sh && !p.Is) break;
+    const int row = sh ? p.T * p.k_max + t : row_of[i * FEW_T + t];
+    if (row == p.zero_row) continue;
+    const int mat = sh ? 0 : l_expert[i], K = sh ? p.Is : p.I;
+    const typename Op::hid* const hr = static_cast<const typename Op::hid*>(p.h) + (size_t)row * p.hw;
+    sum += wave_dot(K, [&](int k) {
+      return Op::h_value(hr, p.plane, k) * Op::value(pick(sh, p.w[5], p.w[2]), mat, n, k, p.d, K, p.blocked);
+    });
+  }
+  return sum;
+}
+
+// Down: a workgroup owns 16 outputs of every token; its waves share the steps of all the
+// experts' intermediate columns, laid end to end.  Tokens without a part in an expert read
+// the row of zeros.
+template <typename T, int NB, int XQ>
+__global__ __launch_bounds__(FEW_RT) void few_down_dense_kernel(FewArgs p) {
+  typedef DenseOp<T> Op;
+  constexpr int SLOT = 2048 + 1024 * XQ, PER = 2 + XQ;
+  extern __shared__ char few_ring[];  // the rings, the waves' sums, the list
+  const RowWeights wr = p.w[2], ws = p.w[5];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int n0 = blockIdx.x * TILE_N;
+  f32x4_t* const red = reinterpret_cast<f32x4_t*>(few_ring + FEW_RW * NB * SLOT);
+  const int32_t* const l_expert = reinterpret_cast<const int32_t*>(red + FEW_RT);
+  const uint16_t* const row_of = reinterpret_cast<const uint16_t*>(l_expert + min(p.E, p.T * p.k_max));
+  const int n_list = few_load_list<FEW_RT>(p, reinterpret_cast<uint32_t*>(red + FEW_RT));
+  __syncthreads();
+  const int spe = p.I / Op::KS, routed = n_list * spe, steps = routed + p.Is / Op::KS;
+  const int beg = steps * wave / FEW_RW, end = steps * (wave + 1) / FEW_RW;
+  const int kstr = w_kstep<T>(p.blocked) * (int)sizeof(T);
+  char* const ring = few_ring + wave * NB * SLOT;
+
+  // requests: step st of expert idx of the list (behind it: the always-on expert)
+  int idx = beg < routed ? (int)((uint32_t)beg / (uint32_t)spe) : n_list, st = beg - min(idx * spe, routed), left = end - beg;
+  const char* rw = nullptr;
+  uint32_t woff[2], xoff[XQ];
+  auto seek = [&]() {
+    const bool sh = idx >= n_list;
+    const int K = sh ? p.Is : p.I;
+    const int mat = sh ? 0 : __builtin_amdgcn_readfirstlane(l_expert[idx]);
+    rw = static_cast<const char*>(sh ? ws.w : wr.w) +
+         ((size_t)mat * p.d * K + Op::corner(n0, K, p.blocked)) * sizeof(T);
+    const int pitch = (p.blocked ? Op::KS : K) * (int)sizeof(T);
 #pragma unroll
-        for (int s = 0; s < XS; ++s) {
-          x[s] = Op::load_x(xrow, min(beg + s, steps - 1));
-          if (col >= p.T) Op::clear(x[s]);
-          Op::finish_x(x[s]);
-        }
-      }
-      typename Op::W ring[NB];
-      auto step_of = [&](int f) { return min(beg + f % XS, steps - 1); };
+    for (int q = 0; q < 2; ++q) woff[q] = (uint32_t)few_copy_row(q) * pitch + few_copy_byte(q);
 #pragma unroll
-      for (int f = 0; f < NB; ++f) ring[f] = Op::load(cur.a[f / XS], step_of(f));
+    for (int q = 0; q < XQ; ++q) {
+      const int t = few_copy_row(q);
+      const int row = sh ? (t < p.T ? p.T * p.k_max + t : p.zero_row) : row_of[idx * FEW_T + t];
+      xoff[q] = (uint32_t)row * p.hw * (uint32_t)sizeof(T) + few_copy_byte(q);
+    }
+  };
+  auto request = [&](int slot) {
+    char* const to = ring + slot * SLOT;
 #pragma unroll
-      for (int f = 0; f < 2 * XS; ++f) {
-        if (f % XS < n) Op::mma(acc[f / XS], ring[f % NB], x[f % XS]);
-        if (f + NB < 2 * XS) ring[f % NB] = Op::load(cur.a[(f + NB) / XS], step_of(f + NB));
+    for (int q = 0; q < 2; ++q) few_copy<2>(rw + (size_t)st * kstr, woff[q], to + 1024 * q);
+#pragma unroll
+    for (int q = 0; q < XQ; ++q) few_copy<0>(static_cast<const char*>(p.h) + st * 128, xoff[q], to + 2048 + 1024 * q);
+    if (left > 1) {  // behind the end: the last step again
+      --left;
+      ++st;
+      if (idx < n_list && st == spe) {
+        ++idx;
+        st = 0;
+        seek();
       }
     }
-    red[par][0][wave * 64 + lane] = acc[0];
-    red[par][1][wave * 64 + lane] = acc[1];
-    __syncthreads();
-    if (wave == 0) {
-      f32x4_t g = few_sum(red[par][0]), u = few_sum(red[par][1]);
-      const bool sh = item >= n_list * ci;
-      const int idx = sh ? 0 : item / ci, n0 = (sh ? item - n_list * ci : item % ci) * TILE_N;
-      const uint32_t m = sh ? (1u << p.T) - 1u : (uint32_t)p.L.mask[idx];
-      if constexpr (Op::Q4) {
-        auto again = [&](const RowWeights& w) {
-          return [&, mat = sh ? 0 : p.L.expert[idx]](int r, int c) {
-            const T* xr = static_cast<const T*>(p.x) + (size_t)c * p.d;
-            return wave_dot(p.d, [&](int k) {
-              return Elt<T>::to_f32(xr[k]) * Op::value(w, mat, n0 + r, k, sh ? p.Is : p.I, p.d, p.blocked);
-            });
-          };
-        };
-        redo_not_finite(g, (m >> col) & 1, again(p.w[sh ? 3 : 0]));
-        redo_not_finite(u, (m >> col) & 1, again(p.w[sh ? 4 : 1]));
-      }
-      if ((m >> col) & 1) {
-        const int row = (sh ? n_rows : p.L.row[idx]) + __popc(m & ((1u << col) - 1u));
-        const float w = sh ? 1.f : p.L.w[col * p.E + p.L.expert[idx]];
-        f32x4_t v;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = w * (silu(g[r]) * u[r]);
-        Op::store_h(static_cast<typename Op::hid*>(p.h) + (size_t)row * p.hw + n0 + 4 * (lane >> 4), p.plane, v);
-      }
+  };
+  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+  if (beg < end) {
+    seek();
+#pragma unroll 1
+    for (int i = 0; i < NB; ++i) request(i);
+    int slot = 0;
+#pragma unroll 1
+    for (int s = beg; s < end; ++s) {
+      vm_wait<PER * (NB - 1)>();
+      compiler_fence();
+      const char* const from = ring + slot * SLOT;
+      const typename Op::W w = few_frag<T>(from), xw = few_frag<T>(from + 2048);
+      lgkm_wait0();
+      compiler_fence();
+      request(slot);
+      slot = slot + 1 == NB ? 0 : slot + 1;
+      Op::mma(acc, w, typename Op::X{{xw.v[0], xw.v[1]}});
     }
+    vm_wait<0>();  // no copy into LDS outlives the workgroup
+  }
+  red[wave * 64 + lane] = acc;
+  __syncthreads();
+  if (wave < 4) {
+    const int j = tid & 15, t = tid >> 4;
+    float v = few_sum<FEW_RW>(red, j, t);
+    redo_not_finite(v, t < p.T, [&](int l) {
+      return few_down_again<Op>(p, l_expert, row_of, n_list, n0 + (l & 15), (wave * 64 + l) >> 4);
+    });
+    if (t < p.T) static_cast<T*>(p.out)[(size_t)t * p.d + n0 + j] = Elt<T>::from_f32(v);
   }
 }
 
-// Down: a workgroup owns 16 outputs of every token; its waves share the steps of all
-// the experts' intermediate columns, laid end to end.
-template <class Op, int NB>
-__global__ __launch_bounds__(FEW_NT) void few_down_kernel(FewFfn p) {
-  __shared__ f32x4_t red[FEW_NW * 64];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int col = lane & 15;
-  const int n_list = p.L.head[0], n_rows = p.L.head[1];
-  const int spe = p.I / Op::KS, routed = n_list * spe, steps = routed + p.Is / Op::KS;
-  const int beg = (int)((long long)steps * wave / FEW_NW), n = (int)((long long)steps * (wave + 1) / FEW_NW) - beg;
-  const int n0 = blockIdx.x * TILE_N;
-  const typename Op::hid* h = static_cast<const typename Op::hid*>(p.h);
+// ---- 4-bit weights ----
+// A wave's share of K a step at a time, straight into registers: a step's codes are 1 KB in
+// a row and its arithmetic (16 rows x 128 codes made bf16, scaled per group) is what takes
+// the time.
+constexpr int FEW_QW = 16;                // waves of a workgroup
+constexpr int FEW_QT = 64 * FEW_QW;
 
-  // where the next requested step lies
-  int idx, st;
-  bool ok;
-  typename Op::Src src;
-  const typename Op::hid* hrow;
-  auto seek = [&]() {
-    const bool sh = idx >= n_list;
-    const uint32_t m = sh ? (1u << p.T) - 1u : (uint32_t)p.L.mask[idx];
-    ok = (m >> col) & 1;
-    src = Op::tile(p.w[sh ? 5 : 2], sh ? 0 : p.L.expert[idx], n0, p.d, sh ? p.Is : p.I, p.blocked);
-    hrow = h + (size_t)((sh ? n_rows : p.L.row[idx]) + (ok ? __popc(m & ((1u << col) - 1u)) : 0)) * p.hw;
-  };
-  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-  if (n > 0) {
-    idx = beg < routed ? beg / spe : n_list;
-    st = beg < routed ? beg % spe : beg - routed;
-    seek();
-    typename Op::W ring[NB];
-    typename Op::X xr[NB];
-    bool live[NB];
-    int at = 0;
-    auto next = [&]() {
-      if (at + 1 < n) {
-        ++at;
-        ++st;
-        if (idx < n_list && st == spe) {
-          ++idx;
-          st = 0;
-          seek();
-        }
-      }
-    };
-#pragma unroll
-    for (int f = 0; f < NB; ++f) {
-      ring[f] = Op::load(src, st);
-      xr[f] = Op::load_h(hrow, p.plane, st);
-      live[f] = ok;
-      next();
+template <class Op>
+__global__ __launch_bounds__(FEW_QT) void few_gateup_q4_kernel(FewArgs p) {
+  extern __shared__ uint32_t few_smem[];  // the waves' sums (the list's scratch before), the list
+  typedef typename Op::elt T;
+  const RowWeights wg = p.w[0], wu = p.w[1], sg = p.w[3], su = p.w[4];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int col = lane & 15;
+  const int steps = p.d / Op::KS;
+  const T* const x0 = static_cast<const T*>(p.x);
+  // columns without a token repeat the first one's activations; their sums are not used
+  const uint32_t xrow = (uint32_t)(col < p.T ? col : 0) * p.d * (uint32_t)sizeof(T);
+  f32x4_t* const red = reinterpret_cast<f32x4_t*>(few_smem);
+  const FewList L = few_carve(few_smem, few_smem + max(2 * FEW_QT * 4, few_scratch_words(p.T, p.E)), p.T, p.E, p.k_max);
+  const int n_list = few_list<FEW_QT>(p, L);
+  const int ci = p.I / TILE_N, routed = n_list * ci;
+  const int n_items = routed + p.Is / TILE_N;
+  if (blockIdx.x == 0) few_zero_row<Op, FEW_QT>(p);
+#pragma unroll 1
+  for (int item = blockIdx.x; item < n_items; item += p.stride) {
+    const bool sh = item >= routed;
+    const int idx = sh ? 0 : (int)((uint32_t)item / (uint32_t)ci);
+    const int n0 = (sh ? item - routed : item - idx * ci) * TILE_N, N = sh ? p.Is : p.I;
+    const int mat = sh ? 0 : __builtin_amdgcn_readfirstlane(L.expert[idx]);
+    const typename Op::Src gsrc = Op::tile(pick(sh, sg, wg), mat, n0, N, p.d, p.blocked);
+    const typename Op::Src usrc = Op::tile(pick(sh, su, wu), mat, n0, N, p.d, p.blocked);
+    f32x4_t ga = {0.f, 0.f, 0.f, 0.f}, ua = ga;
+#pragma unroll 1
+    for (int s = wave; s < steps; s += FEW_QW) {
+      const typename Op::W gw = Op::load(gsrc, s), uw = Op::load(usrc, s);
+      typename Op::X x = Op::load_x(x0, xrow, s);
+      Op::finish_x(x);
+      Op::mma(ga, gw, x);
+      Op::mma(ua, uw, x);
     }
-    for (int s0 = 0; s0 < n; s0 += NB) {
+    red[wave * 64 + lane] = ga;
+    red[FEW_QT + wave * 64 + lane] = ua;
+    __syncthreads();
+    if (wave < 4) {
+      const int j = tid & 15, t = tid >> 4;
+      float g = few_sum<FEW_QW>(red, j, t), u = few_sum<FEW_QW>(red + FEW_QT, j, t);
+      const int row = sh ? p.T * p.k_max + t : few_row(L, idx, t);
+      const bool mine = t < p.T && row != p.zero_row;
+      auto again = [&](RowWeights rw, float& val) {
+        redo_not_finite(val, mine, [&](int l) {
+          const T* xr = x0 + (size_t)((wave * 64 + l) >> 4) * p.d;
+          const int nn = n0 + (l & 15);
+          return wave_dot(p.d, [&](int k) {
+            return Elt<T>::to_f32(xr[k]) * Op::value(rw, mat, nn, k, N, p.d, p.blocked);
+          });
+        });
+      };
+      again(pick(sh, sg, wg), g);
+      again(pick(sh, su, wu), u);
+      if (mine) few_store_h<Op>(p, L, sh, idx, n0 + j, t, g, u, row);
+    }
+    __syncthreads();
+  }
+}
+
+template <class Op, int U>
+__global__ __launch_bounds__(FEW_QT) void few_down_q4_kernel(FewArgs p) {
+  extern __shared__ uint32_t few_smem[];
+  __shared__ f32x4_t red[FEW_QT];
+  const RowWeights wr = p.w[2], ws = p.w[5];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int col = lane & 15, n0 = blockIdx.x * TILE_N;
+  const int n_list = few_load_list<FEW_QT>(p, few_smem);
+  const int32_t* const l_expert = reinterpret_cast<const int32_t*>(few_smem);
+  const uint16_t* const row_of = reinterpret_cast<const uint16_t*>(few_smem + min(p.E, p.T * p.k_max));
+  const typename Op::hid* const h = static_cast<const typename Op::hid*>(p.h);
+  const int spe = p.I / Op::KS, routed = n_list * spe, steps = routed + p.Is / Op::KS;
+  const int beg = steps * wave / FEW_QW, end = steps * (wave + 1) / FEW_QW;
+  int idx = beg < routed ? (int)((uint32_t)beg / (uint32_t)spe) : n_list, st = beg - min(idx * spe, routed);
+  const int own = col < p.T ? p.T * p.k_max + col : p.zero_row;  // the always-on expert's
+  __syncthreads();
+
+  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int s = beg; s < end; s += U) {
+    typename Op::W w[U];
+    typename Op::X x[U];
 #pragma unroll
-      for (int f = 0; f < NB; ++f) {
-        if (s0 + f < n) {
-          typename Op::X x = xr[f];
-          if (!live[f]) Op::clear(x);
-          Op::finish_x(x);
-          Op::mma(acc, ring[f], x);
-        }
-        ring[f] = Op::load(src, st);
-        xr[f] = Op::load_h(hrow, p.plane, st);
-        live[f] = ok;
-        next();
+    for (int u = 0; u < U; ++u) {
+      const bool sh = idx >= n_list;
+      const int i = sh ? 0 : idx;
+      const int e = sh ? 0 : __builtin_amdgcn_readfirstlane(l_expert[i]);
+      const int row = sh ? own : row_of[i * FEW_T + col];
+      w[u] = Op::load(Op::tile(pick(sh, ws, wr), e, n0, p.d, sh ? p.Is : p.I, p.blocked), st);
+      x[u] = Op::load_h(h, (uint32_t)row * p.hw * (uint32_t)sizeof(typename Op::hid), p.plane, st);
+      // the last step again behind the end
+      const bool more = s + u + 1 < end, turn = more && !sh && st + 1 == spe;
+      st = turn ? 0 : st + (more ? 1 : 0);
+      idx += turn ? 1 : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (s + u < end) {
+        Op::finish_x(x[u]);
+        Op::mma(acc, w[u], x[u]);
       }
+  }
+  red[wave * 64 + lane] = acc;
+  __syncthreads();
+  if (wave < 4) {
+    const int j = tid & 15, t = tid >> 4;
+    float v = few_sum<FEW_QW>(red, j, t);
+    redo_not_finite(v, t < p.T, [&](int l) {
+      return few_down_again<Op>(p, l_expert, row_of, n_list, n0 + (l & 15), (wave * 64 + l) >> 4);
+    });
+    if (t < p.T) static_cast<typename Op::elt*>(p.out)[(size_t)t * p.d + n0 + j] = Elt<typename Op::elt>::from_f32(v);
+  }
+}
+
+// Partial logits part[FEW_S][T][E] in float64 on the f64 matrix instruction: a workgroup
+// takes 16 experts and a slice of d for all tokens, its 8 waves a share each, added in
+// wave order.  (Lane l supplies the values of row l % 16 from LE (l / 16) on of a step,
+// value i of every lane in instruction i.)
+constexpr int FEW_LW = 8;
+typedef double f64x4_t __attribute__((ext_vector_type(4)));
+
+template <typename T>
+__global__ __launch_bounds__(64 * FEW_LW) void few_logits_kernel(const T* __restrict__ x, const T* __restrict__ w,
+                                                                 int T_, int d, int E, double* __restrict__ part) {
+  constexpr int LE = 16 / (int)sizeof(T), KS = 4 * LE;
+  __shared__ f64x4_t red[FEW_LW * 64];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int l16 = lane & 15, lg = lane >> 4;
+  const int e0 = blockIdx.x * 16, steps = d / KS, nq = FEW_S * FEW_LW, q = blockIdx.y * FEW_LW + wave;
+  const int s0 = steps * q / nq, s1 = steps * (q + 1) / nq;
+  const T* wr = w + (size_t)min(e0 + l16, E - 1) * d + lg * LE;
+  const T* xr = x + (size_t)min(l16, T_ - 1) * d + lg * LE;
+  f64x4_t acc = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll 4
+  for (int s = s0; s < s1; ++s) {
+    const u32x4_t wv = *reinterpret_cast<const u32x4_t*>(wr + (size_t)s * KS);
+    const u32x4_t xv = *reinterpret_cast<const u32x4_t*>(xr + (size_t)s * KS);
+#pragma unroll
+    for (int i = 0; i < LE; ++i) {
+      double a, b;
+      if constexpr (sizeof(T) == 2) {
+        a = (double)__uint_as_float((i & 1) ? wv[i / 2] & 0xffff0000u : wv[i / 2] << 16);
+        b = (double)__uint_as_float((i & 1) ? xv[i / 2] & 0xffff0000u : xv[i / 2] << 16);
+      } else {
+        a = (double)__uint_as_float(wv[i]);
+        b = (double)__uint_as_float(xv[i]);
+      }
+      acc = __builtin_amdgcn_mfma_f64_16x16x4f64(a, b, acc, 0, 0, 0);
     }
   }
   red[wave * 64 + lane] = acc;
   __syncthreads();
-  if (wave == 0) {
-    f32x4_t v = few_sum(red);
-    redo_not_finite(v, col < p.T, [&](int r, int c) {
-      float s = 0.f;
-      for (int i = 0; i <= n_list; ++i) {
-        const bool sh = i == n_list;
-        const uint32_t m = sh ? (p.Is ? (1u << p.T) - 1u : 0u) : (uint32_t)p.L.mask[i];
-        if (!((m >> c) & 1)) continue;
-        const typename Op::hid* hr = h + (size_t)((sh ? n_rows : p.L.row[i]) + __popc(m & ((1u << c) - 1u))) * p.hw;
-        const int mat = sh ? 0 : p.L.expert[i], K = sh ? p.Is : p.I;
-        s += wave_dot(K, [&](int k) {
-          return Op::h_value(hr, p.plane, k) * Op::value(p.w[sh ? 5 : 2], mat, n0 + r, k, p.d, K, p.blocked);
-        });
-      }
-      return s;
-    });
-    if (col < p.T) store_row4(static_cast<typename Op::elt*>(p.out) + (size_t)col * p.d + n0 + 4 * (lane >> 4), v);
+  // acc[i]: expert 4 i + lg, token l16; a thread sums one value
+  if (threadIdx.x < 256) {
+    const int src = threadIdx.x & 63, i = threadIdx.x >> 6;
+    const int e = e0 + 4 * i + (src >> 4), t = src & 15;
+    double s = 0.0;
+#pragma unroll
+    for (int v = 0; v < FEW_LW; ++v) s += red[v * 64 + src][i];
+    if (t < T_ && e < E) part[((size_t)blockIdx.y * T_ + t) * E + e] = s;
   }
+}
+
+// No tokens: no counts, a status of 0.
+__global__ void few_none_kernel(int32_t* stats, int n, int32_t* status) {
+  for (int i = threadIdx.x; i < n && stats; i += blockDim.x) stats[i] = 0;
+  if (threadIdx.x == 0 && status) status[0] = 0;
 }
 
 // -------------------------------------------------------------------- launches
 
-// LDS of the selection: the masks, and each token's scratch and weights.
-static size_t few_sel_lds(int T, int E, int k_max) {
-  return (size_t)((E + 1) / 2) * 8 + (size_t)T * (k_max + 1) * 8 + (size_t)T * k_max * 4;
-}
-
-template <class Op, int XS, int NB, int NBD>
-static hipError_t few_ffn(const FewFfn& p, int cap_items, hipStream_t st) {
-  const int grid = min(256, cap_items);
-  if (grid > 0) hipLaunchKernelGGL((few_gateup_kernel<Op, XS, NB>), dim3(grid), dim3(FEW_NT), 0, st, p);
-  hipLaunchKernelGGL((few_down_kernel<Op, NBD>), dim3(p.d / TILE_N), dim3(FEW_NT), 0, st, p);
+template <class K>
+static hipError_t few_launch(K kernel, int grid, int threads, size_t lds, const FewArgs& p, hipStream_t st) {
+  hipLaunchKernelGGL(kernel, dim3(grid), dim3(threads), lds, st, p);
   return hipGetLastError();
 }
 
-// Activation steps that stay in a wave's registers: the fewest that hold its share of d.
-template <class Op, int A, int NA, int B, int NB_, int C, int NC, int NBD>
-static hipError_t few_ffn_xs(const FewFfn& p, int cap_items, hipStream_t st) {
-  const int need = ceil_div(p.d / Op::KS, FEW_NW);
-  if (need <= A) return few_ffn<Op, A, NA, NBD>(p, cap_items, st);
-  if (need <= B) return few_ffn<Op, B, NB_, NBD>(p, cap_items, st);
-  return few_ffn<Op, C, NC, NBD>(p, cap_items, st);
+template <typename T, int NBG, int NBD, int XQ>
+static hipError_t few_dense(const FewArgs& p, hipStream_t st) {
+  const int scratch = few_scratch_words(p.T, p.E) * 4, kept = few_kept_words(p.T, p.E, p.k_max) * 4;
+  const size_t lds = (size_t)max(FEW_RW * NBG * (4096 + 1024 * XQ), scratch) + 2 * FEW_RT * 16 + kept;
+  const hipError_t e =
+      few_launch(few_gateup_dense_kernel<T, NBG, XQ>, p.stride, FEW_RT, lds, p, st);
+  if (e != hipSuccess) return e;
+  return few_launch(few_down_dense_kernel<T, NBD, XQ>, p.d / TILE_N, FEW_RT,
+                    (size_t)FEW_RW * NBD * (2048 + 1024 * XQ) + FEW_RT * 16 + 36 * min(p.E, p.T * p.k_max), p, st);
+}
+
+template <class Op, int U>
+static hipError_t few_q4(const FewArgs& p, hipStream_t st) {
+  const size_t lds = ((size_t)max(2 * FEW_QT * 4, few_scratch_words(p.T, p.E)) + few_kept_words(p.T, p.E, p.k_max)) * 4;
+  const hipError_t e = few_launch(few_gateup_q4_kernel<Op>, p.stride, FEW_QT, lds, p, st);
+  if (e != hipSuccess) return e;
+  return few_launch(few_down_q4_kernel<Op, U>, p.d / TILE_N, FEW_QT, (size_t)36 * min(p.E, p.T * p.k_max), p, st);
 }
 
 template <typename T>
-static hipError_t few_ffn_type(const FewFfn& p, int group, int zeros, int cap, hipStream_t st) {
-  if (group == 0) return few_ffn_xs<DenseOp<T>, 4, 8, 8, 8, 14, 7, 4>(p, cap, st);
-#define MOE_FEW_Q4(G, Z)                                                                      \
-  do {                                                                                        \
-    if constexpr (sizeof(T) == 2) return few_ffn_xs<Q4Op<T, G, Z>, 2, 4, 4, 8, 7, 7, 4>(p, cap, st); \
-    else return few_ffn<Q4Op<T, G, Z>, 2, 4, 2>(p, cap, st);                                  \
-  } while (0)
-#define MOE_FEW_G(G) do { if (zeros) MOE_FEW_Q4(G, true); else MOE_FEW_Q4(G, false); } while (0)
-  if (group == 32) MOE_FEW_G(32);
-  if (group == 64) MOE_FEW_G(64);
-  MOE_FEW_G(128);
-#undef MOE_FEW_G
-#undef MOE_FEW_Q4
+static hipError_t few_ffn(const FewArgs& p, int group, int zeros, hipStream_t st) {
+  if (group == 0) return p.T <= 8 ? few_dense<T, 3, 4, 1>(p, st) : few_dense<T, 2, 4, 2>(p, st);
+  constexpr int U = sizeof(T) == 2 ? 2 : 1;
+  if (group == 32) return zeros ? few_q4<Q4Op<T, 32, true>, U>(p, st) : few_q4<Q4Op<T, 32, false>, U>(p, st);
+  if (group == 64) return zeros ? few_q4<Q4Op<T, 64, true>, U>(p, st) : few_q4<Q4Op<T, 64, false>, U>(p, st);
+  return zeros ? few_q4<Q4Op<T, 128, true>, U>(p, st) : few_q4<Q4Op<T, 128, false>, U>(p, st);
 }
 
+size_t few_part_count(int T, int E) { return (size_t)FEW_S * T * E; }
 size_t few_h_bytes(int dtype, int q4, int T, int k_max, int I, int Is) {
-  const size_t rows = (size_t)T * k_max + (Is ? T : 0);
+  const size_t rows = (size_t)T * k_max + T + 1;  // choices, the always-on expert's, zeros
   return rows * max(I, Is) * (dtype == DT_BF16 ? 2 : (q4 ? 6 : 4));
 }
 
 hipError_t launch_few(const FewLaunch& a, hipStream_t st) {
-  if (a.T == 0 && !a.w_router) return hipSuccess;
-  FewFfn p;
-  p.T = a.T, p.d = a.d, p.E = a.E, p.I = a.I, p.Is = a.Is, p.blocked = a.blocked;
+  if (a.T == 0) {
+    if (a.stats || a.status)
+      hipLaunchKernelGGL(few_none_kernel, dim3(1), dim3(256), 0, st, a.stats, a.E + 2, a.status);
+    return hipGetLastError();
+  }
+  FewArgs p{};
+  p.T = a.T, p.d = a.d, p.E = a.E, p.I = a.I, p.Is = a.Is, p.k_max = a.k_max, p.blocked = a.blocked;
   p.x = a.x;
   for (int i = 0; i < 6; ++i) p.w[i] = RowWeights{a.w[i], a.scales[i], static_cast<const uint8_t*>(a.zeros[i])};
-  p.L = FewList{a.head, a.expert, a.mask, a.row, a.wt};
+  p.off = a.in_off, p.ids = a.in_ids, p.wts = a.in_w;
+  p.stats = a.stats, p.status = a.status;
+  p.n_list = a.n_list, p.expert = a.expert, p.rows = a.rows;
   p.h = a.h;
   p.hw = max(a.I, a.Is);
-  p.plane = ((size_t)a.T * a.k_max + (a.Is ? a.T : 0)) * p.hw;
+  p.stride = min(256, min(a.E, a.T * a.k_max) * (a.I / TILE_N) + a.Is / TILE_N);
+  p.zero_row = a.T * a.k_max + a.T;
+  p.plane = ((size_t)p.zero_row + 1) * p.hw;
   p.out = a.out;
-  const size_t lds = few_sel_lds(a.T, a.E, a.k_max);
-  hipError_t e;
   if (a.w_router) {
-    e = launch_logits_f64(a.dtype, a.x, a.w_router, a.k, a.T, a.d, a.E, a.k_max, a.pol, a.S, a.part, a.tok_off,
-                          a.status, st);
+    p.part = a.part, p.bias = a.bias, p.k = a.k, p.pol = a.pol, p.scale = a.scale;
+    const dim3 grid(ceil_div(a.E, 16), FEW_S);
+    if (a.dtype == DT_BF16)
+      hipLaunchKernelGGL(few_logits_kernel<bf16_t>, grid, dim3(64 * FEW_LW), 0, st, (const bf16_t*)a.x,
+                         (const bf16_t*)a.w_router, a.T, a.d, a.E, a.part);
+    else
+      hipLaunchKernelGGL(few_logits_kernel<float>, grid, dim3(64 * FEW_LW), 0, st, (const float*)a.x,
+                         (const float*)a.w_router, a.T, a.d, a.E, a.part);
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-#define MOE_FEW_SELECT(KPL)                                                                                        \
-  hipLaunchKernelGGL(few_select_kernel<KPL>, dim3(1), dim3(FEW_SEL_NT), lds, st, a.part, a.S, a.bias, a.tok_off, a.T, \
-                     a.E, a.k_max, a.scale, p.L, a.stats)
-    if (a.E <= 64) MOE_FEW_SELECT(1);
-    else if (a.E <= 128) MOE_FEW_SELECT(2);
-    else if (a.E <= 256) MOE_FEW_SELECT(4);
-    else if (a.E <= 512) MOE_FEW_SELECT(8);
-    else MOE_FEW_SELECT(16);
-#undef MOE_FEW_SELECT
-  } else {
-    hipLaunchKernelGGL(few_routes_kernel, dim3(1), dim3(FEW_SEL_NT), lds, st, a.in_off, a.in_ids, a.in_w, a.T, a.E,
-                       a.k_max, p.L);
   }
-  e = hipGetLastError();
-  if (e != hipSuccess || a.T == 0) return e;  // no tokens: the counts and the status only
-  const int cap = min(a.E, a.T * a.k_max) * (a.I / TILE_N) + a.Is / TILE_N;
-  return a.dtype == DT_BF16 ? few_ffn_type<bf16_t>(p, a.group, a.zeros[0] != nullptr, cap, st)
-                            : few_ffn_type<float>(p, a.group, a.zeros[0] != nullptr, cap, st);
+  return a.dtype == DT_BF16 ? few_ffn<bf16_t>(p, a.group, a.zeros[0] != nullptr, st)
+                            : few_ffn<float>(p, a.group, a.zeros[0] != nullptr, st);
 }
 
 }  // namespace moe

@@ -244,15 +244,14 @@ struct FewLaunch {
   int group;                           // 0: element weights; else inputs of a scale
   const void *w[6], *scales[6], *zeros[6];  // gate, up, down, and the always-on expert's
   // scratch
-  double* part;                        // [S][T][E]
-  int S;
-  int32_t *tok_off, *status;           // [T + 1], [1] (the caller's status, if any)
-  int32_t *head, *expert, *mask, *row; // the list of chosen experts
-  float* wt;                           // [T][E]
+  double* part;                        // few_part_count
+  int32_t *n_list, *expert;            // the list of chosen experts: [1], [min(E, T k_max)],
+  uint32_t* rows;                      // [min(E, T k_max)][8]
   void* h;                             // few_h_bytes
-  int32_t* stats;
+  int32_t *stats, *status;             // each may be null
   void* out;
 };
+size_t few_part_count(int T, int E);
 size_t few_h_bytes(int dtype, int q4, int T, int k_max, int I, int Is);
 hipError_t launch_few(const FewLaunch& a, hipStream_t st);
 

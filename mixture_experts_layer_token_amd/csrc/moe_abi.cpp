@@ -210,24 +210,18 @@ void plan_grouped(const moe_desc& d, Carver& c, GroupedWs& w) {
   w.wn = p ? w.xn + nx : nullptr;
 }
 
-// The few-token layer: partial logits, the list of chosen experts and their
-// intermediate rows (of the wider of float32's forms: the weights' kind is not in the
-// descriptor).
-struct FewWs { double* part; int splits; int32_t *tok_off, *status, *head, *expert, *mask, *row; float* wt; void* h; };
+// The few-token layer: partial logits, the list of chosen experts and their intermediate
+// rows (of the wider of float32's forms: the weights' kind is not in the descriptor).
+struct FewWs { double* part; int32_t *n_list, *expert; uint32_t* rows; void* h; };
 moe_status few_ok(const moe_desc& d) {
   return d.T > MOE_FEW_MAX_T || d.k_max > 64 ? MOE_ERR_SHAPE : MOE_OK;
 }
 void plan_few(const moe_desc& d, Carver& c, FewWs& w) {
+  w.part = c.take<double>(few_part_count(d.T, d.E));
   const size_t cap = std::min<size_t>(d.E, a_cap(d));
-  w.splits = logits_f64_splits(d.T, d.d, d.E, d.dtype);
-  w.part = c.take<double>((size_t)w.splits * d.T * d.E);
-  w.tok_off = c.take<int32_t>((size_t)d.T + 1);
-  w.status = c.take<int32_t>(1);
-  w.head = c.take<int32_t>(2);
+  w.n_list = c.take<int32_t>(1);
   w.expert = c.take<int32_t>(cap);
-  w.mask = c.take<int32_t>(cap);
-  w.row = c.take<int32_t>(cap);
-  w.wt = c.take<float>((size_t)d.T * d.E);
+  w.rows = c.take<uint32_t>(cap * 8);
   w.h = c.take_bytes(few_h_bytes(d.dtype, 1, d.T, d.k_max, d.I, d.I_shared));
 }
 
@@ -1053,8 +1047,7 @@ static moe_status few_operands(const moe_desc& d, const void* x, const void* con
   a.pol = budget(d);
   a.x = x;
   a.out = out;
-  a.part = fw.part, a.S = fw.splits, a.tok_off = fw.tok_off, a.status = fw.status;
-  a.head = fw.head, a.expert = fw.expert, a.mask = fw.mask, a.row = fw.row, a.wt = fw.wt, a.h = fw.h;
+  a.part = fw.part, a.n_list = fw.n_list, a.expert = fw.expert, a.rows = fw.rows, a.h = fw.h;
   return MOE_OK;
 }
 
@@ -1073,7 +1066,7 @@ moe_status moe_forward_few(const moe_desc* desc, const void* x, const void* w_ro
   a.bias = router_bias;
   a.k = k;
   a.stats = stats;
-  if (dev_status) a.status = dev_status;
+  a.status = dev_status;
   return launched(launch_few(a, static_cast<hipStream_t>(stream)));
 }
 

@@ -185,38 +185,33 @@ __global__ __launch_bounds__(64 * QL_NW) void q4_linear_kernel(const typename Op
   const int n0 = blockIdx.x * TILE_N, row = blockIdx.y * 16 + col;
   const int steps = ceil_div(K, Q4_K);
   const int beg = steps * wave / QL_NW, end = steps * (wave + 1) / QL_NW;
-  const T* xrow = x + (size_t)(row < rows ? row : 0) * K;
+  const T* x0 = x + (size_t)blockIdx.y * 16 * K;
+  const uint32_t xrow = (uint32_t)(row < rows ? col : 0) * K * (uint32_t)sizeof(T);
   const typename Op::Src src = Op::tile(w, 0, n0, N, K, 0);
   f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
   for (int s = beg; s < end; ++s) {
     const typename Op::W v = Op::load(src, s);
-    typename Op::X xv = Op::load_x(xrow, s, K);
+    typename Op::X xv = Op::load_x(x0, xrow, s, K);
     if (row >= rows) Op::clear(xv);
     Op::finish_x(xv);
     Op::mma(acc, v, xv);
   }
   red[wave * 64 + lane] = acc;
   __syncthreads();
-  if (wave > 0) return;
-  f32x4_t v = red[lane];
+  if (wave >= 4) return;
+  // thread: output j of row r of the tile
+  const int j = threadIdx.x & 15, r = threadIdx.x >> 4, n = n0 + j;
+  const float* q = reinterpret_cast<const float*>(red) + ((j >> 2) * 16 + r) * 4 + (j & 3);
+  float v = 0.f;
 #pragma unroll
-  for (int q = 1; q < QL_NW; ++q) v += red[q * 64 + lane];
-  redo_not_finite(v, row < rows, [&](int r, int c) {
-    const T* xr = x + (size_t)(blockIdx.y * 16 + c) * K;
-    const int n = min(n0 + r, N - 1);
-    return wave_dot(K, [&](int k) { return Elt<T>::to_f32(xr[k]) * Op::value(w, 0, n, k, N, K, 0); });
+  for (int i = 0; i < QL_NW; ++i) v += q[i * 256];
+  const bool mine = blockIdx.y * 16 + r < rows && n < N;
+  redo_not_finite(v, mine, [&](int l) {
+    const T* xr = x0 + (size_t)((wave * 64 + l) >> 4) * K;
+    const int nn = n0 + (l & 15);
+    return wave_dot(K, [&](int k) { return Elt<T>::to_f32(xr[k]) * Op::value(w, 0, nn, k, N, K, 0); });
   });
-  if (row < rows) {
-    T* p = y + (size_t)row * N + n0 + 4 * (lane >> 4);
-    const int left = N - n0 - 4 * (lane >> 4);
-    if (left >= 4 && (N & 3) == 0) {
-      store_row4(p, v);
-    } else {
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (r < left) p[r] = Elt<T>::from_f32(v[r]);
-    }
-  }
+  if (mine) y[(size_t)(blockIdx.y * 16 + r) * N + n] = Elt<T>::from_f32(v);
 }
 
 // -------------------------------------------------------------------- launches

@@ -23,6 +23,9 @@
 // 24 bits, and run as three instructions: the float32 matrix instruction takes
 // four times the time of all three.
 //
+// Matrix instructions run whatever the lanes' mask says, so a condition around one has to
+// be scalar (the same for the wave, and known to the compiler to be).
+//
 // Order of the codes: 1 KB per 16 rows x 128 inputs, lane l's 16 bytes at 16 l:
 // row l % 16, word i (of 4) inputs 32 i + 8 (l / 16) + 0..7, input 2 j in bits 4 j
 // and input 2 j + 1 in bits 16 + 4 j, which the masks above take apart in place.
@@ -47,6 +50,13 @@ struct RowWeights {
 };
 
 __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// A load at `bytes` of a lane from what its wave has in common (a scalar base and a 32-bit
+// offset: one vector register where a pointer takes two for each load in flight).
+template <typename V>
+__device__ __forceinline__ V at(const void* base, uint32_t bytes, int ahead = 0) {
+  return *reinterpret_cast<const V*>(static_cast<const char*>(base) + bytes + ahead);
+}
 
 // Four consecutive elements of a row (8- or 16-byte aligned).
 __device__ __forceinline__ void store_row4(bf16_t* p, f32x4_t v) {
@@ -78,24 +88,33 @@ struct DenseOp {
   static constexpr bool Q4 = false;
   struct W { u32x4_t v[2]; };
   struct X { u32x4_t v[2]; };
-  struct Src { const T* p; int kstr; };
+  // A tile: what the wave has in common, and the lane's place in it (the same for every
+  // tile of matrices of one K), so that tiles cost scalar registers only.
+  struct Src { const T* p; int kstr; uint32_t lane; };  // lane: bytes
 
+  // w_offset of row n0's first element; a block's rows are KS elements long.
+  __device__ __forceinline__ static size_t corner(int n0, int K, int blocked) {
+    return blocked ? (size_t)(n0 & ~63) * K + (n0 & 63) * KS : (size_t)n0 * K;
+  }
   // Tile of rows n0 .. n0 + 15 of matrix `mat` of a stack of [N][K].
   __device__ __forceinline__ static Src tile(const RowWeights& m, int mat, int n0, int N, int K, int blocked) {
     const int lane = threadIdx.x & 63;
-    const T* w = static_cast<const T*>(m.w) + (size_t)mat * N * K;
-    return Src{w + w_offset<T>(n0 + (lane & 15), (lane >> 4) * LE, K, blocked), w_kstep<T>(blocked)};
+    return Src{static_cast<const T*>(m.w) + (size_t)mat * N * K + corner(n0, K, blocked), w_kstep<T>(blocked),
+               (uint32_t)((lane & 15) * (blocked ? KS : K) + (lane >> 4) * LE) * (uint32_t)sizeof(T)};
   }
   __device__ __forceinline__ static W load(const Src& s, int step) {
     const T* p = s.p + (size_t)step * s.kstr;
-    return W{{*reinterpret_cast<const u32x4_t*>(p), *reinterpret_cast<const u32x4_t*>(p + 4 * LE)}};
+    return W{{at<u32x4_t>(p, s.lane), at<u32x4_t>(p, s.lane, 64)}};
   }
-  // Activations of a step: `row` is the lane's row (any row it may read if it has none).
-  __device__ __forceinline__ static X load_x(const T* row, int step) {
-    const T* p = row + step * KS + ((threadIdx.x & 63) >> 4) * LE;
-    return X{{*reinterpret_cast<const u32x4_t*>(p), *reinterpret_cast<const u32x4_t*>(p + 4 * LE)}};
+  // Activations of a step: the lane's row starts `row` bytes behind base (any row that it
+  // may read if it has none).
+  __device__ __forceinline__ static X load_x(const T* base, uint32_t row, int step) {
+    const uint32_t o = row + ((threadIdx.x & 63) >> 4) * 16;
+    return X{{at<u32x4_t>(base + step * KS, o), at<u32x4_t>(base + step * KS, o, 64)}};
   }
-  __device__ __forceinline__ static X load_h(const hid* row, size_t, int step) { return load_x(row, step); }
+  __device__ __forceinline__ static X load_h(const hid* base, uint32_t row, size_t, int step) {
+    return load_x(base, row, step);
+  }
   __device__ __forceinline__ static void clear(X& x) { x.v[0] = x.v[1] = u32x4_t{0, 0, 0, 0}; }
   __device__ __forceinline__ static void finish_x(X&) {}
   __device__ __forceinline__ static void mma(f32x4_t& acc, const W& w, const X& x) {
@@ -114,8 +133,8 @@ struct DenseOp {
     return Elt<T>::to_f32(static_cast<const T*>(m.w)[(size_t)mat * N * K + w_offset<T>(n, k, K, blocked)]);
   }
   __device__ __forceinline__ static float h_value(const hid* row, size_t, int k) { return Elt<T>::to_f32(row[k]); }
-  // Four intermediate values (one rounding to the element type, as moe_ffn keeps H).
-  __device__ __forceinline__ static void store_h(hid* p, size_t, f32x4_t v) { store_row4(p, v); }
+  // An intermediate value (one rounding to the element type, as moe_ffn keeps H).
+  __device__ __forceinline__ static void store_h(hid* p, size_t, float v) { *p = Elt<T>::from_f32(v); }
 };
 
 template <typename T, int GROUP, bool ZEROS>
@@ -137,20 +156,21 @@ struct Q4Op {
   struct Src { const u32x4_t* q; const T* s; const uint8_t* z; int Np; };
 
   __device__ __forceinline__ static Src tile(const RowWeights& m, int mat, int n0, int N, int K, int) {
-    const int lane = threadIdx.x & 63, kt = ceil_div(K, Q4_K), nt = ceil_div(N, TILE_N), Np = nt * TILE_N;
-    const size_t g = (size_t)mat * kt * NG * Np + n0 + 4 * (lane >> 4);
-    return Src{static_cast<const u32x4_t*>(m.w) + ((size_t)mat * nt + n0 / TILE_N) * kt * 64 + lane,
+    const int kt = ceil_div(K, Q4_K), nt = ceil_div(N, TILE_N), Np = nt * TILE_N;
+    const size_t g = (size_t)mat * kt * NG * Np + n0;
+    return Src{static_cast<const u32x4_t*>(m.w) + ((size_t)mat * nt + n0 / TILE_N) * kt * 64,
                static_cast<const T*>(m.scales) + g, ZEROS ? m.zeros + g : nullptr, Np};
   }
   __device__ __forceinline__ static W load(const Src& s, int step) {
     W w;
-    w.q = s.q[(size_t)step * 64];
+    const uint32_t lane = threadIdx.x & 63, row = 4 * (lane >> 4);
+    w.q = at<u32x4_t>(s.q + (size_t)step * 64, lane * 16);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       const size_t o = (size_t)(step * NG + g) * s.Np;
-      if constexpr (sizeof(T) == 2) w.s2[g] = *reinterpret_cast<const u32x2_t*>(s.s + o);
-      else w.s4[g] = *reinterpret_cast<const f32x4_t*>(s.s + o);
-      if constexpr (ZEROS) w.z[g] = *reinterpret_cast<const uint32_t*>(s.z + o);
+      if constexpr (sizeof(T) == 2) w.s2[g] = at<u32x2_t>(s.s + o, row * 2);
+      else w.s4[g] = at<f32x4_t>(s.s + o, row * 4);
+      if constexpr (ZEROS) w.z[g] = at<uint32_t>(s.z + o, row);
     }
     return w;
   }
@@ -164,36 +184,37 @@ struct Q4Op {
       for (int p = 0; p < PLANES; ++p) x.v[p][i][j] = (l[p] >> 16) | h[p];
     }
   }
-  __device__ __forceinline__ static X load_x(const T* row, int step) {
-    return load_x(row, step, 1 << 30);
-  }
-  // Inputs from K on read as zero (K a multiple of 8).
-  __device__ __forceinline__ static X load_x(const T* row, int step, int K) {
+  // Activations of a step: the lane's row starts `row` bytes behind base.  Inputs from K on
+  // read as zero (K a multiple of 8).
+  __device__ __forceinline__ static X load_x(const T* base, uint32_t row, int step, int K = 1 << 30) {
     X x;
+    const uint32_t o = row + 8 * sizeof(T) * ((threadIdx.x & 63) >> 4);
     const int k0 = step * KS + 8 * ((threadIdx.x & 63) >> 4);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int k = k0 + 32 * i;
-      const T* p = row + (k < K ? k : 0);
+      const bool in = k0 + 32 * i < K;
+      const T* p = base + step * KS + 32 * i;
+      const uint32_t off = in ? o : 0;
+      if (!in) p = base;
       if constexpr (sizeof(T) == 2) {
-        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(p);
-        x.v[0][i] = k < K ? v : u32x4_t{0, 0, 0, 0};
+        const u32x4_t v = at<u32x4_t>(p, off);
+        x.v[0][i] = in ? v : u32x4_t{0, 0, 0, 0};
       } else {
-        f32x4_t a = *reinterpret_cast<const f32x4_t*>(p), b = *reinterpret_cast<const f32x4_t*>(p + 4);
-        if (k >= K) a = b = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        f32x4_t a = at<f32x4_t>(p, off), b = at<f32x4_t>(p, off, 16);
+        if (!in) a = b = f32x4_t{0.f, 0.f, 0.f, 0.f};
         set3(x, i, a, b);
       }
     }
     return x;
   }
   // Plane p of an intermediate row lies `plane` elements behind plane p - 1.
-  __device__ __forceinline__ static X load_h(const hid* row, size_t plane, int step) {
+  __device__ __forceinline__ static X load_h(const hid* base, uint32_t row, size_t plane, int step) {
     X x;
-    const hid* p0 = row + step * KS + 8 * ((threadIdx.x & 63) >> 4);
+    const uint32_t o = row + 16 * ((threadIdx.x & 63) >> 4);
 #pragma unroll
     for (int p = 0; p < PLANES; ++p)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x.v[p][i] = *reinterpret_cast<const u32x4_t*>(p0 + p * plane + 32 * i);
+      for (int i = 0; i < 4; ++i) x.v[p][i] = at<u32x4_t>(base + p * plane + step * KS, o, 64 * i);
     return x;
   }
   __device__ __forceinline__ static void clear(X& x) {
@@ -257,16 +278,15 @@ struct Q4Op {
     for (int p = PLANES - 1; p >= 0; --p) v += bf16_to_f32(row[p * plane + k]);
     return v;
   }
-  __device__ __forceinline__ static void store_h(hid* p, size_t plane, f32x4_t v) {
+  __device__ __forceinline__ static void store_h(hid* p, size_t plane, float v) {
     if constexpr (PLANES == 1) {
-      store_row4(p, v);
+      *p = Elt<T>::from_f32(v);
     } else {
-      uint32_t a[4], b[4], c[4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) split3(v[r], a[r], b[r], c[r]);
-      *reinterpret_cast<u32x2_t*>(p) = u32x2_t{(a[0] >> 16) | a[1], (a[2] >> 16) | a[3]};
-      *reinterpret_cast<u32x2_t*>(p + plane) = u32x2_t{(b[0] >> 16) | b[1], (b[2] >> 16) | b[3]};
-      *reinterpret_cast<u32x2_t*>(p + 2 * plane) = u32x2_t{(c[0] >> 16) | c[1], (c[2] >> 16) | c[3]};
+      uint32_t a, b, c;
+      split3(v, a, b, c);
+      p[0] = (hid)(a >> 16);
+      p[plane] = (hid)(b >> 16);
+      p[2 * plane] = (hid)(c >> 16);
     }
   }
 };
@@ -288,30 +308,16 @@ __device__ __forceinline__ float wave_dot(int K, F f) {
   return s;
 }
 
-// Replaces the values of a tile that are not finite (in lanes with `mine`) by
-// f(row of the tile, column).
+// Replaces a lane's value that is not finite (where `mine`) by f(lane).
 template <class F>
-__device__ __forceinline__ void redo_not_finite(f32x4_t& v, bool mine, F f) {
-  bool bad = false;
-#pragma unroll
-  for (int r = 0; r < 4; ++r) bad |= not_finite(v[r]);
-  uint64_t todo = __ballot(bad && mine);
+__device__ __forceinline__ void redo_not_finite(float& v, bool mine, F f) {
+  uint64_t todo = __ballot(mine && not_finite(v));
+#pragma unroll 1
   while (todo) {
     const int l = __builtin_ctzll(todo);
     todo &= todo - 1;
-    const bool own = (int)(threadIdx.x & 63) == l;
-#pragma unroll 1
-    for (int r = 0; r < 4; ++r) {
-      const float old = __shfl(r == 0 ? v[0] : r == 1 ? v[1] : r == 2 ? v[2] : v[3], l, 64);
-      if (!not_finite(old)) continue;
-      const float s = f(4 * (l >> 4) + r, l & 15);
-      if (own) {
-        if (r == 0) v[0] = s;
-        if (r == 1) v[1] = s;
-        if (r == 2) v[2] = s;
-        if (r == 3) v[3] = s;
-      }
-    }
+    const float s = f(l);
+    if ((int)(threadIdx.x & 63) == l) v = s;
   }
 }
 
