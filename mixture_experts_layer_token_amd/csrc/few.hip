@@ -29,7 +29,10 @@
 namespace moe {
 
 constexpr int FEW_T = MOE_FEW_MAX_T;
-constexpr int FEW_S = 8;                  // slices of the partial logits
+constexpr int FEW_S = 8;                  // slices of the partial logits, at most
+// Slices that the logits are summed in: 4 for up to 2048 inputs (every gate/up workgroup
+// reads them all), else 8 (twice the workgroups for the products).
+__host__ __device__ __forceinline__ int few_slices(int d) { return d <= 2048 ? 4 : 8; }
 
 // What the launches take.
 struct FewArgs {
@@ -105,30 +108,70 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-// A token's choice from its keys (E <= 64 KPL), by one wave: the largest key kt times,
-// ties to the lowest expert (select.h's keys and order; its radix search takes fewer steps
-// from some 20 experts a token on, but many times the code).  Lane j ends with the j-th
-// choice (kt <= 64) and its logit.
-template <int KPL>
-__device__ __forceinline__ void few_choose(const uint32_t* keys, int E, int kt, int& mine, float& logit) {
+// A token's choice from its keys, by one wave: the largest key kt times, ties to the lowest
+// expert (select.h's keys and order; its radix search takes fewer steps from some 20 experts
+// a token on, but many times the code).  Lane j ends with the j-th choice (kt <= 64) and its
+// logit.
+// Up to 256 experts: every lane sorts its four keys once, so that a round is the largest of
+// the lanes' first keys (some 150 cycles; with four keys to look at in each round, 500).
+__device__ __forceinline__ void few_choose256(const uint32_t* keys, int E, int kt, int& mine, float& logit) {
   const int lane = threadIdx.x & 63;
-  uint32_t key[KPL];
+  uint32_t k[4];
+  int e[4];
 #pragma unroll
-  for (int s = 0; s < KPL; ++s) key[s] = lane + 64 * s < E ? keys[lane + 64 * s] : 0;  // 0: none, or chosen
+  for (int s = 0; s < 4; ++s) {
+    e[s] = lane + 64 * s;
+    k[s] = e[s] < E ? keys[e[s]] : 0;  // 0: none
+  }
+  // equal keys keep their order
+  auto order = [&](int a, int b) {
+    const bool swap = k[b] > k[a];
+    const uint32_t ka = k[a];
+    const int ea = e[a];
+    k[a] = swap ? k[b] : ka;
+    e[a] = swap ? e[b] : ea;
+    k[b] = swap ? ka : k[b];
+    e[b] = swap ? ea : e[b];
+  };
+  order(0, 1), order(1, 2), order(2, 3), order(0, 1), order(1, 2), order(0, 1);
+#pragma unroll 1
+  for (int j = 0; j < kt; ++j) {
+    const uint32_t m = wave_max_u32(k[0]);
+    uint64_t has = __ballot(k[0] == m);
+    if (has & (has - 1))  // several lanes: the lowest expert
+      has = __ballot(k[0] == m && e[0] == (int)~wave_max_u32(k[0] == m ? ~(uint32_t)e[0] : 0u));
+    const int l = __builtin_ctzll(has), pick = __builtin_amdgcn_readlane(e[0], l);
+    mine = lane == j ? pick : mine;
+    logit = lane == j ? key_logit(m) : logit;
+    const bool own = lane == l;
+#pragma unroll
+    for (int s = 0; s < 3; ++s) {
+      k[s] = own ? k[s + 1] : k[s];
+      e[s] = own ? e[s + 1] : e[s];
+    }
+    k[3] = own ? 0 : k[3];
+  }
+}
+// Up to 1024.
+__device__ __forceinline__ void few_choose1024(const uint32_t* keys, int E, int kt, int& mine, float& logit) {
+  const int lane = threadIdx.x & 63;
+  uint32_t key[16];
+#pragma unroll
+  for (int s = 0; s < 16; ++s) key[s] = lane + 64 * s < E ? keys[lane + 64 * s] : 0;  // 0: none, or chosen
 #pragma unroll 1
   for (int j = 0; j < kt; ++j) {
     uint32_t m = key[0];
 #pragma unroll
-    for (int s = 1; s < KPL; ++s) m = max(m, key[s]);
+    for (int s = 1; s < 16; ++s) m = max(m, key[s]);
     m = wave_max_u32(m);
     int e = 0;
 #pragma unroll
-    for (int s = KPL - 1; s >= 0; --s) {
+    for (int s = 15; s >= 0; --s) {
       const uint64_t has = __ballot(key[s] == m);
       e = has ? 64 * s + __builtin_ctzll(has) : e;
     }
 #pragma unroll
-    for (int s = 0; s < KPL; ++s) key[s] = e == lane + 64 * s ? 0 : key[s];
+    for (int s = 0; s < 16; ++s) key[s] = e == lane + 64 * s ? 0 : key[s];
     mine = lane == j ? e : mine;
     logit = lane == j ? key_logit(m) : logit;
   }
@@ -145,18 +188,26 @@ __device__ __forceinline__ int few_list(const FewArgs& p, const FewList& L) {
   int v = 0;
   if (p.part) {
     v = lane < p.T ? p.k[lane] : 0;
+    const int n = p.T * p.E, slices = few_slices(p.d);
 #pragma unroll 1
-    for (int i = tid; i < p.T * p.E; i += NT) {
-      const int e = i % p.E;
-      double part[FEW_S];
+    for (int i = tid; i < n; i += 2 * NT) {  // two values in flight
+      double part[2][FEW_S];
+      float b[2];
 #pragma unroll
-      for (int q = 0; q < FEW_S; ++q) part[q] = p.part[(size_t)q * (p.T * p.E) + i];
-      double l = 0.0;
-      const float b = p.bias ? p.bias[e] : 0.f;
+      for (int u = 0; u < 2; ++u) {
+        const int iu = min(i + u * NT, n - 1);
 #pragma unroll
-      for (int q = 0; q < FEW_S; ++q) l += part[q];
-      if (p.bias) l += (double)b;
-      L.keys[i] = max(logit_key((float)l), 1u);
+        for (int q = 0; q < FEW_S; ++q) part[u][q] = q < 4 || slices > 4 ? p.part[(size_t)q * n + iu] : 0.0;
+        b[u] = p.bias ? p.bias[(uint32_t)iu % (uint32_t)p.E] : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        double l = 0.0;
+#pragma unroll
+        for (int q = 0; q < FEW_S; ++q) l += part[u][q];
+        if (p.bias) l += (double)b[u];
+        if (i + u * NT < n) L.keys[i + u * NT] = max(logit_key((float)l), 1u);
+      }
     }
   }
 #pragma unroll 1
@@ -176,8 +227,8 @@ __device__ __forceinline__ int few_list(const FewArgs& p, const FewList& L) {
     float w = 0.f;
     if (p.part) {
       const int kt = __builtin_amdgcn_readlane(exec, t);
-      if (p.E <= 256) few_choose<4>(L.keys + t * p.E, p.E, kt, e, w);
-      else few_choose<16>(L.keys + t * p.E, p.E, kt, e, w);
+      if (p.E <= 256) few_choose256(L.keys + t * p.E, p.E, kt, e, w);
+      else few_choose1024(L.keys + t * p.E, p.E, kt, e, w);
       const float ex = e >= 0 ? expf(w - __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(w)))) : 0.f;
       float sum = ex;
 #pragma unroll 1
@@ -269,10 +320,10 @@ __device__ __forceinline__ void few_zero_row(const FewArgs& p) {
     for (int i = threadIdx.x; i < p.hw; i += NT) h[q * p.plane + (size_t)p.zero_row * p.hw + i] = 0;
 }
 
-// H of one value of an item: output j of the tile, token t.
+// H of column n of a row.
 template <class Op>
-__device__ __forceinline__ void few_store_h(const FewArgs& p, const FewList& L, bool sh, int idx, int n, int t, float g,
-                                            float u, int row) {
+__device__ __forceinline__ void few_store_h(const FewArgs& p, const FewList& L, bool sh, int n, float g, float u,
+                                            int row) {
   const float rw = sh ? 1.f : L.w[row];
   Op::store_h(static_cast<typename Op::hid*>(p.h) + (size_t)row * p.hw + n, p.plane, rw * (silu(g) * u));
 }
@@ -315,29 +366,32 @@ __device__ __forceinline__ typename DenseOp<T>::W few_frag(const char* tile) {
   return w;
 }
 
-// Gate and up: a workgroup takes every p.stride-th item, 16 intermediate columns of one
-// expert.  XQ: copies of the activations, 1 for up to 8 tokens.
+// Gate and up: a workgroup takes every p.stride-th item, 8 intermediate columns of one expert:
+// a tile of 8 gate rows and the same 8 up rows.  (16 columns, two tiles, leave one token's 384
+// items on 256 workgroups: 15.7 us for the last one where 11.1 did the first.)  XQ: copies of
+// the activations, 1 for up to 8 tokens.
 template <typename T, int NB, int XQ>
 __global__ __launch_bounds__(FEW_RT) void few_gateup_dense_kernel(FewArgs p) {
   typedef DenseOp<T> Op;
-  constexpr int SLOT = 4096 + 1024 * XQ, PER = 4 + XQ;
+  constexpr int SLOT = 2048 + 1024 * XQ, PER = 2 + XQ;
   extern __shared__ char few_ring[];  // the rings (the list's scratch before), the waves' sums, the list
   const RowWeights wg = p.w[0], wu = p.w[1], sg = p.w[3], su = p.w[4];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int ring_bytes = max(FEW_RW * NB * SLOT, few_scratch_words(p.T, p.E) * 4);
   f32x4_t* const red = reinterpret_cast<f32x4_t*>(few_ring + ring_bytes);
-  const FewList L = few_carve(reinterpret_cast<uint32_t*>(few_ring), reinterpret_cast<uint32_t*>(red + 2 * FEW_RT), p.T,
-                              p.E, p.k_max);
+  const FewList L = few_carve(reinterpret_cast<uint32_t*>(few_ring), reinterpret_cast<uint32_t*>(red + FEW_RT), p.T, p.E,
+                              p.k_max);
   const int n_list = few_list<FEW_RT>(p, L);
   if (blockIdx.x == 0) few_zero_row<Op, FEW_RT>(p);
-  const int ci = p.I / TILE_N, routed = n_list * ci;
-  const int n_items = routed + p.Is / TILE_N;
+  const int ci = p.I / 8, routed = n_list * ci;
+  const int n_items = routed + p.Is / 8;
   const int steps = p.d / Op::KS, kstr = w_kstep<T>(p.blocked) * (int)sizeof(T);
   const int beg = steps * wave / FEW_RW, end = steps * (wave + 1) / FEW_RW;
   const int pitch = (p.blocked ? Op::KS : p.d) * (int)sizeof(T);
-  uint32_t woff[2], xoff[XQ];
-#pragma unroll
-  for (int q = 0; q < 2; ++q) woff[q] = (uint32_t)few_copy_row(q) * pitch + few_copy_byte(q);
+  // a lane's place in the copies: tile rows 0..7 of gate, 8..15 (rows 0..7 of up)
+  const uint32_t row0 = (uint32_t)few_copy_row(0) * pitch;
+  const uint32_t goff = row0 + few_copy_byte(0), uoff = row0 + few_copy_byte(1);
+  uint32_t xoff[XQ];
 #pragma unroll
   for (int q = 0; q < XQ; ++q)  // rows behind the last token repeat it; their sums are not used
     xoff[q] = (uint32_t)min(few_copy_row(q), p.T - 1) * p.d * (uint32_t)sizeof(T) + few_copy_byte(q);
@@ -349,7 +403,7 @@ __global__ __launch_bounds__(FEW_RT) void few_gateup_dense_kernel(FewArgs p) {
   auto seek = [&]() {
     const bool sh = want >= routed;
     const int idx = sh ? 0 : (int)((uint32_t)want / (uint32_t)ci);
-    const int n0 = (sh ? want - routed : want - idx * ci) * TILE_N, N = sh ? p.Is : p.I;
+    const int n0 = (sh ? want - routed : want - idx * ci) * 8, N = sh ? p.Is : p.I;
     const int mat = sh ? 0 : __builtin_amdgcn_readfirstlane(L.expert[idx]);
     const size_t o = ((size_t)mat * N * p.d + Op::corner(n0, p.d, p.blocked)) * sizeof(T);
     rg = static_cast<const char*>(sh ? sg.w : wg.w) + o;
@@ -358,13 +412,10 @@ __global__ __launch_bounds__(FEW_RT) void few_gateup_dense_kernel(FewArgs p) {
   auto request = [&](int slot) {
     char* const to = ring + slot * SLOT;
     const size_t o = (size_t)rs * kstr;
+    few_copy<2>(rg + o, goff, to);
+    few_copy<2>(ru + o, uoff, to + 1024);
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      few_copy<2>(rg + o, woff[q], to + 1024 * q);
-      few_copy<2>(ru + o, woff[q], to + 2048 + 1024 * q);
-    }
-#pragma unroll
-    for (int q = 0; q < XQ; ++q) few_copy<0>(static_cast<const char*>(p.x) + rs * 128, xoff[q], to + 4096 + 1024 * q);
+    for (int q = 0; q < XQ; ++q) few_copy<0>(static_cast<const char*>(p.x) + rs * 128, xoff[q], to + 2048 + 1024 * q);
     if (rs + 1 < end) {
       ++rs;
     } else if (want + p.stride < n_items) {
@@ -382,32 +433,30 @@ __global__ __launch_bounds__(FEW_RT) void few_gateup_dense_kernel(FewArgs p) {
   int slot = 0;
 #pragma unroll 1
   for (int item = blockIdx.x; item < n_items; item += p.stride) {
-    f32x4_t ga = {0.f, 0.f, 0.f, 0.f}, ua = ga;
+    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
     for (int s = beg; s < end; ++s) {
       vm_wait<PER * (NB - 1)>();
       compiler_fence();
       const char* const from = ring + slot * SLOT;
-      const typename Op::W gw = few_frag<T>(from), uw = few_frag<T>(from + 2048), xw = few_frag<T>(from + 4096);
+      const typename Op::W w = few_frag<T>(from), xw = few_frag<T>(from + 2048);
       lgkm_wait0();  // read before the slot is filled again
       compiler_fence();
       request(slot);
       slot = slot + 1 == NB ? 0 : slot + 1;
-      const typename Op::X x{{xw.v[0], xw.v[1]}};
-      Op::mma(ga, gw, x);
-      Op::mma(ua, uw, x);
+      Op::mma(acc, w, typename Op::X{{xw.v[0], xw.v[1]}});
     }
-    red[wave * 64 + lane] = ga;
-    red[FEW_RT + wave * 64 + lane] = ua;
+    settle(acc);
+    red[wave * 64 + lane] = acc;
     few_barrier();
-    if (wave < 4) {
+    if (wave < 2) {
       const bool sh = item >= routed;
       const int idx = sh ? 0 : (int)((uint32_t)item / (uint32_t)ci);
-      const int n0 = (sh ? item - routed : item - idx * ci) * TILE_N;
-      const int j = tid & 15, t = tid >> 4;
-      const float g = few_sum<FEW_RW>(red, j, t), u = few_sum<FEW_RW>(red + FEW_RT, j, t);
+      const int n0 = (sh ? item - routed : item - idx * ci) * 8;
+      const int j = tid & 7, t = tid >> 3;
+      const float g = few_sum<FEW_RW>(red, j, t), u = few_sum<FEW_RW>(red, j + 8, t);
       const int row = sh ? p.T * p.k_max + t : few_row(L, idx, t);
-      if (t < p.T && row != p.zero_row) few_store_h<Op>(p, L, sh, idx, n0 + j, t, g, u, row);
+      if (t < p.T && row != p.zero_row) few_store_h<Op>(p, L, sh, n0 + j, g, u, row);
     }
     few_barrier();
   }
@@ -444,17 +493,21 @@ __device__ __forceinline__ float few_down_again(const FewArgs& p, const int32_t*
   return sum;
 }
 
-// Down: a workgroup owns 16 outputs of every token; its waves share the steps of all the
+// Down: a workgroup owns some outputs of every token; its waves share the steps of all the
 // experts' intermediate columns, laid end to end.  Tokens without a part in an expert read
 // the row of zeros.
-template <typename T, int NB, int XQ>
+// PAIR (up to 8 tokens): a tile is 8 outputs at two steps, rows 8 .. 15 and columns 8 .. 15
+// those of the second, and what a step's rows have with the other's columns is not used.  Of
+// 2048 outputs that gives 256 workgroups where tiles of 16 leave half of the GPU idle.
+// Otherwise 16 outputs, a step at a time.
+template <typename T, int NB, bool PAIR>
 __global__ __launch_bounds__(FEW_RT) void few_down_dense_kernel(FewArgs p) {
   typedef DenseOp<T> Op;
-  constexpr int SLOT = 2048 + 1024 * XQ, PER = 2 + XQ;
+  constexpr int SLOT = 4096, PER = 4, ROWS = PAIR ? 8 : 16, H = PAIR ? 1 : 2;
   extern __shared__ char few_ring[];  // the rings, the waves' sums, the list
   const RowWeights wr = p.w[2], ws = p.w[5];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-  const int n0 = blockIdx.x * TILE_N;
+  const int n0 = blockIdx.x * ROWS;
   f32x4_t* const red = reinterpret_cast<f32x4_t*>(few_ring + FEW_RW * NB * SLOT);
   const int32_t* const l_expert = reinterpret_cast<const int32_t*>(red + FEW_RT);
   const uint16_t* const row_of = reinterpret_cast<const uint16_t*>(l_expert + min(p.E, p.T * p.k_max));
@@ -462,13 +515,17 @@ __global__ __launch_bounds__(FEW_RT) void few_down_dense_kernel(FewArgs p) {
   __syncthreads();
   const int spe = p.I / Op::KS, routed = n_list * spe, steps = routed + p.Is / Op::KS;
   const int beg = steps * wave / FEW_RW, end = steps * (wave + 1) / FEW_RW;
+  const int rounds = PAIR ? (end - beg + 1) / 2 : end - beg;
   const int kstr = w_kstep<T>(p.blocked) * (int)sizeof(T);
   char* const ring = few_ring + wave * NB * SLOT;
 
-  // requests: step st of expert idx of the list (behind it: the always-on expert)
+  // requests: step st of expert idx of the list (behind it: the always-on expert); behind the
+  // wave's end its last step again, in a pair with rows of zeros
   int idx = beg < routed ? (int)((uint32_t)beg / (uint32_t)spe) : n_list, st = beg - min(idx * spe, routed), left = end - beg;
   const char* rw = nullptr;
-  uint32_t woff[2], xoff[XQ];
+  uint32_t woff = 0, hoff[H];
+  uint32_t wjump = 0;  // from a tile's row to the one 8 further
+  const uint32_t zero = (uint32_t)p.zero_row * p.hw * (uint32_t)sizeof(T);
   auto seek = [&]() {
     const bool sh = idx >= n_list;
     const int K = sh ? p.Is : p.I;
@@ -476,29 +533,35 @@ __global__ __launch_bounds__(FEW_RT) void few_down_dense_kernel(FewArgs p) {
     rw = static_cast<const char*>(sh ? ws.w : wr.w) +
          ((size_t)mat * p.d * K + Op::corner(n0, K, p.blocked)) * sizeof(T);
     const int pitch = (p.blocked ? Op::KS : K) * (int)sizeof(T);
+    woff = (uint32_t)few_copy_row(0) * pitch;
+    wjump = 8u * pitch;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) woff[q] = (uint32_t)few_copy_row(q) * pitch + few_copy_byte(q);
-#pragma unroll
-    for (int q = 0; q < XQ; ++q) {
+    for (int q = 0; q < H; ++q) {
       const int t = few_copy_row(q);
       const int row = sh ? (t < p.T ? p.T * p.k_max + t : p.zero_row) : row_of[idx * FEW_T + t];
-      xoff[q] = (uint32_t)row * p.hw * (uint32_t)sizeof(T) + few_copy_byte(q);
+      hoff[q] = (uint32_t)row * p.hw * (uint32_t)sizeof(T);
     }
   };
-  auto request = [&](int slot) {
-    char* const to = ring + slot * SLOT;
-#pragma unroll
-    for (int q = 0; q < 2; ++q) few_copy<2>(rw + (size_t)st * kstr, woff[q], to + 1024 * q);
-#pragma unroll
-    for (int q = 0; q < XQ; ++q) few_copy<0>(static_cast<const char*>(p.h) + st * 128, xoff[q], to + 2048 + 1024 * q);
-    if (left > 1) {  // behind the end: the last step again
-      --left;
+  auto advance = [&]() {
+    --left;
+    if (left > 0) {
       ++st;
       if (idx < n_list && st == spe) {
         ++idx;
         st = 0;
         seek();
       }
+    }
+  };
+  auto request = [&](int slot) {
+    char* const to = ring + slot * SLOT;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const char* const h = static_cast<const char*>(p.h) + st * 128;
+      const uint32_t b = few_copy_byte(q);
+      few_copy<2>(rw + (size_t)st * kstr + (PAIR ? 0u : q * wjump), woff + b, to + 1024 * q);
+      few_copy<0>(h, (PAIR && left <= 0 ? zero : hoff[PAIR ? 0 : q]) + b, to + 2048 + 1024 * q);
+      if (PAIR || q == 1) advance();
     }
   };
   f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
@@ -508,7 +571,7 @@ __global__ __launch_bounds__(FEW_RT) void few_down_dense_kernel(FewArgs p) {
     for (int i = 0; i < NB; ++i) request(i);
     int slot = 0;
 #pragma unroll 1
-    for (int s = beg; s < end; ++s) {
+    for (int s = 0; s < rounds; ++s) {
       vm_wait<PER * (NB - 1)>();
       compiler_fence();
       const char* const from = ring + slot * SLOT;
@@ -521,13 +584,16 @@ __global__ __launch_bounds__(FEW_RT) void few_down_dense_kernel(FewArgs p) {
     }
     vm_wait<0>();  // no copy into LDS outlives the workgroup
   }
+  settle(acc);
   red[wave * 64 + lane] = acc;
   __syncthreads();
-  if (wave < 4) {
-    const int j = tid & 15, t = tid >> 4;
+  if (wave < (PAIR ? 1 : 4)) {
+    const int j = tid % ROWS, t = tid / ROWS;
     float v = few_sum<FEW_RW>(red, j, t);
+    if (PAIR) v += few_sum<FEW_RW>(red, j + 8, t + 8);
     redo_not_finite(v, t < p.T, [&](int l) {
-      return few_down_again<Op>(p, l_expert, row_of, n_list, n0 + (l & 15), (wave * 64 + l) >> 4);
+      const int i = wave * 64 + l;
+      return few_down_again<Op>(p, l_expert, row_of, n_list, n0 + i % ROWS, i / ROWS);
     });
     if (t < p.T) static_cast<T*>(p.out)[(size_t)t * p.d + n0 + j] = Elt<T>::from_f32(v);
   }
@@ -574,6 +640,8 @@ __global__ __launch_bounds__(FEW_QT) void few_gateup_q4_kernel(FewArgs p) {
       Op::mma(ga, gw, x);
       Op::mma(ua, uw, x);
     }
+    settle(ga);
+    settle(ua);
     red[wave * 64 + lane] = ga;
     red[FEW_QT + wave * 64 + lane] = ua;
     __syncthreads();
@@ -593,7 +661,7 @@ __global__ __launch_bounds__(FEW_QT) void few_gateup_q4_kernel(FewArgs p) {
       };
       again(pick(sh, sg, wg), g);
       again(pick(sh, su, wu), u);
-      if (mine) few_store_h<Op>(p, L, sh, idx, n0 + j, t, g, u, row);
+      if (mine) few_store_h<Op>(p, L, sh, n0 + j, g, u, row);
     }
     __syncthreads();
   }
@@ -641,6 +709,7 @@ __global__ __launch_bounds__(FEW_QT) void few_down_q4_kernel(FewArgs p) {
         Op::mma(acc, w[u], x[u]);
       }
   }
+  settle(acc);
   red[wave * 64 + lane] = acc;
   __syncthreads();
   if (wave < 4) {
@@ -653,7 +722,7 @@ __global__ __launch_bounds__(FEW_QT) void few_down_q4_kernel(FewArgs p) {
   }
 }
 
-// Partial logits part[FEW_S][T][E] in float64 on the f64 matrix instruction: a workgroup
+// Partial logits part[slices][T][E] in float64 on the f64 matrix instruction: a workgroup
 // takes 16 experts and a slice of d for all tokens, its 8 waves a share each, added in
 // wave order.  (Lane l supplies the values of row l % 16 from LE (l / 16) on of a step,
 // value i of every lane in instruction i.)
@@ -667,7 +736,7 @@ __global__ __launch_bounds__(64 * FEW_LW) void few_logits_kernel(const T* __rest
   __shared__ f64x4_t red[FEW_LW * 64];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int l16 = lane & 15, lg = lane >> 4;
-  const int e0 = blockIdx.x * 16, steps = d / KS, nq = FEW_S * FEW_LW, q = blockIdx.y * FEW_LW + wave;
+  const int e0 = blockIdx.x * 16, steps = d / KS, nq = gridDim.y * FEW_LW, q = blockIdx.y * FEW_LW + wave;
   const int s0 = steps * q / nq, s1 = steps * (q + 1) / nq;
   const T* wr = w + (size_t)min(e0 + l16, E - 1) * d + lg * LE;
   const T* xr = x + (size_t)min(l16, T_ - 1) * d + lg * LE;
@@ -689,6 +758,7 @@ __global__ __launch_bounds__(64 * FEW_LW) void few_logits_kernel(const T* __rest
       acc = __builtin_amdgcn_mfma_f64_16x16x4f64(a, b, acc, 0, 0, 0);
     }
   }
+  settle(acc);
   red[wave * 64 + lane] = acc;
   __syncthreads();
   // acc[i]: expert 4 i + lg, token l16; a thread sums one value
@@ -716,15 +786,28 @@ static hipError_t few_launch(K kernel, int grid, int threads, size_t lds, const 
   return hipGetLastError();
 }
 
-template <typename T, int NBG, int NBD, int XQ>
-static hipError_t few_dense(const FewArgs& p, hipStream_t st) {
-  const int scratch = few_scratch_words(p.T, p.E) * 4, kept = few_kept_words(p.T, p.E, p.k_max) * 4;
-  const size_t lds = (size_t)max(FEW_RW * NBG * (4096 + 1024 * XQ), scratch) + 2 * FEW_RT * 16 + kept;
+// Ring depths: as many steps as 160 KB of LDS hold beside the list (5 with one copy of
+// activations, 4 with two, one less where the list is long).
+constexpr int FEW_LDS = 160 * 1024;
+
+template <typename T, int NB, int XQ>
+static hipError_t few_dense(FewArgs p, hipStream_t st) {
+  constexpr int RING = FEW_RW * NB * (2048 + 1024 * XQ), LESS = FEW_RW * (NB - 1) * (2048 + 1024 * XQ);
+  p.stride = min(256, min(p.E, p.T * p.k_max) * (p.I / 8) + p.Is / 8);
+  const int scratch = few_scratch_words(p.T, p.E) * 4, sums = FEW_RT * 16;
+  const int kept = few_kept_words(p.T, p.E, p.k_max) * 4, list = 36 * min(p.E, p.T * p.k_max);
+  const int up = max(RING, scratch) + sums + kept;
   const hipError_t e =
-      few_launch(few_gateup_dense_kernel<T, NBG, XQ>, p.stride, FEW_RT, lds, p, st);
+      up <= FEW_LDS ? few_launch(few_gateup_dense_kernel<T, NB, XQ>, p.stride, FEW_RT, up, p, st)
+                    : few_launch(few_gateup_dense_kernel<T, NB - 1, XQ>, p.stride, FEW_RT,
+                                 max(LESS, scratch) + sums + kept, p, st);
   if (e != hipSuccess) return e;
-  return few_launch(few_down_dense_kernel<T, NBD, XQ>, p.d / TILE_N, FEW_RT,
-                    (size_t)FEW_RW * NBD * (2048 + 1024 * XQ) + FEW_RT * 16 + 36 * min(p.E, p.T * p.k_max), p, st);
+  constexpr bool PAIR = XQ == 1;
+  constexpr int DOWN = FEW_RW * 4 * 4096, DOWN_LESS = FEW_RW * 3 * 4096;
+  const int tiles = p.d / (PAIR ? 8 : 16);
+  return DOWN + sums + list <= FEW_LDS
+             ? few_launch(few_down_dense_kernel<T, 4, PAIR>, tiles, FEW_RT, DOWN + sums + list, p, st)
+             : few_launch(few_down_dense_kernel<T, 3, PAIR>, tiles, FEW_RT, DOWN_LESS + sums + list, p, st);
 }
 
 template <class Op, int U>
@@ -737,7 +820,7 @@ static hipError_t few_q4(const FewArgs& p, hipStream_t st) {
 
 template <typename T>
 static hipError_t few_ffn(const FewArgs& p, int group, int zeros, hipStream_t st) {
-  if (group == 0) return p.T <= 8 ? few_dense<T, 3, 4, 1>(p, st) : few_dense<T, 2, 4, 2>(p, st);
+  if (group == 0) return p.T <= 8 ? few_dense<T, 5, 1>(p, st) : few_dense<T, 4, 2>(p, st);
   constexpr int U = sizeof(T) == 2 ? 2 : 1;
   if (group == 32) return zeros ? few_q4<Q4Op<T, 32, true>, U>(p, st) : few_q4<Q4Op<T, 32, false>, U>(p, st);
   if (group == 64) return zeros ? few_q4<Q4Op<T, 64, true>, U>(p, st) : few_q4<Q4Op<T, 64, false>, U>(p, st);
@@ -771,7 +854,7 @@ hipError_t launch_few(const FewLaunch& a, hipStream_t st) {
   p.out = a.out;
   if (a.w_router) {
     p.part = a.part, p.bias = a.bias, p.k = a.k, p.pol = a.pol, p.scale = a.scale;
-    const dim3 grid(ceil_div(a.E, 16), FEW_S);
+    const dim3 grid(ceil_div(a.E, 16), few_slices(a.d));
     if (a.dtype == DT_BF16)
       hipLaunchKernelGGL(few_logits_kernel<bf16_t>, grid, dim3(64 * FEW_LW), 0, st, (const bf16_t*)a.x,
                          (const bf16_t*)a.w_router, a.T, a.d, a.E, a.part);

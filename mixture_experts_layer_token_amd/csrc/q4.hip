@@ -196,6 +196,7 @@ __global__ __launch_bounds__(64 * QL_NW) void q4_linear_kernel(const typename Op
     Op::finish_x(xv);
     Op::mma(acc, v, xv);
   }
+  settle(acc);
   red[wave * 64 + lane] = acc;
   __syncthreads();
   if (wave >= 4) return;

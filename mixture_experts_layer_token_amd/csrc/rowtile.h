@@ -291,6 +291,13 @@ struct Q4Op {
   }
 };
 
+// Wait states between the last matrix instruction of a loop and the first use of its result
+// behind the loop: a block that is entered from the loop's end and from elsewhere came out
+// without them (a store to LDS right behind the branch took one of the four values before it
+// was there).  19 are the most that the longest instruction asks for.
+template <typename V>
+__device__ __forceinline__ void settle(V& acc) { asm volatile("s_nop 15\n\ts_nop 3" : "+v"(acc)); }
+
 // ---- sums that are not finite ----
 // A matrix instruction multiplies every column with every row: an infinity or NaN among
 // the weights turns the zeros of tokens that have no part in them into NaN, and the
