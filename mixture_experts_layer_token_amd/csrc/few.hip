@@ -55,6 +55,8 @@ struct FewArgs {
   const void* x;
   void* h;                  // in planes
   size_t plane;             // elements of a plane
+  const void* xh;           // 4-bit weights: x, as H is kept
+  size_t xplane;
   void* out;
   RowWeights w[6];          // gate, up, down, and the always-on expert's
 };
@@ -600,62 +602,191 @@ __global__ __launch_bounds__(FEW_RT) void few_down_dense_kernel(FewArgs p) {
 }
 
 // ---- 4-bit weights ----
-// A wave's share of K a step at a time, straight into registers: a step's codes are 1 KB in
-// a row and its arithmetic (16 rows x 128 codes made bf16, scaled per group) is what takes
-// the time.
-constexpr int FEW_QW = 16;                // waves of a workgroup
-constexpr int FEW_QT = 64 * FEW_QW;
-
-template <class Op>
-__global__ __launch_bounds__(FEW_QT) void few_gateup_q4_kernel(FewArgs p) {
-  extern __shared__ uint32_t few_smem[];  // the waves' sums (the list's scratch before), the list
+// As with element weights, a wave streams its share of K through a ring in LDS: at each step
+// NT tiles' codes (1 KB each in a row), their scales and zero points, and the activations,
+// which the tiles share.
+// Float32 activations are read as the three bf16 parts that few_split_kernel leaves in the
+// workspace: to take them apart beside each tile costs more than the tile.
+// XQ 1: up to 8 tokens lie in rows 0, 1, 4, 5, .. of the 16, and a lane scales two results
+// where it has four of 16 tokens (the vector instructions are as long as the copies).
+template <class Op, int NT, int XQ>
+struct FewQ {
   typedef typename Op::elt T;
-  const RowWeights wg = p.w[0], wu = p.w[1], sg = p.w[3], su = p.w[4];
-  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-  const int col = lane & 15;
-  const int steps = p.d / Op::KS;
-  const T* const x0 = static_cast<const T*>(p.x);
-  // columns without a token repeat the first one's activations; their sums are not used
-  const uint32_t xrow = (uint32_t)(col < p.T ? col : 0) * p.d * (uint32_t)sizeof(T);
-  f32x4_t* const red = reinterpret_cast<f32x4_t*>(few_smem);
-  const FewList L = few_carve(few_smem, few_smem + max(2 * FEW_QT * 4, few_scratch_words(p.T, p.E)), p.T, p.E, p.k_max);
-  const int n_list = few_list<FEW_QT>(p, L);
-  const int ci = p.I / TILE_N, routed = n_list * ci;
-  const int n_items = routed + p.Is / TILE_N;
-  if (blockIdx.x == 0) few_zero_row<Op, FEW_QT>(p);
-#pragma unroll 1
-  for (int item = blockIdx.x; item < n_items; item += p.stride) {
-    const bool sh = item >= routed;
-    const int idx = sh ? 0 : (int)((uint32_t)item / (uint32_t)ci);
-    const int n0 = (sh ? item - routed : item - idx * ci) * TILE_N, N = sh ? p.Is : p.I;
-    const int mat = sh ? 0 : __builtin_amdgcn_readfirstlane(L.expert[idx]);
-    const typename Op::Src gsrc = Op::tile(pick(sh, sg, wg), mat, n0, N, p.d, p.blocked);
-    const typename Op::Src usrc = Op::tile(pick(sh, su, wu), mat, n0, N, p.d, p.blocked);
-    f32x4_t ga = {0.f, 0.f, 0.f, 0.f}, ua = ga;
-#pragma unroll 1
-    for (int s = wave; s < steps; s += FEW_QW) {
-      const typename Op::W gw = Op::load(gsrc, s), uw = Op::load(usrc, s);
-      typename Op::X x = Op::load_x(x0, xrow, s);
-      Op::finish_x(x);
-      Op::mma(ga, gw, x);
-      Op::mma(ua, uw, x);
+  typedef typename Op::hid H;
+  static constexpr int RT = XQ == 1 ? 2 : 4;              // results of a lane
+  static constexpr int RUN = 16 * (int)sizeof(T);         // a tile's scales of one group
+  static constexpr int SB = NT * Op::NG * RUN, SC = SB > 256 ? 2 : 1, ZB = NT * Op::NG * 16;
+  static constexpr int X0 = NT * 1024, S0 = X0 + 2048 * XQ * Op::PLANES, Z0 = S0 + 256 * SC;
+  static constexpr int SLOT = Z0 + (Op::ZP ? 256 : 0);
+  static constexpr int SW = Op::PLANES * XQ > 3 ? 4 : FEW_RW;  // waves that stream: 16 float32 tokens' slots fit 4
+  static constexpr int RING = SW * SLOT, SUMS = NT * SW * 64 * RT * 4;  // bytes: one slot of each, their sums
+  static constexpr int PER = NT + 2 * XQ * Op::PLANES + SC + (Op::ZP ? 1 : 0);
+
+  // where a step's operands come from
+  const char* q[NT];
+  const char* s[SC];            // of a lane
+  const char* z;
+  size_t s_step, z_step;
+
+  __device__ __forceinline__ void seek(const typename Op::Src (&t)[NT]) {
+    const int lane = threadIdx.x & 63;
+    s_step = (size_t)Op::NG * t[0].Np * sizeof(T);
+    z_step = (size_t)Op::NG * t[0].Np;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) q[i] = reinterpret_cast<const char*>(t[i].q);
+#pragma unroll
+    for (int c = 0; c < SC; ++c) {  // lanes behind the scales copy some again
+      const int b = (256 * c + 4 * lane) % SB;
+      const T* const base = NT == 1 || b < SB / 2 ? t[0].s : t[NT - 1].s;
+      s[c] = reinterpret_cast<const char*>(base) + (size_t)(b / RUN % Op::NG) * t[0].Np * sizeof(T) + b % RUN;
     }
-    settle(ga);
-    settle(ua);
-    red[wave * 64 + lane] = ga;
-    red[FEW_QT + wave * 64 + lane] = ua;
-    __syncthreads();
-    if (wave < 4) {
+    if (Op::ZP) {
+      const int b = 4 * lane % ZB;
+      const uint8_t* const base = NT == 1 || b < ZB / 2 ? t[0].z : t[NT - 1].z;
+      z = reinterpret_cast<const char*>(base) + (size_t)(b / 16 % Op::NG) * t[0].Np + b % 16;
+    }
+  }
+  // Activations: a lane's rows start off[] bytes behind x, planes `plane` elements apart.
+  __device__ __forceinline__ void request(char* to, int step, const H* x, size_t plane, const uint32_t (&off)[XQ]) const {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) few_copy<2>(q[i] + (size_t)step * 1024, (threadIdx.x & 63) * 16, to + 1024 * i);
+#pragma unroll
+    for (int c = 0; c < SC; ++c)
+      __builtin_amdgcn_global_load_lds((gbl_ptr_t)(s[c] + step * s_step), (lds_ptr_t)(to + S0 + 256 * c), 4, 0, 0);
+    if (Op::ZP) __builtin_amdgcn_global_load_lds((gbl_ptr_t)(z + step * z_step), (lds_ptr_t)(to + Z0), 4, 0, 0);
+#pragma unroll
+    for (int p = 0; p < Op::PLANES; ++p)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int c = 0; c < XQ; ++c)
+          few_copy<0>(x + p * plane + step * Op::KS + 64 * h, off[c], to + X0 + 1024 * ((p * 2 + h) * XQ + c));
+  }
+  __device__ __forceinline__ static void load(const char* from, typename Op::W (&w)[NT], typename Op::X& x) {
+    const int lane = threadIdx.x & 63, n = lane & 15, row = XQ == 1 ? (n >> 2) * 2 + (n & 1) : n;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      w[i].q = *reinterpret_cast<const u32x4_t*>(from + 1024 * i + 16 * lane);
+#pragma unroll
+      for (int g = 0; g < Op::NG; ++g) {
+        w[i].s[g] = *reinterpret_cast<const T*>(from + S0 + (i * Op::NG + g) * RUN + n * (int)sizeof(T));
+        if (Op::ZP) w[i].z[g] = *reinterpret_cast<const uint8_t*>(from + Z0 + (i * Op::NG + g) * 16 + n);
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < Op::PLANES; ++p)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        x.v[p][i] = *reinterpret_cast<const u32x4_t*>(from + X0 + 1024 * XQ * (p * 2 + i / 2) +
+                                                      lds_off(row, (lane >> 4) + 4 * (i & 1)));
+  }
+  // The waves' results of tile i in LDS, and their sum for output n of token t, in wave order.
+  __device__ __forceinline__ static void keep(float* red, int i, f32x4_t acc) {
+    if (SW < FEW_RW && threadIdx.x >= SW * 64) return;
+#pragma unroll
+    for (int r = 0; r < RT; ++r) red[(i * SW * 64 + threadIdx.x) * RT + r] = acc[r];
+  }
+  __device__ __forceinline__ static float sum(const float* red, int i, int n, int t) {
+    const float* const r = red + (i * SW * 64 + t / RT * 16 + n) * RT + t % RT;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < SW; ++w) v += r[w * 64 * RT];
+    return v;
+  }
+};
+
+// Neighbouring tiles share their scales' 128-byte lines, so the workgroups of one XCD (every
+// eighth) take neighbours: tile of workgroup b of n.
+__device__ __forceinline__ int few_near(int b, int n) { return n & 7 ? b : (b & 7) * (n >> 3) + (b >> 3); }
+
+template <class Op, int NB, int XQ>
+__global__ __launch_bounds__(FEW_RT) void few_gateup_q4_kernel(FewArgs p) {
+  typedef FewQ<Op, 2, XQ> Q;
+  typedef typename Op::elt T;
+  typedef typename Op::hid H;
+  extern __shared__ char few_ring[];  // the rings (the list's scratch before), the waves' sums, the list
+  const RowWeights wg = p.w[0], wu = p.w[1], sg = p.w[3], su = p.w[4];
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int ring_bytes = max(NB * Q::RING, few_scratch_words(p.T, p.E) * 4);
+  float* const red = reinterpret_cast<float*>(few_ring + ring_bytes);
+  const FewList L = few_carve(reinterpret_cast<uint32_t*>(few_ring),
+                              reinterpret_cast<uint32_t*>(red + Q::SUMS / 4), p.T, p.E, p.k_max);
+  const int n_list = few_list<FEW_RT>(p, L);
+  if (blockIdx.x == 0) few_zero_row<Op, FEW_RT>(p);
+  const int ci = p.I / TILE_N, routed = n_list * ci;
+  const int n_items = routed + p.Is / TILE_N, first = few_near(blockIdx.x, p.stride);
+  const int steps = p.d / Op::KS;
+  const int beg = wave < Q::SW ? steps * wave / Q::SW : 0, end = wave < Q::SW ? steps * (wave + 1) / Q::SW : 0;
+  uint32_t xoff[XQ];
+#pragma unroll
+  for (int c = 0; c < XQ; ++c)  // rows behind the last token repeat it; their sums are not used
+    xoff[c] = (uint32_t)min(few_copy_row(c), p.T - 1) * p.d * (uint32_t)sizeof(H) + few_copy_byte(c);
+  char* const ring = few_ring + wave * NB * Q::SLOT;
+
+  // requests: a step of the item `want`; behind the last item its last step again
+  Q rq;
+  int want = first, rs = beg;
+  auto seek = [&]() {
+    const bool sh = want >= routed;
+    const int idx = sh ? 0 : (int)((uint32_t)want / (uint32_t)ci);
+    const int n0 = (sh ? want - routed : want - idx * ci) * TILE_N, N = sh ? p.Is : p.I;
+    const int mat = sh ? 0 : __builtin_amdgcn_readfirstlane(L.expert[idx]);
+    rq.seek({Op::tile(pick(sh, sg, wg), mat, n0, N, p.d), Op::tile(pick(sh, su, wu), mat, n0, N, p.d)});
+  };
+  auto request = [&](int slot) {
+    rq.request(ring + slot * Q::SLOT, rs, static_cast<const H*>(p.xh), p.xplane, xoff);
+    if (rs + 1 < end) {
+      ++rs;
+    } else if (want + p.stride < n_items) {
+      want += p.stride;
+      rs = beg;
+      seek();
+    }
+  };
+  if (beg < end && want < n_items) {
+    seek();
+#pragma unroll 1
+    for (int i = 0; i < NB; ++i) request(i);
+  }
+  int slot = 0;
+#pragma unroll 1
+  for (int item = first; item < n_items; item += p.stride) {
+    f32x4_t ga[1] = {{0.f, 0.f, 0.f, 0.f}}, ua[1] = {{0.f, 0.f, 0.f, 0.f}};
+#pragma unroll 1
+    for (int s = beg; s < end; ++s) {
+      vm_wait<Q::PER * (NB - 1)>();
+      compiler_fence();
+      typename Op::W w[2];
+      typename Op::X x[1];
+      Q::load(ring + slot * Q::SLOT, w, x[0]);
+      lgkm_wait0();  // read before the slot is filled again
+      compiler_fence();
+      request(slot);
+      slot = slot + 1 == NB ? 0 : slot + 1;
+      const typename Op::Sum sum[1] = {Op::sums(x[0])};
+      Op::template mma<1, Q::RT>(ga, w[0], x, sum);
+      Op::template mma<1, Q::RT>(ua, w[1], x, sum);
+    }
+    settle(ga[0]);
+    settle(ua[0]);
+    Q::keep(red, 0, ga[0]);
+    Q::keep(red, 1, ua[0]);
+    few_barrier();
+    if (wave < 2 * XQ) {
+      const bool sh = item >= routed;
+      const int idx = sh ? 0 : (int)((uint32_t)item / (uint32_t)ci);
+      const int n0 = (sh ? item - routed : item - idx * ci) * TILE_N, N = sh ? p.Is : p.I;
+      const int mat = sh ? 0 : __builtin_amdgcn_readfirstlane(L.expert[idx]);
       const int j = tid & 15, t = tid >> 4;
-      float g = few_sum<FEW_QW>(red, j, t), u = few_sum<FEW_QW>(red + FEW_QT, j, t);
+      float g = Q::sum(red, 0, j, t), u = Q::sum(red, 1, j, t);
       const int row = sh ? p.T * p.k_max + t : few_row(L, idx, t);
       const bool mine = t < p.T && row != p.zero_row;
       auto again = [&](RowWeights rw, float& val) {
         redo_not_finite(val, mine, [&](int l) {
-          const T* xr = x0 + (size_t)((wave * 64 + l) >> 4) * p.d;
+          const T* xr = static_cast<const T*>(p.x) + (size_t)((wave * 64 + l) >> 4) * p.d;
           const int nn = n0 + (l & 15);
           return wave_dot(p.d, [&](int k) {
-            return Elt<T>::to_f32(xr[k]) * Op::value(rw, mat, nn, k, N, p.d, p.blocked);
+            return Elt<T>::to_f32(xr[k]) * Op::value(rw, mat, nn, k, N, p.d, 0);
           });
         });
       };
@@ -663,63 +794,111 @@ __global__ __launch_bounds__(FEW_QT) void few_gateup_q4_kernel(FewArgs p) {
       again(pick(sh, su, wu), u);
       if (mine) few_store_h<Op>(p, L, sh, n0 + j, g, u, row);
     }
-    __syncthreads();
+    few_barrier();
   }
+  vm_wait<0>();  // no copy into LDS outlives the workgroup
 }
 
-template <class Op, int U>
-__global__ __launch_bounds__(FEW_QT) void few_down_q4_kernel(FewArgs p) {
-  extern __shared__ uint32_t few_smem[];
-  __shared__ f32x4_t red[FEW_QT];
+// Down: NT tiles of 16 outputs for every token, otherwise as with element weights.
+template <class Op, int NB, int XQ, int NT>
+__global__ __launch_bounds__(FEW_RT) void few_down_q4_kernel(FewArgs p) {
+  typedef FewQ<Op, NT, XQ> Q;
+  typedef typename Op::hid H;
+  extern __shared__ char few_ring[];  // the rings, the waves' sums, the list
   const RowWeights wr = p.w[2], ws = p.w[5];
-  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-  const int col = lane & 15, n0 = blockIdx.x * TILE_N;
-  const int n_list = few_load_list<FEW_QT>(p, few_smem);
-  const int32_t* const l_expert = reinterpret_cast<const int32_t*>(few_smem);
-  const uint16_t* const row_of = reinterpret_cast<const uint16_t*>(few_smem + min(p.E, p.T * p.k_max));
-  const typename Op::hid* const h = static_cast<const typename Op::hid*>(p.h);
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n0 = few_near(blockIdx.x, gridDim.x) * (NT * TILE_N);
+  float* const red = reinterpret_cast<float*>(few_ring + NB * Q::RING);
+  int32_t* const list = reinterpret_cast<int32_t*>(red + Q::SUMS / 4);
+  const int32_t* const l_expert = list;
+  const uint16_t* const row_of = reinterpret_cast<const uint16_t*>(list + min(p.E, p.T * p.k_max));
+  const int n_list = few_load_list<FEW_RT>(p, reinterpret_cast<uint32_t*>(list));
+  __syncthreads();
   const int spe = p.I / Op::KS, routed = n_list * spe, steps = routed + p.Is / Op::KS;
-  const int beg = steps * wave / FEW_QW, end = steps * (wave + 1) / FEW_QW;
-  int idx = beg < routed ? (int)((uint32_t)beg / (uint32_t)spe) : n_list, st = beg - min(idx * spe, routed);
-  const int own = col < p.T ? p.T * p.k_max + col : p.zero_row;  // the always-on expert's
-  __syncthreads();
+  const int beg = wave < Q::SW ? steps * wave / Q::SW : 0, end = wave < Q::SW ? steps * (wave + 1) / Q::SW : 0;
+  char* const ring = few_ring + wave * NB * Q::SLOT;
 
-  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-  for (int s = beg; s < end; s += U) {
-    typename Op::W w[U];
-    typename Op::X x[U];
+  // requests: step st of expert idx of the list (behind it: the always-on expert); behind the
+  // wave's end its last step again
+  int idx = beg < routed ? (int)((uint32_t)beg / (uint32_t)spe) : n_list, st = beg - min(idx * spe, routed), left = end - beg;
+  Q rq;
+  uint32_t hoff[XQ];
+  auto seek = [&]() {
+    const bool sh = idx >= n_list;
+    const int mat = sh ? 0 : __builtin_amdgcn_readfirstlane(l_expert[idx]);
+    typename Op::Src t[NT];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool sh = idx >= n_list;
-      const int i = sh ? 0 : idx;
-      const int e = sh ? 0 : __builtin_amdgcn_readfirstlane(l_expert[i]);
-      const int row = sh ? own : row_of[i * FEW_T + col];
-      w[u] = Op::load(Op::tile(pick(sh, ws, wr), e, n0, p.d, sh ? p.Is : p.I, p.blocked), st);
-      x[u] = Op::load_h(h, (uint32_t)row * p.hw * (uint32_t)sizeof(typename Op::hid), p.plane, st);
-      // the last step again behind the end
-      const bool more = s + u + 1 < end, turn = more && !sh && st + 1 == spe;
-      st = turn ? 0 : st + (more ? 1 : 0);
-      idx += turn ? 1 : 0;
+    for (int i = 0; i < NT; ++i) t[i] = Op::tile(pick(sh, ws, wr), mat, n0 + i * TILE_N, p.d, sh ? p.Is : p.I);
+    rq.seek(t);
+#pragma unroll
+    for (int c = 0; c < XQ; ++c) {
+      const int tok = few_copy_row(c);
+      const int row = sh ? (tok < p.T ? p.T * p.k_max + tok : p.zero_row) : row_of[idx * FEW_T + tok];
+      hoff[c] = (uint32_t)row * p.hw * (uint32_t)sizeof(H) + few_copy_byte(c);
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (s + u < end) {
-        Op::finish_x(x[u]);
-        Op::mma(acc, w[u], x[u]);
+  };
+  auto request = [&](int slot) {
+    rq.request(ring + slot * Q::SLOT, st, static_cast<const H*>(p.h), p.plane, hoff);
+    if (--left > 0) {
+      ++st;
+      if (idx < n_list && st == spe) {
+        ++idx;
+        st = 0;
+        seek();
       }
+    }
+  };
+  f32x4_t acc[NT][1];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) acc[i][0] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  if (beg < end) {
+    seek();
+#pragma unroll 1
+    for (int i = 0; i < NB; ++i) request(i);
+    int slot = 0;
+#pragma unroll 1
+    for (int s = beg; s < end; ++s) {
+      vm_wait<Q::PER * (NB - 1)>();
+      compiler_fence();
+      typename Op::W w[NT];
+      typename Op::X x[1];
+      Q::load(ring + slot * Q::SLOT, w, x[0]);
+      lgkm_wait0();
+      compiler_fence();
+      request(slot);
+      slot = slot + 1 == NB ? 0 : slot + 1;
+      const typename Op::Sum sum[1] = {Op::sums(x[0])};
+#pragma unroll
+      for (int i = 0; i < NT; ++i) Op::template mma<1, Q::RT>(acc[i], w[i], x, sum);
+    }
+    vm_wait<0>();  // no copy into LDS outlives the workgroup
   }
-  settle(acc);
-  red[wave * 64 + lane] = acc;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    settle(acc[i][0]);
+    Q::keep(red, i, acc[i][0]);
+  }
   __syncthreads();
-  if (wave < 4) {
-    const int j = tid & 15, t = tid >> 4;
-    float v = few_sum<FEW_QW>(red, j, t);
+  if (wave < 2 * XQ * NT) {
+    const int j = tid % (NT * 16), t = tid / (NT * 16);
+    float v = Q::sum(red, j >> 4, j & 15, t);
     redo_not_finite(v, t < p.T, [&](int l) {
-      return few_down_again<Op>(p, l_expert, row_of, n_list, n0 + (l & 15), (wave * 64 + l) >> 4);
+      const int i = wave * 64 + l;
+      return few_down_again<Op>(p, l_expert, row_of, n_list, n0 + i % (NT * 16), i / (NT * 16));
     });
     if (t < p.T) static_cast<typename Op::elt*>(p.out)[(size_t)t * p.d + n0 + j] = Elt<typename Op::elt>::from_f32(v);
   }
+}
+
+// The three bf16 parts of float32 activations.
+__global__ __launch_bounds__(256) void few_split_kernel(const float* __restrict__ x, int n, bf16_t* __restrict__ to) {
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  uint32_t a, b, c;
+  split3(x[i], a, b, c);
+  to[i] = (bf16_t)(a >> 16);
+  to[n + i] = (bf16_t)(b >> 16);
+  to[2 * n + i] = (bf16_t)(c >> 16);
 }
 
 // Partial logits part[slices][T][E] in float64 on the f64 matrix instruction: a workgroup
@@ -810,27 +989,67 @@ static hipError_t few_dense(FewArgs p, hipStream_t st) {
              : few_launch(few_down_dense_kernel<T, 3, PAIR>, tiles, FEW_RT, DOWN_LESS + sums + list, p, st);
 }
 
-template <class Op, int U>
-static hipError_t few_q4(const FewArgs& p, hipStream_t st) {
-  const size_t lds = ((size_t)max(2 * FEW_QT * 4, few_scratch_words(p.T, p.E)) + few_kept_words(p.T, p.E, p.k_max)) * 4;
-  const hipError_t e = few_launch(few_gateup_q4_kernel<Op>, p.stride, FEW_QT, lds, p, st);
+constexpr int FEW_Q_WIDE = 4096;
+// Steps of a ring: 160 KB less the sums and 8 KB for a list.
+constexpr int few_depth(int ring, int sums, int most) {
+  const int deep = (FEW_LDS - 8192 - sums) / ring;
+  return deep < 1 ? 1 : deep < most ? deep : most;
+}
+
+template <class Op, int XQ, int NT>
+static hipError_t few_q4_down(const FewArgs& p, int list, hipStream_t st) {
+  typedef FewQ<Op, NT, XQ> Q;
+  constexpr int SUMS = Q::SUMS, NB = few_depth(Q::RING, SUMS, 5), LESS = NB > 1 ? NB - 1 : 1;
+  const int lds = NB * Q::RING + SUMS + list, tiles = p.d / (NT * TILE_N);
+  return lds <= FEW_LDS ? few_launch(few_down_q4_kernel<Op, NB, XQ, NT>, tiles, FEW_RT, lds, p, st)
+                        : few_launch(few_down_q4_kernel<Op, LESS, XQ, NT>, tiles, FEW_RT,
+                                     LESS * Q::RING + SUMS + list, p, st);
+}
+
+template <class Op, int XQ>
+static hipError_t few_q4_as(FewArgs p, hipStream_t st) {
+  if (Op::PLANES == 1) {
+    p.xh = p.x;
+  } else {
+    const int n = p.T * p.d;
+    bf16_t* const to = static_cast<bf16_t*>(p.h) + Op::PLANES * p.plane;
+    p.xh = to, p.xplane = n;
+    hipLaunchKernelGGL(few_split_kernel, dim3(ceil_div(n, 256)), dim3(256), 0, st, (const float*)p.x, n, to);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  const int kept = few_kept_words(p.T, p.E, p.k_max) * 4, list = 36 * min(p.E, p.T * p.k_max);
+  p.stride = min(256, min(p.E, p.T * p.k_max) * (p.I / TILE_N) + p.Is / TILE_N);
+  // ring depths: as many steps as 160 KB of LDS hold, one less where the list is long
+  typedef FewQ<Op, 2, XQ> Q;
+  constexpr int SUMS = Q::SUMS, NB = few_depth(Q::RING, SUMS, 4), LESS = NB > 1 ? NB - 1 : 1;
+  const int scratch = few_scratch_words(p.T, p.E) * 4;
+  const int up = max(NB * Q::RING, scratch) + SUMS + kept;
+  hipError_t e;
+  if (up <= FEW_LDS) e = few_launch(few_gateup_q4_kernel<Op, NB, XQ>, p.stride, FEW_RT, up, p, st);
+  else e = few_launch(few_gateup_q4_kernel<Op, LESS, XQ>, p.stride, FEW_RT, max(LESS * Q::RING, scratch) + SUMS + kept, p, st);
   if (e != hipSuccess) return e;
-  return few_launch(few_down_q4_kernel<Op, U>, p.d / TILE_N, FEW_QT, (size_t)36 * min(p.E, p.T * p.k_max), p, st);
+  return p.d >= FEW_Q_WIDE ? few_q4_down<Op, XQ, 2>(p, list, st) : few_q4_down<Op, XQ, 1>(p, list, st);
+}
+
+template <class Op>
+static hipError_t few_q4(const FewArgs& p, hipStream_t st) {
+  return p.T <= 8 ? few_q4_as<Op, 1>(p, st) : few_q4_as<Op, 2>(p, st);
 }
 
 template <typename T>
 static hipError_t few_ffn(const FewArgs& p, int group, int zeros, hipStream_t st) {
   if (group == 0) return p.T <= 8 ? few_dense<T, 5, 1>(p, st) : few_dense<T, 4, 2>(p, st);
-  constexpr int U = sizeof(T) == 2 ? 2 : 1;
-  if (group == 32) return zeros ? few_q4<Q4Op<T, 32, true>, U>(p, st) : few_q4<Q4Op<T, 32, false>, U>(p, st);
-  if (group == 64) return zeros ? few_q4<Q4Op<T, 64, true>, U>(p, st) : few_q4<Q4Op<T, 64, false>, U>(p, st);
-  return zeros ? few_q4<Q4Op<T, 128, true>, U>(p, st) : few_q4<Q4Op<T, 128, false>, U>(p, st);
+  if (group == 32) return zeros ? few_q4<Q4Op<T, 32, true>>(p, st) : few_q4<Q4Op<T, 32, false>>(p, st);
+  if (group == 64) return zeros ? few_q4<Q4Op<T, 64, true>>(p, st) : few_q4<Q4Op<T, 64, false>>(p, st);
+  return zeros ? few_q4<Q4Op<T, 128, true>>(p, st) : few_q4<Q4Op<T, 128, false>>(p, st);
 }
 
 size_t few_part_count(int T, int E) { return (size_t)FEW_S * T * E; }
-size_t few_h_bytes(int dtype, int q4, int T, int k_max, int I, int Is) {
+size_t few_h_bytes(int dtype, int T, int d, int k_max, int I, int Is) {
   const size_t rows = (size_t)T * k_max + T + 1;  // choices, the always-on expert's, zeros
-  return rows * max(I, Is) * (dtype == DT_BF16 ? 2 : (q4 ? 6 : 4));
+  // float32 with 4-bit weights: three planes, and x in three planes behind them
+  return dtype == DT_BF16 ? rows * max(I, Is) * 2 : (rows * max(I, Is) + (size_t)T * d) * 6;
 }
 
 hipError_t launch_few(const FewLaunch& a, hipStream_t st) {
@@ -848,7 +1067,6 @@ hipError_t launch_few(const FewLaunch& a, hipStream_t st) {
   p.n_list = a.n_list, p.expert = a.expert, p.rows = a.rows;
   p.h = a.h;
   p.hw = max(a.I, a.Is);
-  p.stride = min(256, min(a.E, a.T * a.k_max) * (a.I / TILE_N) + a.Is / TILE_N);
   p.zero_row = a.T * a.k_max + a.T;
   p.plane = ((size_t)p.zero_row + 1) * p.hw;
   p.out = a.out;

@@ -252,7 +252,7 @@ struct FewLaunch {
   void* out;
 };
 size_t few_part_count(int T, int E);
-size_t few_h_bytes(int dtype, int q4, int T, int k_max, int I, int Is);
+size_t few_h_bytes(int dtype, int T, int d, int k_max, int I, int Is);
 hipError_t launch_few(const FewLaunch& a, hipStream_t st);
 
 // q4.hip -- 4-bit weights (rowtile.h has the order of the codes).

@@ -222,7 +222,7 @@ void plan_few(const moe_desc& d, Carver& c, FewWs& w) {
   w.n_list = c.take<int32_t>(1);
   w.expert = c.take<int32_t>(cap);
   w.rows = c.take<uint32_t>(cap * 8);
-  w.h = c.take_bytes(few_h_bytes(d.dtype, 1, d.T, d.k_max, d.I, d.I_shared));
+  w.h = c.take_bytes(few_h_bytes(d.dtype, d.T, d.d, d.k_max, d.I, d.I_shared));
 }
 
 // What moe_forward asks of its workspace: its own regions, and as much as folding

@@ -170,49 +170,81 @@ __global__ __launch_bounds__(256) void q4_unpack_kernel(const uint32_t* __restri
 }
 
 // -------------------------------------------------------------- few-row product
-// y[r][n] = sum_k x[r][k] W[n][k].  A workgroup takes 16 outputs of up to 16 rows, its
-// waves a share of K each, and adds their sums in LDS.  (More rows: one more pass over
-// the weights for each 16, which the caches hold for all but the widest.)
-constexpr int QL_NW = 8;
-
-template <class Op>
-__global__ __launch_bounds__(64 * QL_NW) void q4_linear_kernel(const typename Op::elt* __restrict__ x, RowWeights w,
-                                                               int rows, int N, int K,
-                                                               typename Op::elt* __restrict__ y) {
+// y[r][n] = sum_k x[r][k] W[n][k].  A workgroup takes NT tiles of 16 outputs and R blocks of
+// 16 rows, its waves a share of K each, and adds their sums in LDS.
+template <class Op, int R, int NT, int U, int NW>
+__global__ __launch_bounds__(64 * NW) void q4_linear_kernel(const typename Op::elt* __restrict__ x, RowWeights w,
+                                                            int rows, int N, int K,
+                                                            typename Op::elt* __restrict__ y) {
   typedef typename Op::elt T;
-  __shared__ f32x4_t red[QL_NW * 64];
+  __shared__ f32x4_t red[NT][NW * 64];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, col = lane & 15;
-  const int n0 = blockIdx.x * TILE_N, row = blockIdx.y * 16 + col;
+  const int n0 = blockIdx.x * (NT * TILE_N), r0 = blockIdx.y * (16 * R);
   const int steps = ceil_div(K, Q4_K);
-  const int beg = steps * wave / QL_NW, end = steps * (wave + 1) / QL_NW;
-  const T* x0 = x + (size_t)blockIdx.y * 16 * K;
-  const uint32_t xrow = (uint32_t)(row < rows ? col : 0) * K * (uint32_t)sizeof(T);
-  const typename Op::Src src = Op::tile(w, 0, n0, N, K, 0);
-  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-  for (int s = beg; s < end; ++s) {
-    const typename Op::W v = Op::load(src, s);
-    typename Op::X xv = Op::load_x(x0, xrow, s, K);
-    if (row >= rows) Op::clear(xv);
-    Op::finish_x(xv);
-    Op::mma(acc, v, xv);
-  }
-  settle(acc);
-  red[wave * 64 + lane] = acc;
-  __syncthreads();
-  if (wave >= 4) return;
-  // thread: output j of row r of the tile
-  const int j = threadIdx.x & 15, r = threadIdx.x >> 4, n = n0 + j;
-  const float* q = reinterpret_cast<const float*>(red) + ((j >> 2) * 16 + r) * 4 + (j & 3);
-  float v = 0.f;
+  const int beg = steps * wave / NW, end = steps * (wave + 1) / NW;
+  const T* const x0 = x + (size_t)r0 * K;
+  uint32_t xrow[R];
 #pragma unroll
-  for (int i = 0; i < QL_NW; ++i) v += q[i * 256];
-  const bool mine = blockIdx.y * 16 + r < rows && n < N;
-  redo_not_finite(v, mine, [&](int l) {
-    const T* xr = x0 + (size_t)((wave * 64 + l) >> 4) * K;
-    const int nn = n0 + (l & 15);
-    return wave_dot(K, [&](int k) { return Elt<T>::to_f32(xr[k]) * Op::value(w, 0, nn, k, N, K, 0); });
-  });
-  if (mine) y[(size_t)(blockIdx.y * 16 + r) * N + n] = Elt<T>::from_f32(v);
+  for (int r = 0; r < R; ++r)  // rows behind the last repeat it; their sums are not used
+    xrow[r] = (uint32_t)min(16 * r + col, rows - 1 - r0) * K * (uint32_t)sizeof(T);
+  f32x4_t acc[NT][R];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int r = 0; r < R; ++r) acc[t][r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  typename Op::Src src[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)  // tiles behind the last repeat it
+    src[t] = Op::tile(w, 0, min(n0 + t * TILE_N, ceil_div(N, TILE_N) * TILE_N - TILE_N), N, K);
+#pragma unroll 1
+  for (int s = beg; s < end; s += U) {
+    typename Op::W v[U][NT];
+    typename Op::X xv[U][R];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = min(s + u, end - 1);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) v[u][t] = Op::load(src[t], at);
+#pragma unroll
+      for (int r = 0; r < R; ++r) xv[u][r] = Op::load_x(x0, xrow[r], at, K);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (s + u < end) {
+        typename Op::Sum sum[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) sum[r] = Op::sums(xv[u][r]);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) Op::mma(acc[t], v[u][t], xv[u], sum);
+      }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      settle(acc[t][r]);
+      red[t][wave * 64 + lane] = acc[t][r];
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int i = threadIdx.x; i < NT * 256; i += 64 * NW) {
+      // output j of row c of the block
+      const int j = i % (NT * 16), c = i / (NT * 16), n = n0 + j, row = r0 + 16 * r + c;
+      const float* q = reinterpret_cast<const float*>(red[j >> 4]) + ((c >> 2) * 16 + (j & 15)) * 4 + (c & 3);
+      float sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < NW; ++k) sum += q[k * 256];
+      const bool mine = row < rows && n < N;
+      redo_not_finite(sum, mine, [&](int l) {
+        const int e = i - lane + l;
+        const T* xr = x0 + (size_t)(16 * r + e / (NT * 16)) * K;
+        const int nn = n0 + e % (NT * 16);
+        return wave_dot(K, [&](int k) { return Elt<T>::to_f32(xr[k]) * Op::value(w, 0, nn, k, N, K, 0); });
+      });
+      if (mine) y[(size_t)row * N + n] = Elt<T>::from_f32(sum);
+    }
+    if (r + 1 < R) __syncthreads();
+  }
 }
 
 // -------------------------------------------------------------------- launches
@@ -258,14 +290,30 @@ static void unpack_t(const Q4Shape& s, const void* codes, const void* scales, co
   MOE_Q4_ALL(MOE_CALL);
 #undef MOE_CALL
 }
+constexpr int QL_WIDE = 8192;
+
+template <class Op, int R, int NT, int U, int NW>
+static void linear_as(const Q4Shape& s, int rows, const void* x, const RowWeights& w, void* y, hipStream_t st) {
+  typedef typename Op::elt T;
+  hipLaunchKernelGGL((q4_linear_kernel<Op, R, NT, U, NW>), dim3(ceil_div(s.N, NT * TILE_N), ceil_div(rows, 16 * R)),
+                     dim3(64 * NW), 0, st, (const T*)x, w, rows, s.N, s.K, (T*)y);
+}
+template <class Op>
+static void linear_op(const Q4Shape& s, int rows, const void* x, const RowWeights& w, void* y, hipStream_t st) {
+  const bool wide = s.N >= QL_WIDE;
+  if constexpr (Op::PLANES == 1) {
+    if (rows <= 16) wide ? linear_as<Op, 1, 4, 1, 8>(s, rows, x, w, y, st) : linear_as<Op, 1, 1, 4, 16>(s, rows, x, w, y, st);
+    else if (rows <= 32) wide ? linear_as<Op, 2, 4, 1, 8>(s, rows, x, w, y, st) : linear_as<Op, 2, 1, 2, 16>(s, rows, x, w, y, st);
+    else wide ? linear_as<Op, 4, 2, 1, 8>(s, rows, x, w, y, st) : linear_as<Op, 4, 1, 1, 16>(s, rows, x, w, y, st);
+  } else {
+    wide ? linear_as<Op, 1, 4, 1, 8>(s, rows, x, w, y, st) : linear_as<Op, 1, 1, 2, 8>(s, rows, x, w, y, st);
+  }
+}
 template <typename T>
 static void linear_t(const Q4Shape& s, int rows, const void* x, const void* codes, const void* scales,
                      const void* zeros, void* y, hipStream_t st) {
   const RowWeights w{codes, scales, static_cast<const uint8_t*>(zeros)};
-  const dim3 grid(ceil_div(s.N, TILE_N), ceil_div(rows, 16));
-#define MOE_CALL(GR_, ZP_)                                                                                           \
-  hipLaunchKernelGGL((q4_linear_kernel<Q4Op<T, GR_, ZP_>>), grid, dim3(64 * QL_NW), 0, st, (const T*)x, w, rows, s.N, \
-                     s.K, (T*)y)
+#define MOE_CALL(GR_, ZP_) linear_op<Q4Op<T, GR_, ZP_>>(s, rows, x, w, y, st)
   MOE_Q4_ALL(MOE_CALL);
 #undef MOE_CALL
 }

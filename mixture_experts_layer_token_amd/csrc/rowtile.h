@@ -1,11 +1,12 @@
 // Few activation rows against streamed weights: operands of 16-row weight tiles.
 //
 // A wave multiplies a tile of 16 weight rows with up to 16 activation rows by
-// 16x16 matrix instructions whose A side is the weights (row lane % 16) and whose
-// B side the activations (column lane % 16); the result holds rows 4 * (lane / 16)
-// + r of column lane % 16.  With few rows the weights' bytes are the time, so an
-// operand's `W` is what one lane loads of a tile for one step of K, `X` the
-// matching activations:
+// 16x16 matrix instructions; lane l supplies row l % 16 of either side, and the
+// result holds rows 4 * (l / 16) + r of the first side and column l % 16, a row of the
+// second.  Element weights are the first side.  4-bit weights are the second, so that a
+// lane's results share one scale and one zero point.  With few rows the weights' bytes are
+// the time, so an operand's `W` is what one lane loads of a tile for one step of K, `X`
+// the matching activations:
 //
 //   DenseOp<bf16>   64 of K: two 16-byte loads, 2 instructions
 //   DenseOp<float>  32 of K: two 16-byte loads, 8 instructions
@@ -143,34 +144,34 @@ struct Q4Op {
   typedef bf16_t hid;                             // float32: three planes of it
   static constexpr int KS = Q4_K;
   static constexpr int PLANES = sizeof(T) == 2 ? 1 : 3;
-  static constexpr bool Q4 = true;
+  static constexpr bool Q4 = true, ZP = ZEROS;
   static constexpr int NG = Q4_K / GROUP;         // groups of a step
   static constexpr int PER = 4 / NG;              // instructions of a group
   struct W {
     u32x4_t q;
-    u32x2_t s2[sizeof(T) == 2 ? NG : 1];          // four rows' scales, bf16
-    f32x4_t s4[sizeof(T) == 2 ? 1 : NG];          // or float32
-    uint32_t z[ZEROS ? NG : 1];
+    T s[NG];                                      // of row lane % 16
+    uint8_t z[ZEROS ? NG : 1];
   };
-  struct X { u32x4_t v[PLANES][4]; float sum[NG]; };
+  struct X { u32x4_t v[PLANES][4]; };
+  struct Sum { f32x4_t v[NG]; };                  // the groups' sums of x, as the results lie
   struct Src { const u32x4_t* q; const T* s; const uint8_t* z; int Np; };
 
-  __device__ __forceinline__ static Src tile(const RowWeights& m, int mat, int n0, int N, int K, int) {
+  __device__ __forceinline__ static Src tile(const RowWeights& m, int mat, int n0, int N, int K) {
     const int kt = ceil_div(K, Q4_K), nt = ceil_div(N, TILE_N), Np = nt * TILE_N;
     const size_t g = (size_t)mat * kt * NG * Np + n0;
     return Src{static_cast<const u32x4_t*>(m.w) + ((size_t)mat * nt + n0 / TILE_N) * kt * 64,
                static_cast<const T*>(m.scales) + g, ZEROS ? m.zeros + g : nullptr, Np};
   }
+  // Codes are read once: past the caches.
   __device__ __forceinline__ static W load(const Src& s, int step) {
     W w;
-    const uint32_t lane = threadIdx.x & 63, row = 4 * (lane >> 4);
-    w.q = at<u32x4_t>(s.q + (size_t)step * 64, lane * 16);
+    const uint32_t lane = threadIdx.x & 63, row = lane & 15;
+    w.q = __builtin_nontemporal_load(s.q + (size_t)step * 64 + lane);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       const size_t o = (size_t)(step * NG + g) * s.Np;
-      if constexpr (sizeof(T) == 2) w.s2[g] = at<u32x2_t>(s.s + o, row * 2);
-      else w.s4[g] = at<f32x4_t>(s.s + o, row * 4);
-      if constexpr (ZEROS) w.z[g] = at<uint32_t>(s.z + o, row);
+      w.s[g] = at<T>(s.s + o, row * (uint32_t)sizeof(T));
+      if constexpr (ZEROS) w.z[g] = at<uint8_t>(s.z + o, row);
     }
     return w;
   }
@@ -186,7 +187,7 @@ struct Q4Op {
   }
   // Activations of a step: the lane's row starts `row` bytes behind base.  Inputs from K on
   // read as zero (K a multiple of 8).
-  __device__ __forceinline__ static X load_x(const T* base, uint32_t row, int step, int K = 1 << 30) {
+  __device__ __forceinline__ static X load_x(const T* base, uint32_t row, int step, int K) {
     X x;
     const uint32_t o = row + 8 * sizeof(T) * ((threadIdx.x & 63) >> 4);
     const int k0 = step * KS + 8 * ((threadIdx.x & 63) >> 4);
@@ -207,62 +208,46 @@ struct Q4Op {
     }
     return x;
   }
-  // Plane p of an intermediate row lies `plane` elements behind plane p - 1.
-  __device__ __forceinline__ static X load_h(const hid* base, uint32_t row, size_t plane, int step) {
-    X x;
-    const uint32_t o = row + 16 * ((threadIdx.x & 63) >> 4);
-#pragma unroll
-    for (int p = 0; p < PLANES; ++p)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x.v[p][i] = at<u32x4_t>(base + p * plane + step * KS, o, 64 * i);
-    return x;
-  }
-  __device__ __forceinline__ static void clear(X& x) {
-#pragma unroll
-    for (int p = 0; p < PLANES; ++p)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x.v[p][i] = u32x4_t{0, 0, 0, 0};
-  }
-  // The groups' sums of x, in every lane of its column.
-  __device__ __forceinline__ static void finish_x(X& x) {
+  __device__ __forceinline__ static Sum sums(const X& x) {
     const u32x4_t one = {BF16_ONES, BF16_ONES, BF16_ONES, BF16_ONES};
+    Sum sum;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       f32x4_t a = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = g * PER; i < (g + 1) * PER; ++i)
 #pragma unroll
-        for (int p = PLANES - 1; p >= 0; --p) a = Mfma<bf16_t>::step(one, x.v[p][i], a);
-      x.sum[g] = a[0];
+        for (int p = PLANES - 1; p >= 0; --p) a = Mfma<bf16_t>::step(x.v[p][i], one, a);
+      sum.v[g] = a;
     }
+    return sum;
   }
   // A word's eight codes as bf16 values 16 + q.
   __device__ __forceinline__ static u32x4_t widen(uint32_t q) {
     return u32x4_t{((q << 3) & 0x00780078u) | 0x41804180u, ((q >> 1) & 0x00780078u) | 0x41804180u,
                    ((q >> 5) & 0x00780078u) | 0x41804180u, ((q >> 9) & 0x00780078u) | 0x41804180u};
   }
-  __device__ __forceinline__ static void mma(f32x4_t& acc, const W& w, const X& x) {
+  // A step of R blocks of 16 activation rows, the first RT of a lane's four results of each.
+  template <int R, int RT = 4>
+  __device__ __forceinline__ static void mma(f32x4_t (&acc)[R], const W& w, const X (&x)[R], const Sum (&sum)[R]) {
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      f32x4_t a = {0.f, 0.f, 0.f, 0.f};
+      f32x4_t a[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) a[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = g * PER; i < (g + 1) * PER; ++i) {
         const u32x4_t b = widen(w.q[i]);
 #pragma unroll
-        for (int p = PLANES - 1; p >= 0; --p) a = Mfma<bf16_t>::step(b, x.v[p][i], a);
-      }
+        for (int p = PLANES - 1; p >= 0; --p)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        float s;
-        if constexpr (sizeof(T) == 2) {
-          const uint32_t u = w.s2[g][r >> 1];
-          s = __uint_as_float((r & 1) ? u & 0xffff0000u : u << 16);
-        } else {
-          s = w.s4[g][r];
-        }
-        const float z = ZEROS ? 16.f + (float)((w.z[g] >> (8 * r)) & 0xffu) : 24.f;
-        acc[r] = fmaf(s, fmaf(-z, x.sum[g], a[r]), acc[r]);
+          for (int r = 0; r < R; ++r) a[r] = Mfma<bf16_t>::step(x[r].v[p][i], b, a[r]);
       }
+      const float s = Elt<T>::to_f32(w.s[g]), z = ZEROS ? 16.f + (float)w.z[g] : 24.f;
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < RT; ++i) acc[r][i] = fmaf(s, fmaf(-z, sum[r].v[g][i], a[r][i]), acc[r][i]);
     }
   }
   __device__ __forceinline__ static float value(const RowWeights& m, int mat, int n, int k, int N, int K, int) {
