@@ -340,17 +340,6 @@ __device__ __forceinline__ void few_store_h(const FewArgs& p, const FewList& L, 
 constexpr int FEW_RW = 8;                 // waves of a workgroup
 constexpr int FEW_RT = 64 * FEW_RW;
 
-// One 1 KB copy: eight rows of 128 bytes, lane l to 16 l.
-template <int AUX>
-__device__ __forceinline__ void few_copy(const void* base, uint32_t lane_off, char* lds) {
-  __builtin_amdgcn_global_load_lds((gbl_ptr_t)(static_cast<const char*>(base) + lane_off), (lds_ptr_t)lds, 16, 0, AUX);
-}
-// Row (0..7) and byte of a lane in copy q of a 16-row tile, its chunks swizzled as lds_off
-// reads them.
-__device__ __forceinline__ int few_copy_row(int q) { return 8 * q + ((int)(threadIdx.x & 63) >> 3); }
-__device__ __forceinline__ uint32_t few_copy_byte(int q) {
-  return 16 * ((threadIdx.x & 7) ^ lds_swz(few_copy_row(q)));
-}
 __device__ __forceinline__ void few_barrier() {
   lgkm_wait0();
   compiler_fence();
@@ -391,12 +380,12 @@ __global__ __launch_bounds__(FEW_RT) void few_gateup_dense_kernel(FewArgs p) {
   const int beg = steps * wave / FEW_RW, end = steps * (wave + 1) / FEW_RW;
   const int pitch = (p.blocked ? Op::KS : p.d) * (int)sizeof(T);
   // a lane's place in the copies: tile rows 0..7 of gate, 8..15 (rows 0..7 of up)
-  const uint32_t row0 = (uint32_t)few_copy_row(0) * pitch;
-  const uint32_t goff = row0 + few_copy_byte(0), uoff = row0 + few_copy_byte(1);
+  const uint32_t row0 = (uint32_t)copy_row(0) * pitch;
+  const uint32_t goff = row0 + copy_byte(0), uoff = row0 + copy_byte(1);
   uint32_t xoff[XQ];
 #pragma unroll
   for (int q = 0; q < XQ; ++q)  // rows behind the last token repeat it; their sums are not used
-    xoff[q] = (uint32_t)min(few_copy_row(q), p.T - 1) * p.d * (uint32_t)sizeof(T) + few_copy_byte(q);
+    xoff[q] = (uint32_t)min(copy_row(q), p.T - 1) * p.d * (uint32_t)sizeof(T) + copy_byte(q);
   char* const ring = few_ring + wave * NB * SLOT;
 
   // requests: a step of the item `want`; behind the last item its last step again
@@ -414,10 +403,10 @@ __global__ __launch_bounds__(FEW_RT) void few_gateup_dense_kernel(FewArgs p) {
   auto request = [&](int slot) {
     char* const to = ring + slot * SLOT;
     const size_t o = (size_t)rs * kstr;
-    few_copy<2>(rg + o, goff, to);
-    few_copy<2>(ru + o, uoff, to + 1024);
+    copy_rows<2>(rg + o, goff, to);
+    copy_rows<2>(ru + o, uoff, to + 1024);
 #pragma unroll
-    for (int q = 0; q < XQ; ++q) few_copy<0>(static_cast<const char*>(p.x) + rs * 128, xoff[q], to + 2048 + 1024 * q);
+    for (int q = 0; q < XQ; ++q) copy_rows<0>(static_cast<const char*>(p.x) + rs * 128, xoff[q], to + 2048 + 1024 * q);
     if (rs + 1 < end) {
       ++rs;
     } else if (want + p.stride < n_items) {
@@ -535,11 +524,11 @@ __global__ __launch_bounds__(FEW_RT) void few_down_dense_kernel(FewArgs p) {
     rw = static_cast<const char*>(sh ? ws.w : wr.w) +
          ((size_t)mat * p.d * K + Op::corner(n0, K, p.blocked)) * sizeof(T);
     const int pitch = (p.blocked ? Op::KS : K) * (int)sizeof(T);
-    woff = (uint32_t)few_copy_row(0) * pitch;
+    woff = (uint32_t)copy_row(0) * pitch;
     wjump = 8u * pitch;
 #pragma unroll
     for (int q = 0; q < H; ++q) {
-      const int t = few_copy_row(q);
+      const int t = copy_row(q);
       const int row = sh ? (t < p.T ? p.T * p.k_max + t : p.zero_row) : row_of[idx * FEW_T + t];
       hoff[q] = (uint32_t)row * p.hw * (uint32_t)sizeof(T);
     }
@@ -560,9 +549,9 @@ __global__ __launch_bounds__(FEW_RT) void few_down_dense_kernel(FewArgs p) {
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const char* const h = static_cast<const char*>(p.h) + st * 128;
-      const uint32_t b = few_copy_byte(q);
-      few_copy<2>(rw + (size_t)st * kstr + (PAIR ? 0u : q * wjump), woff + b, to + 1024 * q);
-      few_copy<0>(h, (PAIR && left <= 0 ? zero : hoff[PAIR ? 0 : q]) + b, to + 2048 + 1024 * q);
+      const uint32_t b = copy_byte(q);
+      copy_rows<2>(rw + (size_t)st * kstr + (PAIR ? 0u : q * wjump), woff + b, to + 1024 * q);
+      copy_rows<0>(h, (PAIR && left <= 0 ? zero : hoff[PAIR ? 0 : q]) + b, to + 2048 + 1024 * q);
       if (PAIR || q == 1) advance();
     }
   };
@@ -649,7 +638,7 @@ struct FewQ {
   // Activations: a lane's rows start off[] bytes behind x, planes `plane` elements apart.
   __device__ __forceinline__ void request(char* to, int step, const H* x, size_t plane, const uint32_t (&off)[XQ]) const {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) few_copy<2>(q[i] + (size_t)step * 1024, (threadIdx.x & 63) * 16, to + 1024 * i);
+    for (int i = 0; i < NT; ++i) copy_rows<2>(q[i] + (size_t)step * 1024, (threadIdx.x & 63) * 16, to + 1024 * i);
 #pragma unroll
     for (int c = 0; c < SC; ++c)
       __builtin_amdgcn_global_load_lds((gbl_ptr_t)(s[c] + step * s_step), (lds_ptr_t)(to + S0 + 256 * c), 4, 0, 0);
@@ -660,7 +649,7 @@ struct FewQ {
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int c = 0; c < XQ; ++c)
-          few_copy<0>(x + p * plane + step * Op::KS + 64 * h, off[c], to + X0 + 1024 * ((p * 2 + h) * XQ + c));
+          copy_rows<0>(x + p * plane + step * Op::KS + 64 * h, off[c], to + X0 + 1024 * ((p * 2 + h) * XQ + c));
   }
   __device__ __forceinline__ static void load(const char* from, typename Op::W (&w)[NT], typename Op::X& x) {
     const int lane = threadIdx.x & 63, n = lane & 15, row = XQ == 1 ? (n >> 2) * 2 + (n & 1) : n;
@@ -695,10 +684,6 @@ struct FewQ {
   }
 };
 
-// Neighbouring tiles share their scales' 128-byte lines, so the workgroups of one XCD (every
-// eighth) take neighbours: tile of workgroup b of n.
-__device__ __forceinline__ int few_near(int b, int n) { return n & 7 ? b : (b & 7) * (n >> 3) + (b >> 3); }
-
 template <class Op, int NB, int XQ>
 __global__ __launch_bounds__(FEW_RT) void few_gateup_q4_kernel(FewArgs p) {
   typedef FewQ<Op, 2, XQ> Q;
@@ -714,13 +699,13 @@ __global__ __launch_bounds__(FEW_RT) void few_gateup_q4_kernel(FewArgs p) {
   const int n_list = few_list<FEW_RT>(p, L);
   if (blockIdx.x == 0) few_zero_row<Op, FEW_RT>(p);
   const int ci = p.I / TILE_N, routed = n_list * ci;
-  const int n_items = routed + p.Is / TILE_N, first = few_near(blockIdx.x, p.stride);
+  const int n_items = routed + p.Is / TILE_N, first = near_tile(blockIdx.x, p.stride);
   const int steps = p.d / Op::KS;
   const int beg = wave < Q::SW ? steps * wave / Q::SW : 0, end = wave < Q::SW ? steps * (wave + 1) / Q::SW : 0;
   uint32_t xoff[XQ];
 #pragma unroll
   for (int c = 0; c < XQ; ++c)  // rows behind the last token repeat it; their sums are not used
-    xoff[c] = (uint32_t)min(few_copy_row(c), p.T - 1) * p.d * (uint32_t)sizeof(H) + few_copy_byte(c);
+    xoff[c] = (uint32_t)min(copy_row(c), p.T - 1) * p.d * (uint32_t)sizeof(H) + copy_byte(c);
   char* const ring = few_ring + wave * NB * Q::SLOT;
 
   // requests: a step of the item `want`; behind the last item its last step again
@@ -751,7 +736,7 @@ __global__ __launch_bounds__(FEW_RT) void few_gateup_q4_kernel(FewArgs p) {
   int slot = 0;
 #pragma unroll 1
   for (int item = first; item < n_items; item += p.stride) {
-    f32x4_t ga[1] = {{0.f, 0.f, 0.f, 0.f}}, ua[1] = {{0.f, 0.f, 0.f, 0.f}};
+    f32x4_t acc[2][1] = {{{0.f, 0.f, 0.f, 0.f}}, {{0.f, 0.f, 0.f, 0.f}}};
 #pragma unroll 1
     for (int s = beg; s < end; ++s) {
       vm_wait<Q::PER * (NB - 1)>();
@@ -763,14 +748,12 @@ __global__ __launch_bounds__(FEW_RT) void few_gateup_q4_kernel(FewArgs p) {
       compiler_fence();
       request(slot);
       slot = slot + 1 == NB ? 0 : slot + 1;
-      const typename Op::Sum sum[1] = {Op::sums(x[0])};
-      Op::template mma<1, Q::RT>(ga, w[0], x, sum);
-      Op::template mma<1, Q::RT>(ua, w[1], x, sum);
+      Op::template step<Q::RT>(acc, w, x);
     }
-    settle(ga[0]);
-    settle(ua[0]);
-    Q::keep(red, 0, ga[0]);
-    Q::keep(red, 1, ua[0]);
+    settle(acc[0][0]);
+    settle(acc[1][0]);
+    Q::keep(red, 0, acc[0][0]);
+    Q::keep(red, 1, acc[1][0]);
     few_barrier();
     if (wave < 2 * XQ) {
       const bool sh = item >= routed;
@@ -807,7 +790,7 @@ __global__ __launch_bounds__(FEW_RT) void few_down_q4_kernel(FewArgs p) {
   extern __shared__ char few_ring[];  // the rings, the waves' sums, the list
   const RowWeights wr = p.w[2], ws = p.w[5];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int n0 = few_near(blockIdx.x, gridDim.x) * (NT * TILE_N);
+  const int n0 = near_tile(blockIdx.x, gridDim.x) * (NT * TILE_N);
   float* const red = reinterpret_cast<float*>(few_ring + NB * Q::RING);
   int32_t* const list = reinterpret_cast<int32_t*>(red + Q::SUMS / 4);
   const int32_t* const l_expert = list;
@@ -832,9 +815,9 @@ __global__ __launch_bounds__(FEW_RT) void few_down_q4_kernel(FewArgs p) {
     rq.seek(t);
 #pragma unroll
     for (int c = 0; c < XQ; ++c) {
-      const int tok = few_copy_row(c);
+      const int tok = copy_row(c);
       const int row = sh ? (tok < p.T ? p.T * p.k_max + tok : p.zero_row) : row_of[idx * FEW_T + tok];
-      hoff[c] = (uint32_t)row * p.hw * (uint32_t)sizeof(H) + few_copy_byte(c);
+      hoff[c] = (uint32_t)row * p.hw * (uint32_t)sizeof(H) + copy_byte(c);
     }
   };
   auto request = [&](int slot) {
@@ -867,9 +850,7 @@ __global__ __launch_bounds__(FEW_RT) void few_down_q4_kernel(FewArgs p) {
       compiler_fence();
       request(slot);
       slot = slot + 1 == NB ? 0 : slot + 1;
-      const typename Op::Sum sum[1] = {Op::sums(x[0])};
-#pragma unroll
-      for (int i = 0; i < NT; ++i) Op::template mma<1, Q::RT>(acc[i], w[i], x, sum);
+      Op::template step<Q::RT>(acc, w, x);
     }
     vm_wait<0>();  // no copy into LDS outlives the workgroup
   }

@@ -211,11 +211,7 @@ __global__ __launch_bounds__(64 * NW) void q4_linear_kernel(const typename Op::e
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (s + u < end) {
-        typename Op::Sum sum[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) sum[r] = Op::sums(xv[u][r]);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) Op::mma(acc[t], v[u][t], xv[u], sum);
+        Op::template step<4>(acc, v[u], xv[u]);
       }
   }
 #pragma unroll
@@ -244,6 +240,139 @@ __global__ __launch_bounds__(64 * NW) void q4_linear_kernel(const typename Op::e
       if (mine) y[(size_t)row * N + n] = Elt<T>::from_f32(sum);
     }
     if (r + 1 < R) __syncthreads();
+  }
+}
+
+// Many outputs: the waves of a workgroup take NT tiles each and walk K together, the
+// activations of a step in LDS for all of them (each wave by itself would read four to
+// sixteen times the codes' bytes from L2).  Codes, scales and zero points come through a
+// ring of the wave's own, NB - 1 steps ahead, the activations with them.
+constexpr int QL_WW = 8;
+
+template <class Op, int R, int NT, int NB>
+__global__ __launch_bounds__(64 * QL_WW) void q4_wide_kernel(const typename Op::elt* __restrict__ x, RowWeights w,
+                                                             int rows, int N, int K,
+                                                             typename Op::elt* __restrict__ y) {
+  typedef typename Op::elt T;
+  static_assert(sizeof(T) == 2, "bf16 activations");
+  constexpr int RUN = 32, SB = Op::NG * RUN;            // a tile's scales of a step
+  constexpr int XP = R < 2 ? 1 : R / 2;                 // copies of activations of a wave
+  constexpr int TILE = 1024 + 256 + (Op::ZP ? 256 : 0), MINE = NT * TILE, XB = 4096 * R;
+  constexpr int PER = NT * (2 + (Op::ZP ? 1 : 0)) + XP;
+  extern __shared__ char ql_ring[];                     // [NB][XB], then [waves][NB][MINE]
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, col = lane & 15;
+  const int nt = ceil_div(N, TILE_N), r0 = blockIdx.y * (16 * R), steps = ceil_div(K, Q4_K);
+  const int tile0 = (near_tile(blockIdx.x, gridDim.x) * QL_WW + wave) * NT;
+  const T* const x0 = x + (size_t)r0 * K;
+  char* const mine = ql_ring + NB * XB + wave * (NB * MINE);
+
+  // copy c of a step's activations: rows 16 (c / 4) + 8 (c % 2) .., inputs 64 (c / 2 % 2) ..
+  uint32_t xoff[XP];
+#pragma unroll
+  for (int i = 0; i < XP; ++i) {
+    const int c = (wave + QL_WW * i) % (4 * R);
+    xoff[i] = (uint32_t)min(16 * (c >> 2) + copy_row(c & 1), rows - 1 - r0) * K * 2u;
+  }
+  typename Op::Src src[NT];
+  const char* sp[NT];
+  const char* zp[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {  // tiles behind the last repeat it
+    src[t] = Op::tile(w, 0, min(tile0 + t, nt - 1) * TILE_N, N, K);
+    const int b = 4 * lane % SB, c = 4 * lane % (16 * Op::NG);
+    sp[t] = reinterpret_cast<const char*>(src[t].s) + (size_t)(b / RUN) * src[t].Np * 2 + b % RUN;
+    if (Op::ZP) zp[t] = reinterpret_cast<const char*>(src[t].z) + (size_t)(c / 16) * src[t].Np + c % 16;
+  }
+  const size_t Np = src[0].Np;
+  auto request = [&](int s, int slot) {
+    s = min(s, steps - 1);  // behind the end the last step again
+    char* to = mine + slot * MINE;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      copy_rows<2>(src[t].q + (size_t)s * 64, 16 * lane, to + t * TILE);
+      __builtin_amdgcn_global_load_lds((gbl_ptr_t)(sp[t] + s * Op::NG * Np * 2), (lds_ptr_t)(to + t * TILE + 1024), 4, 0, 0);
+      if (Op::ZP) __builtin_amdgcn_global_load_lds((gbl_ptr_t)(zp[t] + s * Op::NG * Np), (lds_ptr_t)(to + t * TILE + 1280), 4, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < XP; ++i) {
+      const int c = (wave + QL_WW * i) % (4 * R);
+      // inputs behind K: any of the row's, taken out below
+      const uint32_t k = min(s * 256u + (c >> 1 & 1) * 128u + copy_byte(c & 1), 2u * K - 16u);
+      copy_rows<0>(x0, xoff[i] + k, ql_ring + slot * XB + (c >> 2) * 4096 + (c >> 1 & 1) * 2048 + (c & 1) * 1024);
+    }
+  };
+  f32x4_t acc[NT][R];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int r = 0; r < R; ++r) acc[t][r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int i = 0; i < NB - 1; ++i) request(i, i);
+  int slot = 0;
+#pragma unroll 1
+  for (int s = 0; s < steps; ++s) {
+    vm_wait<PER * (NB - 2)>();
+    compiler_fence();
+    __builtin_amdgcn_s_barrier();  // everyone's copies of this step; everyone has read the last one's
+    compiler_fence();
+    request(s + NB - 1, slot == 0 ? NB - 1 : slot - 1);
+    const char* const from = mine + slot * MINE;
+    typename Op::W v[NT];
+    typename Op::X xv[R];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      v[t].q = *reinterpret_cast<const u32x4_t*>(from + t * TILE + 16 * lane);
+#pragma unroll
+      for (int g = 0; g < Op::NG; ++g) {
+        v[t].s[g] = *reinterpret_cast<const T*>(from + t * TILE + 1024 + g * RUN + 2 * col);
+        if (Op::ZP) v[t].z[g] = *reinterpret_cast<const uint8_t*>(from + t * TILE + 1280 + g * 16 + col);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        xv[r].v[0][i] = *reinterpret_cast<const u32x4_t*>(ql_ring + slot * XB + r * 4096 + (i >> 1) * 2048 +
+                                                          lds_off(col, (lane >> 4) + 4 * (i & 1)));
+    lgkm_wait0();
+    compiler_fence();
+    if (s == steps - 1 && K % Q4_K) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (s * Q4_K + 32 * i + 8 * (lane >> 4) >= K) {
+#pragma unroll
+          for (int r = 0; r < R; ++r) xv[r].v[0][i] = u32x4_t{0, 0, 0, 0};
+        }
+    }
+    Op::template step<4>(acc, v, xv);
+    slot = slot + 1 == NB ? 0 : slot + 1;
+  }
+  vm_wait<0>();  // no copy into LDS outlives the workgroup
+  compiler_fence();
+  // a wave's results through its own part of the ring: value i of a lane at 64 i
+  float* const out = reinterpret_cast<float*>(mine);
+  static_assert(NT * R * 1024 <= NB * MINE, "the results fit the ring");
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      settle(acc[t][r]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) out[((t * R + r) * 4 + i) * 64 + lane] = acc[t][r][i];
+    }
+  lgkm_wait0();
+  compiler_fence();
+#pragma unroll 1
+  for (int e = 0; e < NT * R * 4; ++e) {
+    const int n = (tile0 + e / (4 * R)) * TILE_N + col, rb = r0 + 16 * (e / 4 % R) + e % 4, row = rb + 4 * (lane >> 4);
+    float v = out[e * 64 + lane];
+    const bool good = row < rows && n < N;
+    redo_not_finite(v, good, [&](int l) {
+      const T* xr = x + (size_t)(rb + 4 * (l >> 4)) * K;
+      const int nn = n - col + (l & 15);
+      return wave_dot(K, [&](int k) { return Elt<T>::to_f32(xr[k]) * Op::value(w, 0, nn, k, N, K, 0); });
+    });
+    if (good) y[(size_t)row * N + n] = Elt<T>::from_f32(v);
   }
 }
 
@@ -290,7 +419,7 @@ static void unpack_t(const Q4Shape& s, const void* codes, const void* scales, co
   MOE_Q4_ALL(MOE_CALL);
 #undef MOE_CALL
 }
-constexpr int QL_WIDE = 8192;
+constexpr int QL_WIDE = 16384;
 
 template <class Op, int R, int NT, int U, int NW>
 static void linear_as(const Q4Shape& s, int rows, const void* x, const RowWeights& w, void* y, hipStream_t st) {
@@ -298,13 +427,20 @@ static void linear_as(const Q4Shape& s, int rows, const void* x, const RowWeight
   hipLaunchKernelGGL((q4_linear_kernel<Op, R, NT, U, NW>), dim3(ceil_div(s.N, NT * TILE_N), ceil_div(rows, 16 * R)),
                      dim3(64 * NW), 0, st, (const T*)x, w, rows, s.N, s.K, (T*)y);
 }
+template <class Op, int R, int NT, int NB>
+static void wide_as(const Q4Shape& s, int rows, const void* x, const RowWeights& w, void* y, hipStream_t st) {
+  typedef typename Op::elt T;
+  constexpr int LDS = NB * (4096 * R + QL_WW * NT * (1024 + 256 + (Op::ZP ? 256 : 0)));
+  hipLaunchKernelGGL((q4_wide_kernel<Op, R, NT, NB>), dim3(ceil_div(s.N, QL_WW * NT * TILE_N), ceil_div(rows, 16 * R)),
+                     dim3(64 * QL_WW), LDS, st, (const T*)x, w, rows, s.N, s.K, (T*)y);
+}
 template <class Op>
 static void linear_op(const Q4Shape& s, int rows, const void* x, const RowWeights& w, void* y, hipStream_t st) {
   const bool wide = s.N >= QL_WIDE;
   if constexpr (Op::PLANES == 1) {
-    if (rows <= 16) wide ? linear_as<Op, 1, 4, 1, 8>(s, rows, x, w, y, st) : linear_as<Op, 1, 1, 4, 16>(s, rows, x, w, y, st);
-    else if (rows <= 32) wide ? linear_as<Op, 2, 4, 1, 8>(s, rows, x, w, y, st) : linear_as<Op, 2, 1, 2, 16>(s, rows, x, w, y, st);
-    else wide ? linear_as<Op, 4, 2, 1, 8>(s, rows, x, w, y, st) : linear_as<Op, 4, 1, 1, 16>(s, rows, x, w, y, st);
+    if (rows <= 16) wide ? wide_as<Op, 1, 1, 4>(s, rows, x, w, y, st) : linear_as<Op, 1, 1, 4, 16>(s, rows, x, w, y, st);
+    else if (rows <= 32) wide ? wide_as<Op, 2, 1, 4>(s, rows, x, w, y, st) : linear_as<Op, 2, 1, 2, 16>(s, rows, x, w, y, st);
+    else wide ? wide_as<Op, 4, 1, 4>(s, rows, x, w, y, st) : linear_as<Op, 4, 1, 1, 16>(s, rows, x, w, y, st);
   } else {
     wide ? linear_as<Op, 1, 4, 1, 8>(s, rows, x, w, y, st) : linear_as<Op, 1, 1, 2, 8>(s, rows, x, w, y, st);
   }

@@ -59,6 +59,20 @@ __device__ __forceinline__ V at(const void* base, uint32_t bytes, int ahead = 0)
   return *reinterpret_cast<const V*>(static_cast<const char*>(base) + bytes + ahead);
 }
 
+// One 1 KB copy into LDS: eight rows of 128 bytes, lane l to 16 l.
+template <int AUX>
+__device__ __forceinline__ void copy_rows(const void* base, uint32_t lane_off, char* lds) {
+  __builtin_amdgcn_global_load_lds((gbl_ptr_t)(static_cast<const char*>(base) + lane_off), (lds_ptr_t)lds, 16, 0, AUX);
+}
+// Row (0..7) and byte of a lane in copy q of a 16-row tile, its chunks swizzled as lds_off
+// reads them.
+__device__ __forceinline__ int copy_row(int q) { return 8 * q + ((int)(threadIdx.x & 63) >> 3); }
+__device__ __forceinline__ uint32_t copy_byte(int q) { return 16 * ((threadIdx.x & 7) ^ lds_swz(copy_row(q))); }
+
+// Tiles side by side share their scales' 128-byte lines, so the workgroups of one XCD (every
+// eighth) take neighbours: the tile of workgroup b of n.
+__device__ __forceinline__ int near_tile(int b, int n) { return n & 7 ? b : (b & 7) * (n >> 3) + (b >> 3); }
+
 // Four consecutive elements of a row (8- or 16-byte aligned).
 __device__ __forceinline__ void store_row4(bf16_t* p, f32x4_t v) {
   u32x2_t o;
@@ -153,7 +167,6 @@ struct Q4Op {
     uint8_t z[ZEROS ? NG : 1];
   };
   struct X { u32x4_t v[PLANES][4]; };
-  struct Sum { f32x4_t v[NG]; };                  // the groups' sums of x, as the results lie
   struct Src { const u32x4_t* q; const T* s; const uint8_t* z; int Np; };
 
   __device__ __forceinline__ static Src tile(const RowWeights& m, int mat, int n0, int N, int K) {
@@ -208,47 +221,57 @@ struct Q4Op {
     }
     return x;
   }
-  __device__ __forceinline__ static Sum sums(const X& x) {
-    const u32x4_t one = {BF16_ONES, BF16_ONES, BF16_ONES, BF16_ONES};
-    Sum sum;
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      f32x4_t a = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int i = g * PER; i < (g + 1) * PER; ++i)
-#pragma unroll
-        for (int p = PLANES - 1; p >= 0; --p) a = Mfma<bf16_t>::step(x.v[p][i], one, a);
-      sum.v[g] = a;
-    }
-    return sum;
-  }
-  // A word's eight codes as bf16 values 16 + q.
+  // A word's eight codes as bf16 values 16 + q.  (`base` as a value the compiler does not know
+  // makes mask and or one instruction: of two constants it can hold one.)
   __device__ __forceinline__ static u32x4_t widen(uint32_t q) {
-    return u32x4_t{((q << 3) & 0x00780078u) | 0x41804180u, ((q >> 1) & 0x00780078u) | 0x41804180u,
-                   ((q >> 5) & 0x00780078u) | 0x41804180u, ((q >> 9) & 0x00780078u) | 0x41804180u};
+    uint32_t base = 0x41804180u;
+    asm("" : "+v"(base));
+    return u32x4_t{((q << 3) & 0x00780078u) | base, ((q >> 1) & 0x00780078u) | base,
+                   ((q >> 5) & 0x00780078u) | base, ((q >> 9) & 0x00780078u) | base};
   }
-  // A step of R blocks of 16 activation rows, the first RT of a lane's four results of each.
-  template <int R, int RT = 4>
-  __device__ __forceinline__ static void mma(f32x4_t (&acc)[R], const W& w, const X (&x)[R], const Sum (&sum)[R]) {
+  // A step of NT tiles and R blocks of 16 activation rows, the first RT of a lane's four
+  // results of each.  The tiles' products run side by side (one waits for the one before it
+  // in its sum), and a group is scaled behind the next one's.
+  template <int RT, int NT, int R>
+  __device__ __forceinline__ static void step(f32x4_t (&acc)[NT][R], const W (&w)[NT], const X (&x)[R]) {
+    const u32x4_t one = {BF16_ONES, BF16_ONES, BF16_ONES, BF16_ONES};
+    f32x4_t a[2][NT][R], sum[2][R];
+    auto scale = [&](int g) {
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      f32x4_t a[R];
+      for (int t = 0; t < NT; ++t) {
+        const float s = Elt<T>::to_f32(w[t].s[g]), z = ZEROS ? 16.f + (float)w[t].z[g] : 24.f;
 #pragma unroll
-      for (int r = 0; r < R; ++r) a[r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int i = g * PER; i < (g + 1) * PER; ++i) {
-        const u32x4_t b = widen(w.q[i]);
-#pragma unroll
-        for (int p = PLANES - 1; p >= 0; --p)
-#pragma unroll
-          for (int r = 0; r < R; ++r) a[r] = Mfma<bf16_t>::step(x[r].v[p][i], b, a[r]);
+          for (int i = 0; i < RT; ++i)
+            acc[t][r][i] = fmaf(s, fmaf(-z, sum[g & 1][r][i], a[g & 1][t][r][i]), acc[t][r][i]);
       }
-      const float s = Elt<T>::to_f32(w.s[g]), z = ZEROS ? 16.f + (float)w.z[g] : 24.f;
+    };
 #pragma unroll
-      for (int r = 0; r < R; ++r)
+    for (int i = 0; i < 4; ++i) {
+      const int g = i / PER, o = g & 1;
+      if (i % PER == 0) {
 #pragma unroll
-        for (int i = 0; i < RT; ++i) acc[r][i] = fmaf(s, fmaf(-z, sum[r].v[g][i], a[r][i]), acc[r][i]);
+        for (int r = 0; r < R; ++r) {
+          sum[o][r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int t = 0; t < NT; ++t) a[o][t][r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        }
+      }
+      u32x4_t b[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) b[t] = widen(w[t].q[i]);
+#pragma unroll
+      for (int p = PLANES - 1; p >= 0; --p)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          sum[o][r] = Mfma<bf16_t>::step(x[r].v[p][i], one, sum[o][r]);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) a[o][t][r] = Mfma<bf16_t>::step(x[r].v[p][i], b[t], a[o][t][r]);
+        }
+      if (i % PER == PER - 1 && g > 0) scale(g - 1);
     }
+    scale(NG - 1);
   }
   __device__ __forceinline__ static float value(const RowWeights& m, int mat, int n, int k, int N, int K, int) {
     const int kt = ceil_div(K, Q4_K), nt = ceil_div(N, TILE_N), c = k % Q4_K;

@@ -245,7 +245,8 @@ def _linear(q, x):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("group,zeros", [(32, True), (64, False), (128, True), (128, False)])
 @pytest.mark.parametrize("rows,K,N", [(1, 128, 16), (1, 2048, 512), (3, 1000, 37), (16, 264, 130), (17, 8, 1),
-                                      (33, 4096, 100), (64, 712, 256), (100, 512, 48)])
+                                      (33, 4096, 100), (64, 712, 256), (100, 512, 48),
+                                      (5, 136, 16500), (20, 1000, 16385), (40, 264, 20001), (70, 8, 16399)])
 def test_q4_linear(dtype, group, zeros, rows, K, N):
     g = _gen(rows + K)
     w = Weight(g, 1, N, K, DT[dtype], group, zeros)
@@ -263,13 +264,13 @@ def test_q4_linear_rows_are_independent():
     """Values that are no numbers, and huge ones, stay in their row; rows behind the
     last are not written."""
     g = _gen(9)
-    for dtype in ("bf16", "f32"):
-        w = Weight(g, 1, 50, 384, DT[dtype], 64, True)
+    for dtype, N in (("bf16", 50), ("f32", 50), ("bf16", 16450)):
+        w = Weight(g, 1, N, 384, DT[dtype], 64, True)
         x = _randn(g, 20, 384, dtype=DT[dtype])
         a = _linear(w.arg, x)
         x2 = x.clone()
         x2[3, 7], x2[11, 380], x2[17, 100] = math.nan, math.inf, -math.inf
-        y = torch.full((30, 50), 5.0, dtype=DT[dtype], device=DEV)
+        y = torch.full((30, N), 5.0, dtype=DT[dtype], device=DEV)
         moe.moe_q4_linear(w.arg, x2, y)
         keep = [r for r in range(20) if r not in (3, 11, 17)]
         assert torch.equal(y[keep], a[keep]) and (y[20:] == 5.0).all()
