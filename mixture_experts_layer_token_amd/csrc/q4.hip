@@ -13,93 +13,141 @@ namespace moe {
 //   s = ELT((hi - lo) / 15), z = rne(-lo / s), codes z + rne(w / s)   with,
 // lo and hi the group's range with 0 in it, codes held in [1, 15] or [0, 15].  The
 // codes are those of the stored scale; rne takes the exact quotient, ties to even.
-// The quotient's float32 value decides unless it lies within an ulp or so of a tie,
-// where the exact remainder does: w - (j + 1/2) s is exact in float64 (24-bit w,
-// 4-bit times 24-bit product).
+// The quotient is w times 1 / s in float32, within 4e-6 of the exact one (no value exceeds
+// 16 of them).  For float32 weights the remainder w - s r, whose sign and comparison with
+// s / 2 are exact in one fused step, then puts right an r on the wrong side of a tie.  For
+// bf16 weights a quotient that is no tie lies 2^-10 or more from each (both mantissas have
+// 8 bits, a tie is an odd number of halves), so that rounding to 2^-12 first leaves ties
+// exactly on theirs and nothing else; that saves the half of pack's time that ties, frequent
+// in bf16, took.
 // A group whose values are all 0 (or whose scale rounds to 0) has scale 0; one with a
 // value that is no finite number has scale NaN.
 
-__device__ __forceinline__ float q4_round(float w, float s) {
-  const float q = w / s;
-  const float r = rintf(q);
-  // near a tie the float32 quotient may lie on the wrong side of it, or on it
-  if (fabsf(fabsf(q - r) - 0.5f) > 1e-5f) return r;
-  const float j = floorf(q);
-  const double d = (double)w - (double)s * ((double)j + 0.5);
-  if (d > 0.0) return j + 1.f;
-  if (d < 0.0) return j;
-  return (((int)j) & 1) ? j + 1.f : j;
+// rne(w / s) of q = w * (1 / s), s not below 2^-100.
+__device__ __forceinline__ float q4_rne(float w, float s, float q) {
+  const float r = rintf(q), e = fmaf(-s, r, w), h = 0.5f * s, up = e > 0.f ? 1.f : -1.f;
+  if (fabsf(e) > h) return r + up;
+  return fabsf(e) == h && ((int)r & 1) ? r + up : r;
 }
 
-// One thread quantises the 8 inputs of one code word; the GROUP / 8 threads of a group
-// agree on its range by shuffles.  A workgroup takes 16 rows x 128 inputs (256 threads:
-// row tid / 16, word tid % 16) and writes the codes through LDS in the tile's order.
+// The largest of a group's GROUP / 8 threads (neighbours), in each of them.
+template <int GROUP, class F>
+__device__ __forceinline__ uint32_t q4_all(uint32_t v, F f) {
+  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0xB1, 0xF, 0xF, false));   // lane ^ 1
+  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x4E, 0xF, 0xF, false));   // lane ^ 2
+  if (GROUP > 32) v = f(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x141, 0xF, 0xF, false));  // halves of 8
+  if (GROUP > 64) v = f(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x140, 0xF, 0xF, false));  // of 16
+  return v;
+}
+
+// Eight elements of a row (16-byte aligned), read once: past the caches.
+__device__ __forceinline__ void q4_load8(const bf16_t* p, float (&v)[8]) {
+  const u32x4_t u = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(u[i] << 16);
+    v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void q4_load8(const float* p, float (&v)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const f32x4_t u = __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(p) + h);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[4 * h + i] = u[i];
+  }
+}
+
+// One thread quantises the 8 inputs of a code word; the GROUP / 8 threads of a group agree
+// on its range.  A workgroup takes 16 rows x QP_T tiles of 128 inputs (256 threads: row
+// tid / 16, word tid % 16 of each tile), whose loads are in flight together, and writes the
+// codes through LDS in the tile's order.
+constexpr int QP_T = 4;
+
 template <typename T, int GROUP, bool ZEROS>
 __global__ __launch_bounds__(256) void q4_pack_kernel(const T* __restrict__ w, int G, int N, int K, int kt_n, int nt_n,
                                                       uint32_t* __restrict__ codes, T* __restrict__ scales,
                                                       uint8_t* __restrict__ zeros) {
-  __shared__ uint32_t buf[256];
+  __shared__ uint32_t buf[QP_T][256];
   constexpr int NG = Q4_K / GROUP;
-  const int tid = threadIdx.x, r = tid >> 4, c = tid & 15;
-  const int kt = blockIdx.x % kt_n, nt = blockIdx.x / kt_n;
-  const int n = nt * TILE_N + r, k = kt * Q4_K + 8 * c;
+  const int tid = threadIdx.x, r = tid >> 4, c = tid & 15, kq = ceil_div(kt_n, QP_T);
+  const int kt0 = blockIdx.x % kq * QP_T, nt = blockIdx.x / kq, tiles = min(QP_T, kt_n - kt0);
+  const int n = nt * TILE_N + r, k0 = kt0 * Q4_K + 8 * c;
   const int Np = nt_n * TILE_N;
   for (int g = blockIdx.y; g < G; g += gridDim.y) {
-    float v[8];
+    const T* const row = w + ((size_t)g * N + n) * K + k0;
+    float v[QP_T][8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 0.f;
-    const bool in = n < N && k < K;
-    if (in) {
-      const T* p = w + ((size_t)g * N + n) * K + k;
+    for (int i = 0; i < QP_T; ++i) {
 #pragma unroll
-      for (int h = 0; h < (int)sizeof(T) / 2; ++h) {
-        const u32x4_t u = *reinterpret_cast<const u32x4_t*>(p + h * (16 / sizeof(T)));
+      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+      if (n < N && k0 + i * Q4_K < K) q4_load8(row + i * Q4_K, v[i]);
+    }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (sizeof(T) == 2) {
-            v[2 * i] = __uint_as_float(u[i] << 16);
-            v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-          } else {
-            v[4 * h + i] = __uint_as_float(u[i]);
-          }
+    for (int i = 0; i < QP_T; ++i) {
+      // |w| as integers: their order, infinities and NaN behind the numbers
+      uint32_t top = 0;
+      float lo = 0.f, hi = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        top = max(top, __float_as_uint(v[i][j]) & 0x7fffffffu);
+        if (ZEROS) lo = fminf(lo, v[i][j]), hi = fmaxf(hi, v[i][j]);
+      }
+      top = q4_all<GROUP>(top, [](uint32_t a, uint32_t b) { return max(a, b); });
+      float s32;
+      if (ZEROS) {
+        lo = __uint_as_float(q4_all<GROUP>(__float_as_uint(lo), [](uint32_t a, uint32_t b) {
+          return __float_as_uint(fminf(__uint_as_float(a), __uint_as_float(b))); }));
+        hi = __uint_as_float(q4_all<GROUP>(__float_as_uint(hi), [](uint32_t a, uint32_t b) {
+          return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b))); }));
+        s32 = (float)(((double)hi - (double)lo) / 15.0);
+      } else {
+        s32 = __uint_as_float(top) / 7.f;
+      }
+      const T st = Elt<T>::from_f32(top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : s32);
+      const float s = Elt<T>::to_f32(st);
+      const bool live = s > 0.f && s < INFINITY;
+      // tiny scales and their weights 2^64 times larger, for 1 / s to exist and w - s r to be exact
+      const float lift = s < 0x1p-100f ? 0x1p64f : 1.f, sl = s * lift, inv = live ? 1.f / sl : 0.f;
+      const float z = !ZEROS ? 8.f : live ? fminf(fmaxf(q4_rne(-lo * lift, sl, -lo * lift * inv), 0.f), 15.f) : 0.f;
+      const float least = ZEROS ? -z : -7.f, most = ZEROS ? 15.f - z : 7.f;
+      float q[8];
+      bool clear = true;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if constexpr (sizeof(T) == 2) {
+          q[j] = fmaf(v[i][j] * lift, inv, 0x1.8p11f) - 0x1.8p11f;
+        } else {
+          q[j] = v[i][j] * lift * inv;
+          clear &= fabsf(q[j] - rintf(q[j])) < 0.49999f;
         }
       }
-    }
-    float lo = 0.f, hi = 0.f;
-    int bad = 0;
+      if (sizeof(T) == 4 && !clear) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      lo = fminf(lo, v[j]);
-      hi = fmaxf(hi, v[j]);
-      bad |= !(fabsf(v[j]) < INFINITY);
-    }
+        for (int j = 0; j < 8; ++j) q[j] = q4_rne(v[i][j] * lift, sl, q[j]);
+      }
+      // 1.5 * 2^23 + q rounds q to even and has it in its low bits; the constants' sum goes out again
+      uint32_t word = 0, base = 0;
 #pragma unroll
-    for (int o = 1; o < GROUP / 8; o <<= 1) {
-      lo = fminf(lo, __shfl_xor(lo, o, 64));
-      hi = fmaxf(hi, __shfl_xor(hi, o, 64));
-      bad |= __shfl_xor(bad, o, 64);
-    }
-    const double range = ZEROS ? ((double)hi - (double)lo) / 15.0 : (double)fmaxf(hi, -lo) / 7.0;
-    const T st = Elt<T>::from_f32(bad ? __uint_as_float(0x7fc00000u) : (float)range);
-    const float s = Elt<T>::to_f32(st);
-    const bool live = s > 0.f && s < INFINITY;
-    const float z = ZEROS ? (live ? fminf(fmaxf(q4_round(-lo, s), 0.f), 15.f) : 0.f) : 8.f;
-    uint32_t word = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float q = z;
-      if (live) q = fminf(fmaxf(q4_round(v[j], s) + z, ZEROS ? 0.f : 1.f), 15.f);
-      word |= (uint32_t)q << (4 * (j >> 1) + 16 * (j & 1));
-    }
-    // word c of row r: instruction c / 4, lane group c % 4
-    buf[((c & 3) * 16 + r) * 4 + (c >> 2)] = word;
-    if ((c & (GROUP / 8 - 1)) == 0) {
-      const size_t o = (((size_t)g * kt_n + kt) * NG + c / (GROUP / 8)) * Np + n;
-      scales[o] = n < N ? st : T(0);
-      if (ZEROS) zeros[o] = (uint8_t)z;
+      for (int j = 0; j < 8; ++j) {
+        const int at = 4 * (j >> 1) + 16 * (j & 1);
+        word += __float_as_uint(fminf(fmaxf(q[j], least), most) + 0x1.8p23f) << at;
+        base += 0x4b400000u << at;
+      }
+      word = (live ? word - base : 0u) + (uint32_t)z * 0x11111111u;
+      // word c of row r: instruction c / 4, lane group c % 4
+      buf[i][((c & 3) * 16 + r) * 4 + (c >> 2)] = word;
+      if (i < tiles && (c & (GROUP / 8 - 1)) == 0) {
+        const size_t o = (((size_t)g * kt_n + kt0 + i) * NG + c / (GROUP / 8)) * Np + n;
+        scales[o] = n < N ? st : T(0);
+        if (ZEROS) zeros[o] = (uint8_t)z;
+      }
     }
     __syncthreads();
-    codes[(((size_t)g * nt_n + nt) * kt_n + kt) * 256 + tid] = buf[tid];
+    // 16 bytes a thread: tiles in a row
+    if (tid < 64 * tiles)
+      __builtin_nontemporal_store(reinterpret_cast<const u32x4_t*>(buf)[tid],
+                                  reinterpret_cast<u32x4_t*>(codes + (((size_t)g * nt_n + nt) * kt_n + kt0) * 256) + tid);
     __syncthreads();
   }
 }
@@ -137,34 +185,52 @@ __global__ __launch_bounds__(256) void q4_tile_kernel(const uint8_t* __restrict_
   }
 }
 
-// The values s (q - z), rounded once to the element type.
+// The values s (q - z), rounded once to the element type; threads and tiles as in packing.
 template <typename T, int GROUP, bool ZEROS>
 __global__ __launch_bounds__(256) void q4_unpack_kernel(const uint32_t* __restrict__ codes,
                                                         const T* __restrict__ scales,
                                                         const uint8_t* __restrict__ zeros, int G, int N, int K,
                                                         int kt_n, int nt_n, T* __restrict__ w) {
-  __shared__ uint32_t buf[256];
+  __shared__ uint32_t buf[QP_T][256];
   constexpr int NG = Q4_K / GROUP;
-  const int tid = threadIdx.x, r = tid >> 4, c = tid & 15;
-  const int kt = blockIdx.x % kt_n, nt = blockIdx.x / kt_n;
-  const int n = nt * TILE_N + r, k = kt * Q4_K + 8 * c;
+  const int tid = threadIdx.x, r = tid >> 4, c = tid & 15, kq = ceil_div(kt_n, QP_T);
+  const int kt0 = blockIdx.x % kq * QP_T, nt = blockIdx.x / kq, tiles = min(QP_T, kt_n - kt0);
+  const int n = nt * TILE_N + r, k0 = kt0 * Q4_K + 8 * c;
   const int Np = nt_n * TILE_N;
   for (int g = blockIdx.y; g < G; g += gridDim.y) {
-    buf[tid] = codes[(((size_t)g * nt_n + nt) * kt_n + kt) * 256 + tid];
-    const size_t o = (((size_t)g * kt_n + kt) * NG + c / (GROUP / 8)) * Np + n;
-    const float s = Elt<T>::to_f32(scales[o]);
-    const int z = ZEROS ? zeros[o] : 8;
-    __syncthreads();
-    if (n < N && k < K) {
-      const uint32_t word = buf[((c & 3) * 16 + r) * 4 + (c >> 2)];
-      f32x4_t v[2];
+    if (tid < 64 * tiles)
+      reinterpret_cast<u32x4_t*>(buf)[tid] = __builtin_nontemporal_load(
+          reinterpret_cast<const u32x4_t*>(codes + (((size_t)g * nt_n + nt) * kt_n + kt0) * 256) + tid);
+    float s[QP_T];
+    int z[QP_T];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        v[j >> 2][j & 3] = s * (float)((int)((word >> (4 * (j >> 1) + 16 * (j & 1))) & 15u) - z);
-      T* p = w + ((size_t)g * N + n) * K + k;
-      store_row4(p, v[0]);
-      store_row4(p + 4, v[1]);
+    for (int i = 0; i < QP_T; ++i) {
+      const size_t o = (((size_t)g * kt_n + min(kt0 + i, kt_n - 1)) * NG + c / (GROUP / 8)) * Np + n;
+      s[i] = Elt<T>::to_f32(scales[o]);
+      z[i] = ZEROS ? zeros[o] : 8;
     }
+    __syncthreads();
+    T* const row = w + ((size_t)g * N + n) * K + k0;
+#pragma unroll
+    for (int i = 0; i < QP_T; ++i)
+      if (n < N && k0 + i * Q4_K < K) {
+        const uint32_t word = buf[i][((c & 3) * 16 + r) * 4 + (c >> 2)];
+        f32x4_t v[2];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          v[j >> 2][j & 3] = s[i] * (float)((int)((word >> (4 * (j >> 1) + 16 * (j & 1))) & 15u) - z[i]);
+        T* const p = row + i * Q4_K;
+        if constexpr (sizeof(T) == 2) {
+          u32x4_t o;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            o[j] = (uint32_t)f32_to_bf16(v[j >> 1][2 * (j & 1)]) | ((uint32_t)f32_to_bf16(v[j >> 1][2 * (j & 1) + 1]) << 16);
+          __builtin_nontemporal_store(o, reinterpret_cast<u32x4_t*>(p));
+        } else {
+          __builtin_nontemporal_store(v[0], reinterpret_cast<f32x4_t*>(p));
+          __builtin_nontemporal_store(v[1], reinterpret_cast<f32x4_t*>(p) + 1);
+        }
+      }
     __syncthreads();
   }
 }
@@ -393,7 +459,7 @@ template <typename T>
 static void pack_t(const Q4Shape& s, const void* w, void* codes, void* scales, void* zeros, hipStream_t st) {
   const int kt = ceil_div(s.K, Q4_K), nt = ceil_div(s.N, TILE_N);
 #define MOE_CALL(GR_, ZP_)                                                                                          \
-  hipLaunchKernelGGL((q4_pack_kernel<T, GR_, ZP_>), dim3((uint32_t)kt * nt, min(s.G, 65535)), dim3(256), 0, st, (const T*)w, s.G, s.N, s.K, \
+  hipLaunchKernelGGL((q4_pack_kernel<T, GR_, ZP_>), dim3((uint32_t)ceil_div(kt, QP_T) * nt, min(s.G, 65535)), dim3(256), 0, st, (const T*)w, s.G, s.N, s.K, \
                      kt, nt, (uint32_t*)codes, (T*)scales, (uint8_t*)zeros)
   MOE_Q4_ALL(MOE_CALL);
 #undef MOE_CALL
@@ -414,7 +480,7 @@ static void unpack_t(const Q4Shape& s, const void* codes, const void* scales, co
                      hipStream_t st) {
   const int kt = ceil_div(s.K, Q4_K), nt = ceil_div(s.N, TILE_N);
 #define MOE_CALL(GR_, ZP_)                                                                                          \
-  hipLaunchKernelGGL((q4_unpack_kernel<T, GR_, ZP_>), dim3((uint32_t)kt * nt, min(s.G, 65535)), dim3(256), 0, st,              \
+  hipLaunchKernelGGL((q4_unpack_kernel<T, GR_, ZP_>), dim3((uint32_t)ceil_div(kt, QP_T) * nt, min(s.G, 65535)), dim3(256), 0, st,              \
                      (const uint32_t*)codes, (const T*)scales, (const uint8_t*)zeros, s.G, s.N, s.K, kt, nt, (T*)w)
   MOE_Q4_ALL(MOE_CALL);
 #undef MOE_CALL
