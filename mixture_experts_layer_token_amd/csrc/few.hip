@@ -598,58 +598,65 @@ __global__ __launch_bounds__(FEW_RT) void few_down_dense_kernel(FewArgs p) {
 // workspace: to take them apart beside each tile costs more than the tile.
 // XQ 1: up to 8 tokens lie in rows 0, 1, 4, 5, .. of the 16, and a lane scales two results
 // where it has four of 16 tokens (the vector instructions are as long as the copies).
-template <class Op, int NT, int XQ>
+template <class Op, int NT, int XQ, int WAVES>
 struct FewQ {
   typedef typename Op::elt T;
   typedef typename Op::hid H;
   static constexpr int RT = XQ == 1 ? 2 : 4;              // results of a lane
   static constexpr int RUN = 16 * (int)sizeof(T);         // a tile's scales of one group
-  static constexpr int SB = NT * Op::NG * RUN, SC = SB > 256 ? 2 : 1, ZB = NT * Op::NG * 16;
-  static constexpr int X0 = NT * 1024, S0 = X0 + 2048 * XQ * Op::PLANES, Z0 = S0 + 256 * SC;
-  static constexpr int SLOT = Z0 + (Op::ZP ? 256 : 0);
-  static constexpr int SW = Op::PLANES * XQ > 3 ? 4 : FEW_RW;  // waves that stream: 16 float32 tokens' slots fit 4
+  // a tile's scales of a step, then its zero points
+  static constexpr int SB = Op::NG * RUN, ZB = Op::ZP ? Op::NG * 16 : 0, SZ = NT * (SB + ZB), SC = (SZ + 255) / 256;
+  static constexpr int X0 = NT * 1024, S0 = X0 + 2048 * XQ * Op::PLANES, SLOT = S0 + 256 * SC;
+  static constexpr int NW = Op::PLANES * XQ == 1 ? WAVES : 8;
+  static constexpr int SW = Op::PLANES * XQ > 3 ? 4 : NW;  // waves that stream: 16 float32 tokens' slots fit 4
   static constexpr int RING = SW * SLOT, SUMS = NT * SW * 64 * RT * 4;  // bytes: one slot of each, their sums
-  static constexpr int PER = NT + 2 * XQ * Op::PLANES + SC + (Op::ZP ? 1 : 0);
+  static constexpr int PER = NT + 2 * XQ * Op::PLANES + SC;
 
-  // where a step's operands come from
+  // where the next step's operands come from
   const char* q[NT];
-  const char* s[SC];            // of a lane
-  const char* z;
-  size_t s_step, z_step;
+  const char* sz[SC];           // of a lane
+  uint32_t sz_step[SC];
+  const H* x;
 
-  __device__ __forceinline__ void seek(const typename Op::Src (&t)[NT]) {
-    const int lane = threadIdx.x & 63;
-    s_step = (size_t)Op::NG * t[0].Np * sizeof(T);
-    z_step = (size_t)Op::NG * t[0].Np;
+  __device__ __forceinline__ void seek(const typename Op::Src (&t)[NT], const H* xs, int step) {
+    const uint32_t lane = threadIdx.x & 63, Np = t[0].Np;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) q[i] = reinterpret_cast<const char*>(t[i].q);
+    for (int i = 0; i < NT; ++i) q[i] = reinterpret_cast<const char*>(t[i].q) + (size_t)step * 1024;
 #pragma unroll
-    for (int c = 0; c < SC; ++c) {  // lanes behind the scales copy some again
-      const int b = (256 * c + 4 * lane) % SB;
-      const T* const base = NT == 1 || b < SB / 2 ? t[0].s : t[NT - 1].s;
-      s[c] = reinterpret_cast<const char*>(base) + (size_t)(b / RUN % Op::NG) * t[0].Np * sizeof(T) + b % RUN;
+    for (int c = 0; c < SC; ++c) {  // lanes behind the last copy some again
+      const uint32_t b = (256 * c + 4 * lane) % SZ, in = b % (SB + ZB);
+      const bool one = NT == 1 || b < SB + ZB, z = ZB && in >= SB;
+      const uintptr_t sa = (uintptr_t)t[0].s, sb = (uintptr_t)t[NT - 1].s, za = (uintptr_t)t[0].z, zb = (uintptr_t)t[NT - 1].z;
+      const uintptr_t at_s = one ? sa : sb, at_z = one ? za : zb;
+      const char* const from = reinterpret_cast<const char*>(z ? at_z : at_s);
+      const uint32_t run = z ? 16u : (uint32_t)RUN, o = z ? in - SB : in, pitch = Np * (z ? 1u : (uint32_t)sizeof(T));
+      sz_step[c] = Op::NG * pitch;
+      sz[c] = from + (o / run * pitch + o % run) + (size_t)step * sz_step[c];
     }
-    if (Op::ZP) {
-      const int b = 4 * lane % ZB;
-      const uint8_t* const base = NT == 1 || b < ZB / 2 ? t[0].z : t[NT - 1].z;
-      z = reinterpret_cast<const char*>(base) + (size_t)(b / 16 % Op::NG) * t[0].Np + b % 16;
-    }
+    x = xs + step * Op::KS;
   }
-  // Activations: a lane's rows start off[] bytes behind x, planes `plane` elements apart.
-  __device__ __forceinline__ void request(char* to, int step, const H* x, size_t plane, const uint32_t (&off)[XQ]) const {
+  // Requests a step and goes on to the next one.  Activations: a lane's rows start off[] bytes
+  // behind x, planes `plane` elements apart.
+  __device__ __forceinline__ void request(char* to, size_t plane, const uint32_t (&off)[XQ], bool on) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) copy_rows<2>(q[i] + (size_t)step * 1024, (threadIdx.x & 63) * 16, to + 1024 * i);
+    for (int i = 0; i < NT; ++i) copy_rows<2>(q[i], (threadIdx.x & 63) * 16, to + 1024 * i);
 #pragma unroll
     for (int c = 0; c < SC; ++c)
-      __builtin_amdgcn_global_load_lds((gbl_ptr_t)(s[c] + step * s_step), (lds_ptr_t)(to + S0 + 256 * c), 4, 0, 0);
-    if (Op::ZP) __builtin_amdgcn_global_load_lds((gbl_ptr_t)(z + step * z_step), (lds_ptr_t)(to + Z0), 4, 0, 0);
+      __builtin_amdgcn_global_load_lds((gbl_ptr_t)sz[c], (lds_ptr_t)(to + S0 + 256 * c), 4, 0, 0);
 #pragma unroll
     for (int p = 0; p < Op::PLANES; ++p)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int c = 0; c < XQ; ++c)
-          copy_rows<0>(x + p * plane + step * Op::KS + 64 * h, off[c], to + X0 + 1024 * ((p * 2 + h) * XQ + c));
+          copy_rows<0>(x + p * plane + 64 * h, off[c], to + X0 + 1024 * ((p * 2 + h) * XQ + c));
+    if (on) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i) q[i] += 1024;
+#pragma unroll
+      for (int c = 0; c < SC; ++c) sz[c] += sz_step[c];
+      x += Op::KS;
+    }
   }
   __device__ __forceinline__ static void load(const char* from, typename Op::W (&w)[NT], typename Op::X& x) {
     const int lane = threadIdx.x & 63, n = lane & 15, row = XQ == 1 ? (n >> 2) * 2 + (n & 1) : n;
@@ -658,8 +665,8 @@ struct FewQ {
       w[i].q = *reinterpret_cast<const u32x4_t*>(from + 1024 * i + 16 * lane);
 #pragma unroll
       for (int g = 0; g < Op::NG; ++g) {
-        w[i].s[g] = *reinterpret_cast<const T*>(from + S0 + (i * Op::NG + g) * RUN + n * (int)sizeof(T));
-        if (Op::ZP) w[i].z[g] = *reinterpret_cast<const uint8_t*>(from + Z0 + (i * Op::NG + g) * 16 + n);
+        w[i].s[g] = *reinterpret_cast<const T*>(from + S0 + i * (SB + ZB) + g * RUN + n * (int)sizeof(T));
+        if (Op::ZP) w[i].z[g] = *reinterpret_cast<const uint8_t*>(from + S0 + i * (SB + ZB) + SB + g * 16 + n);
       }
     }
 #pragma unroll
@@ -671,7 +678,7 @@ struct FewQ {
   }
   // The waves' results of tile i in LDS, and their sum for output n of token t, in wave order.
   __device__ __forceinline__ static void keep(float* red, int i, f32x4_t acc) {
-    if (SW < FEW_RW && threadIdx.x >= SW * 64) return;
+    if (SW < NW && threadIdx.x >= SW * 64) return;
 #pragma unroll
     for (int r = 0; r < RT; ++r) red[(i * SW * 64 + threadIdx.x) * RT + r] = acc[r];
   }
@@ -685,8 +692,8 @@ struct FewQ {
 };
 
 template <class Op, int NB, int XQ>
-__global__ __launch_bounds__(FEW_RT) void few_gateup_q4_kernel(FewArgs p) {
-  typedef FewQ<Op, 2, XQ> Q;
+__global__ __launch_bounds__((64 * FewQ<Op, 2, XQ, 8>::NW)) void few_gateup_q4_kernel(FewArgs p) {
+  typedef FewQ<Op, 2, XQ, 8> Q;
   typedef typename Op::elt T;
   typedef typename Op::hid H;
   extern __shared__ char few_ring[];  // the rings (the list's scratch before), the waves' sums, the list
@@ -695,9 +702,9 @@ __global__ __launch_bounds__(FEW_RT) void few_gateup_q4_kernel(FewArgs p) {
   const int ring_bytes = max(NB * Q::RING, few_scratch_words(p.T, p.E) * 4);
   float* const red = reinterpret_cast<float*>(few_ring + ring_bytes);
   const FewList L = few_carve(reinterpret_cast<uint32_t*>(few_ring),
-                              reinterpret_cast<uint32_t*>(red + Q::SUMS / 4), p.T, p.E, p.k_max);
-  const int n_list = few_list<FEW_RT>(p, L);
-  if (blockIdx.x == 0) few_zero_row<Op, FEW_RT>(p);
+                              reinterpret_cast<uint32_t*>(red + 2 * Q::SUMS / 4), p.T, p.E, p.k_max);
+  const int n_list = few_list<64 * Q::NW>(p, L);
+  if (blockIdx.x == 0) few_zero_row<Op, 64 * Q::NW>(p);
   const int ci = p.I / TILE_N, routed = n_list * ci;
   const int n_items = routed + p.Is / TILE_N, first = near_tile(blockIdx.x, p.stride);
   const int steps = p.d / Op::KS;
@@ -716,11 +723,13 @@ __global__ __launch_bounds__(FEW_RT) void few_gateup_q4_kernel(FewArgs p) {
     const int idx = sh ? 0 : (int)((uint32_t)want / (uint32_t)ci);
     const int n0 = (sh ? want - routed : want - idx * ci) * TILE_N, N = sh ? p.Is : p.I;
     const int mat = sh ? 0 : __builtin_amdgcn_readfirstlane(L.expert[idx]);
-    rq.seek({Op::tile(pick(sh, sg, wg), mat, n0, N, p.d), Op::tile(pick(sh, su, wu), mat, n0, N, p.d)});
+    rq.seek({Op::tile(pick(sh, sg, wg), mat, n0, N, p.d), Op::tile(pick(sh, su, wu), mat, n0, N, p.d)},
+            static_cast<const H*>(p.xh), beg);
   };
   auto request = [&](int slot) {
-    rq.request(ring + slot * Q::SLOT, rs, static_cast<const H*>(p.xh), p.xplane, xoff);
-    if (rs + 1 < end) {
+    const bool on = rs + 1 < end;
+    rq.request(ring + slot * Q::SLOT, p.xplane, xoff, on);
+    if (on) {
       ++rs;
     } else if (want + p.stride < n_items) {
       want += p.stride;
@@ -733,7 +742,7 @@ __global__ __launch_bounds__(FEW_RT) void few_gateup_q4_kernel(FewArgs p) {
 #pragma unroll 1
     for (int i = 0; i < NB; ++i) request(i);
   }
-  int slot = 0;
+  int slot = 0, turn = 0;
 #pragma unroll 1
   for (int item = first; item < n_items; item += p.stride) {
     f32x4_t acc[2][1] = {{{0.f, 0.f, 0.f, 0.f}}, {{0.f, 0.f, 0.f, 0.f}}};
@@ -752,21 +761,25 @@ __global__ __launch_bounds__(FEW_RT) void few_gateup_q4_kernel(FewArgs p) {
     }
     settle(acc[0][0]);
     settle(acc[1][0]);
-    Q::keep(red, 0, acc[0][0]);
-    Q::keep(red, 1, acc[1][0]);
+    // sums of one item and the next by turns: the waves that add them up (others each time) are
+    // past the next barrier before their half is written again
+    float* const part = red + (turn & 1) * (Q::SUMS / 4);
+    Q::keep(part, 0, acc[0][0]);
+    Q::keep(part, 1, acc[1][0]);
     few_barrier();
-    if (wave < 2 * XQ) {
+    const int adds = (wave + 2 * XQ * turn++) % Q::NW;
+    if (adds < 2 * XQ) {
       const bool sh = item >= routed;
       const int idx = sh ? 0 : (int)((uint32_t)item / (uint32_t)ci);
       const int n0 = (sh ? item - routed : item - idx * ci) * TILE_N, N = sh ? p.Is : p.I;
       const int mat = sh ? 0 : __builtin_amdgcn_readfirstlane(L.expert[idx]);
-      const int j = tid & 15, t = tid >> 4;
-      float g = Q::sum(red, 0, j, t), u = Q::sum(red, 1, j, t);
+      const int lane = tid & 63, j = lane & 15, t = 4 * adds + (lane >> 4);
+      float g = Q::sum(part, 0, j, t), u = Q::sum(part, 1, j, t);
       const int row = sh ? p.T * p.k_max + t : few_row(L, idx, t);
       const bool mine = t < p.T && row != p.zero_row;
       auto again = [&](RowWeights rw, float& val) {
         redo_not_finite(val, mine, [&](int l) {
-          const T* xr = static_cast<const T*>(p.x) + (size_t)((wave * 64 + l) >> 4) * p.d;
+          const T* xr = static_cast<const T*>(p.x) + (size_t)(4 * adds + (l >> 4)) * p.d;
           const int nn = n0 + (l & 15);
           return wave_dot(p.d, [&](int k) {
             return Elt<T>::to_f32(xr[k]) * Op::value(rw, mat, nn, k, N, p.d, 0);
@@ -777,15 +790,14 @@ __global__ __launch_bounds__(FEW_RT) void few_gateup_q4_kernel(FewArgs p) {
       again(pick(sh, su, wu), u);
       if (mine) few_store_h<Op>(p, L, sh, n0 + j, g, u, row);
     }
-    few_barrier();
   }
   vm_wait<0>();  // no copy into LDS outlives the workgroup
 }
 
 // Down: NT tiles of 16 outputs for every token, otherwise as with element weights.
 template <class Op, int NB, int XQ, int NT>
-__global__ __launch_bounds__(FEW_RT) void few_down_q4_kernel(FewArgs p) {
-  typedef FewQ<Op, NT, XQ> Q;
+__global__ __launch_bounds__((64 * FewQ<Op, NT, XQ, 16>::NW)) void few_down_q4_kernel(FewArgs p) {
+  typedef FewQ<Op, NT, XQ, 16> Q;
   typedef typename Op::hid H;
   extern __shared__ char few_ring[];  // the rings, the waves' sums, the list
   const RowWeights wr = p.w[2], ws = p.w[5];
@@ -795,7 +807,7 @@ __global__ __launch_bounds__(FEW_RT) void few_down_q4_kernel(FewArgs p) {
   int32_t* const list = reinterpret_cast<int32_t*>(red + Q::SUMS / 4);
   const int32_t* const l_expert = list;
   const uint16_t* const row_of = reinterpret_cast<const uint16_t*>(list + min(p.E, p.T * p.k_max));
-  const int n_list = few_load_list<FEW_RT>(p, reinterpret_cast<uint32_t*>(list));
+  const int n_list = few_load_list<64 * Q::NW>(p, reinterpret_cast<uint32_t*>(list));
   __syncthreads();
   const int spe = p.I / Op::KS, routed = n_list * spe, steps = routed + p.Is / Op::KS;
   const int beg = wave < Q::SW ? steps * wave / Q::SW : 0, end = wave < Q::SW ? steps * (wave + 1) / Q::SW : 0;
@@ -812,7 +824,7 @@ __global__ __launch_bounds__(FEW_RT) void few_down_q4_kernel(FewArgs p) {
     typename Op::Src t[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) t[i] = Op::tile(pick(sh, ws, wr), mat, n0 + i * TILE_N, p.d, sh ? p.Is : p.I);
-    rq.seek(t);
+    rq.seek(t, static_cast<const H*>(p.h), st);
 #pragma unroll
     for (int c = 0; c < XQ; ++c) {
       const int tok = copy_row(c);
@@ -821,8 +833,10 @@ __global__ __launch_bounds__(FEW_RT) void few_down_q4_kernel(FewArgs p) {
     }
   };
   auto request = [&](int slot) {
-    rq.request(ring + slot * Q::SLOT, st, static_cast<const H*>(p.h), p.plane, hoff);
-    if (--left > 0) {
+    const bool on = left > 1;
+    rq.request(ring + slot * Q::SLOT, p.plane, hoff, on);
+    --left;
+    if (on) {
       ++st;
       if (idx < n_list && st == spe) {
         ++idx;
@@ -971,19 +985,19 @@ static hipError_t few_dense(FewArgs p, hipStream_t st) {
 }
 
 constexpr int FEW_Q_WIDE = 4096;
-// Steps of a ring: 160 KB less the sums and 8 KB for a list.
+// Steps of a ring: 160 KB less the sums and 4 KB for a list.
 constexpr int few_depth(int ring, int sums, int most) {
-  const int deep = (FEW_LDS - 8192 - sums) / ring;
+  const int deep = (FEW_LDS - 4096 - sums) / ring;
   return deep < 1 ? 1 : deep < most ? deep : most;
 }
 
 template <class Op, int XQ, int NT>
 static hipError_t few_q4_down(const FewArgs& p, int list, hipStream_t st) {
-  typedef FewQ<Op, NT, XQ> Q;
+  typedef FewQ<Op, NT, XQ, 16> Q;
   constexpr int SUMS = Q::SUMS, NB = few_depth(Q::RING, SUMS, 5), LESS = NB > 1 ? NB - 1 : 1;
   const int lds = NB * Q::RING + SUMS + list, tiles = p.d / (NT * TILE_N);
-  return lds <= FEW_LDS ? few_launch(few_down_q4_kernel<Op, NB, XQ, NT>, tiles, FEW_RT, lds, p, st)
-                        : few_launch(few_down_q4_kernel<Op, LESS, XQ, NT>, tiles, FEW_RT,
+  return lds <= FEW_LDS ? few_launch(few_down_q4_kernel<Op, NB, XQ, NT>, tiles, 64 * Q::NW, lds, p, st)
+                        : few_launch(few_down_q4_kernel<Op, LESS, XQ, NT>, tiles, 64 * Q::NW,
                                      LESS * Q::RING + SUMS + list, p, st);
 }
 
@@ -1002,13 +1016,13 @@ static hipError_t few_q4_as(FewArgs p, hipStream_t st) {
   const int kept = few_kept_words(p.T, p.E, p.k_max) * 4, list = 36 * min(p.E, p.T * p.k_max);
   p.stride = min(256, min(p.E, p.T * p.k_max) * (p.I / TILE_N) + p.Is / TILE_N);
   // ring depths: as many steps as 160 KB of LDS hold, one less where the list is long
-  typedef FewQ<Op, 2, XQ> Q;
-  constexpr int SUMS = Q::SUMS, NB = few_depth(Q::RING, SUMS, 4), LESS = NB > 1 ? NB - 1 : 1;
+  typedef FewQ<Op, 2, XQ, 8> Q;
+  constexpr int SUMS = 2 * Q::SUMS, NB = few_depth(Q::RING, SUMS, 4), LESS = NB > 1 ? NB - 1 : 1;
   const int scratch = few_scratch_words(p.T, p.E) * 4;
   const int up = max(NB * Q::RING, scratch) + SUMS + kept;
   hipError_t e;
-  if (up <= FEW_LDS) e = few_launch(few_gateup_q4_kernel<Op, NB, XQ>, p.stride, FEW_RT, up, p, st);
-  else e = few_launch(few_gateup_q4_kernel<Op, LESS, XQ>, p.stride, FEW_RT, max(LESS * Q::RING, scratch) + SUMS + kept, p, st);
+  if (up <= FEW_LDS) e = few_launch(few_gateup_q4_kernel<Op, NB, XQ>, p.stride, 64 * Q::NW, up, p, st);
+  else e = few_launch(few_gateup_q4_kernel<Op, LESS, XQ>, p.stride, 64 * Q::NW, max(LESS * Q::RING, scratch) + SUMS + kept, p, st);
   if (e != hipSuccess) return e;
   return p.d >= FEW_Q_WIDE ? few_q4_down<Op, XQ, 2>(p, list, st) : few_q4_down<Op, XQ, 1>(p, list, st);
 }

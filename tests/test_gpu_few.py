@@ -223,6 +223,19 @@ def test_q4_pack(dtype, zeros, group, G, N, K):
     _within(out, ref, U[DT[dtype]] * np.abs(ref) + 2.0 ** -150 if dtype == "f32" else U[DT[dtype]] * np.abs(ref) + 2.0 ** -134)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_q4_pack_every_magnitude(dtype, zeros):
+    """Codes of many values, ties among them, at the scales where 1 / s ends and beyond."""
+    w = torch.cat([_randn(_gen(5), 600, 512, dtype=DT[dtype]),
+                   (_randn(_gen(6), 56, 512).double() * 2.0 ** -torch.arange(94, 150, device=DEV)[:, None].double()).to(DT[dtype])])
+    w[600:, ::5] = w[600:, :1] / 2
+    q = moe.q4_pack(w, group=64, zeros=zeros)
+    codes, s, z = quant.q4_quantise(to_f64(w)[None], 64, zeros, _to_elt(dtype))
+    np.testing.assert_array_equal(to_f64(q.scales)[:, :, :656], np.swapaxes(s, 1, 2))
+    np.testing.assert_array_equal(q.codes.cpu().numpy(), quant.q4_tile(codes[0], 656, 512))
+
+
 def test_q4_pack_values_that_are_no_numbers():
     for bad in (math.nan, math.inf, -math.inf):
         for zeros in (False, True):
