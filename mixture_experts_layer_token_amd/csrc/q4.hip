@@ -321,10 +321,12 @@ __global__ __launch_bounds__(64 * QL_WW) void q4_wide_kernel(const typename Op::
                                                              typename Op::elt* __restrict__ y) {
   typedef typename Op::elt T;
   static_assert(sizeof(T) == 2, "bf16 activations");
-  constexpr int RUN = 32, SB = Op::NG * RUN;            // a tile's scales of a step
+  constexpr int RUN = 32, SB = Op::NG * RUN;            // a tile's scales of a step, then its zero points
+  constexpr int SZ = SB + (Op::ZP ? Op::NG * 16 : 0);
   constexpr int XP = R < 2 ? 1 : R / 2;                 // copies of activations of a wave
-  constexpr int TILE = 1024 + 256 + (Op::ZP ? 256 : 0), MINE = NT * TILE, XB = 4096 * R;
-  constexpr int PER = NT * (2 + (Op::ZP ? 1 : 0)) + XP;
+  constexpr int TILE = 1024 + 256, MINE = NT * TILE, XB = 4096 * R;
+  static_assert(SZ <= 256, "one copy");
+  constexpr int PER = 2 * NT + XP;
   extern __shared__ char ql_ring[];                     // [NB][XB], then [waves][NB][MINE]
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, col = lane & 15;
   const int nt = ceil_div(N, TILE_N), r0 = blockIdx.y * (16 * R), steps = ceil_div(K, Q4_K);
@@ -339,32 +341,38 @@ __global__ __launch_bounds__(64 * QL_WW) void q4_wide_kernel(const typename Op::
     const int c = (wave + QL_WW * i) % (4 * R);
     xoff[i] = (uint32_t)min(16 * (c >> 2) + copy_row(c & 1), rows - 1 - r0) * K * 2u;
   }
-  typename Op::Src src[NT];
-  const char* sp[NT];
-  const char* zp[NT];
+  // what the next request copies
+  const char *q[NT], *sz[NT];
+  uint32_t sz_step = 0;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {  // tiles behind the last repeat it
-    src[t] = Op::tile(w, 0, min(tile0 + t, nt - 1) * TILE_N, N, K);
-    const int b = 4 * lane % SB, c = 4 * lane % (16 * Op::NG);
-    sp[t] = reinterpret_cast<const char*>(src[t].s) + (size_t)(b / RUN) * src[t].Np * 2 + b % RUN;
-    if (Op::ZP) zp[t] = reinterpret_cast<const char*>(src[t].z) + (size_t)(c / 16) * src[t].Np + c % 16;
+    const typename Op::Src src = Op::tile(w, 0, min(tile0 + t, nt - 1) * TILE_N, N, K);
+    q[t] = reinterpret_cast<const char*>(src.q);
+    const int b = 4 * lane % SZ, o = b < SB ? b : b - SB;  // lanes behind the last copy some again
+    const uint32_t run = b < SB ? RUN : 16, pitch = src.Np * (b < SB ? 2u : 1u);
+    sz_step = Op::NG * pitch;
+    sz[t] = (b < SB ? reinterpret_cast<const char*>(src.s) : reinterpret_cast<const char*>(src.z)) +
+            (size_t)(o / run * pitch + o % run);
   }
-  const size_t Np = src[0].Np;
-  auto request = [&](int s, int slot) {
-    s = min(s, steps - 1);  // behind the end the last step again
+  int rs = 0;
+  auto request = [&](int slot) {
     char* to = mine + slot * MINE;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      copy_rows<2>(src[t].q + (size_t)s * 64, 16 * lane, to + t * TILE);
-      __builtin_amdgcn_global_load_lds((gbl_ptr_t)(sp[t] + s * Op::NG * Np * 2), (lds_ptr_t)(to + t * TILE + 1024), 4, 0, 0);
-      if (Op::ZP) __builtin_amdgcn_global_load_lds((gbl_ptr_t)(zp[t] + s * Op::NG * Np), (lds_ptr_t)(to + t * TILE + 1280), 4, 0, 0);
+      copy_rows<2>(q[t], 16 * lane, to + t * TILE);
+      __builtin_amdgcn_global_load_lds((gbl_ptr_t)sz[t], (lds_ptr_t)(to + t * TILE + 1024), 4, 0, 0);
     }
 #pragma unroll
     for (int i = 0; i < XP; ++i) {
       const int c = (wave + QL_WW * i) % (4 * R);
       // inputs behind K: any of the row's, taken out below
-      const uint32_t k = min(s * 256u + (c >> 1 & 1) * 128u + copy_byte(c & 1), 2u * K - 16u);
+      const uint32_t k = min(rs * 256u + (c >> 1 & 1) * 128u + copy_byte(c & 1), 2u * K - 16u);
       copy_rows<0>(x0, xoff[i] + k, ql_ring + slot * XB + (c >> 2) * 4096 + (c >> 1 & 1) * 2048 + (c & 1) * 1024);
+    }
+    if (rs + 1 < steps) {  // else the last step again
+      ++rs;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) q[t] += 1024, sz[t] += sz_step;
     }
   };
   f32x4_t acc[NT][R];
@@ -373,7 +381,7 @@ __global__ __launch_bounds__(64 * QL_WW) void q4_wide_kernel(const typename Op::
 #pragma unroll
     for (int r = 0; r < R; ++r) acc[t][r] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-  for (int i = 0; i < NB - 1; ++i) request(i, i);
+  for (int i = 0; i < NB - 1; ++i) request(i);
   int slot = 0;
 #pragma unroll 1
   for (int s = 0; s < steps; ++s) {
@@ -381,7 +389,7 @@ __global__ __launch_bounds__(64 * QL_WW) void q4_wide_kernel(const typename Op::
     compiler_fence();
     __builtin_amdgcn_s_barrier();  // everyone's copies of this step; everyone has read the last one's
     compiler_fence();
-    request(s + NB - 1, slot == 0 ? NB - 1 : slot - 1);
+    request(slot == 0 ? NB - 1 : slot - 1);
     const char* const from = mine + slot * MINE;
     typename Op::W v[NT];
     typename Op::X xv[R];
@@ -391,7 +399,7 @@ __global__ __launch_bounds__(64 * QL_WW) void q4_wide_kernel(const typename Op::
 #pragma unroll
       for (int g = 0; g < Op::NG; ++g) {
         v[t].s[g] = *reinterpret_cast<const T*>(from + t * TILE + 1024 + g * RUN + 2 * col);
-        if (Op::ZP) v[t].z[g] = *reinterpret_cast<const uint8_t*>(from + t * TILE + 1280 + g * 16 + col);
+        if (Op::ZP) v[t].z[g] = *reinterpret_cast<const uint8_t*>(from + t * TILE + 1024 + SB + g * 16 + col);
       }
     }
 #pragma unroll
@@ -496,7 +504,7 @@ static void linear_as(const Q4Shape& s, int rows, const void* x, const RowWeight
 template <class Op, int R, int NT, int NB>
 static void wide_as(const Q4Shape& s, int rows, const void* x, const RowWeights& w, void* y, hipStream_t st) {
   typedef typename Op::elt T;
-  constexpr int LDS = NB * (4096 * R + QL_WW * NT * (1024 + 256 + (Op::ZP ? 256 : 0)));
+  constexpr int LDS = NB * (4096 * R + QL_WW * NT * 1280);
   hipLaunchKernelGGL((q4_wide_kernel<Op, R, NT, NB>), dim3(ceil_div(s.N, QL_WW * NT * TILE_N), ceil_div(rows, 16 * R)),
                      dim3(64 * QL_WW), LDS, st, (const T*)x, w, rows, s.N, s.K, (T*)y);
 }
