@@ -493,8 +493,6 @@ static void unpack_t(const Q4Shape& s, const void* codes, const void* scales, co
   MOE_Q4_ALL(MOE_CALL);
 #undef MOE_CALL
 }
-constexpr int QL_WIDE = 16384;
-
 template <class Op, int R, int NT, int U, int NW>
 static void linear_as(const Q4Shape& s, int rows, const void* x, const RowWeights& w, void* y, hipStream_t st) {
   typedef typename Op::elt T;
@@ -508,15 +506,38 @@ static void wide_as(const Q4Shape& s, int rows, const void* x, const RowWeights&
   hipLaunchKernelGGL((q4_wide_kernel<Op, R, NT, NB>), dim3(ceil_div(s.N, QL_WW * NT * TILE_N), ceil_div(rows, 16 * R)),
                      dim3(64 * QL_WW), LDS, st, (const T*)x, w, rows, s.N, s.K, (T*)y);
 }
+// Tiles of a workgroup by the number of tiles: one where that already leaves a CU more than
+// one workgroup, more where their common activations count (a workgroup of eight waves fills
+// a CU's registers), and past that the kernel that shares them.  Measured at 4096 inputs,
+// groups of 64 with zero points, both sides of each border in us:
+//   16 rows, 512 tiles: 1 tile 12.0, 2 11.5 (one row: 7.8, 11.1); 1536: 2 tiles 22.2, shared 20.1
+//   (one row: 17.1, 20.3); 2048: 29.8, 21.4
+//   32 rows, 256 tiles: 1 tile 12.0, 2 12.4; 512: 22.2, 13.4; 1024: 2 tiles 21.7, 4 17.7, shared
+//   24.2; 1536: 4 tiles 30.2, shared 25.2
+//   64 rows, 256 tiles: 1 tile 19.3, 2 24.2; 512: 33.8, 25.1, shared 36.7; 768: 2 tiles 45.8, 37.1
+//   4 float32 rows, 256 tiles: 1 tile 12.8, 2 14.1; 512: 22.9, 15.2, 4 tiles 21.2; 768: 26.5, 21.5
 template <class Op>
 static void linear_op(const Q4Shape& s, int rows, const void* x, const RowWeights& w, void* y, hipStream_t st) {
-  const bool wide = s.N >= QL_WIDE;
+  const int nt = ceil_div(s.N, TILE_N);
   if constexpr (Op::PLANES == 1) {
-    if (rows <= 16) wide ? wide_as<Op, 1, 1, 4>(s, rows, x, w, y, st) : linear_as<Op, 1, 1, 4, 16>(s, rows, x, w, y, st);
-    else if (rows <= 32) wide ? wide_as<Op, 2, 1, 4>(s, rows, x, w, y, st) : linear_as<Op, 2, 1, 2, 16>(s, rows, x, w, y, st);
-    else wide ? wide_as<Op, 4, 1, 4>(s, rows, x, w, y, st) : linear_as<Op, 4, 1, 1, 16>(s, rows, x, w, y, st);
+    if (rows <= 16) {
+      if (nt <= 512) linear_as<Op, 1, 1, 2, 16>(s, rows, x, w, y, st);
+      else if (nt <= 1536) linear_as<Op, 1, 2, 2, 8>(s, rows, x, w, y, st);
+      else wide_as<Op, 1, 1, 4>(s, rows, x, w, y, st);
+    } else if (rows <= 32) {
+      if (nt <= 256) linear_as<Op, 2, 1, 1, 8>(s, rows, x, w, y, st);
+      else if (nt <= 512) linear_as<Op, 2, 2, 1, 8>(s, rows, x, w, y, st);
+      else if (nt <= 1024) linear_as<Op, 2, 4, 1, 8>(s, rows, x, w, y, st);
+      else wide_as<Op, 2, 1, 4>(s, rows, x, w, y, st);
+    } else {
+      if (nt <= 256) linear_as<Op, 4, 1, 1, 8>(s, rows, x, w, y, st);
+      else if (nt <= 512) linear_as<Op, 4, 2, 1, 8>(s, rows, x, w, y, st);
+      else wide_as<Op, 4, 1, 4>(s, rows, x, w, y, st);
+    }
   } else {
-    wide ? linear_as<Op, 1, 4, 1, 8>(s, rows, x, w, y, st) : linear_as<Op, 1, 1, 2, 8>(s, rows, x, w, y, st);
+    if (nt <= 256) linear_as<Op, 1, 1, 1, 16>(s, rows, x, w, y, st);
+    else if (nt <= 512) linear_as<Op, 1, 2, 1, 8>(s, rows, x, w, y, st);
+    else linear_as<Op, 1, 4, 1, 8>(s, rows, x, w, y, st);
   }
 }
 template <typename T>

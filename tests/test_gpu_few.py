@@ -259,7 +259,9 @@ def _linear(q, x):
 @pytest.mark.parametrize("group,zeros", [(32, True), (64, False), (128, True), (128, False)])
 @pytest.mark.parametrize("rows,K,N", [(1, 128, 16), (1, 2048, 512), (3, 1000, 37), (16, 264, 130), (17, 8, 1),
                                       (33, 4096, 100), (64, 712, 256), (100, 512, 48),
-                                      (5, 136, 16500), (20, 1000, 16385), (40, 264, 20001), (70, 8, 16399)])
+                                      (5, 136, 16500), (20, 1000, 16385), (40, 264, 20001), (70, 8, 16399),
+                                      (2, 136, 24600), (20, 264, 8200), (20, 520, 4100), (64, 136, 4100),
+                                      (64, 136, 8200), (16, 136, 8200)])
 def test_q4_linear(dtype, group, zeros, rows, K, N):
     g = _gen(rows + K)
     w = Weight(g, 1, N, K, DT[dtype], group, zeros)
@@ -277,7 +279,7 @@ def test_q4_linear_rows_are_independent():
     """Values that are no numbers, and huge ones, stay in their row; rows behind the
     last are not written."""
     g = _gen(9)
-    for dtype, N in (("bf16", 50), ("f32", 50), ("bf16", 16450)):
+    for dtype, N in (("bf16", 50), ("f32", 50), ("bf16", 16450), ("bf16", 8200), ("f32", 8200)):
         w = Weight(g, 1, N, 384, DT[dtype], 64, True)
         x = _randn(g, 20, 384, dtype=DT[dtype])
         a = _linear(w.arg, x)
