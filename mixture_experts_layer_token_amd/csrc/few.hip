@@ -223,8 +223,23 @@ __device__ __forceinline__ int few_list(const FewArgs& p, const FewList& L) {
     const bool bad = __ballot(!ok) != 0;
     if (first && p.status && tid == 0) p.status[0] = bad ? MOE_DEV_BAD_K_BIT : 0;
   }
+  // Where waves have two tokens and budgets can differ by much, the token with the i-th largest
+  // goes with the one with the i-th least (16 tokens of 256 experts with budgets of 0, 8, 16, 32
+  // by turns, two of 32 on a wave without: gate/up 85.8 -> 81.7 us; the ranks take 0.7).
+  int rank = lane < p.T ? lane : 64;
+  if (p.T > NW && p.k_max > 8) {
+    rank = lane < p.T ? 0 : 64;
 #pragma unroll 1
-  for (int t = wave; t < p.T; t += NW) {
+    for (int t = 0; t < p.T; ++t) {
+      const int other = __builtin_amdgcn_readlane(exec, t);
+      rank += other > exec || (other == exec && t < lane) ? 1 : 0;
+    }
+  }
+#pragma unroll 1
+  for (int i = 0; i < p.T; i += NW) {
+    const uint64_t turn = __ballot(rank == (i & NW ? i + NW - 1 - wave : i + wave));
+    if (!turn) continue;
+    const int t = __builtin_ctzll(turn);
     int e = -1;
     float w = 0.f;
     if (p.part) {
@@ -607,6 +622,9 @@ struct FewQ {
   // a tile's scales of a step, then its zero points
   static constexpr int SB = Op::NG * RUN, ZB = Op::ZP ? Op::NG * 16 : 0, SZ = NT * (SB + ZB), SC = (SZ + 255) / 256;
   static constexpr int X0 = NT * 1024, S0 = X0 + 2048 * XQ * Op::PLANES, SLOT = S0 + 256 * SC;
+  // Waves: 8 for gate/up, whose items all of them end together (16: 210 us where 8 took 197, 256
+  // experts, 8 tokens), 16 for down (8 tokens, 2048 outputs: 51 us of both launches with 16, 54
+  // with 8) where two slots of each fit.
   static constexpr int NW = Op::PLANES * XQ == 1 ? WAVES : 8;
   static constexpr int SW = Op::PLANES * XQ > 3 ? 4 : NW;  // waves that stream: 16 float32 tokens' slots fit 4
   static constexpr int RING = SW * SLOT, SUMS = NT * SW * 64 * RT * 4;  // bytes: one slot of each, their sums
@@ -984,7 +1002,6 @@ static hipError_t few_dense(FewArgs p, hipStream_t st) {
              : few_launch(few_down_dense_kernel<T, 3, PAIR>, tiles, FEW_RT, DOWN_LESS + sums + list, p, st);
 }
 
-constexpr int FEW_Q_WIDE = 4096;
 // Steps of a ring: 160 KB less the sums and 4 KB for a list.
 constexpr int few_depth(int ring, int sums, int most) {
   const int deep = (FEW_LDS - 4096 - sums) / ring;
@@ -1024,7 +1041,10 @@ static hipError_t few_q4_as(FewArgs p, hipStream_t st) {
   if (up <= FEW_LDS) e = few_launch(few_gateup_q4_kernel<Op, NB, XQ>, p.stride, 64 * Q::NW, up, p, st);
   else e = few_launch(few_gateup_q4_kernel<Op, LESS, XQ>, p.stride, 64 * Q::NW, max(LESS * Q::RING, scratch) + SUMS + kept, p, st);
   if (e != hipSuccess) return e;
-  return p.d >= FEW_Q_WIDE ? few_q4_down<Op, XQ, 2>(p, list, st) : few_q4_down<Op, XQ, 1>(p, list, st);
+  // Two tiles of outputs share their activations where more than 256 tiles are there for 256
+  // CUs (8 tokens, 64 experts of 1024, gate/up with it: 5120 outputs 93 us with two, 100 with
+  // one; 4096 outputs 77 and 70).
+  return p.d > 256 * TILE_N ? few_q4_down<Op, XQ, 2>(p, list, st) : few_q4_down<Op, XQ, 1>(p, list, st);
 }
 
 template <class Op>
