@@ -80,7 +80,12 @@ __host__ __device__ __forceinline__ int few_scratch_words(int T, int E) { return
 __host__ __device__ __forceinline__ int few_kept_words(int T, int E, int k_max) {
   return 9 * min(E, T * k_max) + T * k_max;
 }
-__device__ __forceinline__ FewList few_carve(uint32_t* scratch, uint32_t* kept, int T, int E, int k_max) {
+// The list lies behind what else the launch keeps in LDS (`used` bytes) and the scratch,
+// which overlap.
+__device__ __forceinline__ FewList few_carve(char* lds, int used, const FewArgs& p) {
+  const int T = p.T, E = p.E, k_max = p.k_max;
+  uint32_t* const scratch = reinterpret_cast<uint32_t*>(lds);
+  uint32_t* const kept = scratch + max(used / 4, few_scratch_words(T, E));
   const int cap = min(E, T * k_max);
   FewList L;
   L.keys = scratch;
@@ -380,13 +385,11 @@ template <typename T, int NB, int XQ>
 __global__ __launch_bounds__(FEW_RT) void few_gateup_dense_kernel(FewArgs p) {
   typedef DenseOp<T> Op;
   constexpr int SLOT = 2048 + 1024 * XQ, PER = 2 + XQ;
-  extern __shared__ char few_ring[];  // the rings (the list's scratch before), the waves' sums, the list
+  extern __shared__ char few_ring[];  // the rings and the waves' sums (the list's scratch before), the list
   const RowWeights wg = p.w[0], wu = p.w[1], sg = p.w[3], su = p.w[4];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-  const int ring_bytes = max(FEW_RW * NB * SLOT, few_scratch_words(p.T, p.E) * 4);
-  f32x4_t* const red = reinterpret_cast<f32x4_t*>(few_ring + ring_bytes);
-  const FewList L = few_carve(reinterpret_cast<uint32_t*>(few_ring), reinterpret_cast<uint32_t*>(red + FEW_RT), p.T, p.E,
-                              p.k_max);
+  f32x4_t* const red = reinterpret_cast<f32x4_t*>(few_ring + FEW_RW * NB * SLOT);
+  const FewList L = few_carve(few_ring, FEW_RW * NB * SLOT + FEW_RT * 16, p);
   const int n_list = few_list<FEW_RT>(p, L);
   if (blockIdx.x == 0) few_zero_row<Op, FEW_RT>(p);
   const int ci = p.I / 8, routed = n_list * ci;
@@ -625,7 +628,8 @@ struct FewQ {
   // Waves: 8 for gate/up, whose items all of them end together (16: 210 us where 8 took 197, 256
   // experts, 8 tokens), 16 for down (8 tokens, 2048 outputs: 51 us of both launches with 16, 54
   // with 8) where two slots of each fit.
-  static constexpr int NW = Op::PLANES * XQ == 1 ? WAVES : 8;
+  static constexpr bool FITS = 2 * WAVES * SLOT + NT * WAVES * 64 * RT * 4 + 4096 <= 160 * 1024;
+  static constexpr int NW = FITS ? WAVES : 8;
   static constexpr int SW = Op::PLANES * XQ > 3 ? 4 : NW;  // waves that stream: 16 float32 tokens' slots fit 4
   static constexpr int RING = SW * SLOT, SUMS = NT * SW * 64 * RT * 4;  // bytes: one slot of each, their sums
   static constexpr int PER = NT + 2 * XQ * Op::PLANES + SC;
@@ -714,13 +718,11 @@ __global__ __launch_bounds__((64 * FewQ<Op, 2, XQ, 8>::NW)) void few_gateup_q4_k
   typedef FewQ<Op, 2, XQ, 8> Q;
   typedef typename Op::elt T;
   typedef typename Op::hid H;
-  extern __shared__ char few_ring[];  // the rings (the list's scratch before), the waves' sums, the list
+  extern __shared__ char few_ring[];  // the rings and the waves' sums (the list's scratch before), the list
   const RowWeights wg = p.w[0], wu = p.w[1], sg = p.w[3], su = p.w[4];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int ring_bytes = max(NB * Q::RING, few_scratch_words(p.T, p.E) * 4);
-  float* const red = reinterpret_cast<float*>(few_ring + ring_bytes);
-  const FewList L = few_carve(reinterpret_cast<uint32_t*>(few_ring),
-                              reinterpret_cast<uint32_t*>(red + 2 * Q::SUMS / 4), p.T, p.E, p.k_max);
+  float* const red = reinterpret_cast<float*>(few_ring + NB * Q::RING);
+  const FewList L = few_carve(few_ring, NB * Q::RING + 2 * Q::SUMS, p);
   const int n_list = few_list<64 * Q::NW>(p, L);
   if (blockIdx.x == 0) few_zero_row<Op, 64 * Q::NW>(p);
   const int ci = p.I / TILE_N, routed = n_list * ci;
@@ -988,11 +990,11 @@ static hipError_t few_dense(FewArgs p, hipStream_t st) {
   p.stride = min(256, min(p.E, p.T * p.k_max) * (p.I / 8) + p.Is / 8);
   const int scratch = few_scratch_words(p.T, p.E) * 4, sums = FEW_RT * 16;
   const int kept = few_kept_words(p.T, p.E, p.k_max) * 4, list = 36 * min(p.E, p.T * p.k_max);
-  const int up = max(RING, scratch) + sums + kept;
+  const int up = max(RING + sums, scratch) + kept;
   const hipError_t e =
       up <= FEW_LDS ? few_launch(few_gateup_dense_kernel<T, NB, XQ>, p.stride, FEW_RT, up, p, st)
                     : few_launch(few_gateup_dense_kernel<T, NB - 1, XQ>, p.stride, FEW_RT,
-                                 max(LESS, scratch) + sums + kept, p, st);
+                                 max(LESS + sums, scratch) + kept, p, st);
   if (e != hipSuccess) return e;
   constexpr bool PAIR = XQ == 1;
   constexpr int DOWN = FEW_RW * 4 * 4096, DOWN_LESS = FEW_RW * 3 * 4096;
@@ -1036,10 +1038,10 @@ static hipError_t few_q4_as(FewArgs p, hipStream_t st) {
   typedef FewQ<Op, 2, XQ, 8> Q;
   constexpr int SUMS = 2 * Q::SUMS, NB = few_depth(Q::RING, SUMS, 4), LESS = NB > 1 ? NB - 1 : 1;
   const int scratch = few_scratch_words(p.T, p.E) * 4;
-  const int up = max(NB * Q::RING, scratch) + SUMS + kept;
+  const int up = max(NB * Q::RING + SUMS, scratch) + kept;
   hipError_t e;
   if (up <= FEW_LDS) e = few_launch(few_gateup_q4_kernel<Op, NB, XQ>, p.stride, 64 * Q::NW, up, p, st);
-  else e = few_launch(few_gateup_q4_kernel<Op, LESS, XQ>, p.stride, 64 * Q::NW, max(LESS * Q::RING, scratch) + SUMS + kept, p, st);
+  else e = few_launch(few_gateup_q4_kernel<Op, LESS, XQ>, p.stride, 64 * Q::NW, max(LESS * Q::RING + SUMS, scratch) + kept, p, st);
   if (e != hipSuccess) return e;
   // Two tiles of outputs share their activations where more than 256 tiles are there for 256
   // CUs (8 tokens, 64 experts of 1024, gate/up with it: 5120 outputs 93 us with two, 100 with

@@ -305,7 +305,7 @@ SHAPES = [
     ("bf16", 3, 7168, 6, 256, 256, 4), ("f32", 5, 1152, 61, 640, 384, 6), ("bf16", 16, 512, 100, 128, 128, 33),
     ("bf16", 7, 384, 1024, 128, 0, 64), ("f32", 2, 7296, 4, 128, 128, 2), ("bf16", 9, 7296, 3, 128, 0, 3),
     ("bf16", 16, 4096, 8, 1408, 0, 2), ("f32", 1, 640, 600, 256, 128, 5), ("f32", 16, 128, 1024, 128, 128, 64),
-    ("bf16", 8, 128, 1024, 128, 0, 64),
+    ("bf16", 8, 128, 1024, 128, 0, 64), ("bf16", 16, 128, 1024, 128, 128, 64),
 ]
 
 
