@@ -706,7 +706,8 @@ moe_status moe_adapt(const moe_adapter_desc* ad, const void* x, const int32_t* x
  * moe_q4_unpack: w = ELT(s * (q - z)), ELT [G][N][K].
  * moe_q4_linear (G = 1): y[r][n] = sum_k x[r][k] W[n][k] for x ELT [rows][K], y
  * ELT [rows][N]; exact products and float32 sums, scaled per group, one rounding
- * to ELT.  Made for few rows (decode): the weights are read once for every 16.
+ * to ELT.  Made for few rows (decode): the weights are read once for every 64 (float32:
+ * 16).
  * Values that are not finite stay in their own row's and column's outputs, which are
  * then summed again one by one (slow).
  *

@@ -11,16 +11,25 @@
 //            H[row][i] = w * SiLU(x_t . Wg_i) * (x_t . Wu_i), with row and w those of the
 //            token's choice of the expert (row t k_max + j for its j-th) and a row per
 //            token for the always-on expert
-//   down     out[t] = sum over the list of H . Wd: one workgroup owns 16 outputs of
+//   down     out[t] = sum over the list of H . Wd: one workgroup owns 8 to 32 outputs of
 //            all tokens and sums over every expert, so there is no combine
 //
 // The routing weight is applied to H in float32 before its one rounding to the
 // element type, so that the down products of all experts share their accumulators.
 //
-// The code is kept short on purpose: a launch begins with a cold instruction cache, and a
-// 64-byte line of straight code costs some 0.1 us to fetch (a down kernel unrolled over a
-// ring of 8 steps took 16 us for one token where 4 took 11).  Loops are rolled unless their
-// loads must be in flight together.
+// Measured (us; logits, gate/up, down; floor: weights at 7.2 TB/s of reads):
+//   1 token, 128 experts of 768 x 2048, 8 of them: 4.4 + 15.6 + 7.5, floor 10.5 (latency)
+//   4 tokens, 256 experts of 2048 x 7168, budgets 4 and 8: 6 + 207 .. 265 + 112 .. 140 for 23 to
+//     30 experts, 6.8 and 6.3 TB/s
+//   16 tokens, 256 experts of 384 x 2048, budgets 0 to 32: 4.9 + 66 .. 82 + 35 .. 44
+//   codes in groups of 64 with zero points, 8 tokens, 256 experts of 2048 x 7168: 6 + 170 .. 190
+//     + 69 .. 76, floor 152 in all
+// Three launches: one launch with a ticket a phase took 57 us for the one token and 410 for the
+// four, for its fences empty the caches and its workgroup fills a CU.
+//
+// The code is kept short on purpose: a launch begins with a cold instruction cache (a down
+// kernel unrolled over a ring of 8 steps took 16 us for one token where 4 took 11).  Loops are
+// rolled unless their loads must be in flight together.
 #include "common.h"
 #include "launch.h"
 #include "rowtile.h"
@@ -356,7 +365,9 @@ __device__ __forceinline__ void few_store_h(const FewArgs& p, const FewList& L, 
 // x 128 bytes ahead and on into the workgroup's next item, the activations of a step beside
 // its weights.  So the loop is short, needs no barrier, and its loads may carry the
 // non-temporal hint, which would fetch lines twice that two register loads take by halves
-// (reads of 2 GiB: 7.2 TB/s with it, 6.4 without).
+// (reads of 2 GiB: 7.2 TB/s with it, 6.4 without).  Bound by memory: gate/up of 30 experts
+// reads 6.8 TB/s; a ring in registers, two or four steps deep, 37 and 41 us for the one token
+// (now 27 in all) and 362 .. 400 for the four (now 365).
 constexpr int FEW_RW = 8;                 // waves of a workgroup
 constexpr int FEW_RT = 64 * FEW_RW;
 
@@ -611,9 +622,14 @@ __global__ __launch_bounds__(FEW_RT) void few_down_dense_kernel(FewArgs p) {
 // ---- 4-bit weights ----
 // As with element weights, a wave streams its share of K through a ring in LDS: at each step
 // NT tiles' codes (1 KB each in a row), their scales and zero points, and the activations,
-// which the tiles share.
+// which the tiles share.  With every load in registers and none ahead (all 16 waves waiting
+// at the end of each item) the 8 tokens took 284 .. 306 + 150 .. 164 us.  What bounds gate/up
+// now is the copies: 157 .. 172 of 170 .. 190 us without any product; of each 4.35 KB of a step
+// 2 are codes (without the activations 131, without the scales, 32 bytes of a line at a time,
+// 129).  Down reads 5.6 TB/s.
 // Float32 activations are read as the three bf16 parts that few_split_kernel leaves in the
-// workspace: to take them apart beside each tile costs more than the tile.
+// workspace (2.3 us): taken apart beside each tile they were most of 57 us of a gate/up launch
+// that takes 15 now (5 tokens, 61 experts of 640 x 1152, latency).
 // XQ 1: up to 8 tokens lie in rows 0, 1, 4, 5, .. of the 16, and a lane scales two results
 // where it has four of 16 tokens (the vector instructions are as long as the copies).
 template <class Op, int NT, int XQ, int WAVES>
@@ -905,7 +921,7 @@ __global__ __launch_bounds__((64 * FewQ<Op, NT, XQ, 16>::NW)) void few_down_q4_k
   }
 }
 
-// The three bf16 parts of float32 activations.
+// The three bf16 parts of float32 activations (2.3 us, a launch's latency).
 __global__ __launch_bounds__(256) void few_split_kernel(const float* __restrict__ x, int n, bf16_t* __restrict__ to) {
   const int i = blockIdx.x * 256 + threadIdx.x;
   if (i >= n) return;
@@ -918,7 +934,7 @@ __global__ __launch_bounds__(256) void few_split_kernel(const float* __restrict_
 
 // Partial logits part[slices][T][E] in float64 on the f64 matrix instruction: a workgroup
 // takes 16 experts and a slice of d for all tokens, its 8 waves a share each, added in
-// wave order.  (Lane l supplies the values of row l % 16 from LE (l / 16) on of a step,
+// wave order; 2.4 us (8 experts, 256 inputs) to 6.3 (256, 7168), latency.  (Lane l supplies the values of row l % 16 from LE (l / 16) on of a step,
 // value i of every lane in instruction i.)
 constexpr int FEW_LW = 8;
 typedef double f64x4_t __attribute__((ext_vector_type(4)));
@@ -984,6 +1000,15 @@ static hipError_t few_launch(K kernel, int grid, int threads, size_t lds, const 
 // activations, 4 with two, one less where the list is long).
 constexpr int FEW_LDS = 160 * 1024;
 
+template <typename T, bool PAIR>
+static hipError_t few_dense_down(const FewArgs& p, int more, hipStream_t st) {
+  constexpr int SLOTS = FEW_RW * 4096;
+  const int tiles = p.d / (PAIR ? 8 : 16);
+  return 4 * SLOTS + more <= FEW_LDS
+             ? few_launch(few_down_dense_kernel<T, 4, PAIR>, tiles, FEW_RT, 4 * SLOTS + more, p, st)
+             : few_launch(few_down_dense_kernel<T, 3, PAIR>, tiles, FEW_RT, 3 * SLOTS + more, p, st);
+}
+
 template <typename T, int NB, int XQ>
 static hipError_t few_dense(FewArgs p, hipStream_t st) {
   constexpr int RING = FEW_RW * NB * (2048 + 1024 * XQ), LESS = FEW_RW * (NB - 1) * (2048 + 1024 * XQ);
@@ -996,12 +1021,9 @@ static hipError_t few_dense(FewArgs p, hipStream_t st) {
                     : few_launch(few_gateup_dense_kernel<T, NB - 1, XQ>, p.stride, FEW_RT,
                                  max(LESS + sums, scratch) + kept, p, st);
   if (e != hipSuccess) return e;
-  constexpr bool PAIR = XQ == 1;
-  constexpr int DOWN = FEW_RW * 4 * 4096, DOWN_LESS = FEW_RW * 3 * 4096;
-  const int tiles = p.d / (PAIR ? 8 : 16);
-  return DOWN + sums + list <= FEW_LDS
-             ? few_launch(few_down_dense_kernel<T, 4, PAIR>, tiles, FEW_RT, DOWN + sums + list, p, st)
-             : few_launch(few_down_dense_kernel<T, 3, PAIR>, tiles, FEW_RT, DOWN_LESS + sums + list, p, st);
+  // Pairs for up to 8 tokens, unless tiles of 16 fill the CUs evenly: 2048 outputs 8.5 us without,
+  // 7.4 with; 7168 148, 142; 4096 (256 tiles) 70.1, 73.5.
+  return XQ == 1 && p.d / 16 % 256 ? few_dense_down<T, true>(p, sums + list, st) : few_dense_down<T, false>(p, sums + list, st);
 }
 
 // Steps of a ring: 160 KB less the sums and 4 KB for a list.

@@ -306,6 +306,7 @@ SHAPES = [
     ("bf16", 7, 384, 1024, 128, 0, 64), ("f32", 2, 7296, 4, 128, 128, 2), ("bf16", 9, 7296, 3, 128, 0, 3),
     ("bf16", 16, 4096, 8, 1408, 0, 2), ("f32", 1, 640, 600, 256, 128, 5), ("f32", 16, 128, 1024, 128, 128, 64),
     ("bf16", 8, 128, 1024, 128, 0, 64), ("bf16", 16, 128, 1024, 128, 128, 64),
+    ("bf16", 3, 4096, 6, 128, 128, 2),
 ]
 
 
