@@ -119,7 +119,7 @@ typedef enum {
   MOE_OP_FOLD = 5,
   MOE_OP_PATH = 6,  /* moe_path_route and moe_path_sources */
   MOE_OP_ROUTE_GROUPED = 7,
-  MOE_OP_FEW = 8    /* moe_forward_few and moe_experts_few */
+  MOE_OP_FEW = 9    /* moe_forward_few and moe_experts_few */
 } moe_op;
 
 /* Expert scores of moe_route_grouped. */

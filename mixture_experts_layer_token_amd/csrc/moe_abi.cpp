@@ -394,7 +394,7 @@ extern "C" {
 moe_status moe_workspace_size(const moe_desc* desc, int32_t op, size_t* bytes) {
   MOE_TRY(check_desc(desc));
   if (!bytes) return MOE_ERR_NULL;
-  if (op < MOE_OP_ROUTE || op > MOE_OP_FEW) return MOE_ERR_UNSUPPORTED;
+  if (op < MOE_OP_ROUTE || (op > MOE_OP_ROUTE_GROUPED && op != MOE_OP_FEW)) return MOE_ERR_UNSUPPORTED;
   if (op == MOE_OP_FEW) MOE_TRY(few_ok(*desc));
   *bytes = ws_size(*desc, op);
   return MOE_OK;
