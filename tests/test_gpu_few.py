@@ -450,6 +450,40 @@ def test_experts_few(dtype, group):
     _within(out, ref, tol)
 
 
+@pytest.mark.parametrize("T", [6, 12])
+@pytest.mark.parametrize("dtype,group,zeros", [("bf16", 64, True), ("bf16", 32, False), ("f32", 128, True)])
+def test_experts_few_q4_values_that_are_no_numbers(T, dtype, group, zeros):
+    """Tokens and scales that are no numbers stay with the tokens that they belong to."""
+    d = 384
+    c = Case(14, dtype, T, d, 8, 256, 128, 2, group, zeros)
+    off = torch.arange(T + 1, dtype=torch.int32, device=DEV) * 2
+    ids = torch.tensor([[t % 4, 4 + t % 2] for t in range(T)], dtype=torch.int32, device=DEV).flatten()
+    w = torch.rand(2 * T, generator=c.gen, device=DEV) + 0.5
+    a = _experts(c, off, ids, w)
+    wl = to_f64(w)
+    routes = [(t, e, wl[2 * t + j]) for t in range(T) for j, e in enumerate((t % 4, 4 + t % 2))]
+    ref, tol = _layer_ref(to_f64(c.x), routes, c.w, c.sh, c.dt, group, T, d)
+    _within(a, ref, tol)
+    keep = c.x.clone()
+    c.x[2, 9], c.x[3, 380] = math.nan, math.inf
+    b = _experts(c, off, ids, w)
+    rest = [t for t in range(T) if t not in (2, 3)]
+    assert torch.equal(a[rest], b[rest]) and b[2].isnan().all() and not b[3].isfinite().any()
+    c.x.copy_(keep)
+    # expert 1's down scale of output 7, then a gate scale of one of its columns
+    mine, others = [t for t in range(T) if t % 4 == 1], [t for t in range(T) if t % 4 != 1]
+    cols = [n for n in range(d) if n != 7]
+    c.args[2].scales[1, 1, 7] = math.nan
+    b = _experts(c, off, ids, w)
+    assert b[mine, 7].isnan().all() and torch.equal(a[:, cols], b[:, cols])
+    _within(b[others], ref[others], tol[others])
+    c.args[2].scales[1, 1, 7] = 0.0
+    c.args[0].scales[1, 0, 3] = math.inf
+    b = _experts(c, off, ids, w)
+    assert not b[mine].isfinite().any()
+    assert torch.equal(a[others][:, cols], b[others][:, cols])
+
+
 def test_experts_few_behind_grouped_routing():
     """moe_route_grouped, moe_q4_linear beside it and moe_adapt on its output, one stream."""
     c = Case(11, "bf16", 4, 512, 64, 256, 0, 8, 64, True)
