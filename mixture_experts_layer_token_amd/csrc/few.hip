@@ -496,7 +496,7 @@ __device__ __forceinline__ int few_load_list(const FewArgs& p, uint32_t* to) {
 // An output that is not finite, from its own token's products alone.
 template <class Op>
 __device__ __forceinline__ float few_down_again(const FewArgs& p, const int32_t* l_expert, const uint16_t* row_of,
-                                                int n_list, int n, int t) {
+                                                int n_list, int n, int t, bool& nan) {
   float sum = 0.f;
 #pragma unroll 1
   for (int i = 0; i <= n_list; ++i) {
@@ -506,9 +506,9 @@ __device__ __forceinline__ float few_down_again(const FewArgs& p, const int32_t*
     if (row == p.zero_row) continue;
     const int mat = sh ? 0 : l_expert[i], K = sh ? p.Is : p.I;
     const typename Op::hid* const hr = static_cast<const typename Op::hid*>(p.h) + (size_t)row * p.hw;
-    sum += wave_dot(K, [&](int k) {
-      return Op::h_value(hr, p.plane, k) * Op::value(pick(sh, p.w[5], p.w[2]), mat, n, k, p.d, K, p.blocked);
-    });
+    sum += wave_dot(K, [&](int k) { return Op::h_value(hr, p.plane, k); },
+                    [&](int k) { return Op::value(pick(sh, p.w[5], p.w[2]), mat, n, k, p.d, K, p.blocked); }, nan);
+    if (nan) break;
   }
   return sum;
 }
@@ -611,9 +611,9 @@ __global__ __launch_bounds__(FEW_RT) void few_down_dense_kernel(FewArgs p) {
     const int j = tid % ROWS, t = tid / ROWS;
     float v = few_sum<FEW_RW>(red, j, t);
     if (PAIR) v += few_sum<FEW_RW>(red, j + 8, t + 8);
-    redo_not_finite(v, t < p.T, [&](int l) {
+    redo_not_finite(v, t < p.T, t, [&](int l, bool& nan) {
       const int i = wave * 64 + l;
-      return few_down_again<Op>(p, l_expert, row_of, n_list, n0 + i % ROWS, i / ROWS);
+      return few_down_again<Op>(p, l_expert, row_of, n_list, n0 + i % ROWS, i / ROWS, nan);
     });
     if (t < p.T) static_cast<T*>(p.out)[(size_t)t * p.d + n0 + j] = Elt<T>::from_f32(v);
   }
@@ -814,12 +814,11 @@ __global__ __launch_bounds__((64 * FewQ<Op, 2, XQ, 8>::NW)) void few_gateup_q4_k
       const int row = sh ? p.T * p.k_max + t : few_row(L, idx, t);
       const bool mine = t < p.T && row != p.zero_row;
       auto again = [&](RowWeights rw, float& val) {
-        redo_not_finite(val, mine, [&](int l) {
+        redo_not_finite(val, mine, t, [&](int l, bool& nan) {
           const T* xr = static_cast<const T*>(p.x) + (size_t)(4 * adds + (l >> 4)) * p.d;
           const int nn = n0 + (l & 15);
-          return wave_dot(p.d, [&](int k) {
-            return Elt<T>::to_f32(xr[k]) * Op::value(rw, mat, nn, k, N, p.d, 0);
-          });
+          return wave_dot(p.d, [&](int k) { return Elt<T>::to_f32(xr[k]); },
+                          [&](int k) { return Op::value(rw, mat, nn, k, N, p.d, 0); }, nan);
         });
       };
       again(pick(sh, sg, wg), g);
@@ -913,9 +912,9 @@ __global__ __launch_bounds__((64 * FewQ<Op, NT, XQ, 16>::NW)) void few_down_q4_k
   if (wave < 2 * XQ * NT) {
     const int j = tid % (NT * 16), t = tid / (NT * 16);
     float v = Q::sum(red, j >> 4, j & 15, t);
-    redo_not_finite(v, t < p.T, [&](int l) {
+    redo_not_finite(v, t < p.T, t, [&](int l, bool& nan) {
       const int i = wave * 64 + l;
-      return few_down_again<Op>(p, l_expert, row_of, n_list, n0 + i % (NT * 16), i / (NT * 16));
+      return few_down_again<Op>(p, l_expert, row_of, n_list, n0 + i % (NT * 16), i / (NT * 16), nan);
     });
     if (t < p.T) static_cast<typename Op::elt*>(p.out)[(size_t)t * p.d + n0 + j] = Elt<typename Op::elt>::from_f32(v);
   }

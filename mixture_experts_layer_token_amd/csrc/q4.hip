@@ -303,11 +303,12 @@ __global__ __launch_bounds__(64 * NW) void q4_linear_kernel(const typename Op::e
 #pragma unroll
       for (int k = 0; k < NW; ++k) sum += q[k * 256];
       const bool mine = row < rows && n < N;
-      redo_not_finite(sum, mine, [&](int l) {
+      redo_not_finite(sum, mine, c, [&](int l, bool& nan) {
         const int e = i - lane + l;
         const T* xr = x0 + (size_t)(16 * r + e / (NT * 16)) * K;
         const int nn = n0 + e % (NT * 16);
-        return wave_dot(K, [&](int k) { return Elt<T>::to_f32(xr[k]) * Op::value(w, 0, nn, k, N, K, 0); });
+        return wave_dot(K, [&](int k) { return Elt<T>::to_f32(xr[k]); },
+                        [&](int k) { return Op::value(w, 0, nn, k, N, K, 0); }, nan);
       });
       if (mine) y[(size_t)row * N + n] = Elt<T>::from_f32(sum);
     }
@@ -452,10 +453,11 @@ __global__ __launch_bounds__(64 * QL_WW) void q4_wide_kernel(const typename Op::
     const int n = (tile0 + e / (4 * R)) * TILE_N + col, rb = r0 + 16 * (e / 4 % R) + e % 4, row = rb + 4 * (lane >> 4);
     float v = out[e * 64 + lane];
     const bool good = row < rows && n < N;
-    redo_not_finite(v, good, [&](int l) {
+    redo_not_finite(v, good, row, [&](int l, bool& nan) {
       const T* xr = x + (size_t)(rb + 4 * (l >> 4)) * K;
       const int nn = n - col + (l & 15);
-      return wave_dot(K, [&](int k) { return Elt<T>::to_f32(xr[k]) * Op::value(w, 0, nn, k, N, K, 0); });
+      return wave_dot(K, [&](int k) { return Elt<T>::to_f32(xr[k]); },
+                        [&](int k) { return Op::value(w, 0, nn, k, N, K, 0); }, nan);
     });
     if (good) y[(size_t)row * N + n] = Elt<T>::from_f32(v);
   }
