@@ -41,8 +41,6 @@ constexpr int TILE_N = 16;
 constexpr int Q4_K = 128;                         // inputs of a code tile
 constexpr uint32_t BF16_ONES = 0x3f803f80u;       // two bf16 ones
 
-typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
-
 // A weight matrix stack as a kernel takes it: row-major, blocked, or codes.
 struct RowWeights {
   const void* w;       // elements, or codes
@@ -73,15 +71,6 @@ __device__ __forceinline__ uint32_t copy_byte(int q) { return 16 * ((threadIdx.x
 // eighth) take neighbours: the tile of workgroup b of n.
 __device__ __forceinline__ int near_tile(int b, int n) { return n & 7 ? b : (b & 7) * (n >> 3) + (b >> 3); }
 
-// Four consecutive elements of a row (8- or 16-byte aligned).
-__device__ __forceinline__ void store_row4(bf16_t* p, f32x4_t v) {
-  u32x2_t o;
-  o.x = (uint32_t)f32_to_bf16(v[0]) | ((uint32_t)f32_to_bf16(v[1]) << 16);
-  o.y = (uint32_t)f32_to_bf16(v[2]) | ((uint32_t)f32_to_bf16(v[3]) << 16);
-  *reinterpret_cast<u32x2_t*>(p) = o;
-}
-__device__ __forceinline__ void store_row4(float* p, f32x4_t v) { *reinterpret_cast<f32x4_t*>(p) = v; }
-
 // Three bf16 parts of a float32 that add up to it (each cut off after 8 bits); a
 // value that is not finite stays whole in the first.
 __device__ __forceinline__ void split3(float f, uint32_t& a, uint32_t& b, uint32_t& c) {
@@ -98,40 +87,13 @@ struct DenseOp {
   typedef T elt;
   typedef T hid;                                  // element of the intermediate rows
   static constexpr int KS = 128 / sizeof(T);      // of K per step
-  static constexpr int LE = 16 / sizeof(T);
   static constexpr int PLANES = 1;
-  static constexpr bool Q4 = false;
   struct W { u32x4_t v[2]; };
   struct X { u32x4_t v[2]; };
-  // A tile: what the wave has in common, and the lane's place in it (the same for every
-  // tile of matrices of one K), so that tiles cost scalar registers only.
-  struct Src { const T* p; int kstr; uint32_t lane; };  // lane: bytes
-
   // w_offset of row n0's first element; a block's rows are KS elements long.
   __device__ __forceinline__ static size_t corner(int n0, int K, int blocked) {
     return blocked ? (size_t)(n0 & ~63) * K + (n0 & 63) * KS : (size_t)n0 * K;
   }
-  // Tile of rows n0 .. n0 + 15 of matrix `mat` of a stack of [N][K].
-  __device__ __forceinline__ static Src tile(const RowWeights& m, int mat, int n0, int N, int K, int blocked) {
-    const int lane = threadIdx.x & 63;
-    return Src{static_cast<const T*>(m.w) + (size_t)mat * N * K + corner(n0, K, blocked), w_kstep<T>(blocked),
-               (uint32_t)((lane & 15) * (blocked ? KS : K) + (lane >> 4) * LE) * (uint32_t)sizeof(T)};
-  }
-  __device__ __forceinline__ static W load(const Src& s, int step) {
-    const T* p = s.p + (size_t)step * s.kstr;
-    return W{{at<u32x4_t>(p, s.lane), at<u32x4_t>(p, s.lane, 64)}};
-  }
-  // Activations of a step: the lane's row starts `row` bytes behind base (any row that it
-  // may read if it has none).
-  __device__ __forceinline__ static X load_x(const T* base, uint32_t row, int step) {
-    const uint32_t o = row + ((threadIdx.x & 63) >> 4) * 16;
-    return X{{at<u32x4_t>(base + step * KS, o), at<u32x4_t>(base + step * KS, o, 64)}};
-  }
-  __device__ __forceinline__ static X load_h(const hid* base, uint32_t row, size_t, int step) {
-    return load_x(base, row, step);
-  }
-  __device__ __forceinline__ static void clear(X& x) { x.v[0] = x.v[1] = u32x4_t{0, 0, 0, 0}; }
-  __device__ __forceinline__ static void finish_x(X&) {}
   __device__ __forceinline__ static void mma(f32x4_t& acc, const W& w, const X& x) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -158,7 +120,7 @@ struct Q4Op {
   typedef bf16_t hid;                             // float32: three planes of it
   static constexpr int KS = Q4_K;
   static constexpr int PLANES = sizeof(T) == 2 ? 1 : 3;
-  static constexpr bool Q4 = true, ZP = ZEROS;
+  static constexpr bool ZP = ZEROS;
   static constexpr int NG = Q4_K / GROUP;         // groups of a step
   static constexpr int PER = 4 / NG;              // instructions of a group
   struct W {
