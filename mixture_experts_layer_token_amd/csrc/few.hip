@@ -110,7 +110,9 @@ __device__ __forceinline__ int few_row(const FewList& L, int idx, int t) {
 }
 
 // Largest of one value per lane, in every lane: row shifts, then the rows' last lanes
-// passed on, which leaves the maximum in lane 63.
+// passed on, which leaves the maximum in lane 63.  For whole waves only: a lane that a
+// condition has switched off (the right side of && and || too) neither gives its value nor
+// passes on the others', and lane 63 is read whether it is on or not.
 __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
 #define MOE_DPP_MAX(ctrl, rows) \
   v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, rows, 0xf, false))
@@ -153,9 +155,12 @@ __device__ __forceinline__ void few_choose256(const uint32_t* keys, int E, int k
 #pragma unroll 1
   for (int j = 0; j < kt; ++j) {
     const uint32_t m = wave_max_u32(k[0]);
-    uint64_t has = __ballot(k[0] == m);
-    if (has & (has - 1))  // several lanes: the lowest expert
-      has = __ballot(k[0] == m && e[0] == (int)~wave_max_u32(k[0] == m ? ~(uint32_t)e[0] : 0u));
+    const bool top = k[0] == m;
+    uint64_t has = __ballot(top);
+    if (has & (has - 1)) {  // several lanes: the lowest expert
+      const uint32_t low = ~wave_max_u32(top ? ~(uint32_t)e[0] : 0u);
+      has = __ballot(top && (uint32_t)e[0] == low);
+    }
     const int l = __builtin_ctzll(has), pick = __builtin_amdgcn_readlane(e[0], l);
     mine = lane == j ? pick : mine;
     logit = lane == j ? key_logit(m) : logit;
@@ -282,7 +287,7 @@ __device__ __forceinline__ int few_list(const FewArgs& p, const FewList& L) {
         if (same && j < lane) e = -1;
       }
     }
-    if (e >= 0) {
+    if ((uint32_t)e < (uint32_t)p.E) {  // the tables have E rows
       L.w[t * p.k_max + lane] = w;
       reinterpret_cast<uint16_t*>(L.all)[e * FEW_T + t] = (uint16_t)(t * p.k_max + lane);
       atomicOr(&L.mask[e], 1u << t);

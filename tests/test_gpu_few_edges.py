@@ -1,0 +1,86 @@
+"""Edges of the few-token layer on the GPU: logits that tie or are no numbers.
+Tolerances as in test_gpu_few.py."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_layer_token_amd as moe
+from oracle import moe_oracle
+from tests.test_gpu_few import Case, DEV, _k, _layer_ref, _randn, _within
+from workloads import to_f64
+
+pytestmark = pytest.mark.gpu
+
+
+# -------------------------------------------------------------------- routing
+
+def _counts_of_route(c, x, k, router=None, bias=None):
+    """moe_route's choices: per expert, and of each token."""
+    desc = c.desc()
+    i32 = dict(dtype=torch.int32, device=DEV)
+    off, status = torch.empty(c.T + 1, **i32), torch.empty(1, **i32)
+    ids, w = torch.full((c.T * c.k_max,), -1, **i32), torch.empty(c.T * c.k_max, device=DEV)
+    moe.moe_route(desc, x, c.router if router is None else router, bias, k, off, ids, w, status,
+                  moe.alloc_workspace(desc, moe.MOE_OP_ROUTE, DEV))
+    ids, off = ids.cpu().numpy(), off.cpu().numpy()
+    return np.bincount(ids[ids >= 0], minlength=c.E), [ids[off[t]:off[t + 1]] for t in range(c.T)]
+
+
+@pytest.mark.parametrize("E", [2, 8, 61, 64, 100, 128, 256, 600])
+@pytest.mark.parametrize("T", [1, 8, 16])
+@pytest.mark.parametrize("tie", ["zeros", "twins", "apart", "bias", "bias63"])
+def test_forward_few_ties_go_to_the_lower_expert(E, T, tie):
+    """Exactly tied logits: tokens of zeros, equal router rows side by side and 64 apart,
+    equal and -inf biases; the best of them with and without the experts 63, 127, .."""
+    k_max = min(E, 7)
+    c = Case(E + T, "bf16", T, 128, E, 128, 0, k_max)
+    if tie == "zeros":
+        c.x[::2] = 0
+    elif tie == "twins":
+        c.router[1::2] = c.router[0::2][:E // 2].clone()
+    elif tie == "apart":
+        at = torch.arange(E, device=DEV) % min(64, (E + 1) // 2)
+        c.router = c.router[at].contiguous()
+    else:
+        c.x.zero_()
+        c.bias = torch.tensor([0.0, -math.inf, 2.0, 1.0] if tie == "bias" else [-math.inf, 1.0, 0.0, 2.0],
+                              device=DEV)[torch.arange(E, device=DEV) % 4].contiguous()
+        if E == 2:
+            c.bias = torch.zeros(2, device=DEV)
+    c.check(_k(c, k_max, 1, max(1, k_max // 2)))
+
+
+@pytest.mark.parametrize("dtype,group", [("f32", 0), ("bf16", 64), ("f32", 32)])
+@pytest.mark.parametrize("E", [8, 64, 130])
+def test_forward_few_ties_of_other_types(dtype, group, E):
+    c = Case(E, dtype, 9, 256, E, 128, 128, 5, group, bool(group))
+    c.x[3:6] = 0
+    c.router[1::2] = c.router[0::2][:E // 2].clone()
+    c.check(_k(c, 5, 3))
+
+
+@pytest.mark.parametrize("E", [8, 40, 64, 200, 600])
+@pytest.mark.parametrize("T,group", [(1, 0), (5, 0), (16, 0), (5, 64)])
+def test_forward_few_routes_tokens_that_are_no_numbers(E, T, group):
+    """A token with a NaN has NaN for every logit: they tie.  It runs the experts that
+    moe_route gives it, without an always-on expert too its outputs are NaN, and the other
+    tokens' stay right."""
+    k_max, d = min(E, 4), 256
+    c = Case(E + T, "bf16", T, d, E, 128, 0, k_max, group, bool(group))
+    k, bad = _k(c, k_max), T // 2
+    x = c.x.clone()
+    x[bad, 9] = math.nan
+    out, stats, status = c.forward(k, x=x)
+    counts, ids = _counts_of_route(c, x, k)
+    st = stats.cpu().numpy()
+    np.testing.assert_array_equal(st[:E], counts)
+    assert st[E] == (counts > 0).sum() and st[E + 1] == T * k_max and int(status) == 0
+    assert ids[bad].tolist() == list(range(k_max)) and out[bad].isnan().all()
+    r = moe_oracle.route(to_f64(c.x), to_f64(c.router), None, [k_max] * T, k_max)
+    routes = [(j // k_max, int(e), float(w)) for j, (e, w) in enumerate(zip(r["ids"], r["w"])) if j // k_max != bad]
+    keep = [t for t in range(T) if t != bad]
+    if keep:
+        ref, tol = _layer_ref(to_f64(c.x), routes, c.w, None, c.dt, group, T, d)
+        _within(out[keep], ref[keep], tol[keep])
