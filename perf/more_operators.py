@@ -301,9 +301,10 @@ def _own(s):
     if c["op"] == "pack":
         moe.moe_q4_pack(s["w"], h[1])
         moe.moe_q4_unpack(h[1], s["out"])
-        # scales and zero points as [G, N, groups], the order the plain form has them in
-        sc = h[1].scales.transpose(1, 2)[:, :c["N"]]
-        return s["out"], sc, h[1].zeros.transpose(1, 2)[:, :c["N"]] if c["zeros"] else None
+        # scales and zero points as [G, N, groups], the order the plain form has them in, without
+        # the rows and groups that fill up the stored tiles
+        own_part = lambda t: t.transpose(1, 2)[:, :c["N"], :_groups(c["K"], c["group"])]
+        return s["out"], own_part(h[1].scales), own_part(h[1].zeros) if c["zeros"] else None
     if c["op"] == "layer":
         moe.moe_forward_few(h[1], s["x"], s["router"], s["bias"], s["k"], *h[2], s["out"], s["stats"], s["status"],
                             h[3])
