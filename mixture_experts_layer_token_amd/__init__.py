@@ -663,8 +663,9 @@ def moe_adapt(ad, x, x_rows, a, b, ranks, scales, adapter_ids, row_tok, expert_o
 
 class Q4Weight:
     """A stack of G matrices [N, K] in 4 bits with group scales, in the library's order
-    (include/moe.h): codes uint8, scales [G, groups, Np] of the element type (Np: N
-    rounded up to 16) and zero points uint8 of that shape, or None."""
+    (include/moe.h): codes uint8, scales [G, groups, Np] of the element type and zero points
+    uint8 of that shape, or None.  Tiles are whole: Np is N rounded up to 16, and groups are
+    those of K rounded up to 128; a matrix's own are [:, :ceil(K / group), :N], the rest 0."""
 
     __slots__ = ("desc", "codes", "scales", "zeros")
 

@@ -1,5 +1,5 @@
-"""Edges of the few-token layer on the GPU: logits that tie or are no numbers.
-Tolerances as in test_gpu_few.py."""
+"""Edges of the few-token layer and the 4-bit weights on the GPU: logits that tie or are no
+numbers, groups that do not fill a tile.  Tolerances as in test_gpu_few.py."""
 import math
 
 import numpy as np
@@ -8,6 +8,7 @@ import torch
 
 import mixture_experts_layer_token_amd as moe
 from oracle import moe_oracle
+from perf import more_operators
 from tests.test_gpu_few import Case, DEV, _k, _layer_ref, _randn, _within
 from workloads import to_f64
 
@@ -84,3 +85,21 @@ def test_forward_few_routes_tokens_that_are_no_numbers(E, T, group):
     if keep:
         ref, tol = _layer_ref(to_f64(c.x), routes, c.w, None, c.dt, group, T, d)
         _within(out[keep], ref[keep], tol[keep])
+
+
+# ------------------------------------------------------------- 4-bit weights
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("K", [8, 72, 136, 1000, 1032])
+def test_pack_cases_return_the_groups_of_k(monkeypatch, dtype, zeros, group, K):
+    """A pack's scales and zero points as [G, N, ceil(K / group)], whatever fills up the
+    stored tiles of 128 inputs: the measured calls' outputs are the plain form's."""
+    case = dict(op="pack", dtype=dtype, G=2, N=21, K=K, group=group, zeros=zeros)
+    want = more_operators.run(more_operators.prepare(case, 7))
+    monkeypatch.setattr(more_operators, "own", True)
+    got = more_operators.run(more_operators.prepare(case, 7))
+    assert got[1].shape == (2, 21, -(-K // group)) and (got[2] is None) == (not zeros)
+    for a, b in zip(got, want):
+        assert a is None and b is None or a.dtype == b.dtype and torch.equal(a, b)
