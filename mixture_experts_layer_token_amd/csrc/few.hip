@@ -955,7 +955,6 @@ __global__ __launch_bounds__(64 * FEW_LW) void few_logits_kernel(const T* __rest
   const T* wr = w + (size_t)min(e0 + l16, E - 1) * d + lg * LE;
   const T* xr = x + (size_t)min(l16, T_ - 1) * d + lg * LE;
   f64x4_t acc = {0.0, 0.0, 0.0, 0.0};
-#pragma unroll 4
   for (int s = s0; s < s1; ++s) {
     const u32x4_t wv = *reinterpret_cast<const u32x4_t*>(wr + (size_t)s * KS);
     const u32x4_t xv = *reinterpret_cast<const u32x4_t*>(xr + (size_t)s * KS);
