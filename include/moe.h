@@ -748,7 +748,7 @@ moe_status moe_q4_linear(const moe_q4_desc* qd, int32_t rows, const void* x, con
  *          for the always-on expert) and q4 names their group and their scales and
  *          zero points in the same order (zeros: all NULL, or none of those in use);
  *          float32 H is then kept whole
- *   others as in moe_forward; out must not overlap the inputs
+ *   others as in moe_forward; out must not overlap the inputs, and no output the workspace
  *   ws     scratch of moe_workspace_size(MOE_OP_FEW) bytes
  *
  * moe_experts_few: the same behind routes that are given (moe_route_grouped,

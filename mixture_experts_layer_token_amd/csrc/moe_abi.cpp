@@ -1024,20 +1024,28 @@ static moe_status few_operands(const moe_desc& d, const void* x, const void* con
     if (!w[i]) return MOE_ERR_NULL;
   if (!aligned16(x) || !aligned16(out)) return MOE_ERR_ALIGN;
   if (q4 && q4->group != 32 && q4->group != 64 && q4->group != 128) return MOE_ERR_UNSUPPORTED;
+  // No output byte among what the call reads.  (In the workspace it would lie over the list of
+  // experts that other workgroups of the same launch still read.)
   const size_t out_b = (size_t)d.T * d.d * elt_size(d);
-  if (out_b && !disjoint(out, out_b, x, out_b)) return MOE_ERR_SHAPE;
+  auto clear = [&](const void* p, size_t bytes) { return !out_b || !p || disjoint(out, out_b, p, bytes); };
+  if (!clear(x, out_b)) return MOE_ERR_SHAPE;
   for (int i = 0; i < n; ++i) {
     if (!aligned16(w[i])) return MOE_ERR_ALIGN;
+    const int G = i < 3 ? d.E : 1, I = i < 3 ? d.I : d.I_shared;
+    const Q4Bytes b = q4_sizes(moe_q4_desc{G, i % 3 < 2 ? I : d.d, i % 3 < 2 ? d.d : I, q4 ? q4->group : 128, 1, d.dtype});
+    if (!clear(w[i], q4 ? b.codes : b.w)) return MOE_ERR_SHAPE;
     a.w[i] = w[i];
     if (!q4) continue;
     if (!q4->scales[i]) return MOE_ERR_NULL;
     if (!q4->zeros[i] != !q4->zeros[0]) return MOE_ERR_NULL;
     if (!aligned16(q4->scales[i]) || !aligned16(q4->zeros[i])) return MOE_ERR_ALIGN;
+    if (!clear(q4->scales[i], b.scales) || !clear(q4->zeros[i], b.zeros)) return MOE_ERR_SHAPE;
     a.scales[i] = q4->scales[i];
     a.zeros[i] = q4->zeros[i];
   }
   a.group = q4 ? q4->group : 0;
   MOE_TRY(check_ws(d, MOE_OP_FEW, ws, ws_bytes));
+  if (!clear(ws, ws_size(d, MOE_OP_FEW))) return MOE_ERR_SHAPE;
   Carver c(ws);
   FewWs fw;
   plan_few(d, c, fw);
@@ -1062,6 +1070,10 @@ moe_status moe_forward_few(const moe_desc* desc, const void* x, const void* w_ro
   if (!aligned16(w_router)) return MOE_ERR_ALIGN;
   FewLaunch a{};
   MOE_TRY(few_operands(d, x, {w_gate, w_up, w_down, ws_gate, ws_up, ws_down}, q4, out, ws, ws_bytes, a));
+  const size_t out_b = (size_t)d.T * d.d * elt_size(d), need = ws_size(d, MOE_OP_FEW);
+  if (out_b && !disjoint(out, out_b, w_router, (size_t)d.E * d.d * elt_size(d))) return MOE_ERR_SHAPE;
+  if (stats && !disjoint(stats, ((size_t)d.E + 2) * 4, ws, need)) return MOE_ERR_SHAPE;
+  if (dev_status && !disjoint(dev_status, 4, ws, need)) return MOE_ERR_SHAPE;
   a.w_router = w_router;
   a.bias = router_bias;
   a.k = k;
