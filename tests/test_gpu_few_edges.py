@@ -1,5 +1,5 @@
 """Edges of the few-token layer and the 4-bit weights on the GPU: logits that tie or are no
-numbers, groups that do not fill a tile.  Tolerances as in test_gpu_few.py."""
+numbers, groups that do not fill a tile, the largest sizes.  Tolerances as in test_gpu_few.py."""
 import math
 
 import numpy as np
@@ -7,9 +7,9 @@ import pytest
 import torch
 
 import mixture_experts_layer_token_amd as moe
-from oracle import moe_oracle
+from oracle import moe_oracle, quant
 from perf import more_operators
-from tests.test_gpu_few import Case, DEV, _k, _layer_ref, _randn, _within
+from tests.test_gpu_few import DEV, DT, EPS, U, Case, Weight, _gen, _k, _layer_ref, _randn, _to_elt, _within
 from workloads import to_f64
 
 pytestmark = pytest.mark.gpu
@@ -103,3 +103,54 @@ def test_pack_cases_return_the_groups_of_k(monkeypatch, dtype, zeros, group, K):
     assert got[1].shape == (2, 21, -(-K // group)) and (got[2] is None) == (not zeros)
     for a, b in zip(got, want):
         assert a is None and b is None or a.dtype == b.dtype and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype,group,zeros", [("bf16", 32, True), ("f32", 128, False)])
+def test_q4_more_matrices_than_a_grid_has_rows(dtype, group, zeros):
+    """65,600 matrices: packed, re-laid and widened by workgroups that take two of them."""
+    G, N, K = 65600, 2, 40
+    ng = -(-K // group)
+    w = _randn(_gen(1), G, N, K, dtype=DT[dtype])
+    q = moe.q4_pack(w, group=group, zeros=zeros)
+    out = torch.full_like(w, math.nan)
+    moe.moe_q4_unpack(q, out)
+    at = [0, 1, 63, 65534, 65535, 65536, 65599]
+    codes, s, z = quant.q4_quantise(to_f64(w[at]), group, zeros, _to_elt(dtype))
+    np.testing.assert_array_equal(to_f64(q.scales[at])[:, :ng, :N], np.swapaxes(s, 1, 2))
+    ref = quant.q4_values(codes, s, z, group)
+    _within(out[at], ref, U[DT[dtype]] * np.abs(ref))
+    # back from row-major codes: the same bytes
+    step = q.scales[:, :ng, :N].transpose(1, 2)
+    zp = q.zeros[:, :ng, :N].transpose(1, 2) if zeros else None
+    wide = lambda t: t.double().repeat_interleave(group, -1)[..., :K]
+    c = torch.where(wide(step) == 0, 0.0, out.double() / wide(step)).round() + (wide(zp) if zeros else 8)
+    c = c.to(torch.uint8)
+    rm = c[..., 0::2] | (c[..., 1::2] << 4)
+    r = moe.q4_tile(rm, step.contiguous(), zp.contiguous() if zeros else None, group=group)
+    assert torch.equal(r.scales, q.scales) and (not zeros or torch.equal(r.zeros, q.zeros))
+    back = torch.full_like(w, math.nan)
+    moe.moe_q4_unpack(r, back)
+    assert torch.equal(back, out)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,K,N", [(2, 65536, 40), (20, 14336, 300), (1, 16392, 4100), (5, 136, 262144),
+                                      (700, 520, 70), (1000, 72, 8300), (65536, 8, 3)])
+def test_q4_linear_at_its_limits(dtype, rows, K, N):
+    g = _gen(rows + K)
+    w = Weight(g, 1, N, K, DT[dtype], 64, True)
+    x = _randn(g, rows, K, dtype=DT[dtype])
+    y = torch.full((rows, N), math.nan, dtype=DT[dtype], device=DEV)
+    moe.moe_q4_linear(w.arg, x, y)
+    xa = to_f64(x)
+    ref = xa @ w.val[0].T
+    tol = w.order(K) * EPS * (np.abs(xa) @ w.mag[0].T)
+    _within(y, ref, tol + U[DT[dtype]] * (np.abs(ref) + tol))
+
+
+@pytest.mark.parametrize("dtype,group", [("bf16", 0), ("f32", 0), ("bf16", 64), ("f32", 32)])
+@pytest.mark.parametrize("T,d,E,I,Is,k_max", [(3, 65536, 3, 128, 0, 2), (16, 16384, 4, 128, 256, 2),
+                                              (2, 128, 2, 65536, 0, 2), (10, 256, 5, 14336, 128, 3)])
+def test_forward_few_at_its_limits(dtype, group, T, d, E, I, Is, k_max):
+    c = Case(T + d, dtype, T, d, E, I, Is, k_max, group, bool(group))
+    c.check(_k(c, k_max, 1))
