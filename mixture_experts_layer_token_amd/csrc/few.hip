@@ -3,7 +3,8 @@
 // With so few tokens the time is that of the chosen experts' weights and of the
 // launches, so nothing is permuted: every chosen expert's weight tile is multiplied
 // with all tokens at once (one 16-column matrix instruction, rowtile.h) and only the
-// tokens that chose it are kept.  Three launches:
+// tokens that chose it are kept.  Three launches (float32 with 4-bit weights: few_split_kernel
+// before gate/up, four):
 //
 //   logits   float64 partial logits (given routes: none)
 //   gate/up  every workgroup: per token the top k_t and their weights, then the list of
@@ -15,15 +16,20 @@
 //            all tokens and sums over every expert, so there is no combine
 //
 // The routing weight is applied to H in float32 before its one rounding to the
-// element type, so that the down products of all experts share their accumulators.
+// element type, so that the down products of all experts share their accumulators.  (bf16: the
+// matrix instruction takes no more, and moe_ffn rounds there too.  Against float64 the layer is
+// off by 0.0023 of its norm, with H in float32 by 0.0017, of which the outputs' own rounding is
+// most.)
 //
 // Measured (us; logits, gate/up, down; floor: weights at 7.2 TB/s of reads):
 //   1 token, 128 experts of 768 x 2048, 8 of them: 4.4 + 15.6 + 7.5, floor 10.5 (latency)
-//   4 tokens, 256 experts of 2048 x 7168, budgets 4 and 8: 6 + 207 .. 265 + 112 .. 140 for 23 to
-//     30 experts, 6.8 and 6.3 TB/s
-//   16 tokens, 256 experts of 384 x 2048, budgets 0 to 32: 4.9 + 66 .. 82 + 35 .. 44
+//   4 tokens, 256 experts of 2048 x 7168, budgets 4 and 8, an always-on expert: 6 + 207 .. 265 +
+//     112 .. 142 for 23 and 30 experts, 6.8 and 6.3 TB/s, floors 294 and 379
+//   16 tokens, 256 experts of 384 x 2048, budgets 0 to 32: 4.9 + 66 .. 82 + 35 .. 44 for 99 and 132
+//     experts, floors 65 and 87
 //   codes in groups of 64 with zero points, 8 tokens, 256 experts of 2048 x 7168: 6 + 170 .. 190
-//     + 69 .. 76, floor 152 in all
+//     + 69 .. 77 for 50 and 55 experts (190 .. 231 + 77 .. 85 on another card, whose clock was
+//     lower), floors 171 and 187
 // Three launches: one launch with a ticket a phase took 57 us for the one token and 410 for the
 // four, for its fences empty the caches and its workgroup fills a CU.
 //
@@ -40,7 +46,14 @@ namespace moe {
 constexpr int FEW_T = MOE_FEW_MAX_T;
 constexpr int FEW_S = 8;                  // slices of the partial logits, at most
 // Slices that the logits are summed in: 4 for up to 2048 inputs (every gate/up workgroup
-// reads them all), else 8 (twice the workgroups for the products).
+// reads them all), else 8 (twice the workgroups for the products).  Whole layers with experts of
+// 128, us with 4 and with 8, bf16:
+//   inputs                      1024          2048          4096          7168
+//   16 tokens, 256 experts   23.6, 25.4    27.2, 28.2    35.2, 36.0    53.1, 53.0
+//   16 tokens, 8 experts     15.1, 15.2    16.4, 15.5    22.3, 21.0    31.7, 29.7
+//   1 token, 256 experts     13.1, 13.2    14.2, 13.7    15.9, 15.0    27.6, 25.5
+//   1 token, 600 experts     15.1, 15.5    16.1, 16.5    18.2, 18.5    29.7, 30.1
+// float32 likewise (16 tokens, 256 experts: 36.8, 37.7 at 2048; 84.3, 82.9 at 7168).
 __host__ __device__ __forceinline__ int few_slices(int d) { return d <= 2048 ? 4 : 8; }
 
 // What the launches take.
@@ -1024,8 +1037,13 @@ static hipError_t few_dense(FewArgs p, hipStream_t st) {
                     : few_launch(few_gateup_dense_kernel<T, NB - 1, XQ>, p.stride, FEW_RT,
                                  max(LESS + sums, scratch) + kept, p, st);
   if (e != hipSuccess) return e;
-  // Pairs for up to 8 tokens, unless tiles of 16 fill the CUs evenly: 2048 outputs 8.5 us without,
-  // 7.4 with; 7168 148, 142; 4096 (256 tiles) 70.1, 73.5.
+  // Pairs for up to 8 tokens, unless tiles of 16 fill the CUs evenly.  gate/up and down of 4 bf16
+  // tokens, 32 experts of 1024, 4 of them a token, us in tiles of 16 and in pairs:
+  //   2048 outputs (128 tiles) 39.3, 35.3   4096 (256) 53.6, 55.9   8192 (512) 99, 104
+  //   4224 (264) 66.8, 64.8                 6144 (384) 84.5, 83.7   8320 (520) 108.9, 109.1
+  // Where tiles of 16 leave few CUs idle without filling them pairs cost up to 6%: 3968 (248) 53.5,
+  // 56.1; 7168 (448) 95.6, 101.5; of 64 experts of 2048 at 7168 341.9, 340.4, of one token 113.5,
+  // 116.3.  float32: 2048 69, 61; 4096 106, 106; 6144 163, 157; 7168 186, 190; 8192 231, 227.
   return XQ == 1 && p.d / 16 % 256 ? few_dense_down<T, true>(p, sums + list, st) : few_dense_down<T, false>(p, sums + list, st);
 }
 
@@ -1069,8 +1087,9 @@ static hipError_t few_q4_as(FewArgs p, hipStream_t st) {
   else e = few_launch(few_gateup_q4_kernel<Op, LESS, XQ>, p.stride, 64 * Q::NW, max(LESS * Q::RING + SUMS, scratch) + kept, p, st);
   if (e != hipSuccess) return e;
   // Two tiles of outputs share their activations where more than 256 tiles are there for 256
-  // CUs (8 tokens, 64 experts of 1024, gate/up with it: 5120 outputs 93 us with two, 100 with
-  // one; 4096 outputs 77 and 70).
+  // CUs (8 tokens, 32 experts of 1024, gate/up with it, us with one and with two: 4096 outputs
+  // 42, 45; 4224 51, 46; 7168 69, 63; 12288 99, 97; one token 15.6, 17.0; 19.0, 17.0; 21.6, 19.6;
+  // 31.9, 28.8; 16 tokens 61, 65; 76, 66; 100, 89; 153, 145).
   return p.d > 256 * TILE_N ? few_q4_down<Op, XQ, 2>(p, list, st) : few_q4_down<Op, XQ, 1>(p, list, st);
 }
 

@@ -540,6 +540,14 @@ static void wide_as(const Q4Shape& s, int rows, const void* x, const RowWeights&
 //   24.2; 1536: 4 tiles 30.2, shared 25.2
 //   64 rows, 256 tiles: 1 tile 19.3, 2 24.2; 512: 33.8, 25.1, shared 36.7; 768: 2 tiles 45.8, 37.1
 //   4 float32 rows, 256 tiles: 1 tile 12.8, 2 14.1; 512: 22.9, 15.2, 4 tiles 21.2; 768: 26.5, 21.5
+// At other lengths of a row the borders lie elsewhere, by what a workgroup has to do (us):
+//   1024 inputs: one row, 512 tiles: 1 tile 4.9, 2 3.3; 1536: 2 tiles 6.9, shared 7.1; 32 rows, 256
+//   tiles: 4.6, 5.2; 512: 6.9, 5.3; 1024: 2 tiles 7.7, 4 7.2, shared 9.1; 64 rows, 256: 7.1, 8.3; 640:
+//   2 tiles 15.3, shared 13.3; 4 float32 rows, 256: 6.4, 4.9; 640: 2 tiles 8.5, 4 6.6
+//   14336 inputs: one row, 512 tiles: 20.8, 25.9; 1024: 39.7, 34.6; 1536: 2 tiles 56.9, shared 56.7;
+//   32 rows, 256: 29.9, 32.2; 512: 56.5, 32.8; 1024: 62.1, 4 tiles 41.7, shared 72.8; 1536: 4 tiles
+//   78.5, 73.2; 64 rows, 256: 56, 70; 512: 108, 74; 640: 2 tiles 144, shared 115; 4 float32 rows,
+//   256: 33.5, 38.6; 512: 65.8, 39.5; 640: 75.6, 61.3
 template <class Op>
 static void linear_op(const Q4Shape& s, int rows, const void* x, const RowWeights& w, void* y, hipStream_t st) {
   const int nt = ceil_div(s.N, TILE_N);

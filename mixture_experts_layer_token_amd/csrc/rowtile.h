@@ -17,12 +17,17 @@
 // arithmetic: bf16 numbers from 16 to 32 are 1/8 apart, so 0x4180 + 8 q is 16 + q.
 // The matrix instruction sums x (16 + q) over a group, exact products in float32,
 // and the group ends with  acc += s (sum - (16 + z) sum x),  sum x from the same
-// instruction with ones for weights.  (The usual base 128 would lose three more
-// bits to the difference.)  Two mask-and-or operations and shifts for two codes,
+// instruction with ones for weights.  (The usual base 128 would lose two to
+// three more bits to the difference.)  Two mask-and-or operations and shifts for two codes,
 // where a conversion of each would cost four.
+// What that leaves: an error of some roundings of s sum |x| (32 + q + z), the size of what is
+// summed and subtracted again.  For codes all over their range that is 5 (z = 0) to 12 times
+// (z = 8) the result's own sum |x| |q - z|, two to four bits; where all lie next to their zero
+// point it is more.
 // float32 activations are cut into three bf16 parts of 8 bits each, which hold all
-// 24 bits, and run as three instructions: the float32 matrix instruction takes
-// four times the time of all three.
+// 24 bits (of values below 2^-110 the last ones lie under bf16's least: an error of 1e-6 at
+// 2^-114, 2e-5 at 2^-118), and run as three instructions: the float32 matrix instruction
+// takes four times the time of all three.
 //
 // Matrix instructions run whatever the lanes' mask says, so a condition around one has to
 // be scalar (the same for the wave, and known to the compiler to be).
