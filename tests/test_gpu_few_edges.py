@@ -154,3 +154,29 @@ def test_q4_linear_at_its_limits(dtype, rows, K, N):
 def test_forward_few_at_its_limits(dtype, group, T, d, E, I, Is, k_max):
     c = Case(T + d, dtype, T, d, E, I, Is, k_max, group, bool(group))
     c.check(_k(c, k_max, 1))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("E", [8, 40, 200, 600])
+@pytest.mark.parametrize("where", ["row", "bias", "x"])
+@pytest.mark.parametrize("value", [math.nan, -math.nan, math.inf, -math.inf])
+def test_forward_few_routes_like_moe_route_whatever_the_logits(dtype, E, where, value):
+    """NaN of either sign and infinities in one expert's router row or bias, or in one token."""
+    c = Case(E, dtype, 5, 256, E, 128, 0, 4)
+    k, x = _k(c, 4), c.x
+    if where == "row":
+        t, at = c.router, (3, 7)
+    elif where == "bias":
+        t, at = torch.zeros(E, device=DEV), (3,)
+        c.bias = t
+    else:
+        t, at = c.x.clone(), (2, 3)
+        x = t
+    t[at] = math.nan if math.isnan(value) else value
+    if math.copysign(1.0, value) < 0 and math.isnan(value):
+        bits = t.view(torch.int32 if t.dtype == torch.float32 else torch.int16)
+        bits[at] = -(1 << 22) if t.dtype == torch.float32 else -(1 << 6)
+        assert t[at].isnan() and bits[at] < 0
+    stats = c.forward(k, x=x)[1].cpu().numpy()
+    counts, _ = _counts_of_route(c, x, k, None, c.bias)
+    np.testing.assert_array_equal(stats[:E], counts)
