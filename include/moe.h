@@ -764,8 +764,8 @@ moe_status moe_q4_linear(const moe_q4_desc* qd, int32_t rows, const void* x, con
  * names twice gets both weights.
  *   tok_off int32 [T+1], topk_ids int32 [T*k_max], topk_w float [T*k_max]: moe_route's
  *   CSR, at most k_max routes a token (offsets outside [0, T*k_max] are cut off)
- * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE (T or k_max too large, too), MOE_ERR_UNSUPPORTED,
- * MOE_ERR_ALIGN, MOE_ERR_WORKSPACE, MOE_ERR_LAUNCH.
+ * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE (T or k_max too large, outputs that overlap what the
+ * call reads, too), MOE_ERR_UNSUPPORTED, MOE_ERR_ALIGN, MOE_ERR_WORKSPACE, MOE_ERR_LAUNCH.
  */
 #define MOE_FEW_MAX_T 16
 typedef struct moe_few_q4 {
