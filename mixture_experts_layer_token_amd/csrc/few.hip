@@ -28,8 +28,7 @@
 //   16 tokens, 256 experts of 384 x 2048, budgets 0 to 32: 4.9 + 66 .. 82 + 35 .. 44 for 99 and 132
 //     experts, floors 65 and 87
 //   codes in groups of 64 with zero points, 8 tokens, 256 experts of 2048 x 7168: 6 + 170 .. 190
-//     + 69 .. 77 for 50 and 55 experts (190 .. 231 + 77 .. 85 on another card, whose clock was
-//     lower), floors 171 and 187
+//     + 69 .. 77 for 50 and 55 experts (190 .. 231 + 77 .. 85 in another run), floors 171 and 187
 // Three launches: one launch with a ticket a phase took 57 us for the one token and 410 for the
 // four, for its fences empty the caches and its workgroup fills a CU.
 //
